@@ -46,7 +46,7 @@ extern "C" {
 
 typedef struct tgrad_handle tgrad_t;
 
-/* Storage dtype of the weight and the gradient. Optimizer state is always fp32. */
+/* Storage dtype of the weight and the gradient. A tgrad_t's state is always fp32. */
 enum tgrad_dtype { TGRAD_F32 = 0, TGRAD_F16 = 1, TGRAD_BF16 = 2, TGRAD_C64 = 3 };
 
 enum tgrad_status {
@@ -385,6 +385,129 @@ int tgrad_timing_read(tgrad_t *h, int64_t *launches, double *ms, int n_ids);
  * again (the default). Errors: TGRAD_EINVAL (NULL handle, id out of range). */
 int tgrad_timing_only(tgrad_t *h, int id);
 const char *tgrad_kernel_name(int id);
+
+/* ---------------------------------------------------------------- the other tensors.
+ * AdamW over many tensors at once: the biases, norm weights and small products of a model
+ * whose large tensors the calls above optimise. One handle steps n tensors in one launch
+ * for every 240 of them; weights and gradients are the caller's and are passed to every
+ * call. Per value, each operation rounded to fp32:
+ *   g' = g * coefficient (see tgrad_adamw_grad_norm; g' = g without a clip)
+ *   m = b1 m + (1 - b1) g';   v = b2 v + (1 - b2) g'^2
+ *   w <- round(w * decay - (lr / (1 - b1^t)) m / (sqrt(v) / sqrt(1 - b2^t) + eps))
+ * with decay = fp32(1 - lr * weight_decay) and t the step's number, 1 for the first.
+ * complex64 tensors are taken as twice as many real values.
+ *
+ * The state is one flat device buffer of the caller's (tgrad_adamw_state_bytes, 16-byte
+ * aligned), zeroed for a new run or filled with a saved state before the first step. With
+ * S = tgrad_adamw_state_values, in which every tensor's values start at a multiple of 128:
+ *   state_bits 32:  m[S] and v[S], fp32.
+ *   state_bits 8:   m[S] and q[S] codes, one byte each, then ms[S/128] and qs[S/128], one
+ *     byte for every 128 of them. q is sqrt(v). A scale byte is the exponent field f of the
+ *     largest magnitude of its 128 values as fp32 (zero: 0); a code's value is 2^(f - 14)
+ *     times the fp32 number whose bits are code << 20 (m: sign in bit 7, the other 7 bits
+ *     shifted) or code << 19 (q). f = 255 stands for NaN in all 128 values; a value that is
+ *     not finite turns its group into that. Rounding is random and unbiased: to the bits of
+ *     the scaled value, h >> 12 (m) or h & 0x7FFFF (q) is added before the rest is cut off,
+ *     h = mix(place ^ key): h *= 0xBF58476D, h ^= h >> 16, h *= 0x94D049BB, h ^= h >> 13 in
+ *     32 bits, place the value's index in the flat state, key the low half of SplitMix64's
+ *     output for the state seed + t * 0x9E3779B97F4A7C15. A q above zero keeps code 1 at
+ *     least. The step itself uses m and v before they are rounded.
+ *
+ * The step number t is kept on the device and counts on under graph replay; tgrad_adamw_
+ * get_steps and set_steps read and write the steps made (both synchronise the device).
+ * As the other calls, one handle is used by one host thread and one stream at a time.
+ */
+typedef struct tgrad_adamw tgrad_adamw_t;
+
+/* Values of the flat state and its bytes; -1 for invalid sizes (n < 1, a negative numel or
+ * an unknown dtype or state_bits). Host only. */
+int64_t tgrad_adamw_state_values(int n, const int64_t *numel, const int *dtype);
+int64_t tgrad_adamw_state_bytes(int n, const int64_t *numel, const int *dtype, int state_bits);
+
+/*
+ * Create a handle on the current HIP device for n >= 1 tensors (synchronises the device).
+ *   numel[n]         elements of each, >= 0
+ *   dtype[n]         enum tgrad_dtype of the weights
+ *   grad_dtype[n]    of the gradients: the weight's, or TGRAD_F32 for a 16-bit weight
+ *   weight_decay[n]  of each tensor, >= 0
+ *   state_bits       32 or 8
+ *   lr, beta1, beta2, eps   lr >= 0, beta in [0, 1), eps >= 0; lr and eps finite
+ *   seed             of the 8-bit state's rounding
+ *   state            the buffer above; it must outlive the handle. Its contents are neither
+ *                    read nor written by this call.
+ * Errors: TGRAD_EINVAL, TGRAD_ENOMEM, TGRAD_EHIP. *out is NULL on error.
+ */
+int tgrad_adamw_init(tgrad_adamw_t **out, int n, const int64_t *numel, const int *dtype,
+                     const int *grad_dtype, const double *weight_decay, int state_bits, double lr,
+                     double beta1, double beta2, double eps, uint64_t seed, void *state);
+
+/* Free the handle's own device memory (the state stays the caller's). The caller
+ * synchronises first. NULL is a no-op. */
+int tgrad_adamw_destroy(tgrad_adamw_t *h);
+const char *tgrad_adamw_last_error(const tgrad_adamw_t *h);
+
+/* The learning rate from the next step on (>= 0, finite); a captured step keeps its own. */
+int tgrad_adamw_set_lr(tgrad_adamw_t *h, double lr);
+int tgrad_adamw_get_steps(tgrad_adamw_t *h, int64_t *steps);
+int tgrad_adamw_set_steps(tgrad_adamw_t *h, int64_t steps);
+
+/*
+ * One step of every tensor: weights[i] (updated in place) and grads[i] (only read) are
+ * device buffers of numel[i] contiguous elements aligned to their element's real part (both
+ * may be NULL where numel[i] is 0).
+ *   clip          NULL, or two device floats from tgrad_adamw_grad_norm: the gradients are
+ *                 multiplied by clip[1], and where the norm clip[0] is not finite the whole
+ *                 step is left out on the device: weights, state and t stay as they are.
+ *   m_out, v_out  both NULL, or (8-bit state) device buffers of S bf16 values, 16-byte
+ *                 aligned, distinct: the new m and sqrt(v) as the values that the stored
+ *                 codes stand for (at most 5 significant bits, so exact in bf16 above its
+ *                 subnormal range). Left alone where the step is left out.
+ * Errors: TGRAD_EINVAL (a NULL or misaligned argument), TGRAD_EHIP.
+ */
+int tgrad_adamw_step(tgrad_adamw_t *h, void *const *weights, const void *const *grads,
+                     const float *clip, void *m_out, void *v_out, void *stream);
+
+/*
+ * The norm of all gradients together, for clipping and loss scaling, without a host
+ * synchronisation: out[0] = norm = grad_scale * sqrt(sum g^2), out[1] = the coefficient
+ * grad_scale * min(1, max_norm / norm) that turns the gradients as they are into scaled and
+ * clipped ones. The sum is in fp64 and in a fixed order. max_norm > 0 (INFINITY: no
+ * clipping), grad_scale > 0 and finite (1 over the loss scale). out: two device floats.
+ * Errors: TGRAD_EINVAL, TGRAD_EHIP.
+ */
+int tgrad_adamw_grad_norm(tgrad_adamw_t *h, const void *const *grads, double max_norm,
+                          double grad_scale, float *out, void *stream);
+
+/*
+ * Layer norm over the last axis of `rows` rows of `cols` elements, and its gradients; the
+ * weight's and the bias's are among the tensors of a tgrad_adamw_t. Statistics and sums are
+ * fp32, each result is rounded once:
+ *   mean = sum x / cols;  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps);  n = (x - mean) rstd
+ *   y = n weight + bias
+ *   dx = rstd (h - mean(h) - n mean(h n)),  h = dy weight
+ *   dweight = sum over rows of dy n,  dbias = sum over rows of dy
+ * The sums over rows are formed in a fixed order.
+ *   x, dy           device, rows x_stride (dy_stride) >= cols elements apart
+ *   y, dx           device, contiguous
+ *   mean, rstd      device, rows floats: written by forward, read by backward
+ *   weight, bias    device, cols elements of weight_dtype; NULL: 1 and 0
+ *   dweight, dbias  device, cols elements of weight_dtype, each may be NULL
+ *   dtype           TGRAD_F32, TGRAD_F16 or TGRAD_BF16 of x, y, dy and dx
+ *   weight_dtype    the same, or TGRAD_F32
+ *   workspace       device, tgrad_layer_norm_workspace bytes, 16-byte aligned; only needed
+ *                   for dweight or dbias. It may be reused once the stream's work is done.
+ * rows = 0 is valid (dweight and dbias become 0). cols >= 1. Every pointer is aligned to its
+ * element. Errors: TGRAD_EINVAL, TGRAD_EHIP.
+ */
+int tgrad_layer_norm_forward(const void *x, int64_t x_stride, const void *weight, const void *bias,
+                             void *y, float *mean, float *rstd, int64_t rows, int64_t cols,
+                             int dtype, int weight_dtype, double eps, void *stream);
+/* Bytes of the workspace; -1 for invalid sizes. Host only. */
+int64_t tgrad_layer_norm_workspace(int64_t rows, int64_t cols);
+int tgrad_layer_norm_backward(const void *dy, int64_t dy_stride, const void *x, int64_t x_stride,
+                              const void *weight, const float *mean, const float *rstd, void *dx,
+                              void *dweight, void *dbias, int64_t rows, int64_t cols, int dtype,
+                              int weight_dtype, void *workspace, void *stream);
 
 #ifdef __cplusplus
 }

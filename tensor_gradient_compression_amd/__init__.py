@@ -4,6 +4,10 @@ Argument marshalling only: every step of the optimizer runs in the HIP kernels o
 libtgrad.so (built in-tree by tensor_gradient_compression_amd.build). PyTorch supplies
 device memory and the current stream. Loading fails loudly when the library is
 missing; there is no CPU fallback.
+
+TGrad and step_many optimise large weight tensors in a compressed space; AdamW steps all the
+other tensors of a model at once; layer_norm (and its two parts, layer_norm_forward and
+layer_norm_backward) is the normalisation whose small weights are among those.
 """
 from __future__ import annotations
 
@@ -98,6 +102,28 @@ SIGNATURES = [
     ("tgrad_timing_read", ctypes.c_int, [_P, _P, _P, ctypes.c_int]),
     ("tgrad_timing_only", ctypes.c_int, [_P, ctypes.c_int]),
     ("tgrad_kernel_name", ctypes.c_char_p, [ctypes.c_int]),
+    ("tgrad_adamw_state_values", _I64, [ctypes.c_int, ctypes.POINTER(_I64),
+                                        ctypes.POINTER(ctypes.c_int)]),
+    ("tgrad_adamw_state_bytes", _I64, [ctypes.c_int, ctypes.POINTER(_I64),
+                                       ctypes.POINTER(ctypes.c_int), ctypes.c_int]),
+    ("tgrad_adamw_init", ctypes.c_int, [ctypes.POINTER(_P), ctypes.c_int, ctypes.POINTER(_I64),
+                                        ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int),
+                                        ctypes.POINTER(ctypes.c_double), ctypes.c_int,
+                                        ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                        ctypes.c_double, ctypes.c_uint64, _P]),
+    ("tgrad_adamw_destroy", ctypes.c_int, [_P]),
+    ("tgrad_adamw_last_error", ctypes.c_char_p, [_P]),
+    ("tgrad_adamw_set_lr", ctypes.c_int, [_P, ctypes.c_double]),
+    ("tgrad_adamw_get_steps", ctypes.c_int, [_P, ctypes.POINTER(_I64)]),
+    ("tgrad_adamw_set_steps", ctypes.c_int, [_P, _I64]),
+    ("tgrad_adamw_step", ctypes.c_int, [_P, ctypes.POINTER(_P), ctypes.POINTER(_P), _P, _P, _P, _P]),
+    ("tgrad_adamw_grad_norm", ctypes.c_int, [_P, ctypes.POINTER(_P), ctypes.c_double,
+                                             ctypes.c_double, _P, _P]),
+    ("tgrad_layer_norm_forward", ctypes.c_int, [_P, _I64, _P, _P, _P, _P, _P, _I64, _I64,
+                                                ctypes.c_int, ctypes.c_int, ctypes.c_double, _P]),
+    ("tgrad_layer_norm_workspace", _I64, [_I64, _I64]),
+    ("tgrad_layer_norm_backward", ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _I64,
+                                                 _I64, ctypes.c_int, ctypes.c_int, _P, _P]),
 ]
 
 
@@ -115,6 +141,25 @@ def load_library(path: str = LIB_PATH):
         fn.argtypes = args
     _lib = lib
     return lib
+
+
+_binding = None
+
+
+def binding():
+    """The native part of this binding that unpacks torch tensors (csrc/binding.cpp)."""
+    global _binding
+    if _binding is None:
+        load_library()
+        import torch  # noqa: F401  (the binding links against its libraries)
+        try:
+            from . import _tgrad_torch
+        except ImportError as e:
+            raise TGradError(f"the torch binding is not built ({e}); run "
+                             "`python -m tensor_gradient_compression_amd.build`") from e
+        _tgrad_torch.set_error(TGradError)
+        _binding = _tgrad_torch
+    return _binding
 
 
 def kernel_name(i: int) -> str:
@@ -465,3 +510,7 @@ def to_host(t, dtype: str) -> np.ndarray:
     if dtype == "bf16":
         return c.view(torch.int16).numpy().view(np.uint16).copy()
     return c.numpy().copy()
+
+
+from .adamw import AdamW  # noqa: E402
+from .layernorm import layer_norm, layer_norm_backward, layer_norm_forward  # noqa: E402

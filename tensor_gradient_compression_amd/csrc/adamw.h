@@ -1,0 +1,61 @@
+// AdamW over many tensors: what the host side (adamw.hip) and the kernels (k_adamw.hip)
+// share. gfx950 only.
+#pragma once
+#include "tg_common.h"
+
+namespace tg {
+
+// Values that share one scale of the 8-bit state; every tensor's state starts at a multiple.
+constexpr uint32_t ADAMW_GROUP = 128;
+// Tensors whose addresses one launch carries in its arguments (16 bytes each, under 4 KiB).
+constexpr int ADAMW_LAUNCH_TENSORS = 240;
+
+// A workgroup's share of one tensor: `n` values from `start` on, both multiples of
+// ADAMW_GROUP except the tensor's end. `state` is the place of the first in the flat state.
+struct AdamwChunk {
+  uint64_t start, state;
+  double wd;
+  uint32_t tensor, n;
+  uint32_t wdt, gdt;   // Dt of the weight and the gradient, DT_F32 for complex (its parts)
+};
+
+// What a workgroup knows of the step it makes next: its number t (the first is 1), the
+// powers b1^t and b2^t, and the corrections 1 / (1 - b1^t) and 1 / sqrt(1 - b2^t).
+struct AdamwClock {
+  int64_t t;
+  double p1, p2;
+  float ic1, is2;
+};
+
+struct AdamwTable {
+  void* w[ADAMW_LAUNCH_TENSORS];
+  const void* g[ADAMW_LAUNCH_TENSORS];
+};
+
+struct AdamwArgs {
+  const AdamwChunk* chunks;   // of this launch
+  AdamwClock* clocks;         // of this launch
+  uint32_t first_tensor;
+  uint32_t nchunks;
+  int bits;                   // 32 or 8
+  void* m;                    // fp32, or codes
+  void* v;                    // fp32, or codes of sqrt(v)
+  uint8_t* ms;                // 8 bits: the groups' exponent fields
+  uint8_t* vs;
+  uint16_t* m_out;            // 8 bits, or NULL: the new values as bf16
+  uint16_t* v_out;
+  const float* clip;          // NULL, or {norm, coefficient}
+  double lr, b1d, b2d;
+  uint64_t seed;
+  float b1, c1, b2, c2, eps;
+};
+
+hipError_t launch_adamw(const AdamwArgs& a, const AdamwTable& tab, hipStream_t s);
+// partial[i] = the sum of the squares of chunk i's gradients, for the chunks of a launch
+hipError_t launch_adamw_squares(const AdamwChunk* chunks, uint32_t first_tensor, uint32_t nchunks,
+                                const AdamwTable& tab, double* partial, hipStream_t s);
+// out = {norm * scale, scale * min(1, max_norm / (norm * scale))}, norm = sqrt(sum partial)
+hipError_t launch_adamw_norm(const double* partial, uint32_t n, double max_norm, double scale,
+                             float* out, hipStream_t s);
+
+}  // namespace tg

@@ -1,0 +1,223 @@
+"""GPU: layer norm and its gradients against the 64-bit oracle.
+
+The bounds are a priori ones of oracle/layernorm_oracle.py: no sum of a row meets more than
+cols / 64 + 16 additions in a lane and across lanes, and no sum over rows more than rows + 16,
+whatever the kernel's division of the work."""
+import numpy as np
+import pytest
+
+import oracle.layernorm_oracle as L
+import tensor_gradient_compression_amd as tg
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-5
+TYPES = [("f32", "f32"), ("f16", "f32"), ("f16", "f16"), ("bf16", "f32"), ("bf16", "bf16")]
+SHAPES = [(1, 1), (3, 2), (5, 7), (64, 64), (33, 65), (257, 128), (4, 255), (130, 256), (9, 257), (1, 513),
+          (70, 1000), (300, 1024), (6, 1026), (2, 2048), (3, 4099), (5, 8192), (2, 16384), (3, 16385), (1, 70001)]
+
+
+def host(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def inputs(rows, cols, dtype, wdtype, seed, shift=0.5, offset=0, gap=0):
+    """x with rows of their own level, dy, weight, bias; x and dy start `offset` elements into
+    their allocation and have `gap` unused elements between rows."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def normal(*s):
+        return torch.randn(*s, generator=gen, device="cuda")
+
+    def rows_in(t):
+        buf = torch.full((rows * (cols + gap) + offset,), float("nan"), device="cuda").to(tg.torch_dtype(dtype))
+        v = buf[offset:].view(rows, cols + gap)[:, :cols]
+        v.copy_(t)
+        return v
+
+    x = rows_in(normal(rows, cols) * torch.exp(normal(rows, 1)) + shift * normal(rows, 1))
+    dy = rows_in(normal(rows, cols))
+    w = (1 + 0.2 * normal(cols)).to(tg.torch_dtype(wdtype))
+    b = (0.2 * normal(cols)).to(tg.torch_dtype(wdtype))
+    return x, dy, w, b
+
+
+def close(got, true, bound, what):
+    off = np.abs(host(got) - true)
+    assert np.all(off <= bound), f"{what}: {np.nanmax(off / bound):.3g} of the bound"
+
+
+def check(x, dy, w, b, dtype, wdtype, params=True, eps=EPS):
+    rows, cols = x.shape
+    seq = cols / 64 + 16
+    X, W, B = host(x), host(w), host(b)
+    y, mean, rstd = tg.layer_norm_forward(x, w, b, eps=eps)
+    assert y.dtype == x.dtype and y.shape == x.shape and mean.shape == rstd.shape == (rows,)
+    for got, true, bound, what in zip((y, mean, rstd), L.forward(X, W, B, eps),
+                                      L.forward_bounds(X, W, B, eps, dtype, seq), ("y", "mean", "rstd")):
+        close(got, true, bound, what)
+    dx, dw, db = tg.layer_norm_backward(dy, x, w, mean, rstd, params=params)
+    assert dx.dtype == x.dtype and dx.shape == x.shape
+    true = L.backward(host(dy), X, W, host(mean), host(rstd))
+    bounds = L.backward_bounds(host(dy), X, W, host(mean), host(rstd), dtype, wdtype, seq, rows + 16)
+    close(dx, true[0], bounds[0], "dx")
+    if not params:
+        assert dw is None and db is None
+        return
+    assert dw.dtype == db.dtype == (w if w is not None else x).dtype
+    close(dw, true[1], bounds[1], "dweight")
+    close(db, true[2], bounds[2], "dbias")
+
+
+@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("dtype,wdtype", TYPES)
+def test_against_the_oracle(rows, cols, dtype, wdtype):
+    print(f"CASE layer norm {rows} x {cols} {dtype} {wdtype}", flush=True)
+    check(*inputs(rows, cols, dtype, wdtype, seed=rows + cols), dtype, wdtype)
+
+
+@pytest.mark.parametrize("rows,cols", [(5, 64), (7, 333), (40, 1024), (3, 8192), (2, 20000)])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("offset,gap", [(1, 0), (0, 1), (3, 5), (0, 8), (8, 64)])
+def test_rows_apart_and_unaligned(rows, cols, dtype, offset, gap):
+    check(*inputs(rows, cols, dtype, dtype, seed=1, offset=offset, gap=gap), dtype, dtype)
+
+
+@pytest.mark.parametrize("cols", [64, 1000, 8192])
+def test_without_weight_bias_or_parameter_gradients(cols):
+    x, dy, w, b = inputs(37, cols, "bf16", "f32", seed=2)
+    check(x, dy, None, None, "bf16", "bf16")
+    check(x, dy, w, None, "bf16", "f32")
+    check(x, dy, w, b, "bf16", "f32", params=False)
+    y0, mean, rstd = tg.layer_norm_forward(x, None, b)
+    close(y0, L.forward(host(x), None, host(b), EPS)[0], L.forward_bounds(host(x), None, host(b), EPS, "bf16", cols / 64 + 16)[0], "y")
+
+
+@pytest.mark.parametrize("rows,cols", [(70000, 8), (66000, 64), (4097, 256), (2500, 1024)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_rows(rows, cols, dtype):
+    check(*inputs(rows, cols, dtype, "f32", seed=3), dtype, "f32")
+
+
+@pytest.mark.parametrize("cols", [5, 256, 1024, 5000])
+def test_rows_far_from_zero(cols):
+    """A mean 1000 times the deviation: the bounds hold the variance to what the rounding of x's
+    own distances allows, which the mean of squares less the squared mean would not meet."""
+    check(*inputs(20, cols, "f32", "f32", seed=4, shift=1000.0), "f32", "f32")
+
+
+@pytest.mark.parametrize("cols", [1, 3, 256, 3000])
+def test_constant_rows(cols):
+    """A variance of zero: n is 0, y the bias, rstd 1 / sqrt(eps)."""
+    x = torch.full((6, cols), 0.5, device="cuda")
+    _, dy, w, b = inputs(6, cols, "f32", "f32", seed=5)
+    y, mean, rstd = tg.layer_norm_forward(x, w, b, eps=EPS)
+    assert torch.equal(y, b.expand(6, cols)) and torch.equal(mean, torch.full((6,), 0.5, device="cuda"))
+    assert abs(float(rstd[0]) * np.sqrt(EPS) - 1) < 4 * L.EPS32
+    check(x, dy, w, b, "f32", "f32")
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("cols", [64, 1000, 8192])
+def test_rows_that_are_not_finite_stay_apart(bad, cols):
+    x, dy, w, b = inputs(9, cols, "f32", "f32", seed=6)
+    x[4, 3] = bad
+    y, mean, rstd = tg.layer_norm_forward(x, w, b)
+    dx, _, db = tg.layer_norm_backward(dy, x, w, mean, rstd)
+    ok = [i for i in range(9) if i != 4]
+    assert bool(y[4].isnan().all()) and bool(y[ok].isfinite().all())
+    assert bool(dx[4].isnan().all()) and bool(dx[ok].isfinite().all()) and bool(db.isfinite().all())
+
+
+def test_no_rows():
+    for cols in (3, 1024):
+        x = torch.empty(0, cols, device="cuda")
+        w = torch.ones(cols, device="cuda")
+        y, mean, rstd = tg.layer_norm_forward(x, w, w)
+        dx, dw, db = tg.layer_norm_backward(x, x, w, mean, rstd)
+        assert y.shape == dx.shape == (0, cols) and mean.shape == (0,)
+        assert torch.equal(dw, torch.zeros_like(w)) and torch.equal(db, torch.zeros_like(w))
+
+
+def test_shapes_of_several_axes():
+    x, dy, w, b = inputs(6 * 5, 96, "bf16", "f32", seed=7)
+    y, mean, rstd = tg.layer_norm_forward(x, w, b)
+    x3 = x.reshape(6, 5, 96)
+    y3, mean3, rstd3 = tg.layer_norm_forward(x3, w, b)
+    assert torch.equal(y3.view(30, 96), y) and mean3.shape == (6, 5)
+    # every second row block of a larger tensor, and one row
+    z = torch.stack([x3, x3], 2)[:, :, 0]
+    assert torch.equal(tg.layer_norm_forward(z, w, b)[0], y3)
+    y1, m1, _ = tg.layer_norm_forward(x[0], w, b)
+    assert torch.equal(y1, y[0]) and m1.shape == ()
+    dx = tg.layer_norm_backward(dy.reshape(6, 5, 96), z, w, mean3, rstd3)[0]
+    assert torch.equal(dx.view(30, 96), tg.layer_norm_backward(dy, x, w, mean, rstd)[0])
+
+
+def test_sums_over_rows_repeat():
+    x, dy, w, b = inputs(5000, 300, "bf16", "f32", seed=8)
+    _, mean, rstd = tg.layer_norm_forward(x, w, b)
+    first = tg.layer_norm_backward(dy, x, w, mean, rstd)
+    for _ in range(3):
+        assert all(torch.equal(p, q) for p, q in zip(first, tg.layer_norm_backward(dy, x, w, mean, rstd)))
+
+
+def test_differentiable():
+    x, dy, w, b = inputs(50, 200, "f32", "f32", seed=9)
+    a = [t.clone().requires_grad_() for t in (x, w, b)]
+    tg.layer_norm(*a, eps=EPS).backward(dy)
+    _, mean, rstd = tg.layer_norm_forward(x, w, b, eps=EPS)
+    for t, g in zip(a, tg.layer_norm_backward(dy, x, w, mean, rstd)):
+        assert torch.equal(t.grad, g)
+    # an expanded gradient, and inputs that need none
+    x2 = x.clone().requires_grad_()
+    tg.layer_norm(x2).sum().backward()
+    assert float(x2.grad.abs().max()) < 1e-4
+    w2 = w.clone().requires_grad_()
+    tg.layer_norm(x, w2, b).sum().backward()
+    assert w2.grad is not None
+
+
+def test_another_stream_and_graph_replay():
+    x, dy, w, b = inputs(500, 256, "bf16", "f32", seed=10)
+    eager = tg.layer_norm_forward(x, w, b)
+    back = tg.layer_norm_backward(dy, x, w, *eager[1:])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = tg.layer_norm_forward(x, w, b)
+        got += tg.layer_norm_backward(dy, x, w, *got[1:])
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(p, q) for p, q in zip(eager + back, got))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = tg.layer_norm_forward(x, w, b)
+        out += tg.layer_norm_backward(dy, x, w, *out[1:])
+    for k in range(4):
+        x.mul_(1.5)
+        graph.replay()
+        eager = tg.layer_norm_forward(x, w, b)
+        eager += tg.layer_norm_backward(dy, x, w, *eager[1:])
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(eager, out)), f"replay {k}"
+
+
+def test_refusals():
+    x, dy, w, b = inputs(4, 32, "bf16", "f32", seed=11)
+    _, mean, rstd = tg.layer_norm_forward(x, w, b)
+    half = w.half()
+    for args, what in (((x.cpu(), w, b), "GPU"), ((x.double(), w, b), "dtype"), ((x, w[:31], b), "weight"),
+                       ((x, half, half), "weight"), ((x, w, b.bfloat16()), "bias"), ((x.t(), w, b), "last axis"),
+                       ((x[:, :0], None, None), "empty"), ((x, w.cpu(), b), "weight"),
+                       ((torch.zeros(32, 4, 4, device="cuda").transpose(0, 1).expand(4, 32, 4), None, None), "strides"),
+                       ((x[:1].expand(4, 32), w, b), "overlap")):
+        with pytest.raises(ValueError, match=what):
+            tg.layer_norm_forward(*args)
+    with pytest.raises(tg.TGradError, match="invalid argument"):
+        tg.layer_norm_forward(x, w, b, eps=-1.0)
+    for args, what in (((dy[:3], x, w, mean, rstd), "dy"), ((dy.float(), x, w, mean, rstd), "dy"),
+                       ((dy, x, w, mean[:3], rstd), "mean"), ((dy, x, w, mean, rstd.double()), "rstd")):
+        with pytest.raises(ValueError, match=what):
+            tg.layer_norm_backward(*args)
