@@ -10,8 +10,11 @@ constexpr uint32_t ADAMW_GROUP = 128;
 // Tensors whose addresses one launch carries in its arguments (16 bytes each, under 4 KiB).
 constexpr int ADAMW_LAUNCH_TENSORS = 240;
 
-// A workgroup's share of one tensor: `n` values from `start` on, both multiples of
-// ADAMW_GROUP except the tensor's end. `state` is the place of the first in the flat state.
+// Values that one workgroup steps.
+constexpr uint32_t ADAMW_CHUNK = 2048;
+
+// A workgroup's share of one tensor: `n` values from `start` on, all of them multiples of
+// ADAMW_CHUNK except the tensor's end. `state` is the place of the first in the flat state.
 struct AdamwChunk {
   uint64_t start, state;
   double wd;
@@ -19,13 +22,28 @@ struct AdamwChunk {
   uint32_t wdt, gdt;   // Dt of the weight and the gradient, DT_F32 for complex (its parts)
 };
 
+// A workgroup's share of the sum of squares.
+struct AdamwSpan {
+  uint64_t start;
+  uint32_t tensor, n, gdt;
+};
+
 // What a workgroup knows of the step it makes next: its number t (the first is 1), the
-// powers b1^t and b2^t, and the corrections 1 / (1 - b1^t) and 1 / sqrt(1 - b2^t).
+// powers b1^t and b2^t, the corrections 1 / (1 - b1^t) and 1 / sqrt(1 - b2^t), and the key of
+// its random bits.
 struct AdamwClock {
   int64_t t;
   double p1, p2;
   float ic1, is2;
+  uint32_t key;
 };
+// SplitMix64's output for the state seed + t * 0x9E3779B97F4A7C15, its low half
+__host__ __device__ inline uint32_t adamw_step_key(uint64_t seed, uint64_t t) {
+  uint64_t z = seed + t * 0x9E3779B97F4A7C15ull;
+  z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+  z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+  return (uint32_t)(z ^ (z >> 31));
+}
 
 struct AdamwTable {
   void* w[ADAMW_LAUNCH_TENSORS];
@@ -51,8 +69,8 @@ struct AdamwArgs {
 };
 
 hipError_t launch_adamw(const AdamwArgs& a, const AdamwTable& tab, hipStream_t s);
-// partial[i] = the sum of the squares of chunk i's gradients, for the chunks of a launch
-hipError_t launch_adamw_squares(const AdamwChunk* chunks, uint32_t first_tensor, uint32_t nchunks,
+// partial[i] = the sum of the squares of span i's gradients, for the spans of a launch
+hipError_t launch_adamw_squares(const AdamwSpan* spans, uint32_t first_tensor, uint32_t nspans,
                                 const AdamwTable& tab, double* partial, hipStream_t s);
 // out = {norm * scale, scale * min(1, max_norm / (norm * scale))}, norm = sqrt(sum partial)
 hipError_t launch_adamw_norm(const double* partial, uint32_t n, double max_norm, double scale,

@@ -31,6 +31,7 @@ namespace tg {
 namespace {
 
 constexpr int kThreads = 256;
+static_assert(kThreads * 8 == ADAMW_CHUNK, "a workgroup steps its chunk in one pass");
 
 struct StepK {
   float b1, c1, b2, c2, eps, step, is2, decay, coef;
@@ -43,23 +44,41 @@ __device__ __forceinline__ float moments(float g, float& m, float& v, const Step
   return sqrtf(v);
 }
 __device__ __forceinline__ float updated(float w, float m, float q, const StepK& k) {
-  return w * k.decay - (k.step * m) / (q * k.is2 + k.eps);
+  return w * k.decay - (k.step * m) * __builtin_amdgcn_rcpf(q * k.is2 + k.eps);
 }
 
-// SplitMix64's output for the state seed + t * 0x9E3779B97F4A7C15, its low half: the step's
-// key. A value's 32 bits mix its place in the state with the key (two multiplications by the
-// high halves of the same function's constants).
-__device__ __forceinline__ uint32_t step_key(uint64_t seed, uint64_t t) {
-  uint64_t z = seed + t * 0x9E3779B97F4A7C15ull;
-  z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
-  z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
-  return (uint32_t)(z ^ (z >> 31));
-}
+// A value's 32 random bits: its place in the state mixed with the step's key (two
+// multiplications by the high halves of SplitMix64's constants).
 __device__ __forceinline__ uint32_t random_bits(uint32_t place, uint32_t key) {
   uint32_t h = (place ^ key) * 0xBF58476Du;
   h ^= h >> 16;
   h *= 0x94D049BBu;
   return h ^ (h >> 13);
+}
+
+// Whole accesses of 8 or 16 bytes, marked as not to be kept: a step touches every byte once,
+// and what the caches keep of it is gone before the next one.
+template <typename T, int N>
+struct Wide {
+  static constexpr int kBytes = N * sizeof(T) < 16 ? N * sizeof(T) : 16;
+  typedef uint32_t V __attribute__((ext_vector_type(kBytes / 4)));
+  static constexpr int kPieces = N * sizeof(T) / kBytes;
+};
+template <typename T, int N>
+__device__ __forceinline__ void load_wide(const T* __restrict__ p, T (&v)[N]) {
+  using W = Wide<T, N>;
+  typename W::V t[W::kPieces];
+#pragma unroll
+  for (int i = 0; i < W::kPieces; ++i) t[i] = __builtin_nontemporal_load((const typename W::V*)p + i);
+  __builtin_memcpy(v, t, sizeof v);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_wide(T* __restrict__ p, const T (&v)[N]) {
+  using W = Wide<T, N>;
+  typename W::V t[W::kPieces];
+  __builtin_memcpy(t, v, sizeof v);
+#pragma unroll
+  for (int i = 0; i < W::kPieces; ++i) __builtin_nontemporal_store(t[i], (typename W::V*)p + i);
 }
 
 // largest over the 16 lanes of a row, in all of them (rotations within the row)
@@ -74,169 +93,217 @@ __device__ __forceinline__ uint32_t nan_bits(uint32_t field) {
   return field == 255u ? 0x7FC00000u : 0u;
 }
 
-// N values from p on, of which `have` exist (the others read as zero and are not written);
-// ALIGNED: p is aligned to N values and N * sizeof(T) is 8, 16 or 32 bytes.
-template <int N, bool ALIGNED, typename T>
-__device__ __forceinline__ void load(const T* __restrict__ p, int have, float* x) {
-  if (ALIGNED && have >= N) {
-    T v[N];
-    __builtin_memcpy(v, __builtin_assume_aligned(p, N * sizeof(T) < 16 ? N * sizeof(T) : 16), sizeof v);
+// N values of a piece that may end early: `have` of them exist, the others read as zero and
+// are not written.
+template <int N, typename T>
+__device__ __forceinline__ void load_some(const T* __restrict__ p, int have, float* x) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = to_f32(v[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = j < have ? to_f32(p[j]) : 0.0f;
-  }
+  for (int j = 0; j < N; ++j) x[j] = j < have ? to_f32(p[j]) : 0.0f;
 }
-template <int N, bool ALIGNED, typename T>
-__device__ __forceinline__ void store(T* __restrict__ p, int have, const float* x) {
-  if (ALIGNED && have >= N) {
-    T v[N];
+template <int N, typename T>
+__device__ __forceinline__ void store_some(T* __restrict__ p, int have, const float* x) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = from_f32<T>(x[j]);
-    __builtin_memcpy(__builtin_assume_aligned(p, N * sizeof(T) < 16 ? N * sizeof(T) : 16), v, sizeof v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (j < have) p[j] = from_f32<T>(x[j]);
-  }
+  for (int j = 0; j < N; ++j)
+    if (j < have) p[j] = from_f32<T>(x[j]);
 }
 
-// fp32 moments: four values a thread and two such pieces a pass, so that a wave's accesses to
-// the moments are whole 1 KiB runs and both pieces' loads are in flight together.
-template <typename WT, typename GT, bool ALIGNED>
-__device__ __forceinline__ void chunk32(WT* __restrict__ w, const GT* __restrict__ g,
-                                        float* __restrict__ m, float* __restrict__ v, uint32_t n,
+// The weights and gradients of a chunk, two ways. A full chunk at 16-byte aligned addresses:
+// wide accesses of known types, converted apart from their loads, so that every load of the
+// chunk is in flight before the first is waited for.
+template <typename WT, typename GT>
+struct WholeChunk {
+  static constexpr bool kWhole = true;
+  WT* w;
+  const GT* g;
+  template <int N>
+  struct Raw {
+    WT w[N];
+    GT g[N];
+  };
+  template <int N>
+  __device__ __forceinline__ void load(uint32_t i, Raw<N>& r) const {
+    load_wide(w + i, r.w);
+    load_wide(g + i, r.g);
+  }
+  template <int N>
+  __device__ __forceinline__ void values(const Raw<N>& r, float* wx, float* gx) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      wx[j] = to_f32(r.w[j]);
+      gx[j] = to_f32(r.g[j]);
+    }
+  }
+  template <int N>
+  __device__ __forceinline__ void store(uint32_t i, const float* wx) const {
+    WT v[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = from_f32<WT>(wx[j]);
+    store_wide(w + i, v);
+  }
+};
+// A tensor's end, or one that is not aligned: value by value, of any types.
+struct PartChunk {
+  static constexpr bool kWhole = false;
+  void* w;
+  const void* g;
+  uint64_t start;
+  uint32_t n, wdt, gdt;
+  template <int N>
+  struct Raw {
+    float w[N], g[N];
+  };
+  template <int N>
+  __device__ __forceinline__ void load(uint32_t i, Raw<N>& r) const {
+    const int have = (int)n - (int)i;
+    const uint64_t at = start + i;
+    if (wdt == DT_F32) load_some<N>((const float*)w + at, have, r.w);
+    else if (wdt == DT_F16) load_some<N>((const _Float16*)w + at, have, r.w);
+    else load_some<N>((const bf16_t*)w + at, have, r.w);
+    if (gdt == DT_F32) load_some<N>((const float*)g + at, have, r.g);
+    else if (gdt == DT_F16) load_some<N>((const _Float16*)g + at, have, r.g);
+    else load_some<N>((const bf16_t*)g + at, have, r.g);
+  }
+  template <int N>
+  __device__ __forceinline__ void values(const Raw<N>& r, float* wx, float* gx) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      wx[j] = r.w[j];
+      gx[j] = r.g[j];
+    }
+  }
+  template <int N>
+  __device__ __forceinline__ void store(uint32_t i, const float* wx) const {
+    const int have = (int)n - (int)i;
+    const uint64_t at = start + i;
+    if (wdt == DT_F32) store_some<N>((float*)w + at, have, wx);
+    else if (wdt == DT_F16) store_some<N>((_Float16*)w + at, have, wx);
+    else store_some<N>((bf16_t*)w + at, have, wx);
+  }
+};
+
+// fp32 moments: two pieces of four values a thread, so that a wave's accesses to the moments
+// are whole 1 KiB runs and all loads of both pieces are in flight together.
+template <typename Chunk>
+__device__ __forceinline__ void chunk32(const AdamwArgs& a, const AdamwChunk& c, const Chunk& io,
                                         const StepK& k, bool skip) {
-  for (uint32_t base = threadIdx.x * 4; base < n; base += kThreads * 8) {
-    float wx[2][4], gx[2][4], mx[2][4], vx[2][4];
+  float* m = (float*)a.m + c.state;
+  float* v = (float*)a.v + c.state;
+  typename Chunk::template Raw<4> raw[2];
+  float mx[2][4], vx[2][4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint32_t i = base + u * kThreads * 4;
-      if (i >= n) break;
-      load<4, ALIGNED>(w + i, (int)(n - i), wx[u]);
-      load<4, ALIGNED>(g + i, (int)(n - i), gx[u]);
-      load<4, true>(m + i, 4, mx[u]);
-      load<4, true>(v + i, 4, vx[u]);
+  for (int u = 0; u < 2; ++u) {
+    const uint32_t i = (u * kThreads + threadIdx.x) * 4;
+    if (!Chunk::kWhole && i >= c.n) break;
+    load_wide(m + i, mx[u]);
+    load_wide(v + i, vx[u]);
+    io.load(i, raw[u]);
+  }
+  if (skip) return;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint32_t i = (u * kThreads + threadIdx.x) * 4;
+    if (!Chunk::kWhole && i >= c.n) break;
+    float wx[4], gx[4];
+    io.values(raw[u], wx, gx);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float q = moments(gx[j], mx[u][j], vx[u][j], k);
+      wx[j] = updated(wx[j], mx[u][j], q, k);
     }
-    if (skip) continue;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint32_t i = base + u * kThreads * 4;
-      if (i >= n) break;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float q = moments(gx[u][j], mx[u][j], vx[u][j], k);
-        wx[u][j] = updated(wx[u][j], mx[u][j], q, k);
-      }
-      store<4, ALIGNED>(w + i, (int)(n - i), wx[u]);
-      store<4, true>(m + i, 4, mx[u]);
-      store<4, true>(v + i, 4, vx[u]);
-    }
+    io.template store<4>(i, wx);
+    store_wide(m + i, mx[u]);
+    store_wide(v + i, vx[u]);
   }
 }
 
 // 8-bit moments: 16 lanes hold a group, 8 values each
-template <typename WT, typename GT, bool ALIGNED, bool VALUES>
-__device__ __forceinline__ void chunk8(WT* __restrict__ w, const GT* __restrict__ g,
-                                       uint8_t* __restrict__ mc, uint8_t* __restrict__ qc,
-                                       uint8_t* __restrict__ ms, uint8_t* __restrict__ qs,
-                                       uint16_t* __restrict__ mo, uint16_t* __restrict__ qo,
-                                       uint32_t n, uint32_t place, uint32_t key, const StepK& k,
-                                       bool skip) {
-  const uint32_t end = (n + ADAMW_GROUP - 1) / ADAMW_GROUP * ADAMW_GROUP;
-  for (uint32_t i = threadIdx.x * 8; i < end; i += kThreads * 8) {
-    const uint32_t grp = i / ADAMW_GROUP;
-    const int have = (int)n - (int)i;
-    float wx[8], gx[8], m[8], q[8];
-    load<8, ALIGNED>(w + i, have, wx);
-    load<8, ALIGNED>(g + i, have, gx);
-    uint2 cm = *(const uint2*)(mc + i), cq = *(const uint2*)(qc + i);
-    const int fm = ms[grp], fq = qs[grp];
-    if (skip) continue;
-    const uint32_t nan_m = nan_bits(fm), nan_q = nan_bits(fq);
-    uint32_t tm = 0, tq = 0;
+template <bool VALUES, typename Chunk>
+__device__ __forceinline__ void chunk8(const AdamwArgs& a, const AdamwChunk& c, const Chunk& io,
+                                       uint32_t key, const StepK& k, bool skip) {
+  const uint32_t i = threadIdx.x * 8;
+  if (!Chunk::kWhole && i >= (c.n + ADAMW_GROUP - 1) / ADAMW_GROUP * ADAMW_GROUP) return;
+  const uint64_t at = c.state + i;
+  uint2* mc = (uint2*)((uint8_t*)a.m + at);
+  uint2* qc = (uint2*)((uint8_t*)a.v + at);
+  uint8_t *ms = a.ms + at / ADAMW_GROUP, *qs = a.vs + at / ADAMW_GROUP;
+  uint2 cm = *mc, cq = *qc;
+  const int fm = *ms, fq = *qs;
+  typename Chunk::template Raw<8> raw;
+  io.load(i, raw);
+  if (skip) return;
+  float wx[8], gx[8], m[8], q[8];
+  io.values(raw, wx, gx);
+  const uint32_t nan_m = nan_bits(fm), nan_q = nan_bits(fq);
+  uint32_t tm = 0, tq = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t x = (j < 4 ? cm.x : cm.y) >> (8 * (j & 3)), y = (j < 4 ? cq.x : cq.y) >> (8 * (j & 3));
+    m[j] = ldexpf(__uint_as_float(((x & 127u) << 20) | ((x & 128u) << 24) | nan_m), fm - 14);
+    const float old = ldexpf(__uint_as_float(((y & 255u) << 19) | nan_q), fq - 14);
+    float v = old * old;
+    q[j] = moments(gx[j], m[j], v, k);
+    wx[j] = updated(wx[j], m[j], q[j], k);
+    tm = max(tm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
+    tq = max(tq, __float_as_uint(q[j]) & 0x7FFFFFFFu);
+  }
+  io.template store<8>(i, wx);
+  const int nm = (int)(row_max(tm) >> 23), nq = (int)(row_max(tq) >> 23);
+  uint32_t ym[8], yq[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t h = random_bits((uint32_t)at + j, key);
+    // the sign stays in bit 31: a code's magnitude ends below bit 27, and so does the sum
+    ym[j] = __float_as_uint(ldexpf(m[j], 14 - nm)) + (h >> 12);
+    yq[j] = __float_as_uint(ldexpf(q[j], 14 - nq)) + (h & 0x7FFFFu);
+    // a q above zero is above 2^-75, so its bits are more than the least code's
+    yq[j] = max(yq[j], min(__float_as_uint(q[j]), 1u << 19));
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t x = ((ym[j] >> 20) & 127u) | ((ym[j] >> 24) & 128u), y = (yq[j] >> 19) & 255u;
+    uint32_t &mw = j < 4 ? cm.x : cm.y, &qw = j < 4 ? cq.x : cq.y;
+    mw = (j & 3) ? mw | x << (8 * (j & 3)) : x;
+    qw = (j & 3) ? qw | y << (8 * (j & 3)) : y;
+  }
+  *mc = cm;
+  *qc = cq;
+  if ((threadIdx.x & 15) == 0) {
+    *ms = (uint8_t)nm;
+    *qs = (uint8_t)nq;
+  }
+  if (VALUES) {
+    // at most five significant bits: the upper half of the fp32 value is the bf16 one
+    uint32_t om[8], oq[8];
+    const uint32_t new_nan_m = nan_bits(nm), new_nan_q = nan_bits(nq);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t a = (j < 4 ? cm.x : cm.y) >> (8 * (j & 3)), b = (j < 4 ? cq.x : cq.y) >> (8 * (j & 3));
-      m[j] = ldexpf(__uint_as_float(((a & 127u) << 20) | ((a & 128u) << 24) | nan_m), fm - 14);
-      const float old = ldexpf(__uint_as_float(((b & 255u) << 19) | nan_q), fq - 14);
-      float v = old * old;
-      q[j] = moments(gx[j], m[j], v, k);
-      wx[j] = updated(wx[j], m[j], q[j], k);
-      tm = max(tm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
-      tq = max(tq, __float_as_uint(q[j]) & 0x7FFFFFFFu);
+      om[j] = __float_as_uint(ldexpf(__uint_as_float((ym[j] & 0x87F00000u) | new_nan_m), nm - 14));
+      oq[j] = __float_as_uint(ldexpf(__uint_as_float((yq[j] & 0x07F80000u) | new_nan_q), nq - 14));
     }
-    store<8, ALIGNED>(w + i, have, wx);
-    const int nm = (int)(row_max(tm) >> 23), nq = (int)(row_max(tq) >> 23);
-    uint32_t ym[8], yq[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t h = random_bits(place + i + j, key);
-      // the sign stays in bit 31: a code's magnitude ends below bit 27, and so does the sum
-      ym[j] = __float_as_uint(ldexpf(m[j], 14 - nm)) + (h >> 12);
-      yq[j] = __float_as_uint(ldexpf(q[j], 14 - nq)) + (h & 0x7FFFFu);
-      // a q above zero is above 2^-75, so its bits are more than the least code's
-      yq[j] = max(yq[j], min(__float_as_uint(q[j]), 1u << 19));
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t a = ((ym[j] >> 20) & 127u) | ((ym[j] >> 24) & 128u), b = (yq[j] >> 19) & 255u;
-      uint32_t &x = j < 4 ? cm.x : cm.y, &y = j < 4 ? cq.x : cq.y;
-      x = (j & 3) ? x | a << (8 * (j & 3)) : a;
-      y = (j & 3) ? y | b << (8 * (j & 3)) : b;
-    }
-    *(uint2*)(mc + i) = cm;
-    *(uint2*)(qc + i) = cq;
-    if ((threadIdx.x & 15) == 0) {
-      ms[grp] = (uint8_t)nm;
-      qs[grp] = (uint8_t)nq;
-    }
-    if (VALUES) {
-      // at most five significant bits: the upper half of the fp32 value is the bf16 one
-      uint32_t om[8], oq[8];
-      const uint32_t new_nan_m = nan_bits(nm), new_nan_q = nan_bits(nq);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        om[j] = __float_as_uint(ldexpf(__uint_as_float((ym[j] & 0x87F00000u) | new_nan_m), nm - 14));
-        oq[j] = __float_as_uint(ldexpf(__uint_as_float((yq[j] & 0x07F80000u) | new_nan_q), nq - 14));
-      }
-      uint4 a, b;
-      a.x = __builtin_amdgcn_perm(om[1], om[0], 0x07060302u);
-      a.y = __builtin_amdgcn_perm(om[3], om[2], 0x07060302u);
-      a.z = __builtin_amdgcn_perm(om[5], om[4], 0x07060302u);
-      a.w = __builtin_amdgcn_perm(om[7], om[6], 0x07060302u);
-      b.x = __builtin_amdgcn_perm(oq[1], oq[0], 0x07060302u);
-      b.y = __builtin_amdgcn_perm(oq[3], oq[2], 0x07060302u);
-      b.z = __builtin_amdgcn_perm(oq[5], oq[4], 0x07060302u);
-      b.w = __builtin_amdgcn_perm(oq[7], oq[6], 0x07060302u);
-      *(uint4*)(mo + i) = a;
-      *(uint4*)(qo + i) = b;
-    }
+    uint4 x, y;
+    x.x = __builtin_amdgcn_perm(om[1], om[0], 0x07060302u);
+    x.y = __builtin_amdgcn_perm(om[3], om[2], 0x07060302u);
+    x.z = __builtin_amdgcn_perm(om[5], om[4], 0x07060302u);
+    x.w = __builtin_amdgcn_perm(om[7], om[6], 0x07060302u);
+    y.x = __builtin_amdgcn_perm(oq[1], oq[0], 0x07060302u);
+    y.y = __builtin_amdgcn_perm(oq[3], oq[2], 0x07060302u);
+    y.z = __builtin_amdgcn_perm(oq[5], oq[4], 0x07060302u);
+    y.w = __builtin_amdgcn_perm(oq[7], oq[6], 0x07060302u);
+    *(uint4*)(a.m_out + at) = x;
+    *(uint4*)(a.v_out + at) = y;
   }
 }
 
-template <int BITS, bool VALUES, typename WT, typename GT, bool ALIGNED>
-__device__ __forceinline__ void chunk_as(const AdamwArgs& a, const AdamwChunk& c, WT* w, const GT* g,
-                                         uint32_t key, const StepK& k, bool skip) {
-  if (BITS == 32)
-    chunk32<WT, GT, ALIGNED>(w, g, (float*)a.m + c.state, (float*)a.v + c.state, c.n, k, skip);
-  else
-    chunk8<WT, GT, ALIGNED, VALUES>(w, g, (uint8_t*)a.m + c.state, (uint8_t*)a.v + c.state,
-                                    a.ms + c.state / ADAMW_GROUP, a.vs + c.state / ADAMW_GROUP,
-                                    a.m_out + c.state, a.v_out + c.state, c.n, (uint32_t)c.state, key, k,
-                                    skip);
-}
-
-// Wide accesses where both addresses allow them: chunks start at multiples of 128 values, so
-// the tensors' own addresses decide.
-template <int BITS, bool VALUES, typename WT, typename GT>
-__device__ __forceinline__ void chunk(const AdamwArgs& a, const AdamwChunk& c, void* w, const void* g,
+template <int BITS, bool VALUES, typename Chunk>
+__device__ __forceinline__ void chunk(const AdamwArgs& a, const AdamwChunk& c, const Chunk& io,
                                       uint32_t key, const StepK& k, bool skip) {
-  if ((((uintptr_t)w | (uintptr_t)g) & 15u) == 0)
-    chunk_as<BITS, VALUES, WT, GT, true>(a, c, (WT*)w + c.start, (const GT*)g + c.start, key, k, skip);
-  else
-    chunk_as<BITS, VALUES, WT, GT, false>(a, c, (WT*)w + c.start, (const GT*)g + c.start, key, k, skip);
+  if (BITS == 32) chunk32(a, c, io, k, skip);
+  else chunk8<VALUES>(a, c, io, key, k, skip);
+}
+template <int BITS, bool VALUES, typename WT, typename GT>
+__device__ __forceinline__ void whole(const AdamwArgs& a, const AdamwChunk& c, void* w, const void* g,
+                                      uint32_t key, const StepK& k, bool skip) {
+  chunk<BITS, VALUES>(a, c, WholeChunk<WT, GT>{(WT*)w + c.start, (const GT*)g + c.start}, key, k, skip);
 }
 
 template <int BITS, bool VALUES>
@@ -245,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) k_adamw(AdamwArgs a, AdamwTable tab)
   const AdamwClock now = a.clocks[blockIdx.x];
   StepK k;
   k.coef = 1.0f;
-  // a norm that is not finite: some gradient is not, and the step is left out. The chunks'
+  // a norm that is not finite: some gradient is not, and the step is left out. The chunk's
   // loads do not wait for that.
   bool skip = false;
   if (a.clip) {
@@ -262,12 +329,13 @@ __global__ void __launch_bounds__(kThreads) k_adamw(AdamwArgs a, AdamwTable tab)
   k.decay = (float)(1.0 - a.lr * c.wd);
   void* w = tab.w[c.tensor - a.first_tensor];
   const void* g = tab.g[c.tensor - a.first_tensor];
-  const uint32_t key = BITS == 8 ? step_key(a.seed, (uint64_t)now.t) : 0;
-  if (c.wdt == DT_F32) chunk<BITS, VALUES, float, float>(a, c, w, g, key, k, skip);
-  else if (c.wdt == DT_F16 && c.gdt == DT_F16) chunk<BITS, VALUES, _Float16, _Float16>(a, c, w, g, key, k, skip);
-  else if (c.wdt == DT_F16) chunk<BITS, VALUES, _Float16, float>(a, c, w, g, key, k, skip);
-  else if (c.gdt == DT_BF16) chunk<BITS, VALUES, bf16_t, bf16_t>(a, c, w, g, key, k, skip);
-  else chunk<BITS, VALUES, bf16_t, float>(a, c, w, g, key, k, skip);
+  if (c.n < ADAMW_CHUNK || (((uintptr_t)w | (uintptr_t)g) & 15u) != 0)
+    chunk<BITS, VALUES>(a, c, PartChunk{w, g, c.start, c.n, c.wdt, c.gdt}, now.key, k, skip);
+  else if (c.wdt == DT_F32) whole<BITS, VALUES, float, float>(a, c, w, g, now.key, k, skip);
+  else if (c.wdt == DT_F16 && c.gdt == DT_F16) whole<BITS, VALUES, _Float16, _Float16>(a, c, w, g, now.key, k, skip);
+  else if (c.wdt == DT_F16) whole<BITS, VALUES, _Float16, float>(a, c, w, g, now.key, k, skip);
+  else if (c.gdt == DT_BF16) whole<BITS, VALUES, bf16_t, bf16_t>(a, c, w, g, now.key, k, skip);
+  else whole<BITS, VALUES, bf16_t, float>(a, c, w, g, now.key, k, skip);
   __syncthreads();   // every wave has read its clock
   if (threadIdx.x == 0 && !skip) {
     AdamwClock next;
@@ -276,6 +344,7 @@ __global__ void __launch_bounds__(kThreads) k_adamw(AdamwArgs a, AdamwTable tab)
     next.p2 = now.p2 * a.b2d;
     next.ic1 = (float)(1.0 / (1.0 - next.p1));
     next.is2 = (float)(1.0 / sqrt(1.0 - next.p2));
+    next.key = adamw_step_key(a.seed, (uint64_t)next.t);
     a.clocks[blockIdx.x] = next;
   }
 }
@@ -296,7 +365,13 @@ __device__ double squares(const GT* __restrict__ g, uint32_t n) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const uint32_t i = base + u * kThreads * N;
-      load<N, true>(g + i, (int)n - (int)i, x[u]);
+      if (i + N <= n) {
+        GT v[N];
+        load_wide(g + i, v);
+        for (int j = 0; j < N; ++j) x[u][j] = to_f32(v[j]);
+      } else {
+        load_some<N>(g + i, (int)n - (int)i, x[u]);
+      }
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
@@ -314,11 +389,11 @@ __device__ __forceinline__ double block_sum(double s, double* lds) {
   return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
 
-__global__ void __launch_bounds__(kThreads) k_adamw_squares(const AdamwChunk* __restrict__ chunks,
+__global__ void __launch_bounds__(kThreads) k_adamw_squares(const AdamwSpan* __restrict__ spans,
                                                             uint32_t first, AdamwTable tab,
                                                             double* __restrict__ partial) {
   __shared__ double lds[4];
-  const AdamwChunk c = chunks[blockIdx.x];
+  const AdamwSpan c = spans[blockIdx.x];
   const void* g = tab.g[c.tensor - first];
   double s;
   if (c.gdt == DT_F32) s = squares((const float*)g + c.start, c.n);
@@ -351,9 +426,9 @@ hipError_t launch_adamw(const AdamwArgs& a, const AdamwTable& tab, hipStream_t s
   return hipGetLastError();
 }
 
-hipError_t launch_adamw_squares(const AdamwChunk* chunks, uint32_t first_tensor, uint32_t nchunks,
+hipError_t launch_adamw_squares(const AdamwSpan* spans, uint32_t first_tensor, uint32_t nspans,
                                 const AdamwTable& tab, double* partial, hipStream_t s) {
-  k_adamw_squares<<<nchunks, kThreads, 0, s>>>(chunks, first_tensor, tab, partial);
+  k_adamw_squares<<<nspans, kThreads, 0, s>>>(spans, first_tensor, tab, partial);
   return hipGetLastError();
 }
 
