@@ -405,8 +405,8 @@ const char *tgrad_kernel_name(int id);
  *     byte for every 128 of them. q is sqrt(v). A scale byte is the exponent field f of the
  *     largest magnitude of its 128 values as fp32 (zero: 0); a code's value is 2^(f - 14)
  *     times the fp32 number whose bits are code << 20 (m: sign in bit 7, the other 7 bits
- *     shifted) or code << 19 (q). f = 255 stands for NaN in all 128 values; a value that is
- *     not finite turns its group into that. Rounding is random and unbiased: to the bits of
+ *     shifted) or code << 19 (q). f = 255 stands for NaN in all 128 values; a q that is
+ *     not finite turns its group and m's into that. Rounding is random and unbiased: to the bits of
  *     the scaled value, h >> 12 (m) or h & 0x7FFFF (q) is added before the rest is cut off,
  *     h = mix(place ^ key): h *= 0xBF58476D, h ^= h >> 16, h *= 0x94D049BB, h ^= h >> 13 in
  *     32 bits, place the value's index in the flat state, key the low half of SplitMix64's

@@ -56,6 +56,7 @@ struct AdamwArgs {
   uint32_t first_tensor;
   uint32_t nchunks;
   int bits;                   // 32 or 8
+  uint32_t lds;               // 32 bits: LDS that a workgroup reserves, unused
   void* m;                    // fp32, or codes
   void* v;                    // fp32, or codes of sqrt(v)
   uint8_t* ms;                // 8 bits: the groups' exponent fields

@@ -37,11 +37,10 @@ struct StepK {
   float b1, c1, b2, c2, eps, step, is2, decay, coef;
 };
 
-__device__ __forceinline__ float moments(float g, float& m, float& v, const StepK& k) {
+__device__ __forceinline__ void moments(float g, float& m, float& v, const StepK& k) {
   const float gc = g * k.coef;
   m = k.b1 * m + k.c1 * gc;
   v = k.b2 * v + k.c2 * (gc * gc);
-  return sqrtf(v);
 }
 __device__ __forceinline__ float updated(float w, float m, float q, const StepK& k) {
   return w * k.decay - (k.step * m) * __builtin_amdgcn_rcpf(q * k.is2 + k.eps);
@@ -49,12 +48,23 @@ __device__ __forceinline__ float updated(float w, float m, float q, const StepK&
 
 // A value's 32 random bits: its place in the state mixed with the step's key (two
 // multiplications by the high halves of SplitMix64's constants).
-__device__ __forceinline__ uint32_t random_bits(uint32_t place, uint32_t key) {
-  uint32_t h = (place ^ key) * 0xBF58476Du;
-  h ^= h >> 16;
+// `head` is (place ^ key) * 0xBF58476D.
+__device__ __forceinline__ uint32_t random_bits(uint32_t head) {
+  uint32_t h = head ^ (head >> 16);
   h *= 0x94D049BBu;
   return h ^ (h >> 13);
 }
+
+// sqrt(v), correctly rounded for 2^-96 <= v <= 2^126 and for 0: v times its reciprocal root
+// and one correction by the exact residual. Compared with sqrtf for every mantissa of both
+// exponent parities at both ends of that range and between; sqrtf's own care for the rest
+// costs twice the instructions. kRootLow and kRootHigh bound the results of that range.
+__device__ __forceinline__ float root(float v) {
+  const float y = __builtin_amdgcn_rsqf(fmaxf(v, 0x1p-96f));
+  const float s = v * y, h = 0.5f * y;
+  return __builtin_fmaf(__builtin_fmaf(-s, s, v), h, s);
+}
+constexpr uint32_t kRootLow = (127 - 48) << 23, kRootHigh = (127 + 63) << 23;
 
 // Whole accesses of 8 or 16 bytes, marked as not to be kept: a step touches every byte once,
 // and what the caches keep of it is gone before the next one.
@@ -91,6 +101,16 @@ __device__ __forceinline__ uint32_t row_max(uint32_t x) {
 
 __device__ __forceinline__ uint32_t nan_bits(uint32_t field) {
   return field == 255u ? 0x7FC00000u : 0u;
+}
+
+// The upper bytes of four words, the first lowest.
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0C0C0703u), hi = __builtin_amdgcn_perm(d, c, 0x0C0C0703u);
+  return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+}
+// The upper halves of two words.
+__device__ __forceinline__ uint32_t top_halves(uint32_t a, uint32_t b) {
+  return __builtin_amdgcn_perm(b, a, 0x07060302u);
 }
 
 // N values of a piece that may end early: `have` of them exist, the others read as zero and
@@ -207,8 +227,8 @@ __device__ __forceinline__ void chunk32(const AdamwArgs& a, const AdamwChunk& c,
     io.values(raw[u], wx, gx);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float q = moments(gx[j], mx[u][j], vx[u][j], k);
-      wx[j] = updated(wx[j], mx[u][j], q, k);
+      moments(gx[j], mx[u][j], vx[u][j], k);
+      wx[j] = updated(wx[j], mx[u][j], sqrtf(vx[u][j]), k);
     }
     io.template store<4>(i, wx);
     store_wide(m + i, mx[u]);
@@ -226,47 +246,74 @@ __device__ __forceinline__ void chunk8(const AdamwArgs& a, const AdamwChunk& c, 
   uint2* mc = (uint2*)((uint8_t*)a.m + at);
   uint2* qc = (uint2*)((uint8_t*)a.v + at);
   uint8_t *ms = a.ms + at / ADAMW_GROUP, *qs = a.vs + at / ADAMW_GROUP;
-  uint2 cm = *mc, cq = *qc;
+  const uint2 cm = *mc, cq = *qc;
   const int fm = *ms, fq = *qs;
   typename Chunk::template Raw<8> raw;
   io.load(i, raw);
   if (skip) return;
   float wx[8], gx[8], m[8], q[8];
   io.values(raw, wx, gx);
-  const uint32_t nan_m = nan_bits(fm), nan_q = nan_bits(fq);
-  uint32_t tm = 0, tq = 0;
+  // m's codes are the fp8 numbers (4 bits of exponent, 3 of mantissa) that the hardware
+  // converts in pairs: those stand for 2^120 times the number with the bits code << 20. A
+  // group that stands for NaN makes its products with b1 and b2 that.
+  typedef float Pair __attribute__((ext_vector_type(2)));
+  const float sm = ldexpf(1.0f, fm - 134);
+  StepK kg = k;
+  if (fm == 255) kg.b1 = kg.b2 = __uint_as_float(0x7FC00000u);
+  if (fq == 255) kg.b2 = __uint_as_float(0x7FC00000u);
+  const Pair p0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)cm.x, false), p1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)cm.x, true);
+  const Pair p2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)cm.y, false), p3 = __builtin_amdgcn_cvt_pk_f32_fp8((int)cm.y, true);
+  m[0] = p0.x, m[1] = p0.y, m[2] = p1.x, m[3] = p1.y, m[4] = p2.x, m[5] = p2.y, m[6] = p3.x, m[7] = p3.y;
+  float v[8], tm = 0.0f;
+  uint32_t tq = 0, lq = 0xFFFFFFFFu;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t x = (j < 4 ? cm.x : cm.y) >> (8 * (j & 3)), y = (j < 4 ? cq.x : cq.y) >> (8 * (j & 3));
-    m[j] = ldexpf(__uint_as_float(((x & 127u) << 20) | ((x & 128u) << 24) | nan_m), fm - 14);
-    const float old = ldexpf(__uint_as_float(((y & 255u) << 19) | nan_q), fq - 14);
-    float v = old * old;
-    q[j] = moments(gx[j], m[j], v, k);
-    wx[j] = updated(wx[j], m[j], q[j], k);
-    tm = max(tm, __float_as_uint(m[j]) & 0x7FFFFFFFu);
+    const uint32_t y = ((j < 4 ? cq.x : cq.y) >> (8 * (j & 3))) & 255u;
+    const float old = ldexpf(__uint_as_float(y << 19), fq - 14);
+    m[j] *= sm;
+    v[j] = old * old;
+    moments(gx[j], m[j], v[j], kg);
+    q[j] = root(v[j]);
+    tm = fmaxf(tm, fabsf(m[j]));
     tq = max(tq, __float_as_uint(q[j]) & 0x7FFFFFFFu);
+    lq = min(lq, __float_as_uint(q[j]));
   }
+  if (__any(tq >= kRootHigh || lq < kRootLow)) {   // zeros among them
+    tq = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      __asm__ volatile("" : "+v"(v[j]));   // a branch of its own, not computed beside the other
+      q[j] = sqrtf(v[j]);
+      tq = max(tq, __float_as_uint(q[j]) & 0x7FFFFFFFu);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) wx[j] = updated(wx[j], m[j], q[j], k);
   io.template store<8>(i, wx);
-  const int nm = (int)(row_max(tm) >> 23), nq = (int)(row_max(tq) >> 23);
+  // where m is not finite v is not either: both groups then stand for NaN
+  const int nq = (int)(row_max(tq) >> 23);
+  const int nm = nq == 255 ? 255 : (int)(row_max(__float_as_uint(tm)) >> 23);
+  const uint32_t ks = (uint32_t)__builtin_amdgcn_readfirstlane((int)key), low = ks & 7u;
+  const uint32_t head = ((uint32_t)at ^ (ks & ~7u)) * 0xBF58476Du;
   uint32_t ym[8], yq[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t h = random_bits((uint32_t)at + j, key);
+    // (at + j) ^ key: at is a multiple of 8, so its product and that of the low bits add up
+    const uint32_t h = random_bits(head + (j ^ low) * 0xBF58476Du);
     // the sign stays in bit 31: a code's magnitude ends below bit 27, and so does the sum
     ym[j] = __float_as_uint(ldexpf(m[j], 14 - nm)) + (h >> 12);
     yq[j] = __float_as_uint(ldexpf(q[j], 14 - nq)) + (h & 0x7FFFFu);
     // a q above zero is above 2^-75, so its bits are more than the least code's
     yq[j] = max(yq[j], min(__float_as_uint(q[j]), 1u << 19));
   }
+  uint32_t bm[8], bq[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t x = ((ym[j] >> 20) & 127u) | ((ym[j] >> 24) & 128u), y = (yq[j] >> 19) & 255u;
-    uint32_t &mw = j < 4 ? cm.x : cm.y, &qw = j < 4 ? cq.x : cq.y;
-    mw = (j & 3) ? mw | x << (8 * (j & 3)) : x;
-    qw = (j & 3) ? qw | y << (8 * (j & 3)) : y;
+    bm[j] = (ym[j] & 0x80000000u) | ((ym[j] << 4) & 0x7F000000u);
+    bq[j] = yq[j] << 5;
   }
-  *mc = cm;
-  *qc = cq;
+  *mc = make_uint2(top_bytes(bm[0], bm[1], bm[2], bm[3]), top_bytes(bm[4], bm[5], bm[6], bm[7]));
+  *qc = make_uint2(top_bytes(bq[0], bq[1], bq[2], bq[3]), top_bytes(bq[4], bq[5], bq[6], bq[7]));
   if ((threadIdx.x & 15) == 0) {
     *ms = (uint8_t)nm;
     *qs = (uint8_t)nq;
@@ -274,23 +321,16 @@ __device__ __forceinline__ void chunk8(const AdamwArgs& a, const AdamwChunk& c, 
   if (VALUES) {
     // at most five significant bits: the upper half of the fp32 value is the bf16 one
     uint32_t om[8], oq[8];
-    const uint32_t new_nan_m = nan_bits(nm), new_nan_q = nan_bits(nq);
+    const uint32_t nan_m = nan_bits(nm), nan_q = nan_bits(nq);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      om[j] = __float_as_uint(ldexpf(__uint_as_float((ym[j] & 0x87F00000u) | new_nan_m), nm - 14));
-      oq[j] = __float_as_uint(ldexpf(__uint_as_float((yq[j] & 0x07F80000u) | new_nan_q), nq - 14));
+      om[j] = __float_as_uint(ldexpf(__uint_as_float((ym[j] & 0x87F00000u) | nan_m), nm - 14));
+      oq[j] = __float_as_uint(ldexpf(__uint_as_float((yq[j] & 0x07F80000u) | nan_q), nq - 14));
     }
-    uint4 x, y;
-    x.x = __builtin_amdgcn_perm(om[1], om[0], 0x07060302u);
-    x.y = __builtin_amdgcn_perm(om[3], om[2], 0x07060302u);
-    x.z = __builtin_amdgcn_perm(om[5], om[4], 0x07060302u);
-    x.w = __builtin_amdgcn_perm(om[7], om[6], 0x07060302u);
-    y.x = __builtin_amdgcn_perm(oq[1], oq[0], 0x07060302u);
-    y.y = __builtin_amdgcn_perm(oq[3], oq[2], 0x07060302u);
-    y.z = __builtin_amdgcn_perm(oq[5], oq[4], 0x07060302u);
-    y.w = __builtin_amdgcn_perm(oq[7], oq[6], 0x07060302u);
-    *(uint4*)(a.m_out + at) = x;
-    *(uint4*)(a.v_out + at) = y;
+    *(uint4*)(a.m_out + at) = make_uint4(top_halves(om[0], om[1]), top_halves(om[2], om[3]),
+                                         top_halves(om[4], om[5]), top_halves(om[6], om[7]));
+    *(uint4*)(a.v_out + at) = make_uint4(top_halves(oq[0], oq[1]), top_halves(oq[2], oq[3]),
+                                         top_halves(oq[4], oq[5]), top_halves(oq[6], oq[7]));
   }
 }
 
@@ -420,7 +460,7 @@ __global__ void __launch_bounds__(kThreads) k_adamw_norm(const double* __restric
 }  // namespace
 
 hipError_t launch_adamw(const AdamwArgs& a, const AdamwTable& tab, hipStream_t s) {
-  if (a.bits == 32) k_adamw<32, false><<<a.nchunks, kThreads, 0, s>>>(a, tab);
+  if (a.bits == 32) k_adamw<32, false><<<a.nchunks, kThreads, a.lds, s>>>(a, tab);
   else if (!a.m_out) k_adamw<8, false><<<a.nchunks, kThreads, 0, s>>>(a, tab);
   else k_adamw<8, true><<<a.nchunks, kThreads, 0, s>>>(a, tab);
   return hipGetLastError();
