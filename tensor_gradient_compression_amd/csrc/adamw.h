@@ -70,11 +70,20 @@ struct AdamwArgs {
 };
 
 hipError_t launch_adamw(const AdamwArgs& a, const AdamwTable& tab, hipStream_t s);
-// partial[i] = the sum of the squares of span i's gradients, for the spans of a launch
-hipError_t launch_adamw_squares(const AdamwSpan* spans, uint32_t first_tensor, uint32_t nspans,
-                                const AdamwTable& tab, double* partial, hipStream_t s);
-// out = {norm * scale, scale * min(1, max_norm / (norm * scale))}, norm = sqrt(sum partial)
-hipError_t launch_adamw_norm(const double* partial, uint32_t n, double max_norm, double scale,
-                             float* out, hipStream_t s);
+
+struct AdamwNorm {
+  const AdamwSpan* spans;     // of this launch
+  double* partial;            // a sum of squares for each of them (the result's: for all)
+  uint32_t* done;             // join: workgroups that have finished; 0 between calls
+  uint32_t first_tensor;      // of this launch
+  uint32_t total_spans;
+  float* out;                 // {norm, coefficient}
+  double max_norm, scale;
+};
+// The sums of squares of a launch's spans, with join also the result.
+hipError_t launch_adamw_squares(const AdamwNorm& a, uint32_t nspans, bool join, const AdamwTable& tab,
+                                hipStream_t s);
+// norm = scale * sqrt(sum of squares), coefficient = scale * min(1, max_norm / norm)
+hipError_t launch_adamw_norm(const AdamwNorm& a, hipStream_t s);
 
 }  // namespace tg

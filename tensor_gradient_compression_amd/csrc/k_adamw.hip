@@ -378,12 +378,16 @@ __global__ void __launch_bounds__(kThreads) k_adamw(AdamwArgs a, AdamwTable tab)
   else whole<BITS, VALUES, bf16_t, float>(a, c, w, g, now.key, k, skip);
   __syncthreads();   // every wave has read its clock
   if (threadIdx.x == 0 && !skip) {
+    // the hardware's estimates (2^-26 and better) with one Newton step each are exact far
+    // below fp32's rounding, and shorter than a division and a root
     AdamwClock next;
     next.t = now.t + 1;
     next.p1 = now.p1 * a.b1d;
     next.p2 = now.p2 * a.b2d;
-    next.ic1 = (float)(1.0 / (1.0 - next.p1));
-    next.is2 = (float)(1.0 / sqrt(1.0 - next.p2));
+    const double d1 = 1.0 - next.p1, d2 = 1.0 - next.p2;
+    const double r = __builtin_amdgcn_rcp(d1), q = __builtin_amdgcn_rsq(d2);
+    next.ic1 = (float)__builtin_fma(__builtin_fma(-d1, r, 1.0), r, r);
+    next.is2 = (float)__builtin_fma(__builtin_fma(-d2 * q, q, 1.0), 0.5 * q, q);
     next.key = adamw_step_key(a.seed, (uint64_t)next.t);
     a.clocks[blockIdx.x] = next;
   }
@@ -424,37 +428,64 @@ __device__ double squares(const GT* __restrict__ g, uint32_t n) {
 __device__ __forceinline__ double block_sum(double s, double* lds) {
 #pragma unroll
   for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o, 64);
+  __syncthreads();
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
   __syncthreads();
   return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
 
-__global__ void __launch_bounds__(kThreads) k_adamw_squares(const AdamwSpan* __restrict__ spans,
-                                                            uint32_t first, AdamwTable tab,
-                                                            double* __restrict__ partial) {
+__device__ __forceinline__ void write_norm(const AdamwNorm& a, double squares) {
+  const double norm = sqrt(squares) * a.scale;
+  a.out[0] = (float)norm;
+  a.out[1] = (float)(norm > a.max_norm ? a.scale * (a.max_norm / norm) : a.scale);
+}
+
+// The sums of squares of one launch's spans. JOIN (one launch of few spans): the workgroup that
+// finishes last also adds the sums up, in their order, and writes the result. The sums go
+// through atomic exchanges, whose answers the count waits for, and atomic loads: both act
+// where every workgroup sees them, so no cache has to be written back in between.
+template <bool JOIN>
+__global__ void __launch_bounds__(kThreads) k_adamw_squares(AdamwNorm a, AdamwTable tab) {
   __shared__ double lds[4];
-  const AdamwSpan c = spans[blockIdx.x];
-  const void* g = tab.g[c.tensor - first];
+  __shared__ uint32_t before;
+  const AdamwSpan c = a.spans[blockIdx.x];
+  const void* g = tab.g[c.tensor - a.first_tensor];
   double s;
   if (c.gdt == DT_F32) s = squares((const float*)g + c.start, c.n);
   else if (c.gdt == DT_F16) s = squares((const _Float16*)g + c.start, c.n);
   else s = squares((const bf16_t*)g + c.start, c.n);
   s = block_sum(s, lds);
-  if (threadIdx.x == 0) partial[blockIdx.x] = s;
-}
-
-__global__ void __launch_bounds__(kThreads) k_adamw_norm(const double* __restrict__ partial, uint32_t n,
-                                                         double max_norm, double scale,
-                                                         float* __restrict__ out) {
-  __shared__ double lds[4];
-  double s = 0.0;
-  for (uint32_t i = threadIdx.x; i < n; i += kThreads) s += partial[i];
+  if (!JOIN) {
+    if (threadIdx.x == 0) a.partial[blockIdx.x] = s;
+    return;
+  }
+  if (threadIdx.x == 0) {
+    unsigned long long old = __hip_atomic_exchange((unsigned long long*)a.partial + blockIdx.x,
+                                                   __double_as_longlong(s), __ATOMIC_RELAXED,
+                                                   __HIP_MEMORY_SCOPE_AGENT);
+    uint32_t one = 1;
+    __asm__ volatile("" : "+v"(one), "+v"(old));   // the count waits for the exchange
+    before = __hip_atomic_fetch_add(a.done, one, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (before != gridDim.x - 1) return;
+  s = 0.0;
+  for (uint32_t i = threadIdx.x; i < a.total_spans; i += kThreads)
+    s += __longlong_as_double(__hip_atomic_load((unsigned long long*)a.partial + i, __ATOMIC_RELAXED,
+                                                __HIP_MEMORY_SCOPE_AGENT));
   s = block_sum(s, lds);
   if (threadIdx.x == 0) {
-    const double norm = sqrt(s) * scale;
-    out[0] = (float)norm;
-    out[1] = (float)(norm > max_norm ? scale * (max_norm / norm) : scale);
+    write_norm(a, s);
+    *a.done = 0;
   }
+}
+
+__global__ void __launch_bounds__(kThreads) k_adamw_norm(AdamwNorm a) {
+  __shared__ double lds[4];
+  double s = 0.0;
+  for (uint32_t i = threadIdx.x; i < a.total_spans; i += kThreads) s += a.partial[i];
+  s = block_sum(s, lds);
+  if (threadIdx.x == 0) write_norm(a, s);
 }
 
 }  // namespace
@@ -466,15 +497,15 @@ hipError_t launch_adamw(const AdamwArgs& a, const AdamwTable& tab, hipStream_t s
   return hipGetLastError();
 }
 
-hipError_t launch_adamw_squares(const AdamwSpan* spans, uint32_t first_tensor, uint32_t nspans,
-                                const AdamwTable& tab, double* partial, hipStream_t s) {
-  k_adamw_squares<<<nspans, kThreads, 0, s>>>(spans, first_tensor, tab, partial);
+hipError_t launch_adamw_squares(const AdamwNorm& a, uint32_t nspans, bool join, const AdamwTable& tab,
+                                hipStream_t s) {
+  if (join) k_adamw_squares<true><<<nspans, kThreads, 0, s>>>(a, tab);
+  else k_adamw_squares<false><<<nspans, kThreads, 0, s>>>(a, tab);
   return hipGetLastError();
 }
 
-hipError_t launch_adamw_norm(const double* partial, uint32_t n, double max_norm, double scale,
-                             float* out, hipStream_t s) {
-  k_adamw_norm<<<1, kThreads, 0, s>>>(partial, n, max_norm, scale, out);
+hipError_t launch_adamw_norm(const AdamwNorm& a, hipStream_t s) {
+  k_adamw_norm<<<1, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
