@@ -1,0 +1,271 @@
+// The gradients of layer norm over the last axis of (rows, cols), from its inputs and
+// statistics:
+//   n = (x - mean) rstd;  h = dy w;  dx = rstd (h - mean(h) - n mean(h n))
+//   dw = sum_rows dy n;  db = sum_rows dy
+// Sums are fp32, results are rounded once. Rows and threads: layernorm_rows.h. Each thread
+// also sums dy n and dy over its rows for its own columns; a workgroup's sums become one row of
+// `partial`, and a second kernel adds those rows up, always in the same order.
+#include "layernorm_rows.h"
+
+namespace tg {
+
+namespace {
+
+// Up to 16 values a thread their sums over rows, the weights and two rows fit the registers;
+// with 16 waves and 16 values (128 registers a thread) the weights are read again for each row.
+template <typename T, int WAVES, int LANES, int NV, int COLS>
+__global__ void __launch_bounds__((RowThreads<WAVES, LANES>::kThreads)) k_ln_backward(LnBackward a) {
+  using RT = RowThreads<WAVES, LANES>;
+  constexpr int V = Piece<T>::V, K = NV / V;
+  constexpr bool kKeep = !(WAVES == 16 && NV == 16);
+  __shared__ float lds[WAVES > 1 ? RT::kLds : 4 * 2 * NV * LANES];
+  RT rt{lds};
+  const int64_t stride = (int64_t)gridDim.x * RT::kRows;
+  const float inv = 1.0f / (float)a.cols;
+  int64_t row = (int64_t)blockIdx.x * RT::kRows + RT::row();
+  Place<T, COLS> at[K];
+  Piece<T> xn[K], dn[K];
+  float mean_n = 0.0f, rstd_n = 0.0f;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    at[k] = Place<T, COLS>((RT::index() + k * RT::kCount) * V, a.cols);
+    clear(xn[k]);
+    clear(dn[k]);
+    if (row < a.rows) {
+      at[k].load((const T*)a.x + row * a.x_stride, a.cols, xn[k]);
+      at[k].load((const T*)a.dy + row * a.dy_stride, a.cols, dn[k]);
+    }
+  }
+  if (row < a.rows) mean_n = a.mean[row], rstd_n = a.rstd[row];
+  float w[kKeep ? NV : V], sw[NV], sb[NV];
+  if (kKeep)
+#pragma unroll
+    for (int k = 0; k < K; ++k) at[k].weights(a.w, a.wdt, a.cols, 1.0f, w + (kKeep ? k * V : 0));
+#pragma unroll
+  for (int i = 0; i < NV; ++i) sw[i] = sb[i] = 0.0f;
+  for (int64_t base = (int64_t)blockIdx.x * RT::kRows; base < a.rows; base += stride, row += stride) {
+    Piece<T> xp[K], dp[K];
+    const float mean = mean_n, rstd = rstd_n;
+    float s = 0.0f, u = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      xp[k] = xn[k];
+      dp[k] = dn[k];
+    }
+    if (row + stride < a.rows) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        at[k].load((const T*)a.x + (row + stride) * a.x_stride, a.cols, xn[k]);
+        at[k].load((const T*)a.dy + (row + stride) * a.dy_stride, a.cols, dn[k]);
+      }
+      mean_n = a.mean[row + stride];
+      rstd_n = a.rstd[row + stride];
+    } else {
+      // a row past the end adds zeros
+#pragma unroll
+      for (int k = 0; k < K; ++k) clear(dn[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (!kKeep) at[k].weights(a.w, a.wdt, a.cols, 1.0f, w);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int i = k * V + j;
+        const float dy = to_f32(dp[k].v[j]), n = (to_f32(xp[k].v[j]) - mean) * rstd;
+        const float h = COLS == RAGGED && !at[k].mine(j, a.cols) ? 0.0f : dy * w[kKeep ? i : j];
+        s += h;
+        u = __builtin_fmaf(h, n, u);
+        sw[i] = __builtin_fmaf(dy, n, sw[i]);
+        sb[i] += dy;
+      }
+    }
+    rt.template sum<true>(s, u);
+    s *= inv;
+    u *= inv;
+    if (row >= a.rows) continue;
+    T* dx = (T*)a.dx + row * (int64_t)a.cols;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float o[V];
+      if (!kKeep) at[k].weights(a.w, a.wdt, a.cols, 1.0f, w);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float n = (to_f32(xp[k].v[j]) - mean) * rstd, h = to_f32(dp[k].v[j]) * w[kKeep ? k * V + j : j];
+        o[j] = rstd * ((h - s) - n * u);
+      }
+      at[k].store(dx, a.cols, o);
+    }
+  }
+  if (!a.partial) return;
+  float* pw = a.partial + (uint64_t)blockIdx.x * 2 * a.cols;
+  if (WAVES == 1) {
+    // the row groups of a wave, then the four waves, always in the same order
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int o = LANES; o < 64; o <<= 1) {
+        sw[i] += __shfl_xor(sw[i], o, 64);
+        sb[i] += __shfl_xor(sb[i], o, 64);
+      }
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (lane < LANES) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        lds[(wave * 2 * NV + i) * LANES + lane] = sw[i];
+        lds[(wave * 2 * NV + NV + i) * LANES + lane] = sb[i];
+      }
+    }
+    __syncthreads();
+    if (wave > 0 || lane >= LANES) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int q = 1; q < 4; ++q) {
+        sw[i] += lds[(q * 2 * NV + i) * LANES + lane];
+        sb[i] += lds[(q * 2 * NV + NV + i) * LANES + lane];
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (at[k].own < V && at[k].mine(j, a.cols)) {
+        pw[at[k].c + j] = sw[k * V + j];
+        pw[a.cols + at[k].c + j] = sb[k * V + j];
+      }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(LN_LONG) k_ln_dx_long(LnBackward a) {
+  using RT = RowThreads<LN_LONG / 64, 64>;
+  constexpr int V = Piece<T>::V;
+  __shared__ float lds[RT::kLds];
+  RT rt{lds};
+  const int64_t row = blockIdx.x;
+  const T* x = (const T*)a.x + row * a.x_stride;
+  const T* dy = (const T*)a.dy + row * a.dy_stride;
+  const float mean = a.mean[row], rstd = a.rstd[row];
+  float s = 0.0f, u = 0.0f, w[V];
+  Piece<T> p, q;
+  for (uint32_t c = threadIdx.x * V; c < a.cols; c += LN_LONG * V) {
+    const Place<T, RAGGED> at(c, a.cols);
+    at.load(x, a.cols, p);
+    at.load(dy, a.cols, q);
+    at.weights(a.w, a.wdt, a.cols, 1.0f, w);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float h = at.mine(j, a.cols) ? to_f32(q.v[j]) * w[j] : 0.0f;
+      s += h;
+      u = __builtin_fmaf(h, (to_f32(p.v[j]) - mean) * rstd, u);
+    }
+  }
+  rt.template sum<true>(s, u);
+  s /= (float)a.cols;
+  u /= (float)a.cols;
+  for (uint32_t c = threadIdx.x * V; c < a.cols; c += LN_LONG * V) {
+    const Place<T, RAGGED> at(c, a.cols);
+    float o[V];
+    at.load(x, a.cols, p);
+    at.load(dy, a.cols, q);
+    at.weights(a.w, a.wdt, a.cols, 1.0f, w);
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      o[j] = rstd * ((to_f32(q.v[j]) * w[j] - s) - (to_f32(p.v[j]) - mean) * rstd * u);
+    at.store((T*)a.dx + row * (int64_t)a.cols, a.cols, o);
+  }
+}
+
+// partial row r: the sums over rows r, r + gridDim.y, ...
+template <typename T>
+__global__ void __launch_bounds__(256) k_ln_columns(LnBackward a) {
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.cols) return;
+  float s = 0.0f, t = 0.0f;
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    const float dy = to_f32(((const T*)a.dy)[row * a.dy_stride + i]);
+    s = __builtin_fmaf(dy, (to_f32(((const T*)a.x)[row * a.x_stride + i]) - a.mean[row]) * a.rstd[row], s);
+    t += dy;
+  }
+  a.partial[(uint64_t)blockIdx.y * 2 * a.cols + i] = s;
+  a.partial[((uint64_t)blockIdx.y * 2 + 1) * a.cols + i] = t;
+}
+
+// The partial rows' sums. blockIdx.y: dw or db; 32 columns a workgroup, 32 threads a column.
+template <typename WT>
+__global__ void __launch_bounds__(1024) k_ln_reduce(const float* __restrict__ partial, uint32_t n, uint32_t cols,
+                                                    WT* __restrict__ dw, WT* __restrict__ db) {
+  __shared__ float lds[32][33];
+  const uint32_t tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
+  WT* out = blockIdx.y ? db : dw;
+  if (!out) return;
+  float s = 0.0f;
+  if (c < cols) {
+    const float* p = partial + (uint64_t)blockIdx.y * cols + c;
+#pragma unroll 8
+    for (uint32_t r = ty; r < n; r += 32) s += p[(uint64_t)r * 2 * cols];
+  }
+  lds[ty][tx] = s;
+  __syncthreads();
+  s = group_sum<32>(lds[tx][ty]);
+  const uint32_t o = blockIdx.x * 32 + ty;
+  if (tx == 0 && o < cols) out[o] = from_f32<WT>(s);
+}
+
+template <typename T>
+struct Backward {
+  const LnBackward& a;
+  uint32_t n;
+  hipStream_t s;
+  template <int WAVES, int LANES, int NV>
+  void run() const {
+    using RT = RowThreads<WAVES, LANES>;
+    constexpr uint32_t V = Piece<T>::V;
+    if (LANES == 1 && a.cols < V) k_ln_backward<T, 1, 1, 8, TINY><<<n, RT::kThreads, 0, s>>>(a);
+    else if (a.cols % V == 0) k_ln_backward<T, WAVES, LANES, NV, WHOLE><<<n, RT::kThreads, 0, s>>>(a);
+    else k_ln_backward<T, WAVES, LANES, NV, RAGGED><<<n, RT::kThreads, 0, s>>>(a);
+  }
+};
+struct PartialRows {
+  int64_t rows;
+  uint32_t& n;
+  template <int WAVES, int LANES, int NV>
+  void run() const {
+    n = ln_walk(rows, RowThreads<WAVES, LANES>::kRows, WAVES == 16 ? 512 : 1024);
+  }
+};
+
+template <typename T>
+hipError_t backward(LnBackward a, hipStream_t s) {
+  const uint32_t n = ln_partial_rows(a.rows, a.cols);
+  const bool params = a.dw || a.db;
+  if (!params) a.partial = nullptr;
+  if (a.rows && !ln_dispatch(a.cols, Backward<T>{a, n, s})) {
+    k_ln_dx_long<T><<<(uint32_t)a.rows, LN_LONG, 0, s>>>(a);
+    if (params) k_ln_columns<T><<<dim3((a.cols + 255) / 256, n), 256, 0, s>>>(a);
+  }
+  if (params) {
+    const dim3 grid((a.cols + 31) / 32, 2);
+    if (a.wdt == DT_F32) k_ln_reduce<float><<<grid, 1024, 0, s>>>(a.partial, n, a.cols, (float*)a.dw, (float*)a.db);
+    else k_ln_reduce<T><<<grid, 1024, 0, s>>>(a.partial, n, a.cols, (T*)a.dw, (T*)a.db);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// Workgroups of the backward walk, each of which leaves one row of sums: as many as keep the
+// CUs busy, and no more than there are rows for.
+uint32_t ln_partial_rows(int64_t rows, uint32_t cols) {
+  uint32_t n = 0;
+  if (!ln_dispatch(cols, PartialRows{rows, n})) n = ln_walk(rows, 1, 512);
+  return n;
+}
+
+hipError_t launch_ln_backward(const LnBackward& a, hipStream_t s) {
+  if (a.dt == DT_F32) return backward<float>(a, s);
+  if (a.dt == DT_F16) return backward<_Float16>(a, s);
+  return backward<bf16_t>(a, s);
+}
+
+}  // namespace tg
