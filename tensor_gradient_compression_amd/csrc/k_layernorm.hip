@@ -10,12 +10,12 @@ namespace tg {
 
 namespace {
 
-template <typename T, int WAVES, int LANES, int NV, int COLS>
-__global__ void __launch_bounds__((RowThreads<WAVES, LANES>::kThreads)) k_ln_forward(LnForward a) {
-  using RT = RowThreads<WAVES, LANES>;
+template <typename T, int LANES, int NV, int COLS>
+__global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_forward_waves(NV) / 4) k_ln_forward(LnForward a, bool once) {
+  using RT = RowThreads<LANES>;
   constexpr int V = Piece<T>::V, K = NV / V;
   __shared__ float lds[RT::kLds];
-  RT rt{lds};
+  RT rt(lds);
   const int64_t stride = (int64_t)gridDim.x * RT::kRows;
   const float inv = 1.0f / (float)a.cols;
   Place<T, COLS> at[K];
@@ -23,9 +23,9 @@ __global__ void __launch_bounds__((RowThreads<WAVES, LANES>::kThreads)) k_ln_for
   int64_t row = (int64_t)blockIdx.x * RT::kRows + RT::row();
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    at[k] = Place<T, COLS>((RT::index() + k * RT::kCount) * V, a.cols);
+    at[k] = Place<T, COLS>((RT::index() + k * RT::count()) * V, a.cols);
     clear(next[k]);
-    if (row < a.rows) at[k].load((const T*)a.x + row * a.x_stride, a.cols, next[k]);
+    if (row < a.rows) at[k].load((const T*)a.x + row * a.x_stride, a.cols, once, next[k]);
   }
   float w[NV], b[NV];
 #pragma unroll
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__((RowThreads<WAVES, LANES>::kThreads)) k_ln_for
       }
     if (row + stride < a.rows)
 #pragma unroll
-      for (int k = 0; k < K; ++k) at[k].load((const T*)a.x + (row + stride) * a.x_stride, a.cols, next[k]);
+      for (int k = 0; k < K; ++k) at[k].load((const T*)a.x + (row + stride) * a.x_stride, a.cols, once, next[k]);
     rt.template sum<false>(s, unused);
     const float mean = s * inv;
     s = 0.0f;
@@ -81,17 +81,17 @@ __global__ void __launch_bounds__((RowThreads<WAVES, LANES>::kThreads)) k_ln_for
 
 template <typename T>
 __global__ void __launch_bounds__(LN_LONG) k_ln_forward_long(LnForward a) {
-  using RT = RowThreads<LN_LONG / 64, 64>;
+  using RT = RowThreads<0>;
   constexpr int V = Piece<T>::V;
   __shared__ float lds[RT::kLds];
-  RT rt{lds};
+  RT rt(lds);
   const int64_t row = blockIdx.x;
   const T* x = (const T*)a.x + row * a.x_stride;
   float s = 0.0f, unused;
   Piece<T> p;
   for (uint32_t c = threadIdx.x * V; c < a.cols; c += LN_LONG * V) {
     const Place<T, RAGGED> at(c, a.cols);
-    at.load(x, a.cols, p);
+    at.load(x, a.cols, false, p);
 #pragma unroll
     for (int j = 0; j < V; ++j) s += at.mine(j, a.cols) ? to_f32(p.v[j]) : 0.0f;
   }
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(LN_LONG) k_ln_forward_long(LnForward a) {
   s = 0.0f;
   for (uint32_t c = threadIdx.x * V; c < a.cols; c += LN_LONG * V) {
     const Place<T, RAGGED> at(c, a.cols);
-    at.load(x, a.cols, p);
+    at.load(x, a.cols, false, p);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const float d = to_f32(p.v[j]) - mean;
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(LN_LONG) k_ln_forward_long(LnForward a) {
   for (uint32_t c = threadIdx.x * V; c < a.cols; c += LN_LONG * V) {
     const Place<T, RAGGED> at(c, a.cols);
     float w[V], b[V], o[V];
-    at.load(x, a.cols, p);
+    at.load(x, a.cols, false, p);
     at.weights(a.w, a.wdt, a.cols, 1.0f, w);
     at.weights(a.b, a.wdt, a.cols, 0.0f, b);
 #pragma unroll
@@ -129,14 +129,14 @@ template <typename T>
 struct Forward {
   const LnForward& a;
   hipStream_t s;
-  template <int WAVES, int LANES, int NV>
-  void run() const {
-    using RT = RowThreads<WAVES, LANES>;
+  template <int LANES, int NV>
+  void run(uint32_t threads) const {
     constexpr uint32_t V = Piece<T>::V;
-    const uint32_t n = ln_walk(a.rows, RT::kRows, WAVES == 16 ? 512 : 2048);
-    if (LANES == 1 && a.cols < V) k_ln_forward<T, 1, 1, 8, TINY><<<n, RT::kThreads, 0, s>>>(a);
-    else if (a.cols % V == 0) k_ln_forward<T, WAVES, LANES, NV, WHOLE><<<n, RT::kThreads, 0, s>>>(a);
-    else k_ln_forward<T, WAVES, LANES, NV, RAGGED><<<n, RT::kThreads, 0, s>>>(a);
+    const uint32_t n = ln_walk(a.rows, RowThreads<LANES>::kRows, LN_CUS * (ln_forward_waves(NV) / (threads / 64)));
+    const bool once = ln_once(a.rows * a.cols * 2 * (int64_t)sizeof(T));
+    if (LANES == 1 && a.cols < V) k_ln_forward<T, 1, 8, TINY><<<n, threads, 0, s>>>(a, once);
+    else if (a.cols % V == 0) k_ln_forward<T, LANES, NV, WHOLE><<<n, threads, 0, s>>>(a, once);
+    else k_ln_forward<T, LANES, NV, RAGGED><<<n, threads, 0, s>>>(a, once);
   }
 };
 

@@ -13,13 +13,15 @@ namespace {
 
 // Up to 16 values a thread their sums over rows, the weights and two rows fit the registers;
 // with 16 waves and 16 values (128 registers a thread) the weights are read again for each row.
-template <typename T, int WAVES, int LANES, int NV, int COLS>
-__global__ void __launch_bounds__((RowThreads<WAVES, LANES>::kThreads)) k_ln_backward(LnBackward a) {
-  using RT = RowThreads<WAVES, LANES>;
+// ONCE: see ln_once; as an argument the choice between two loads makes every one wait at once.
+template <typename T, int LANES, int NV, int COLS, bool ONCE>
+__global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_backward_waves(LANES, NV) / 4)
+    k_ln_backward(LnBackward a) {
+  using RT = RowThreads<LANES>;
   constexpr int V = Piece<T>::V, K = NV / V;
-  constexpr bool kKeep = !(WAVES == 16 && NV == 16);
-  __shared__ float lds[WAVES > 1 ? RT::kLds : 4 * 2 * NV * LANES];
-  RT rt{lds};
+  constexpr bool kKeep = !(LANES == 0 && NV == 16);
+  __shared__ float lds[RT::kWave ? 4 * 2 * NV * LANES : RT::kLds];
+  RT rt(lds);
   const int64_t stride = (int64_t)gridDim.x * RT::kRows;
   const float inv = 1.0f / (float)a.cols;
   int64_t row = (int64_t)blockIdx.x * RT::kRows + RT::row();
@@ -28,12 +30,12 @@ __global__ void __launch_bounds__((RowThreads<WAVES, LANES>::kThreads)) k_ln_bac
   float mean_n = 0.0f, rstd_n = 0.0f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    at[k] = Place<T, COLS>((RT::index() + k * RT::kCount) * V, a.cols);
+    at[k] = Place<T, COLS>((RT::index() + k * RT::count()) * V, a.cols);
     clear(xn[k]);
     clear(dn[k]);
     if (row < a.rows) {
-      at[k].load((const T*)a.x + row * a.x_stride, a.cols, xn[k]);
-      at[k].load((const T*)a.dy + row * a.dy_stride, a.cols, dn[k]);
+      at[k].load((const T*)a.x + row * a.x_stride, a.cols, ONCE, xn[k]);
+      at[k].load((const T*)a.dy + row * a.dy_stride, a.cols, ONCE, dn[k]);
     }
   }
   if (row < a.rows) mean_n = a.mean[row], rstd_n = a.rstd[row];
@@ -55,8 +57,8 @@ __global__ void __launch_bounds__((RowThreads<WAVES, LANES>::kThreads)) k_ln_bac
     if (row + stride < a.rows) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        at[k].load((const T*)a.x + (row + stride) * a.x_stride, a.cols, xn[k]);
-        at[k].load((const T*)a.dy + (row + stride) * a.dy_stride, a.cols, dn[k]);
+        at[k].load((const T*)a.x + (row + stride) * a.x_stride, a.cols, ONCE, xn[k]);
+        at[k].load((const T*)a.dy + (row + stride) * a.dy_stride, a.cols, ONCE, dn[k]);
       }
       mean_n = a.mean[row + stride];
       rstd_n = a.rstd[row + stride];
@@ -71,17 +73,17 @@ __global__ void __launch_bounds__((RowThreads<WAVES, LANES>::kThreads)) k_ln_bac
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int i = k * V + j;
-        const float dy = to_f32(dp[k].v[j]), n = (to_f32(xp[k].v[j]) - mean) * rstd;
+        const float dy = to_f32(dp[k].v[j]), d = to_f32(xp[k].v[j]) - mean;
         const float h = COLS == RAGGED && !at[k].mine(j, a.cols) ? 0.0f : dy * w[kKeep ? i : j];
         s += h;
-        u = __builtin_fmaf(h, n, u);
-        sw[i] = __builtin_fmaf(dy, n, sw[i]);
+        u = __builtin_fmaf(h, d, u);
+        sw[i] = __builtin_fmaf(dy, d * rstd, sw[i]);
         sb[i] += dy;
       }
     }
     rt.template sum<true>(s, u);
-    s *= inv;
-    u *= inv;
+    // dx = rstd h + d du + ds, with d = x - mean
+    const float ds = -rstd * (s * inv), du = -rstd * rstd * (rstd * (u * inv));
     if (row >= a.rows) continue;
     T* dx = (T*)a.dx + row * (int64_t)a.cols;
 #pragma unroll
@@ -90,20 +92,20 @@ __global__ void __launch_bounds__((RowThreads<WAVES, LANES>::kThreads)) k_ln_bac
       if (!kKeep) at[k].weights(a.w, a.wdt, a.cols, 1.0f, w);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float n = (to_f32(xp[k].v[j]) - mean) * rstd, h = to_f32(dp[k].v[j]) * w[kKeep ? k * V + j : j];
-        o[j] = rstd * ((h - s) - n * u);
+        const float d = to_f32(xp[k].v[j]) - mean, h = to_f32(dp[k].v[j]) * w[kKeep ? k * V + j : j];
+        o[j] = __builtin_fmaf(h, rstd, __builtin_fmaf(d, du, ds));
       }
       at[k].store(dx, a.cols, o);
     }
   }
   if (!a.partial) return;
   float* pw = a.partial + (uint64_t)blockIdx.x * 2 * a.cols;
-  if (WAVES == 1) {
+  if (RT::kWave) {
     // the row groups of a wave, then the four waves, always in the same order
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int o = LANES; o < 64; o <<= 1) {
+      for (int o = LANES + !LANES; o < 64; o <<= 1) {
         sw[i] += __shfl_xor(sw[i], o, 64);
         sb[i] += __shfl_xor(sb[i], o, 64);
       }
@@ -138,10 +140,10 @@ __global__ void __launch_bounds__((RowThreads<WAVES, LANES>::kThreads)) k_ln_bac
 
 template <typename T>
 __global__ void __launch_bounds__(LN_LONG) k_ln_dx_long(LnBackward a) {
-  using RT = RowThreads<LN_LONG / 64, 64>;
+  using RT = RowThreads<0>;
   constexpr int V = Piece<T>::V;
   __shared__ float lds[RT::kLds];
-  RT rt{lds};
+  RT rt(lds);
   const int64_t row = blockIdx.x;
   const T* x = (const T*)a.x + row * a.x_stride;
   const T* dy = (const T*)a.dy + row * a.dy_stride;
@@ -150,8 +152,8 @@ __global__ void __launch_bounds__(LN_LONG) k_ln_dx_long(LnBackward a) {
   Piece<T> p, q;
   for (uint32_t c = threadIdx.x * V; c < a.cols; c += LN_LONG * V) {
     const Place<T, RAGGED> at(c, a.cols);
-    at.load(x, a.cols, p);
-    at.load(dy, a.cols, q);
+    at.load(x, a.cols, false, p);
+    at.load(dy, a.cols, false, q);
     at.weights(a.w, a.wdt, a.cols, 1.0f, w);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -166,8 +168,8 @@ __global__ void __launch_bounds__(LN_LONG) k_ln_dx_long(LnBackward a) {
   for (uint32_t c = threadIdx.x * V; c < a.cols; c += LN_LONG * V) {
     const Place<T, RAGGED> at(c, a.cols);
     float o[V];
-    at.load(x, a.cols, p);
-    at.load(dy, a.cols, q);
+    at.load(x, a.cols, false, p);
+    at.load(dy, a.cols, false, q);
     at.weights(a.w, a.wdt, a.cols, 1.0f, w);
 #pragma unroll
     for (int j = 0; j < V; ++j)
@@ -216,31 +218,39 @@ template <typename T>
 struct Backward {
   const LnBackward& a;
   uint32_t n;
+  bool once;
   hipStream_t s;
-  template <int WAVES, int LANES, int NV>
-  void run() const {
-    using RT = RowThreads<WAVES, LANES>;
+  template <int LANES, int NV>
+  void run(uint32_t threads) const {
     constexpr uint32_t V = Piece<T>::V;
-    if (LANES == 1 && a.cols < V) k_ln_backward<T, 1, 1, 8, TINY><<<n, RT::kThreads, 0, s>>>(a);
-    else if (a.cols % V == 0) k_ln_backward<T, WAVES, LANES, NV, WHOLE><<<n, RT::kThreads, 0, s>>>(a);
-    else k_ln_backward<T, WAVES, LANES, NV, RAGGED><<<n, RT::kThreads, 0, s>>>(a);
+    if (LANES == 1 && a.cols < V) k_ln_backward<T, 1, 8, TINY, false><<<n, threads, 0, s>>>(a);
+    else if (a.cols % V == 0 && once) k_ln_backward<T, LANES, NV, WHOLE, true><<<n, threads, 0, s>>>(a);
+    else if (a.cols % V == 0) k_ln_backward<T, LANES, NV, WHOLE, false><<<n, threads, 0, s>>>(a);
+    else if (once) k_ln_backward<T, LANES, NV, RAGGED, true><<<n, threads, 0, s>>>(a);
+    else k_ln_backward<T, LANES, NV, RAGGED, false><<<n, threads, 0, s>>>(a);
   }
 };
+// Workgroups of the backward walk, each of which leaves one row of sums: as many as run at
+// once, so that none waits for a place (8192 columns of bf16: 80 us with 256 workgroups of 16
+// waves, 90 with 512), at most 768, and few enough that each has four turns: fewer rows of sums
+// are sooner added up (4M values of bf16 in rows of 1024: 16 -> 13 us).
 struct PartialRows {
   int64_t rows;
   uint32_t& n;
-  template <int WAVES, int LANES, int NV>
-  void run() const {
-    n = ln_walk(rows, RowThreads<WAVES, LANES>::kRows, WAVES == 16 ? 512 : 1024);
+  template <int LANES, int NV>
+  void run(uint32_t threads) const {
+    const uint32_t most = LN_CUS * (ln_backward_waves(LANES, NV) / (threads / 64));
+    n = ln_walk(rows, RowThreads<LANES>::kRows * 4, most < 768 ? most : 768);
   }
 };
 
 template <typename T>
 hipError_t backward(LnBackward a, hipStream_t s) {
+  const bool once = ln_once(a.rows * a.cols * 3 * (int64_t)sizeof(T));
   const uint32_t n = ln_partial_rows(a.rows, a.cols);
   const bool params = a.dw || a.db;
   if (!params) a.partial = nullptr;
-  if (a.rows && !ln_dispatch(a.cols, Backward<T>{a, n, s})) {
+  if (a.rows && !ln_dispatch(a.cols, Backward<T>{a, n, once, s})) {
     k_ln_dx_long<T><<<(uint32_t)a.rows, LN_LONG, 0, s>>>(a);
     if (params) k_ln_columns<T><<<dim3((a.cols + 255) / 256, n), 256, 0, s>>>(a);
   }
@@ -254,8 +264,6 @@ hipError_t backward(LnBackward a, hipStream_t s) {
 
 }  // namespace
 
-// Workgroups of the backward walk, each of which leaves one row of sums: as many as keep the
-// CUs busy, and no more than there are rows for.
 uint32_t ln_partial_rows(int64_t rows, uint32_t cols) {
   uint32_t n = 0;
   if (!ln_dispatch(cols, PartialRows{rows, n})) n = ln_walk(rows, 1, 512);

@@ -3,11 +3,11 @@
 //
 // Both directions read and write every value once: a row stays in the registers of its
 // threads, 8 or 16 values each, between the sums and the result. LANES lanes of a wave hold a
-// row of up to 1024 columns (a wave then works on 64 / LANES rows at once); a workgroup of 4
-// waves holds one of up to 4096 and one of 16 waves one of up to 16384, whose waves meet in LDS
-// once for each sum. A workgroup walks over rows: the weight and the bias stay in registers,
-// and the next row is loaded while the sums of this one are formed. Longer rows are read again
-// from the cache for each sum.
+// row of up to 1024 columns (a wave then works on 64 / LANES rows at once); longer rows of up
+// to 16384 columns are held by as many waves as they need, which meet in LDS
+// once for each sum. A workgroup walks over rows: the weight and the bias stay in registers, and
+// the next row is loaded while the sums of this one are formed. Longer rows are read again from
+// the cache for each sum.
 //
 // Every access is 16 bytes wide, at the element's alignment, which the hardware takes for
 // global memory: rows start anywhere (odd column counts, strides). Where the columns do not
@@ -32,6 +32,14 @@ struct __attribute__((packed, aligned(sizeof(T)))) Unaligned {
 template <typename T>
 __device__ __forceinline__ void load_piece(const T* __restrict__ p, Piece<T>& x) {
   __builtin_memcpy(x.v, (const Unaligned<T, Piece<T>::V>*)p, 16);
+}
+// The same, marked as not to be kept in the caches.
+template <typename T>
+__device__ __forceinline__ void load_piece_once(const T* __restrict__ p, Piece<T>& x) {
+  typedef uint32_t Q __attribute__((ext_vector_type(4)));
+  typedef Q QU __attribute__((aligned(2)));
+  const Q q = __builtin_nontemporal_load((const QU*)p);
+  __builtin_memcpy(x.v, &q, 16);
 }
 template <typename T>
 __device__ __forceinline__ void store_piece(T* __restrict__ p, const float* x) {
@@ -64,13 +72,14 @@ struct Place {
   __device__ __forceinline__ bool mine(int j, uint32_t cols) const {
     return COLS == TINY ? c + j < cols : j >= own;
   }
-  __device__ __forceinline__ void load(const T* __restrict__ row, uint32_t cols, Piece<T>& x) const {
+  __device__ __forceinline__ void load(const T* __restrict__ row, uint32_t cols, bool once, Piece<T>& x) const {
     if (COLS == TINY) {
 #pragma unroll
       for (int j = 0; j < V; ++j)
         if (c + j < cols) x.v[j] = row[c + j];
     } else if (own < V) {
-      load_piece(row + c, x);
+      if (once) load_piece_once(row + c, x);
+      else load_piece(row + c, x);
     }
   }
   __device__ __forceinline__ void store(T* __restrict__ row, uint32_t cols, const float* x) const {
@@ -130,57 +139,77 @@ __device__ __forceinline__ float group_sum(float x) {
   return x;
 }
 
-// The threads of a row: LANES lanes of a wave, or (LANES = 64) all WAVES waves of the
-// workgroup.
-template <int WAVES, int LANES>
+// The threads of a row: LANES lanes of a wave in a workgroup of 4 waves, or (LANES = 0) all
+// threads of the workgroup, up to 16 waves.
+template <int LANES>
 struct RowThreads {
-  static constexpr int kThreads = WAVES == 1 ? 256 : WAVES * 64;   // of a workgroup
-  static constexpr int kCount = WAVES * LANES;
-  static constexpr int kRows = kThreads / kCount;                   // of a workgroup at a time
-  static constexpr int kLds = WAVES > 1 ? 4 * WAVES : 1;
+  static constexpr bool kWave = LANES > 0;
+  static constexpr int kMost = kWave ? 256 : 1024;           // threads of a workgroup
+  static constexpr int kRows = kWave ? 256 / (LANES + !LANES) : 1;   // of a workgroup at a time
+  static constexpr int kLds = kWave ? 1 : 64;
   float* lds;
   int turn = 0;
-  static __device__ __forceinline__ uint32_t index() { return threadIdx.x % kCount; }
-  static __device__ __forceinline__ uint32_t row() { return threadIdx.x / kCount; }
+  __device__ __forceinline__ explicit RowThreads(float* l) : lds(l) {
+    // the places of waves that the workgroup does not have stay zero
+    if (!kWave && threadIdx.x < 64) lds[threadIdx.x] = 0.0f;
+    if (!kWave) lds_barrier();
+  }
+  static __device__ __forceinline__ uint32_t count() { return kWave ? LANES : blockDim.x; }
+  static __device__ __forceinline__ uint32_t index() { return kWave ? threadIdx.x % (LANES + !LANES) : threadIdx.x; }
+  static __device__ __forceinline__ uint32_t row() { return kWave ? threadIdx.x / (LANES + !LANES) : 0; }
   // s and t summed over the row's threads. The waves' sums alternate between two places, so
   // that one barrier a sum is enough: before a place is written again, every wave has passed
   // the barrier of the sum between.
   template <bool TWO>
   __device__ __forceinline__ void sum(float& s, float& t) {
-    s = group_sum<LANES>(s);
-    if (TWO) t = group_sum<LANES>(t);
-    if (WAVES == 1) return;
-    float* at = lds + turn * 2 * WAVES;
+    s = group_sum<kWave ? LANES : 64>(s);
+    if (TWO) t = group_sum<kWave ? LANES : 64>(t);
+    if (kWave) return;
+    float* at = lds + turn * 32;
     turn ^= 1;
     if ((threadIdx.x & 63) == 0) {
       at[threadIdx.x >> 6] = s;
-      if (TWO) at[WAVES + (threadIdx.x >> 6)] = t;
+      if (TWO) at[16 + (threadIdx.x >> 6)] = t;
     }
     lds_barrier();
-    s = group_sum<WAVES>(at[threadIdx.x & (WAVES - 1)]);
-    if (TWO) t = group_sum<WAVES>(at[WAVES + (threadIdx.x & (WAVES - 1))]);
+    s = group_sum<16>(at[threadIdx.x & 15]);
+    if (TWO) t = group_sum<16>(at[16 + (threadIdx.x & 15)]);
   }
 };
 
+// Waves of a kernel that a CU holds at once; the launch bounds keep the registers to that. A
+// walk takes as many workgroups as then run at the same time: with some more the last ones
+// start alone (1536 columns of bf16, forward: 5.8 TB/s, 5.2 with 7% too many).
+constexpr uint32_t LN_CUS = 256;
+constexpr uint32_t ln_forward_waves(int nv) { return nv == 8 ? 32 : 20; }
+constexpr uint32_t ln_backward_waves(int lanes, int nv) { return nv == 8 ? 20 : lanes ? 12 : 16; }
+
 constexpr uint32_t LN_MAX_COLS = 16384;   // of a row in registers
 
-// Calls f.template operator()<WAVES, LANES, NV>() for the threads that hold rows of `cols`
-// values, `v` to a piece: as few lanes as hold it with 8 or 16 values each.
+// Calls f.run<LANES, NV>(threads) for the threads that hold rows of `cols` values: as few lanes
+// of a wave as do with 8 values each, a wave with 16, or a workgroup of as many waves as do with
+// 8 or 16.
 template <typename F>
 bool ln_dispatch(uint32_t cols, F f) {
-  if (cols <= 8) f.template run<1, 1, 8>();
-  else if (cols <= 32) f.template run<1, 4, 8>();
-  else if (cols <= 128) f.template run<1, 16, 8>();
-  else if (cols <= 256) f.template run<1, 16, 16>();
-  else if (cols <= 512) f.template run<1, 64, 8>();
-  else if (cols <= 1024) f.template run<1, 64, 16>();
-  else if (cols <= 2048) f.template run<4, 64, 8>();
-  else if (cols <= 4096) f.template run<4, 64, 16>();
-  else if (cols <= 8192) f.template run<16, 64, 8>();
-  else if (cols <= LN_MAX_COLS) f.template run<16, 64, 16>();
+  if (cols <= 8) f.template run<1, 8>(256);
+  else if (cols <= 16) f.template run<2, 8>(256);
+  else if (cols <= 32) f.template run<4, 8>(256);
+  else if (cols <= 64) f.template run<8, 8>(256);
+  else if (cols <= 128) f.template run<16, 8>(256);
+  else if (cols <= 256) f.template run<32, 8>(256);
+  else if (cols <= 512) f.template run<64, 8>(256);
+  else if (cols <= 1024) f.template run<64, 16>(256);
+  else if (cols <= 8192) f.template run<0, 8>((cols + 511) / 512 * 64);
+  else if (cols <= LN_MAX_COLS) f.template run<0, 16>((cols + 1023) / 1024 * 64);
   else return false;
   return true;
 }
+
+// Whether a call that reads and writes this much asks the caches not to keep what it reads:
+// more than they hold anyway (fp32, 67M values: forward 5.3 -> 6.5 TB/s, backward 5.2 -> 6.2;
+// bf16 backward 5.2 -> 5.8). Below, part of it may be there still (bf16 forward, 268 MB: 5.9
+// with and 5.6 TB/s without).
+inline bool ln_once(int64_t bytes) { return bytes > 300000000; }
 
 // Workgroups of a walk over `rows`, `per` rows at a time: no more than `most`.
 inline uint32_t ln_walk(int64_t rows, int per, uint32_t most) {
