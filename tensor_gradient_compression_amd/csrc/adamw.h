@@ -71,10 +71,15 @@ struct AdamwArgs {
 
 hipError_t launch_adamw(const AdamwArgs& a, const AdamwTable& tab, hipStream_t s);
 
+// Counts of workgroups that have finished, by their number's remainder, and one of the groups,
+// each in a cache line of its own.
+constexpr uint32_t ADAMW_COUNTS = 16, ADAMW_COUNT_PITCH = 64;
+
 struct AdamwNorm {
   const AdamwSpan* spans;     // of this launch
-  double* partial;            // a sum of squares for each of them (the result's: for all)
-  uint32_t* done;             // join: workgroups that have finished; 0 between calls
+  double* partial;            // a sum of squares for each of them
+  double* all_partial;        // those of all launches
+  uint32_t* counts;           // join: workgroups that have finished; 0 between calls
   uint32_t first_tensor;      // of this launch
   uint32_t total_spans;
   float* out;                 // {norm, coefficient}

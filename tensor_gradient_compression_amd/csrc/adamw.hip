@@ -29,11 +29,11 @@ struct tgrad_adamw {
   std::vector<Tensor> tensors;
   std::vector<Launch> launches;
   uint32_t nchunks = 0, nspans = 0;
-  AdamwChunk* chunks = nullptr;   // device, one block of memory with the four below
+  AdamwChunk* chunks = nullptr;   // device, one block of memory with those below
   AdamwClock* clocks = nullptr;
   AdamwSpan* spans = nullptr;
   double* partial = nullptr;
-  uint32_t* done = nullptr;
+  uint32_t* counts = nullptr;
   void* block = nullptr;
   void* state = nullptr;          // the caller's
   std::string err;
@@ -49,10 +49,7 @@ namespace {
 constexpr uint64_t kStreamBytes = 1500000000;
 constexpr uint32_t kStreamLds = 80 * 1024;
 
-// Up to this many spans the norm's last workgroup joins the sums: its count costs 11 ns a
-// workgroup (14 spans 4.9 us in all, 1897 spans 32 us); above, a second kernel does, which
-// costs about 5 us with the gap before it (14 spans 3.5 + 1.5 us and a gap, 1897 spans 11 + 4.6).
-constexpr uint32_t kJoinSpans = 512;
+constexpr size_t kCountBytes = (ADAMW_COUNTS + 1) * ADAMW_COUNT_PITCH * sizeof(uint32_t);
 
 struct OnDevice {
   int prev = -1;
@@ -207,19 +204,20 @@ int tgrad_adamw_init(tgrad_adamw_t** out, int n, const int64_t* numel, const int
     h->nspans = (uint32_t)spans.size();
     const size_t bc = chunks.size() * sizeof(AdamwChunk), bk = chunks.size() * sizeof(AdamwClock);
     const size_t bs = spans.size() * sizeof(AdamwSpan), bp = spans.size() * sizeof(double);
-    if (hipMalloc(&h->block, bc + bk + bs + bp + sizeof(uint32_t)) != hipSuccess) {
+    if (hipMalloc(&h->block, kCountBytes + bc + bk + bs + bp) != hipSuccess) {
       delete h;
       return TGRAD_ENOMEM;
     }
-    h->chunks = (AdamwChunk*)h->block;
-    h->clocks = (AdamwClock*)((char*)h->block + bc);
-    h->spans = (AdamwSpan*)((char*)h->block + bc + bk);
-    h->partial = (double*)((char*)h->block + bc + bk + bs);
-    h->done = (uint32_t*)((char*)h->block + bc + bk + bs + bp);
+    char* at_block = (char*)h->block;
+    h->counts = (uint32_t*)at_block;
+    h->chunks = (AdamwChunk*)(at_block += kCountBytes);
+    h->clocks = (AdamwClock*)(at_block += bc);
+    h->spans = (AdamwSpan*)(at_block += bk);
+    h->partial = (double*)(at_block += bs);
     const std::vector<AdamwClock> clocks(chunks.size(), clock_after(h, 0));
     hipError_t e = hipMemcpy(h->chunks, chunks.data(), bc, hipMemcpyHostToDevice);
     if (e == hipSuccess && bs) e = hipMemcpy(h->spans, spans.data(), bs, hipMemcpyHostToDevice);
-    if (e == hipSuccess) e = hipMemset(h->done, 0, sizeof(uint32_t));
+    if (e == hipSuccess) e = hipMemset(h->counts, 0, kCountBytes);
     if (e == hipSuccess) e = set_clocks(h, clocks);
     if (e != hipSuccess) {
       (void)hipFree(h->block);
@@ -340,12 +338,12 @@ int tgrad_adamw_grad_norm(tgrad_adamw_t* h, const void* const* grads, double max
   }
   OnDevice g(h->device);
   AdamwNorm a{};
-  a.done = h->done;
+  a.counts = h->counts;
+  a.all_partial = h->partial;
   a.total_spans = h->nspans;
   a.out = out;
   a.max_norm = max_norm;
   a.scale = grad_scale;
-  const bool join = h->launches.size() == 1 && h->nspans > 0 && h->nspans <= kJoinSpans;
   for (const auto& l : h->launches) {
     if (!l.spans) continue;
     AdamwTable tab;
@@ -356,12 +354,12 @@ int tgrad_adamw_grad_norm(tgrad_adamw_t* h, const void* const* grads, double max
     a.spans = h->spans + l.first_span;
     a.partial = h->partial + l.first_span;
     a.first_tensor = (uint32_t)l.first_tensor;
+    const bool join = l.first_span + l.spans == h->nspans;
     const hipError_t e = launch_adamw_squares(a, l.spans, join, tab, (hipStream_t)stream);
     if (e != hipSuccess) return fail(h, e, "gradient norm");
   }
-  if (join) return TGRAD_OK;
-  a.partial = h->partial;
-  const hipError_t e = launch_adamw_norm(a, (hipStream_t)stream);
+  if (h->nspans) return TGRAD_OK;
+  const hipError_t e = launch_adamw_norm(a, (hipStream_t)stream);   // no gradients at all
   return e == hipSuccess ? TGRAD_OK : fail(h, e, "gradient norm");
 }
 

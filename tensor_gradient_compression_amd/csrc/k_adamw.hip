@@ -440,14 +440,26 @@ __device__ __forceinline__ void write_norm(const AdamwNorm& a, double squares) {
   a.out[1] = (float)(norm > a.max_norm ? a.scale * (a.max_norm / norm) : a.scale);
 }
 
-// The sums of squares of one launch's spans. JOIN (one launch of few spans): the workgroup that
-// finishes last also adds the sums up, in their order, and writes the result. The sums go
-// through atomic exchanges, whose answers the count waits for, and atomic loads: both act
-// where every workgroup sees them, so no cache has to be written back in between.
+// Adds one to a count and returns whether it is the last of `n`, which also clears it. The
+// count is made where every workgroup sees it.
+__device__ __forceinline__ bool last_of(uint32_t* count, uint32_t one, uint32_t n) {
+  const uint32_t before = __hip_atomic_fetch_add(count, one, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (before != n - 1) return false;
+  __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return true;
+}
+
+// The sums of squares of one launch's spans. JOIN (a call's last launch): the workgroup that
+// finishes last also adds all the sums up, in their order, and writes the result; a kernel of
+// its own for that would take 5 us with the gap before it. The sums go through atomic
+// exchanges, whose answers the count waits for, and atomic loads: both act where every
+// workgroup sees them, so no cache has to be written back in between (with fences that did,
+// 32 ns a workgroup). Counting at one place takes 11 ns a workgroup; so 16 groups of them count
+// apart, and their last ones together.
 template <bool JOIN>
 __global__ void __launch_bounds__(kThreads) k_adamw_squares(AdamwNorm a, AdamwTable tab) {
   __shared__ double lds[4];
-  __shared__ uint32_t before;
+  __shared__ bool last;
   const AdamwSpan c = a.spans[blockIdx.x];
   const void* g = tab.g[c.tensor - a.first_tensor];
   double s;
@@ -465,25 +477,26 @@ __global__ void __launch_bounds__(kThreads) k_adamw_squares(AdamwNorm a, AdamwTa
                                                    __HIP_MEMORY_SCOPE_AGENT);
     uint32_t one = 1;
     __asm__ volatile("" : "+v"(one), "+v"(old));   // the count waits for the exchange
-    before = __hip_atomic_fetch_add(a.done, one, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t groups = gridDim.x < ADAMW_COUNTS ? gridDim.x : ADAMW_COUNTS, mine = blockIdx.x % ADAMW_COUNTS;
+    const uint32_t members = (gridDim.x - mine + ADAMW_COUNTS - 1) / ADAMW_COUNTS;
+    last = last_of(a.counts + mine * ADAMW_COUNT_PITCH, one, members) &&
+           last_of(a.counts + ADAMW_COUNTS * ADAMW_COUNT_PITCH, one, groups);
   }
   __syncthreads();
-  if (before != gridDim.x - 1) return;
+  if (!last) return;
   s = 0.0;
   for (uint32_t i = threadIdx.x; i < a.total_spans; i += kThreads)
-    s += __longlong_as_double(__hip_atomic_load((unsigned long long*)a.partial + i, __ATOMIC_RELAXED,
+    s += __longlong_as_double(__hip_atomic_load((unsigned long long*)a.all_partial + i, __ATOMIC_RELAXED,
                                                 __HIP_MEMORY_SCOPE_AGENT));
   s = block_sum(s, lds);
-  if (threadIdx.x == 0) {
-    write_norm(a, s);
-    *a.done = 0;
-  }
+  if (threadIdx.x == 0) write_norm(a, s);
 }
 
+// The result of no gradients at all.
 __global__ void __launch_bounds__(kThreads) k_adamw_norm(AdamwNorm a) {
   __shared__ double lds[4];
   double s = 0.0;
-  for (uint32_t i = threadIdx.x; i < a.total_spans; i += kThreads) s += a.partial[i];
+  for (uint32_t i = threadIdx.x; i < a.total_spans; i += kThreads) s += a.all_partial[i];
   s = block_sum(s, lds);
   if (threadIdx.x == 0) write_norm(a, s);
 }
