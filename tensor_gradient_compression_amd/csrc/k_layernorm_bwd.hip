@@ -12,7 +12,7 @@ namespace tg {
 namespace {
 
 // Up to 16 values a thread their sums over rows, the weights and two rows fit the registers;
-// with 16 waves and 16 values (128 registers a thread) the weights are read again for each row.
+// with 16 waves and 16 values (128 registers a thread) the weights stay in LDS as fp32.
 // ONCE: see ln_once; as an argument the choice between two loads makes every one wait at once.
 template <typename T, int LANES, int NV, int COLS, bool ONCE>
 __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_backward_waves(LANES, NV) / 4)
@@ -21,6 +21,7 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_backward_waves(LA
   constexpr int V = Piece<T>::V, K = NV / V;
   constexpr bool kKeep = !(LANES == 0 && NV == 16);
   __shared__ float lds[RT::kWave ? 4 * 2 * NV * LANES : RT::kLds];
+  __shared__ float wl[kKeep ? 1 : LN_MAX_COLS];
   RT rt(lds);
   const int64_t stride = (int64_t)gridDim.x * RT::kRows;
   const float inv = 1.0f / (float)a.cols;
@@ -40,9 +41,14 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_backward_waves(LA
   }
   if (row < a.rows) mean_n = a.mean[row], rstd_n = a.rstd[row];
   float w[kKeep ? NV : V], sw[NV], sb[NV];
-  if (kKeep)
 #pragma unroll
-    for (int k = 0; k < K; ++k) at[k].weights(a.w, a.wdt, a.cols, 1.0f, w + (kKeep ? k * V : 0));
+  for (int k = 0; k < K; ++k) {
+    at[k].weights(a.w, a.wdt, a.cols, 1.0f, w + (kKeep ? k * V : 0));
+    if (!kKeep) {   // read back by this thread alone
+#pragma unroll
+      for (int j = 0; j < V; ++j) wl[(k * V + j) * 1024 + threadIdx.x] = w[j];
+    }
+  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) sw[i] = sb[i] = 0.0f;
   for (int64_t base = (int64_t)blockIdx.x * RT::kRows; base < a.rows; base += stride, row += stride) {
@@ -69,7 +75,10 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_backward_waves(LA
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (!kKeep) at[k].weights(a.w, a.wdt, a.cols, 1.0f, w);
+      if (!kKeep) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) w[j] = wl[(k * V + j) * 1024 + threadIdx.x];
+      }
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int i = k * V + j;
@@ -89,7 +98,10 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_backward_waves(LA
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float o[V];
-      if (!kKeep) at[k].weights(a.w, a.wdt, a.cols, 1.0f, w);
+      if (!kKeep) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) w[j] = wl[(k * V + j) * 1024 + threadIdx.x];
+      }
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float d = to_f32(xp[k].v[j]) - mean, h = to_f32(dp[k].v[j]) * w[kKeep ? k * V + j : j];
