@@ -1,6 +1,7 @@
 // Host side of AdamW over many tensors: the handle, its division of the tensors into
 // workgroups' chunks, and the launches. Kernels and arithmetic: k_adamw.hip.
 #include <cmath>
+#include <cstring>
 #include <new>
 #include <string>
 #include <vector>
@@ -101,7 +102,6 @@ hipError_t set_clocks(tgrad_adamw_t* h, const std::vector<AdamwClock>& host) {
   hipError_t e = hipDeviceSynchronize();
   if (e == hipSuccess)
     e = hipMemcpy(h->clocks, host.data(), host.size() * sizeof(AdamwClock), hipMemcpyHostToDevice);
-  if (e == hipSuccess) e = hipDeviceSynchronize();
   return e;
 }
 
@@ -204,7 +204,13 @@ int tgrad_adamw_init(tgrad_adamw_t** out, int n, const int64_t* numel, const int
     h->nspans = (uint32_t)spans.size();
     const size_t bc = chunks.size() * sizeof(AdamwChunk), bk = chunks.size() * sizeof(AdamwClock);
     const size_t bs = spans.size() * sizeof(AdamwSpan), bp = spans.size() * sizeof(double);
-    if (hipMalloc(&h->block, kCountBytes + bc + bk + bs + bp) != hipSuccess) {
+    // one block, filled by one copy: counts of zero, chunks, clocks, spans, room for the sums
+    std::vector<char> host(kCountBytes + bc + bk + bs, 0);
+    const std::vector<AdamwClock> clocks(chunks.size(), clock_after(h, 0));
+    std::memcpy(host.data() + kCountBytes, chunks.data(), bc);
+    std::memcpy(host.data() + kCountBytes + bc, clocks.data(), bk);
+    if (bs) std::memcpy(host.data() + kCountBytes + bc + bk, spans.data(), bs);
+    if (hipMalloc(&h->block, host.size() + bp) != hipSuccess) {
       delete h;
       return TGRAD_ENOMEM;
     }
@@ -214,11 +220,8 @@ int tgrad_adamw_init(tgrad_adamw_t** out, int n, const int64_t* numel, const int
     h->clocks = (AdamwClock*)(at_block += bc);
     h->spans = (AdamwSpan*)(at_block += bk);
     h->partial = (double*)(at_block += bs);
-    const std::vector<AdamwClock> clocks(chunks.size(), clock_after(h, 0));
-    hipError_t e = hipMemcpy(h->chunks, chunks.data(), bc, hipMemcpyHostToDevice);
-    if (e == hipSuccess && bs) e = hipMemcpy(h->spans, spans.data(), bs, hipMemcpyHostToDevice);
-    if (e == hipSuccess) e = hipMemset(h->counts, 0, kCountBytes);
-    if (e == hipSuccess) e = set_clocks(h, clocks);
+    hipError_t e = hipMemcpy(h->block, host.data(), host.size(), hipMemcpyHostToDevice);
+    if (e == hipSuccess) e = hipDeviceSynchronize();
     if (e != hipSuccess) {
       (void)hipFree(h->block);
       delete h;
