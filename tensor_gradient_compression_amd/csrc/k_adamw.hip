@@ -67,11 +67,13 @@ __device__ __forceinline__ float root(float v) {
 constexpr uint32_t kRootLow = (127 - 48) << 23, kRootHigh = (127 + 63) << 23;
 
 // Whole accesses of 8 or 16 bytes, marked as not to be kept: a step touches every byte once,
-// and what the caches keep of it is gone before the next one.
+// and what the caches keep of it is gone before the next one. At the element's alignment, which
+// the hardware takes for global memory: tensors may be views that start anywhere.
 template <typename T, int N>
 struct Wide {
   static constexpr int kBytes = N * sizeof(T) < 16 ? N * sizeof(T) : 16;
   typedef uint32_t V __attribute__((ext_vector_type(kBytes / 4)));
+  typedef V At __attribute__((aligned(2)));
   static constexpr int kPieces = N * sizeof(T) / kBytes;
 };
 template <typename T, int N>
@@ -79,7 +81,7 @@ __device__ __forceinline__ void load_wide(const T* __restrict__ p, T (&v)[N]) {
   using W = Wide<T, N>;
   typename W::V t[W::kPieces];
 #pragma unroll
-  for (int i = 0; i < W::kPieces; ++i) t[i] = __builtin_nontemporal_load((const typename W::V*)p + i);
+  for (int i = 0; i < W::kPieces; ++i) t[i] = __builtin_nontemporal_load((const typename W::At*)p + i);
   __builtin_memcpy(v, t, sizeof v);
 }
 template <typename T, int N>
@@ -88,7 +90,7 @@ __device__ __forceinline__ void store_wide(T* __restrict__ p, const T (&v)[N]) {
   typename W::V t[W::kPieces];
   __builtin_memcpy(t, v, sizeof v);
 #pragma unroll
-  for (int i = 0; i < W::kPieces; ++i) __builtin_nontemporal_store(t[i], (typename W::V*)p + i);
+  for (int i = 0; i < W::kPieces; ++i) __builtin_nontemporal_store(t[i], (typename W::At*)p + i);
 }
 
 // largest over the 16 lanes of a row, in all of them (rotations within the row)
@@ -113,28 +115,15 @@ __device__ __forceinline__ uint32_t top_halves(uint32_t a, uint32_t b) {
   return __builtin_amdgcn_perm(b, a, 0x07060302u);
 }
 
-// N values of a piece that may end early: `have` of them exist, the others read as zero and
-// are not written.
-template <int N, typename T>
-__device__ __forceinline__ void load_some(const T* __restrict__ p, int have, float* x) {
-#pragma unroll
-  for (int j = 0; j < N; ++j) x[j] = j < have ? to_f32(p[j]) : 0.0f;
-}
-template <int N, typename T>
-__device__ __forceinline__ void store_some(T* __restrict__ p, int have, const float* x) {
-#pragma unroll
-  for (int j = 0; j < N; ++j)
-    if (j < have) p[j] = from_f32<T>(x[j]);
-}
-
-// The weights and gradients of a chunk, two ways. A full chunk at 16-byte aligned addresses:
-// wide accesses of known types, converted apart from their loads, so that every load of the
-// chunk is in flight before the first is waited for.
-template <typename WT, typename GT>
-struct WholeChunk {
-  static constexpr bool kWhole = true;
+// The weights and gradients of a chunk. They are converted apart from their loads, so that
+// every load of the chunk is in flight before the first is waited for. In a chunk that ends
+// early (WHOLE false) one lane's piece may end inside: it is read and written value by value.
+template <typename WT, typename GT, bool WHOLE>
+struct Chunk {
+  static constexpr bool kWhole = WHOLE;
   WT* w;
   const GT* g;
+  uint32_t n;
   template <int N>
   struct Raw {
     WT w[N];
@@ -142,8 +131,17 @@ struct WholeChunk {
   };
   template <int N>
   __device__ __forceinline__ void load(uint32_t i, Raw<N>& r) const {
-    load_wide(w + i, r.w);
-    load_wide(g + i, r.g);
+    if (WHOLE || i + N <= n) {
+      load_wide(w + i, r.w);
+      load_wide(g + i, r.g);
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const bool in = i + j < n;
+      r.w[j] = in ? w[i + j] : zero_of<WT>();
+      r.g[j] = in ? g[i + j] : zero_of<GT>();
+    }
   }
   template <int N>
   __device__ __forceinline__ void values(const Raw<N>& r, float* wx, float* gx) const {
@@ -158,62 +156,29 @@ struct WholeChunk {
     WT v[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) v[j] = from_f32<WT>(wx[j]);
-    store_wide(w + i, v);
-  }
-};
-// A tensor's end, or one that is not aligned: value by value, of any types.
-struct PartChunk {
-  static constexpr bool kWhole = false;
-  void* w;
-  const void* g;
-  uint64_t start;
-  uint32_t n, wdt, gdt;
-  template <int N>
-  struct Raw {
-    float w[N], g[N];
-  };
-  template <int N>
-  __device__ __forceinline__ void load(uint32_t i, Raw<N>& r) const {
-    const int have = (int)n - (int)i;
-    const uint64_t at = start + i;
-    if (wdt == DT_F32) load_some<N>((const float*)w + at, have, r.w);
-    else if (wdt == DT_F16) load_some<N>((const _Float16*)w + at, have, r.w);
-    else load_some<N>((const bf16_t*)w + at, have, r.w);
-    if (gdt == DT_F32) load_some<N>((const float*)g + at, have, r.g);
-    else if (gdt == DT_F16) load_some<N>((const _Float16*)g + at, have, r.g);
-    else load_some<N>((const bf16_t*)g + at, have, r.g);
-  }
-  template <int N>
-  __device__ __forceinline__ void values(const Raw<N>& r, float* wx, float* gx) const {
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      wx[j] = r.w[j];
-      gx[j] = r.g[j];
+    if (WHOLE || i + N <= n) {
+      store_wide(w + i, v);
+      return;
     }
-  }
-  template <int N>
-  __device__ __forceinline__ void store(uint32_t i, const float* wx) const {
-    const int have = (int)n - (int)i;
-    const uint64_t at = start + i;
-    if (wdt == DT_F32) store_some<N>((float*)w + at, have, wx);
-    else if (wdt == DT_F16) store_some<N>((_Float16*)w + at, have, wx);
-    else store_some<N>((bf16_t*)w + at, have, wx);
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (i + j < n) w[i + j] = v[j];
   }
 };
 
 // fp32 moments: two pieces of four values a thread, so that a wave's accesses to the moments
 // are whole 1 KiB runs and all loads of both pieces are in flight together.
-template <typename Chunk>
-__device__ __forceinline__ void chunk32(const AdamwArgs& a, const AdamwChunk& c, const Chunk& io,
+template <typename IO>
+__device__ __forceinline__ void chunk32(const AdamwArgs& a, const AdamwChunk& c, const IO& io,
                                         const StepK& k, bool skip) {
   float* m = (float*)a.m + c.state;
   float* v = (float*)a.v + c.state;
-  typename Chunk::template Raw<4> raw[2];
+  typename IO::template Raw<4> raw[2];
   float mx[2][4], vx[2][4];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const uint32_t i = (u * kThreads + threadIdx.x) * 4;
-    if (!Chunk::kWhole && i >= c.n) break;
+    if (!IO::kWhole && i >= c.n) break;
     load_wide(m + i, mx[u]);
     load_wide(v + i, vx[u]);
     io.load(i, raw[u]);
@@ -222,7 +187,7 @@ __device__ __forceinline__ void chunk32(const AdamwArgs& a, const AdamwChunk& c,
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const uint32_t i = (u * kThreads + threadIdx.x) * 4;
-    if (!Chunk::kWhole && i >= c.n) break;
+    if (!IO::kWhole && i >= c.n) break;
     float wx[4], gx[4];
     io.values(raw[u], wx, gx);
 #pragma unroll
@@ -237,18 +202,18 @@ __device__ __forceinline__ void chunk32(const AdamwArgs& a, const AdamwChunk& c,
 }
 
 // 8-bit moments: 16 lanes hold a group, 8 values each
-template <bool VALUES, typename Chunk>
-__device__ __forceinline__ void chunk8(const AdamwArgs& a, const AdamwChunk& c, const Chunk& io,
+template <bool VALUES, typename IO>
+__device__ __forceinline__ void chunk8(const AdamwArgs& a, const AdamwChunk& c, const IO& io,
                                        uint32_t key, const StepK& k, bool skip) {
   const uint32_t i = threadIdx.x * 8;
-  if (!Chunk::kWhole && i >= (c.n + ADAMW_GROUP - 1) / ADAMW_GROUP * ADAMW_GROUP) return;
+  if (!IO::kWhole && i >= (c.n + ADAMW_GROUP - 1) / ADAMW_GROUP * ADAMW_GROUP) return;
   const uint64_t at = c.state + i;
   uint2* mc = (uint2*)((uint8_t*)a.m + at);
   uint2* qc = (uint2*)((uint8_t*)a.v + at);
   uint8_t *ms = a.ms + at / ADAMW_GROUP, *qs = a.vs + at / ADAMW_GROUP;
   const uint2 cm = *mc, cq = *qc;
   const int fm = *ms, fq = *qs;
-  typename Chunk::template Raw<8> raw;
+  typename IO::template Raw<8> raw;
   io.load(i, raw);
   if (skip) return;
   float wx[8], gx[8], m[8], q[8];
@@ -334,16 +299,19 @@ __device__ __forceinline__ void chunk8(const AdamwArgs& a, const AdamwChunk& c, 
   }
 }
 
-template <int BITS, bool VALUES, typename Chunk>
-__device__ __forceinline__ void chunk(const AdamwArgs& a, const AdamwChunk& c, const Chunk& io,
+template <int BITS, bool VALUES, typename IO>
+__device__ __forceinline__ void chunk(const AdamwArgs& a, const AdamwChunk& c, const IO& io,
                                       uint32_t key, const StepK& k, bool skip) {
   if (BITS == 32) chunk32(a, c, io, k, skip);
   else chunk8<VALUES>(a, c, io, key, k, skip);
 }
 template <int BITS, bool VALUES, typename WT, typename GT>
-__device__ __forceinline__ void whole(const AdamwArgs& a, const AdamwChunk& c, void* w, const void* g,
-                                      uint32_t key, const StepK& k, bool skip) {
-  chunk<BITS, VALUES>(a, c, WholeChunk<WT, GT>{(WT*)w + c.start, (const GT*)g + c.start}, key, k, skip);
+__device__ __forceinline__ void chunk_of(const AdamwArgs& a, const AdamwChunk& c, void* w, const void* g,
+                                         uint32_t key, const StepK& k, bool skip) {
+  WT* wp = (WT*)w + c.start;
+  const GT* gp = (const GT*)g + c.start;
+  if (c.n == ADAMW_CHUNK) chunk<BITS, VALUES>(a, c, Chunk<WT, GT, true>{wp, gp, c.n}, key, k, skip);
+  else chunk<BITS, VALUES>(a, c, Chunk<WT, GT, false>{wp, gp, c.n}, key, k, skip);
 }
 
 template <int BITS, bool VALUES>
@@ -369,13 +337,11 @@ __global__ void __launch_bounds__(kThreads) k_adamw(AdamwArgs a, AdamwTable tab)
   k.decay = (float)(1.0 - a.lr * c.wd);
   void* w = tab.w[c.tensor - a.first_tensor];
   const void* g = tab.g[c.tensor - a.first_tensor];
-  if (c.n < ADAMW_CHUNK || (((uintptr_t)w | (uintptr_t)g) & 15u) != 0)
-    chunk<BITS, VALUES>(a, c, PartChunk{w, g, c.start, c.n, c.wdt, c.gdt}, now.key, k, skip);
-  else if (c.wdt == DT_F32) whole<BITS, VALUES, float, float>(a, c, w, g, now.key, k, skip);
-  else if (c.wdt == DT_F16 && c.gdt == DT_F16) whole<BITS, VALUES, _Float16, _Float16>(a, c, w, g, now.key, k, skip);
-  else if (c.wdt == DT_F16) whole<BITS, VALUES, _Float16, float>(a, c, w, g, now.key, k, skip);
-  else if (c.gdt == DT_BF16) whole<BITS, VALUES, bf16_t, bf16_t>(a, c, w, g, now.key, k, skip);
-  else whole<BITS, VALUES, bf16_t, float>(a, c, w, g, now.key, k, skip);
+  if (c.wdt == DT_F32) chunk_of<BITS, VALUES, float, float>(a, c, w, g, now.key, k, skip);
+  else if (c.wdt == DT_F16 && c.gdt == DT_F16) chunk_of<BITS, VALUES, _Float16, _Float16>(a, c, w, g, now.key, k, skip);
+  else if (c.wdt == DT_F16) chunk_of<BITS, VALUES, _Float16, float>(a, c, w, g, now.key, k, skip);
+  else if (c.gdt == DT_BF16) chunk_of<BITS, VALUES, bf16_t, bf16_t>(a, c, w, g, now.key, k, skip);
+  else chunk_of<BITS, VALUES, bf16_t, float>(a, c, w, g, now.key, k, skip);
   __syncthreads();   // every wave has read its clock
   if (threadIdx.x == 0 && !skip) {
     // the hardware's estimates (2^-26 and better) with one Newton step each are exact far
@@ -397,30 +363,25 @@ template <typename GT>
 __device__ double squares(const GT* __restrict__ g, uint32_t n) {
   constexpr int N = 16 / sizeof(GT);
   double s = 0.0;
-  if (((uintptr_t)g & 15u) != 0) {
-    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-      const double x = (double)to_f32(g[i]);
-      s += x * x;
-    }
-    return s;
-  }
   for (uint32_t base = threadIdx.x * N; base < n; base += kThreads * N * 4) {
-    float x[4][N];
+    GT x[4][N];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const uint32_t i = base + u * kThreads * N;
       if (i + N <= n) {
-        GT v[N];
-        load_wide(g + i, v);
-        for (int j = 0; j < N; ++j) x[u][j] = to_f32(v[j]);
+        load_wide(g + i, x[u]);
       } else {
-        load_some<N>(g + i, (int)n - (int)i, x[u]);
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[u][j] = i + j < n ? g[i + j] : zero_of<GT>();
       }
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
-      for (int j = 0; j < N; ++j) s = fma((double)x[u][j], (double)x[u][j], s);
+      for (int j = 0; j < N; ++j) {
+        const double v = (double)to_f32(x[u][j]);
+        s = fma(v, v, s);
+      }
   }
   return s;
 }
