@@ -83,7 +83,7 @@ def _link_binding(obj: str) -> None:
     lib = os.path.join(_torch_dir(), "lib")
     tmp = BINDING + ".tmp"
     _run(["g++", "-shared", "-fPIC", "-o", tmp, obj, "-L", PKG, "-l:libtgrad.so", "-L", lib,
-          "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN",
+          "-ltorch_python", "-ltorch_hip", "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN",
           f"-Wl,-rpath,{lib}"], "linking the binding")
     os.replace(tmp, BINDING)
 
