@@ -75,6 +75,10 @@ hipError_t launch_adamw(const AdamwArgs& a, const AdamwTable& tab, hipStream_t s
 // each in a cache line of its own.
 constexpr uint32_t ADAMW_COUNTS = 16, ADAMW_COUNT_PITCH = 64;
 
+// Spans that one workgroup sums up alone.
+constexpr uint32_t ADAMW_NORM_SPANS = 16;
+
+// norm = scale * sqrt(sum of squares), coefficient = scale * min(1, max_norm / norm)
 struct AdamwNorm {
   const AdamwSpan* spans;     // of this launch
   double* partial;            // a sum of squares for each of them
@@ -88,7 +92,7 @@ struct AdamwNorm {
 // The sums of squares of a launch's spans, with join also the result.
 hipError_t launch_adamw_squares(const AdamwNorm& a, uint32_t nspans, bool join, const AdamwTable& tab,
                                 hipStream_t s);
-// norm = scale * sqrt(sum of squares), coefficient = scale * min(1, max_norm / norm)
-hipError_t launch_adamw_norm(const AdamwNorm& a, hipStream_t s);
+// The result alone, of at most ADAMW_NORM_SPANS spans of one launch.
+hipError_t launch_adamw_norm(const AdamwNorm& a, const AdamwTable& tab, hipStream_t s);
 
 }  // namespace tg

@@ -347,8 +347,10 @@ int tgrad_adamw_grad_norm(tgrad_adamw_t* h, const void* const* grads, double max
   a.out = out;
   a.max_norm = max_norm;
   a.scale = grad_scale;
+  // few spans, in one launch: a workgroup alone, without counting (14 spans 3.4 us against 5.6)
+  const bool alone = h->nspans <= ADAMW_NORM_SPANS && (h->launches.size() == 1 || !h->nspans);
   for (const auto& l : h->launches) {
-    if (!l.spans) continue;
+    if (!l.spans && !alone) continue;
     AdamwTable tab;
     for (int i = 0; i < l.tensors; ++i) {
       tab.w[i] = nullptr;
@@ -358,12 +360,12 @@ int tgrad_adamw_grad_norm(tgrad_adamw_t* h, const void* const* grads, double max
     a.partial = h->partial + l.first_span;
     a.first_tensor = (uint32_t)l.first_tensor;
     const bool join = l.first_span + l.spans == h->nspans;
-    const hipError_t e = launch_adamw_squares(a, l.spans, join, tab, (hipStream_t)stream);
+    const hipError_t e = alone ? launch_adamw_norm(a, tab, (hipStream_t)stream)
+                               : launch_adamw_squares(a, l.spans, join, tab, (hipStream_t)stream);
     if (e != hipSuccess) return fail(h, e, "gradient norm");
+    if (alone) break;
   }
-  if (h->nspans) return TGRAD_OK;
-  const hipError_t e = launch_adamw_norm(a, (hipStream_t)stream);   // no gradients at all
-  return e == hipSuccess ? TGRAD_OK : fail(h, e, "gradient norm");
+  return TGRAD_OK;
 }
 
 }  // extern "C"

@@ -359,15 +359,16 @@ __global__ void __launch_bounds__(kThreads) k_adamw(AdamwArgs a, AdamwTable tab)
   }
 }
 
-template <typename GT>
-__device__ double squares(const GT* __restrict__ g, uint32_t n) {
+// Over n values from g on, by THREADS threads of which this is number `t`.
+template <int THREADS, typename GT>
+__device__ __forceinline__ double squares(const GT* __restrict__ g, uint32_t n, uint32_t t) {
   constexpr int N = 16 / sizeof(GT);
   double s = 0.0;
-  for (uint32_t base = threadIdx.x * N; base < n; base += kThreads * N * 4) {
+  for (uint32_t base = t * N; base < n; base += THREADS * N * 4) {
     GT x[4][N];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const uint32_t i = base + u * kThreads * N;
+      const uint32_t i = base + u * THREADS * N;
       if (i + N <= n) {
         load_wide(g + i, x[u]);
       } else {
@@ -384,6 +385,13 @@ __device__ double squares(const GT* __restrict__ g, uint32_t n) {
       }
   }
   return s;
+}
+
+template <int THREADS>
+__device__ __forceinline__ double span_squares(const AdamwSpan& c, const void* g, uint32_t t) {
+  if (c.gdt == DT_F32) return squares<THREADS>((const float*)g + c.start, c.n, t);
+  if (c.gdt == DT_F16) return squares<THREADS>((const _Float16*)g + c.start, c.n, t);
+  return squares<THREADS>((const bf16_t*)g + c.start, c.n, t);
 }
 
 __device__ __forceinline__ double block_sum(double s, double* lds) {
@@ -422,11 +430,7 @@ __global__ void __launch_bounds__(kThreads) k_adamw_squares(AdamwNorm a, AdamwTa
   __shared__ double lds[4];
   __shared__ bool last;
   const AdamwSpan c = a.spans[blockIdx.x];
-  const void* g = tab.g[c.tensor - a.first_tensor];
-  double s;
-  if (c.gdt == DT_F32) s = squares((const float*)g + c.start, c.n);
-  else if (c.gdt == DT_F16) s = squares((const _Float16*)g + c.start, c.n);
-  else s = squares((const bf16_t*)g + c.start, c.n);
+  double s = span_squares<kThreads>(c, tab.g[c.tensor - a.first_tensor], threadIdx.x);
   s = block_sum(s, lds);
   if (!JOIN) {
     if (threadIdx.x == 0) a.partial[blockIdx.x] = s;
@@ -453,13 +457,23 @@ __global__ void __launch_bounds__(kThreads) k_adamw_squares(AdamwNorm a, AdamwTa
   if (threadIdx.x == 0) write_norm(a, s);
 }
 
-// The result of no gradients at all.
-__global__ void __launch_bounds__(kThreads) k_adamw_norm(AdamwNorm a) {
-  __shared__ double lds[4];
+// The norm of up to 16 spans (of one launch, or none at all): one workgroup, a wave for each.
+__global__ void __launch_bounds__(1024) k_adamw_norm(AdamwNorm a, AdamwTable tab) {
+  __shared__ double lds[16];
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   double s = 0.0;
-  for (uint32_t i = threadIdx.x; i < a.total_spans; i += kThreads) s += a.all_partial[i];
-  s = block_sum(s, lds);
-  if (threadIdx.x == 0) write_norm(a, s);
+  if (wave < a.total_spans) {
+    const AdamwSpan c = a.spans[wave];
+    s = span_squares<64>(c, tab.g[c.tensor - a.first_tensor], threadIdx.x & 63);
+#pragma unroll
+    for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o, 64);
+  }
+  if ((threadIdx.x & 63) == 0) lds[wave] = s;
+  __syncthreads();
+  if (threadIdx.x) return;
+  s = 0.0;
+  for (uint32_t i = 0; i < a.total_spans; ++i) s += lds[i];
+  write_norm(a, s);
 }
 
 }  // namespace
@@ -478,8 +492,8 @@ hipError_t launch_adamw_squares(const AdamwNorm& a, uint32_t nspans, bool join, 
   return hipGetLastError();
 }
 
-hipError_t launch_adamw_norm(const AdamwNorm& a, hipStream_t s) {
-  k_adamw_norm<<<1, kThreads, 0, s>>>(a);
+hipError_t launch_adamw_norm(const AdamwNorm& a, const AdamwTable& tab, hipStream_t s) {
+  k_adamw_norm<<<1, 1024, 0, s>>>(a, tab);
   return hipGetLastError();
 }
 
