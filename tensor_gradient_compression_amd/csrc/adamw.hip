@@ -324,7 +324,7 @@ int tgrad_adamw_step(tgrad_adamw_t* h, void* const* weights, const void* const* 
     a.clocks = h->clocks + l.first_chunk;
     a.first_tensor = (uint32_t)l.first_tensor;
     a.nchunks = l.chunks;
-    const hipError_t e = launch_adamw(a, tab, (hipStream_t)stream);
+    const hipError_t e = launch_adamw(a, l.tensors, tab, (hipStream_t)stream);
     if (e != hipSuccess) return fail(h, e, "AdamW step");
   }
   return TGRAD_OK;
@@ -347,11 +347,8 @@ int tgrad_adamw_grad_norm(tgrad_adamw_t* h, const void* const* grads, double max
   a.out = out;
   a.max_norm = max_norm;
   a.scale = grad_scale;
-  // few spans, in one launch: a workgroup alone, without counting (14 spans 3.4 us against 5.6)
-  const bool alone = h->nspans <= ADAMW_NORM_SPANS && (h->launches.size() == 1 || !h->nspans);
-  for (const auto& l : h->launches) {
-    if (!l.spans && !alone) continue;
-    AdamwTable tab;
+  AdamwTable tab;
+  auto fill = [&](const tgrad_adamw::Launch& l) {
     for (int i = 0; i < l.tensors; ++i) {
       tab.w[i] = nullptr;
       tab.g[i] = grads[l.first_tensor + i];
@@ -359,13 +356,24 @@ int tgrad_adamw_grad_norm(tgrad_adamw_t* h, const void* const* grads, double max
     a.spans = h->spans + l.first_span;
     a.partial = h->partial + l.first_span;
     a.first_tensor = (uint32_t)l.first_tensor;
-    const bool join = l.first_span + l.spans == h->nspans;
-    const hipError_t e = alone ? launch_adamw_norm(a, tab, (hipStream_t)stream)
-                               : launch_adamw_squares(a, l.spans, join, tab, (hipStream_t)stream);
-    if (e != hipSuccess) return fail(h, e, "gradient norm");
-    if (alone) break;
+  };
+  hipError_t e = hipSuccess;
+  if (!h->nspans) {
+    e = launch_adamw_norm(a, 0, tab, (hipStream_t)stream);
+  } else if (h->nspans <= ADAMW_NORM_SPANS && h->launches.size() == 1 &&
+             h->launches[0].tensors <= ADAMW_FEW_TENSORS) {
+    // a workgroup alone, without counting (14 spans 3.4 us against 5.6)
+    fill(h->launches[0]);
+    e = launch_adamw_norm(a, h->launches[0].tensors, tab, (hipStream_t)stream);
+  } else {
+    for (const auto& l : h->launches) {
+      if (!l.spans || e != hipSuccess) continue;
+      fill(l);
+      const bool join = l.first_span + l.spans == h->nspans;
+      e = launch_adamw_squares(a, l.spans, join, l.tensors, tab, (hipStream_t)stream);
+    }
   }
-  return TGRAD_OK;
+  return e == hipSuccess ? TGRAD_OK : fail(h, e, "gradient norm");
 }
 
 }  // extern "C"

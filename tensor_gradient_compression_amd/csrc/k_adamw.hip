@@ -314,8 +314,8 @@ __device__ __forceinline__ void chunk_of(const AdamwArgs& a, const AdamwChunk& c
   else chunk<BITS, VALUES>(a, c, Chunk<WT, GT, false>{wp, gp, c.n}, key, k, skip);
 }
 
-template <int BITS, bool VALUES>
-__global__ void __launch_bounds__(kThreads) k_adamw(AdamwArgs a, AdamwTable tab) {
+template <int BITS, bool VALUES, typename Table>
+__global__ void __launch_bounds__(kThreads) k_adamw(AdamwArgs a, Table tab) {
   const AdamwChunk c = a.chunks[blockIdx.x];
   const AdamwClock now = a.clocks[blockIdx.x];
   StepK k;
@@ -425,8 +425,8 @@ __device__ __forceinline__ bool last_of(uint32_t* count, uint32_t one, uint32_t 
 // workgroup sees them, so no cache has to be written back in between (with fences that did,
 // 32 ns a workgroup). Counting at one place takes 11 ns a workgroup; so 16 groups of them count
 // apart, and their last ones together.
-template <bool JOIN>
-__global__ void __launch_bounds__(kThreads) k_adamw_squares(AdamwNorm a, AdamwTable tab) {
+template <bool JOIN, typename Table>
+__global__ void __launch_bounds__(kThreads) k_adamw_squares(AdamwNorm a, Table tab) {
   __shared__ double lds[4];
   __shared__ bool last;
   const AdamwSpan c = a.spans[blockIdx.x];
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads) k_adamw_squares(AdamwNorm a, AdamwTa
 }
 
 // The norm of up to 16 spans (of one launch, or none at all): one workgroup, a wave for each.
-__global__ void __launch_bounds__(1024) k_adamw_norm(AdamwNorm a, AdamwTable tab) {
+__global__ void __launch_bounds__(1024) k_adamw_norm(AdamwNorm a, AdamwTableOf<ADAMW_FEW_TENSORS> tab) {
   __shared__ double lds[16];
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   double s = 0.0;
@@ -478,22 +478,47 @@ __global__ void __launch_bounds__(1024) k_adamw_norm(AdamwNorm a, AdamwTable tab
 
 }  // namespace
 
-hipError_t launch_adamw(const AdamwArgs& a, const AdamwTable& tab, hipStream_t s) {
+namespace {
+
+using FewTable = AdamwTableOf<ADAMW_FEW_TENSORS>;
+
+FewTable few_of(int tensors, const AdamwTable& tab) {
+  FewTable t;
+  for (int i = 0; i < tensors; ++i) {
+    t.w[i] = tab.w[i];
+    t.g[i] = tab.g[i];
+  }
+  return t;
+}
+
+template <typename Table>
+hipError_t step(const AdamwArgs& a, const Table& tab, hipStream_t s) {
   if (a.bits == 32) k_adamw<32, false><<<a.nchunks, kThreads, a.lds, s>>>(a, tab);
   else if (!a.m_out) k_adamw<8, false><<<a.nchunks, kThreads, 0, s>>>(a, tab);
   else k_adamw<8, true><<<a.nchunks, kThreads, 0, s>>>(a, tab);
   return hipGetLastError();
 }
-
-hipError_t launch_adamw_squares(const AdamwNorm& a, uint32_t nspans, bool join, const AdamwTable& tab,
-                                hipStream_t s) {
+template <typename Table>
+hipError_t sums(const AdamwNorm& a, uint32_t nspans, bool join, const Table& tab, hipStream_t s) {
   if (join) k_adamw_squares<true><<<nspans, kThreads, 0, s>>>(a, tab);
   else k_adamw_squares<false><<<nspans, kThreads, 0, s>>>(a, tab);
   return hipGetLastError();
 }
 
-hipError_t launch_adamw_norm(const AdamwNorm& a, const AdamwTable& tab, hipStream_t s) {
-  k_adamw_norm<<<1, 1024, 0, s>>>(a, tab);
+}  // namespace
+
+hipError_t launch_adamw(const AdamwArgs& a, int tensors, const AdamwTable& tab, hipStream_t s) {
+  return tensors <= ADAMW_FEW_TENSORS ? step(a, few_of(tensors, tab), s) : step(a, tab, s);
+}
+
+hipError_t launch_adamw_squares(const AdamwNorm& a, uint32_t nspans, bool join, int tensors,
+                                const AdamwTable& tab, hipStream_t s) {
+  return tensors <= ADAMW_FEW_TENSORS ? sums(a, nspans, join, few_of(tensors, tab), s)
+                                      : sums(a, nspans, join, tab, s);
+}
+
+hipError_t launch_adamw_norm(const AdamwNorm& a, int tensors, const AdamwTable& tab, hipStream_t s) {
+  k_adamw_norm<<<1, 1024, 0, s>>>(a, few_of(tensors, tab));
   return hipGetLastError();
 }
 

@@ -201,6 +201,21 @@ def test_norm_and_coefficient(dtype, scale):
     assert zero.tolist() == [0.0, 1.0]
 
 
+@pytest.mark.parametrize("numels", [[0], [0] * 300, [0] * 250 + [70], [70] + [0] * 250, [2048] * 16, [2048] * 17,
+                                    [100] * 24, [100] * 25, [100] * 600])
+def test_norm_of_few_and_many_tensors(numels):
+    """The ways the sums are joined: one workgroup alone, a launch, several launches, none."""
+    c = Case(numels, "f32")
+    g = c.gradients()
+    out = c.opt.grad_norm(g, max_norm=1e-3)
+    norm, coef = A.norm_and_coefficient([values(x) for x in g], 1e-3, 1.0)
+    assert abs(float(out[0]) - norm) <= 1.01 * E * norm
+    assert abs(float(out[1]) - coef) <= 1.01 * E * coef
+    for _ in range(2):
+        assert torch.equal(out, c.opt.grad_norm(g, max_norm=1e-3))
+        c.checked_step(g, clip=out)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_clipped_steps(bits):
     c = Case([4000, 77], "f16", bits=bits)
