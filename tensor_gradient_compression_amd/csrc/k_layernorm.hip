@@ -21,12 +21,19 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_forward_waves(NV)
   Place<T, COLS> at[K];
   Piece<T> next[K];
   int64_t row = (int64_t)blockIdx.x * RT::kRows + RT::row();
+  // pointers to the row that is loaded next, and to the one that is written next
+  const T* xr = (const T*)a.x + row * a.x_stride;
+  T* yr = (T*)a.y + row * (int64_t)a.cols;
+  const int64_t x_step = stride * a.x_stride, y_step = stride * (int64_t)a.cols;
+  bool moved = false;   // whether a thread of this wave holds a piece that was moved back
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     at[k] = Place<T, COLS>((RT::index() + k * RT::count()) * V, a.cols);
+    moved = moved || (COLS != WHOLE && at[k].own > 0);
     clear(next[k]);
-    if (row < a.rows) at[k].load((const T*)a.x + row * a.x_stride, a.cols, once, next[k]);
+    if (row < a.rows) at[k].load(xr, a.cols, once, next[k]);
   }
+  moved = COLS == TINY || __any(moved);
   float w[NV], b[NV];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -42,11 +49,19 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_forward_waves(NV)
       for (int j = 0; j < V; ++j) {
         const float v = to_f32(next[k].v[j]);
         x[k * V + j] = v;
-        s += COLS == RAGGED && !at[k].mine(j, a.cols) ? 0.0f : v;
+        s += v;
       }
+    if (COLS == RAGGED && moved) {
+      s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) s += at[k].mine(j, a.cols) ? x[k * V + j] : 0.0f;
+    }
+    xr += x_step;
     if (row + stride < a.rows)
 #pragma unroll
-      for (int k = 0; k < K; ++k) at[k].load((const T*)a.x + (row + stride) * a.x_stride, a.cols, once, next[k]);
+      for (int k = 0; k < K; ++k) at[k].load(xr, a.cols, once, next[k]);
     rt.template sum<false>(s, unused);
     const float mean = s * inv;
     s = 0.0f;
@@ -57,14 +72,25 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_forward_waves(NV)
       for (int j = 0; j < V; ++j) {
         const float d = x[k * V + j] - mean;
         x[k * V + j] = d;
-        sk = __builtin_fmaf(d, COLS != WHOLE && !at[k].mine(j, a.cols) ? 0.0f : d, sk);
+        sk = __builtin_fmaf(d, d, sk);
       }
       s += at[k].own < V ? sk : 0.0f;
     }
+    if (COLS != WHOLE && moved) {
+      s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float d = at[k].mine(j, a.cols) ? x[k * V + j] : 0.0f;
+          s = __builtin_fmaf(d, d, s);
+        }
+    }
     rt.template sum<false>(s, unused);
-    const float rstd = 1.0f / sqrtf(s * inv + a.eps);
+    const float rstd = reciprocal_root(s * inv + a.eps);
+    T* y = yr;
+    yr += y_step;
     if (row >= a.rows) continue;
-    T* y = (T*)a.y + row * (int64_t)a.cols;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float o[V];

@@ -139,6 +139,18 @@ __device__ __forceinline__ float group_sum(float x) {
   return x;
 }
 
+// 1 / sqrt(a): the hardware's estimate and one Newton step, within 1.5 units of the last place;
+// outside a range that keeps both away from overflow and subnormal numbers the slow exact way.
+__device__ __forceinline__ float reciprocal_root(float a) {
+  const float y = __builtin_amdgcn_rsqf(a);
+  float r = __builtin_fmaf(0.5f * y, __builtin_fmaf(-a * y, y, 1.0f), y);
+  if (__any(!(a >= 0x1p-100f && a <= 0x1p100f))) {
+    __asm__ volatile("" : "+v"(a));   // a branch of its own, not computed beside the other
+    r = 1.0f / sqrtf(a);
+  }
+  return r;
+}
+
 // The threads of a row: LANES lanes of a wave in a workgroup of 4 waves, or (LANES = 0) all
 // threads of the workgroup, up to 16 waves.
 template <int LANES>
