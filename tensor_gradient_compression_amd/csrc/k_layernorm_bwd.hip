@@ -91,8 +91,10 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_backward_waves(LA
       }
     }
     rt.template sum<true>(s, u);
-    // dx = rstd h + d du + ds, with d = x - mean
-    const float ds = -rstd * (s * inv), du = -rstd * rstd * (rstd * (u * inv));
+    // dx = rstd (h - mean(h) + d du), with d = x - mean. mean(h) is taken off h itself, where
+    // rstd h less rstd mean(h) would leave the rounding of one product: with a single column,
+    // or the same h in all of them, nothing may be left
+    const float mh = s * inv, du = -rstd * (rstd * (u * inv));
     if (row >= a.rows) continue;
     T* dx = (T*)a.dx + row * (int64_t)a.cols;
 #pragma unroll
@@ -105,7 +107,7 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_backward_waves(LA
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float d = to_f32(xp[k].v[j]) - mean, h = to_f32(dp[k].v[j]) * w[kKeep ? k * V + j : j];
-        o[j] = __builtin_fmaf(h, rstd, __builtin_fmaf(d, du, ds));
+        o[j] = rstd * __builtin_fmaf(d, du, h - mh);
       }
       at[k].store(dx, a.cols, o);
     }

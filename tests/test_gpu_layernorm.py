@@ -118,6 +118,27 @@ def test_constant_rows(cols):
     check(x, dy, w, b, "f32", "f32")
 
 
+@pytest.mark.parametrize("rows", [1, 300, 1705])
+@pytest.mark.parametrize("dtype,wdtype", TYPES)
+def test_one_column_has_no_gradient_of_x(rows, dtype, wdtype):
+    """n is 0 and h its own mean, so dx and dweight are 0 and not the rounding of a product."""
+    x, dy, w, _ = inputs(rows, 1, dtype, wdtype, seed=7)
+    dx, dw, _ = tg.layer_norm_backward(dy, x, w, x[:, 0].float(), torch.full((rows,), EPS ** -0.5, device="cuda"))
+    assert not dx.any() and not dw.any()
+
+
+@pytest.mark.parametrize("cols", [2, 8, 64, 512, 1024, 2048, 8192, 16384])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_the_same_gradient_in_every_column_has_none_of_x(cols, dtype):
+    """Neighbours k and -k, and dy of 0.75 everywhere: every sum is exact in any order, and
+    h - mean(h) and mean(h n) are 0."""
+    k = torch.arange(cols // 2, device="cuda") % 8 + 1
+    x = torch.stack([k, -k], 1).reshape(1, cols).expand(5, cols).to(tg.torch_dtype(dtype)).contiguous()
+    dx, _, db = tg.layer_norm_backward(torch.full_like(x, 0.75), x, None, torch.zeros(5, device="cuda"),
+                                       torch.full((5,), 0.7, device="cuda"))
+    assert not dx.any() and bool((db == 3.75).all())
+
+
 @pytest.mark.parametrize("bad", [float("inf"), float("nan")])
 @pytest.mark.parametrize("cols", [64, 1000, 8192])
 def test_rows_that_are_not_finite_stay_apart(bad, cols):
