@@ -4,12 +4,21 @@
 //   dw = sum_rows dy n;  db = sum_rows dy
 // Sums are fp32, results are rounded once. Rows and threads: layernorm_rows.h. Each thread
 // also sums dy n and dy over its rows for its own columns; a workgroup's sums become one row of
-// `partial`, and a second kernel adds those rows up, always in the same order.
+// `partial`, and a second kernel adds those rows up, always in the same order. A workgroup that
+// is alone writes dw and db at once.
 #include "layernorm_rows.h"
 
 namespace tg {
 
 namespace {
+
+// A value of dw or db.
+template <typename T>
+__device__ __forceinline__ void put(void* out, int wdt, uint32_t c, float x) {
+  if (!out) return;
+  if (wdt == DT_F32) ((float*)out)[c] = x;
+  else ((T*)out)[c] = from_f32<T>(x);
+}
 
 // Up to 16 values a thread their sums over rows, the weights and two rows fit the registers;
 // with 16 waves and 16 values (128 registers a thread) the weights stay in LDS as fp32.
@@ -142,13 +151,20 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_backward_waves(LA
       }
     }
   }
+  const bool alone = gridDim.x == 1;
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int j = 0; j < V; ++j)
       if (at[k].own < V && at[k].mine(j, a.cols)) {
-        pw[at[k].c + j] = sw[k * V + j];
-        pw[a.cols + at[k].c + j] = sb[k * V + j];
+        const uint32_t c = at[k].c + j;
+        if (alone) {
+          put<T>(a.dw, a.wdt, c, sw[k * V + j]);
+          put<T>(a.db, a.wdt, c, sb[k * V + j]);
+        } else {
+          pw[c] = sw[k * V + j];
+          pw[a.cols + c] = sb[k * V + j];
+        }
       }
 }
 
@@ -248,27 +264,44 @@ struct Backward {
 // once, so that none waits for a place (8192 columns of bf16: 80 us with 256 workgroups of 16
 // waves, 90 with 512), at most 768, and few enough that each has four turns: fewer rows of sums
 // are sooner added up (4M values of bf16 in rows of 1024: 16 -> 13 us).
-struct PartialRows {
+// One alone writes dw and db itself, which saves the second launch: up to eight turns of a wave
+// with 8 values a thread (32 x 333 fp32: 8.0 -> 6.5 us a call, but 64 rows 7.9 -> 10.5), else
+// four (4 x 4952 fp32: 9.5 -> 7.2, 8 rows 9.6 -> 10.4).
+// Without dw and db there is nothing to add up, and every row that finds a place has its own
+// (512 x 8192 bf16: 8.4 -> 6.6 us; 4 rows 6.6 -> 4.5).
+struct BackwardGroups {
   int64_t rows;
+  bool params;
   uint32_t& n;
   template <int LANES, int NV>
   void run(uint32_t threads) const {
-    const uint32_t most = LN_CUS * (ln_backward_waves(LANES, NV) / (threads / 64));
-    n = ln_walk(rows, RowThreads<LANES>::kRows * 4, most < 768 ? most : 768);
+    constexpr int kRows = RowThreads<LANES>::kRows;
+    const uint32_t held = LN_CUS * (ln_backward_waves(LANES, NV) / (threads / 64)), most = held < 768 ? held : 768;
+    if (!params) n = ln_walk(rows, kRows, most);
+    else if (rows <= kRows * (LANES && NV == 8 ? 8 : 4)) n = rows > 0;
+    else n = ln_walk(rows, kRows * 4, most);
   }
 };
+
+uint32_t ln_groups(int64_t rows, uint32_t cols, bool params) {
+  uint32_t n = 0;
+  if (!ln_dispatch(cols, BackwardGroups{rows, params, n})) n = ln_walk(rows, 1, 512);
+  return n;
+}
 
 template <typename T>
 hipError_t backward(LnBackward a, hipStream_t s) {
   const bool once = ln_once(a.rows * a.cols * 3 * (int64_t)sizeof(T));
-  const uint32_t n = ln_partial_rows(a.rows, a.cols);
   const bool params = a.dw || a.db;
+  const uint32_t n = ln_groups(a.rows, a.cols, params);
+  bool alone = n == 1;   // that workgroup has written dw and db
   if (!params) a.partial = nullptr;
   if (a.rows && !ln_dispatch(a.cols, Backward<T>{a, n, once, s})) {
+    alone = false;
     k_ln_dx_long<T><<<(uint32_t)a.rows, LN_LONG, 0, s>>>(a);
     if (params) k_ln_columns<T><<<dim3((a.cols + 255) / 256, n), 256, 0, s>>>(a);
   }
-  if (params) {
+  if (params && !alone) {
     const dim3 grid((a.cols + 31) / 32, 2);
     if (a.wdt == DT_F32) k_ln_reduce<float><<<grid, 1024, 0, s>>>(a.partial, n, a.cols, (float*)a.dw, (float*)a.db);
     else k_ln_reduce<T><<<grid, 1024, 0, s>>>(a.partial, n, a.cols, (T*)a.dw, (T*)a.db);
@@ -278,11 +311,7 @@ hipError_t backward(LnBackward a, hipStream_t s) {
 
 }  // namespace
 
-uint32_t ln_partial_rows(int64_t rows, uint32_t cols) {
-  uint32_t n = 0;
-  if (!ln_dispatch(cols, PartialRows{rows, n})) n = ln_walk(rows, 1, 512);
-  return n;
-}
+uint32_t ln_partial_rows(int64_t rows, uint32_t cols) { return ln_groups(rows, cols, true); }
 
 hipError_t launch_ln_backward(const LnBackward& a, hipStream_t s) {
   if (a.dt == DT_F32) return backward<float>(a, s);

@@ -118,6 +118,20 @@ def test_constant_rows(cols):
     check(x, dy, w, b, "f32", "f32")
 
 
+@pytest.mark.parametrize("rows,cols", [(r * t + more, c) for r, t, c in ((256, 8, 5), (64, 8, 27), (8, 8, 256), (4, 8, 333),
+                                                                        (4, 4, 1000), (1, 4, 2050), (1, 4, 9000))
+                                       for t in (1, t) for more in (0, 1)])
+@pytest.mark.parametrize("dtype,wdtype", [("f32", "f32"), ("bf16", "bf16")])
+def test_a_workgroup_alone_and_two(rows, cols, dtype, wdtype):
+    """The most rows that one workgroup takes, and one more; the gradient of x is the same
+    without those of the parameters."""
+    x, dy, w, b = inputs(rows, cols, dtype, wdtype, seed=8)
+    check(x, dy, w, b, dtype, wdtype)
+    _, mean, rstd = tg.layer_norm_forward(x, w, b)
+    assert torch.equal(tg.layer_norm_backward(dy, x, w, mean, rstd, params=False)[0],
+                       tg.layer_norm_backward(dy, x, w, mean, rstd)[0])
+
+
 @pytest.mark.parametrize("rows", [1, 300, 1705])
 @pytest.mark.parametrize("dtype,wdtype", TYPES)
 def test_one_column_has_no_gradient_of_x(rows, dtype, wdtype):
