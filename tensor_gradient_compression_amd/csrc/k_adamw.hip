@@ -374,31 +374,44 @@ __global__ void __launch_bounds__(kThreads) k_adamw(AdamwArgs a, Table tab) {
   }
 }
 
-// Over n values from g on, by THREADS threads of which this is number `t`.
+// Over n values from g on, by THREADS threads of which this is number `t`: four pieces of 16
+// bytes a thread in flight, the last ones by themselves.
 template <int THREADS, typename GT>
 __device__ __forceinline__ double squares(const GT* __restrict__ g, uint32_t n, uint32_t t) {
-  constexpr int N = 16 / sizeof(GT);
+  constexpr uint32_t N = 16 / sizeof(GT), kPass = THREADS * N;
   double s = 0.0;
-  for (uint32_t base = t * N; base < n; base += THREADS * N * 4) {
+  auto add = [&](const GT (&x)[N]) {
+#pragma unroll
+    for (uint32_t j = 0; j < N; ++j) {
+      const double v = (double)to_f32(x[j]);
+      s = fma(v, v, s);
+    }
+  };
+  uint32_t i = t * N, left = n;
+  for (; left >= 4 * kPass; left -= 4 * kPass, i += 4 * kPass) {
     GT x[4][N];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t i = base + u * THREADS * N;
-      if (i + N <= n) {
-        load_wide(g + i, x[u]);
-      } else {
+    for (uint32_t u = 0; u < 4; ++u) load_wide(g + i + u * kPass, x[u]);
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[u][j] = i + j < n ? g[i + j] : zero_of<GT>();
-      }
+    for (uint32_t u = 0; u < 4; ++u) add(x[u]);
+  }
+  if (!left) return s;
+  GT x[4][N];
+#pragma unroll
+  for (uint32_t u = 0; u < 4; ++u) {
+    const uint32_t k = i + u * kPass;
+#pragma unroll
+    for (uint32_t j = 0; j < N; ++j) x[u][j] = zero_of<GT>();
+    if (k + N <= n) load_wide(g + k, x[u]);
+  }
+  // the end of the last piece
+  if (n % N && (n / N) % THREADS == t)
+    for (uint32_t k = n / N * N; k < n; ++k) {
+      const double v = (double)to_f32(g[k]);
+      s = fma(v, v, s);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const double v = (double)to_f32(x[u][j]);
-        s = fma(v, v, s);
-      }
-  }
+  for (uint32_t u = 0; u < 4; ++u) add(x[u]);
   return s;
 }
 
