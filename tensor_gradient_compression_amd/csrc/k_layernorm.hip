@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_forward_waves(NV)
 #pragma unroll
       for (int k = 0; k < K; ++k) at[k].load(xr, a.cols, once, next[k]);
     rt.template sum<false>(s, unused);
-    const float mean = s * inv;
+    const float mean = mean_of(s, (float)a.cols, inv);
     s = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {

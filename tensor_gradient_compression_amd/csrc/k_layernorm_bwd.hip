@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_backward_waves(LA
     // dx = rstd (h - mean(h) + d du), with d = x - mean. mean(h) is taken off h itself, where
     // rstd h less rstd mean(h) would leave the rounding of one product: with a single column,
     // or the same h in all of them, nothing may be left
-    const float mh = s * inv, du = -rstd * (rstd * (u * inv));
+    const float mh = mean_of(s, (float)a.cols, inv), du = -rstd * (rstd * (u * inv));
     if (row >= a.rows) continue;
     T* dx = (T*)a.dx + row * (int64_t)a.cols;
 #pragma unroll

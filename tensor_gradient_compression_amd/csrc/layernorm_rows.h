@@ -145,6 +145,14 @@ __device__ __forceinline__ float group_sum(float x) {
   return x;
 }
 
+// s / cols from the rounded reciprocal `inv`: the product, corrected by its exact residual, so
+// that a quotient that fp32 holds comes out as it is (the product alone is off by a unit for
+// some constant rows of 7, 13, 15 ... columns, and eps makes hundreds of that distance).
+__device__ __forceinline__ float mean_of(float s, float cols, float inv) {
+  const float m = s * inv;
+  return fabsf(m) < INFINITY ? __builtin_fmaf(__builtin_fmaf(-m, cols, s), inv, m) : m;
+}
+
 // 1 / sqrt(a): the hardware's estimate and one Newton step, within 1.5 units of the last place;
 // outside a range that keeps both away from overflow and subnormal numbers the slow exact way.
 __device__ __forceinline__ float reciprocal_root(float a) {

@@ -153,6 +153,19 @@ def test_the_same_gradient_in_every_column_has_none_of_x(cols, dtype):
     assert not dx.any() and bool((db == 3.75).all())
 
 
+@pytest.mark.parametrize("cols", [1, 3, 7, 13, 28, 41, 47, 111, 127, 410, 511, 1000, 1023, 2047, 4095])
+def test_constant_rows_of_any_level(cols):
+    """Values of 12 bits, so every sum is exact and the mean is the value itself: y is the bias
+    and not eps's multiple of a mean that is off by a unit. The same for mean(dy w)."""
+    level = torch.arange(2048.0, 4096.0, device="cuda") * 0.125
+    x = level[:, None].expand(2048, cols).contiguous()
+    b = torch.linspace(-1, 1, cols, device="cuda")
+    y, mean, rstd = tg.layer_norm_forward(x, None, b, eps=EPS)
+    assert torch.equal(mean, level) and torch.equal(y, b.expand(2048, cols))
+    dx, _, _ = tg.layer_norm_backward(x, x, None, mean, rstd)
+    assert not dx.any()
+
+
 @pytest.mark.parametrize("bad", [float("inf"), float("nan")])
 @pytest.mark.parametrize("cols", [64, 1000, 8192])
 def test_rows_that_are_not_finite_stay_apart(bad, cols):
