@@ -489,7 +489,7 @@ int tgrad_adamw_grad_norm(tgrad_adamw_t *h, const void *const *grads, double max
  *   dweight = sum over rows of dy n,  dbias = sum over rows of dy
  * The sums over rows are formed in a fixed order.
  *   x, dy           device, rows x_stride (dy_stride) >= cols elements apart
- *   y, dx           device, contiguous
+ *   y, dx           device, contiguous; no result overlaps an input
  *   mean, rstd      device, rows floats: written by forward, read by backward
  *   weight, bias    device, cols elements of weight_dtype; NULL: 1 and 0
  *   dweight, dbias  device, cols elements of weight_dtype, each may be NULL

@@ -30,6 +30,8 @@ def _layer_norm_function():
             @staticmethod
             def forward(ctx, x, weight, bias, eps):
                 y, mean, rstd = layer_norm_forward(x, weight, bias, eps)
+                if weight is None and bias is not None and bias.dtype != x.dtype:
+                    weight = torch.ones_like(bias)   # backward gives dbias the weight's type
                 ctx.save_for_backward(x, weight, mean, rstd)
                 return y
 

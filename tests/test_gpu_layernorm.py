@@ -269,3 +269,10 @@ def test_refusals():
                        ((dy, x, w, mean[:3], rstd), "mean"), ((dy, x, w, mean, rstd.double()), "rstd")):
         with pytest.raises(ValueError, match=what):
             tg.layer_norm_backward(*args)
+
+
+def test_a_bias_alone_gets_a_gradient_of_its_own_precision():
+    x, dy, _, b = inputs(400, 96, "bf16", "f32", seed=10)
+    b.requires_grad_()
+    tg.layer_norm(x, None, b).backward(dy)
+    close(b.grad, host(dy).sum(0), L.gamma(416) * np.abs(host(dy)).sum(0), "dbias")
