@@ -19,19 +19,19 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_forward_waves(NV)
   const int64_t stride = (int64_t)gridDim.x * RT::kRows;
   const float inv = 1.0f / (float)a.cols;
   Place<T, COLS> at[K];
-  Piece<T> next[K];
+  Raw<T, COLS> next[K];
   int64_t row = (int64_t)blockIdx.x * RT::kRows + RT::row();
-  // pointers to the row that is loaded next, and to the one that is written next
+  // pointers to the row whose values are used next, and to the one that is written next
   const T* xr = (const T*)a.x + row * a.x_stride;
   T* yr = (T*)a.y + row * (int64_t)a.cols;
   const int64_t x_step = stride * a.x_stride, y_step = stride * (int64_t)a.cols;
   bool moved = false;   // whether a thread of this wave holds a piece that was moved back
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    at[k] = Place<T, COLS>((RT::index() + k * RT::count()) * V, a.cols);
+    at[k] = Place<T, COLS>((RT::index() + k * RT::count()) * V, a.cols, RT::last_lane());
     moved = moved || (COLS != WHOLE && at[k].own > 0);
     clear(next[k]);
-    if (row < a.rows) at[k].load(xr, a.cols, once, next[k]);
+    if (row < a.rows) at[k].fetch(xr, a.cols, once, next[k]);
   }
   moved = COLS == TINY || __any(moved);
   float w[NV], b[NV];
@@ -44,14 +44,16 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_forward_waves(NV)
   for (int64_t base = (int64_t)blockIdx.x * RT::kRows; base < a.rows; base += stride, row += stride) {
     float x[NV], s = 0.0f, unused;
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
+      const Piece<T> p = at[k].piece(xr, next[k]);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float v = to_f32(next[k].v[j]);
+        const float v = to_f32(p.v[j]);
         x[k * V + j] = v;
         s += v;
       }
-    if (COLS == RAGGED && moved) {
+    }
+    if (ln_moves(COLS) && moved) {
       s = 0.0f;
 #pragma unroll
       for (int k = 0; k < K; ++k)
@@ -61,7 +63,7 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_forward_waves(NV)
     xr += x_step;
     if (row + stride < a.rows)
 #pragma unroll
-      for (int k = 0; k < K; ++k) at[k].load(xr, a.cols, once, next[k]);
+      for (int k = 0; k < K; ++k) at[k].fetch(xr, a.cols, once, next[k]);
     rt.template sum<false>(s, unused);
     const float mean = mean_of(s, (float)a.cols, inv);
     s = 0.0f;
@@ -160,6 +162,12 @@ struct Forward {
     constexpr uint32_t V = Piece<T>::V;
     const uint32_t n = ln_walk(a.rows, RowThreads<LANES>::kRows, LN_CUS * (ln_forward_waves(NV) / (threads / 64)));
     const bool once = ln_once(a.rows * a.cols * 2 * (int64_t)sizeof(T));
+    if constexpr (LANES == 0 && sizeof(T) == 2) {
+      if (ln_odd<T>(a.x, a.x_stride)) {
+        k_ln_forward<T, LANES, NV, ODD><<<n, threads, 0, s>>>(a, once);
+        return;
+      }
+    }
     if (LANES == 1 && a.cols < V) k_ln_forward<T, 1, 8, TINY><<<n, threads, 0, s>>>(a, once);
     else if (a.cols % V == 0) k_ln_forward<T, LANES, NV, WHOLE><<<n, threads, 0, s>>>(a, once);
     else k_ln_forward<T, LANES, NV, RAGGED><<<n, threads, 0, s>>>(a, once);

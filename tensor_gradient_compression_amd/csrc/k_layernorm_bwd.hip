@@ -36,16 +36,16 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_backward_waves(LA
   const float inv = 1.0f / (float)a.cols;
   int64_t row = (int64_t)blockIdx.x * RT::kRows + RT::row();
   Place<T, COLS> at[K];
-  Piece<T> xn[K], dn[K];
+  Raw<T, COLS> xn[K], dn[K];
   float mean_n = 0.0f, rstd_n = 0.0f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    at[k] = Place<T, COLS>((RT::index() + k * RT::count()) * V, a.cols);
+    at[k] = Place<T, COLS>((RT::index() + k * RT::count()) * V, a.cols, RT::last_lane());
     clear(xn[k]);
     clear(dn[k]);
     if (row < a.rows) {
-      at[k].load((const T*)a.x + row * a.x_stride, a.cols, ONCE, xn[k]);
-      at[k].load((const T*)a.dy + row * a.dy_stride, a.cols, ONCE, dn[k]);
+      at[k].fetch((const T*)a.x + row * a.x_stride, a.cols, ONCE, xn[k]);
+      at[k].fetch((const T*)a.dy + row * a.dy_stride, a.cols, ONCE, dn[k]);
     }
   }
   if (row < a.rows) mean_n = a.mean[row], rstd_n = a.rstd[row];
@@ -66,14 +66,14 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_backward_waves(LA
     float s = 0.0f, u = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      xp[k] = xn[k];
-      dp[k] = dn[k];
+      xp[k] = at[k].piece((const T*)a.x + row * a.x_stride, xn[k]);
+      dp[k] = at[k].piece((const T*)a.dy + row * a.dy_stride, dn[k]);
     }
     if (row + stride < a.rows) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        at[k].load((const T*)a.x + (row + stride) * a.x_stride, a.cols, ONCE, xn[k]);
-        at[k].load((const T*)a.dy + (row + stride) * a.dy_stride, a.cols, ONCE, dn[k]);
+        at[k].fetch((const T*)a.x + (row + stride) * a.x_stride, a.cols, ONCE, xn[k]);
+        at[k].fetch((const T*)a.dy + (row + stride) * a.dy_stride, a.cols, ONCE, dn[k]);
       }
       mean_n = a.mean[row + stride];
       rstd_n = a.rstd[row + stride];
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_backward_waves(LA
       for (int j = 0; j < V; ++j) {
         const int i = k * V + j;
         const float dy = to_f32(dp[k].v[j]), d = to_f32(xp[k].v[j]) - mean;
-        const float h = COLS == RAGGED && !at[k].mine(j, a.cols) ? 0.0f : dy * w[kKeep ? i : j];
+        const float h = ln_moves(COLS) && !at[k].mine(j, a.cols) ? 0.0f : dy * w[kKeep ? i : j];
         s += h;
         u = __builtin_fmaf(h, d, u);
         sw[i] = __builtin_fmaf(dy, d * rstd, sw[i]);
@@ -253,6 +253,13 @@ struct Backward {
   template <int LANES, int NV>
   void run(uint32_t threads) const {
     constexpr uint32_t V = Piece<T>::V;
+    if constexpr (LANES == 0 && sizeof(T) == 2) {
+      if (ln_odd<T>(a.x, a.x_stride) || ln_odd<T>(a.dy, a.dy_stride)) {
+        if (once) k_ln_backward<T, LANES, NV, ODD, true><<<n, threads, 0, s>>>(a);
+        else k_ln_backward<T, LANES, NV, ODD, false><<<n, threads, 0, s>>>(a);
+        return;
+      }
+    }
     if (LANES == 1 && a.cols < V) k_ln_backward<T, 1, 8, TINY, false><<<n, threads, 0, s>>>(a);
     else if (a.cols % V == 0 && once) k_ln_backward<T, LANES, NV, WHOLE, true><<<n, threads, 0, s>>>(a);
     else if (a.cols % V == 0) k_ln_backward<T, LANES, NV, WHOLE, false><<<n, threads, 0, s>>>(a);

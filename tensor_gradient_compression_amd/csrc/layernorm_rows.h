@@ -17,8 +17,8 @@
 //
 // Both directions are bound by memory where rows are many (rates at 67M values): forward 5.8 to
 // 6.2 TB/s in bf16 and 6.2 to 6.7 in fp32, backward 5.0 to 5.8 and 5.3 to 6.3, for whole pieces
-// of any width; bf16 rows that start off the caches' lines and span several waves (4099
-// columns) 5.0 and 3.8. Held by their threads as the fewest lanes with 8 values each, since
+// of any width; bf16 rows of several waves that start at odd values (2001 to 12001 columns) 5.5 to
+// 6.0 and 4.5 to 4.8. Held by their threads as the fewest lanes with 8 values each, since
 // fewer lanes with 16 leave room for fewer waves (backward, 65536 x 256 bf16: 20 us, 18.4).
 #pragma once
 #include "layernorm.h"
@@ -56,9 +56,22 @@ __device__ __forceinline__ void store_piece(T* __restrict__ p, const float* x) {
   __builtin_memcpy((Unaligned<T, V>*)p, v, 16);
 }
 
-// How the columns of a row divide: into whole pieces; with a last piece moved back; or less
-// than one piece, which is read and written value by value.
-enum Columns { WHOLE = 0, RAGGED = 1, TINY = 2 };
+// How the columns of a row divide: into whole pieces; with a last piece moved back; less than
+// one piece, which is read and written value by value; or, of rows of 16-bit values that several
+// waves hold and some of which start at odd ones, as RAGGED but read by whole words. Accesses off
+// the words cost about twice as much (33M fp16 values: 4099 columns forward 30 -> 27 us, 2001
+// backward 59 -> 50, 12001 76 -> 58; rows that a wave holds gain nothing, 255 columns 44 -> 48).
+enum Columns { WHOLE = 0, RAGGED = 1, TINY = 2, ODD = 3 };
+constexpr bool ln_moves(int columns) { return columns == RAGGED || columns == ODD; }
+
+// A piece as it is loaded. ODD: as the four words that begin at its first value or one before
+// (which is in the same word); the value that ends it then comes from the next lane, or by itself
+// where that holds no neighbour.
+template <typename T, int COLS>
+struct Raw {
+  Piece<T> x;
+  uint32_t end;
+};
 
 // One piece of a row: its first column, and from which of its values on they are its own (V
 // where the piece lies past the row's end: nothing is read or written).
@@ -67,9 +80,11 @@ struct Place {
   static constexpr int V = Piece<T>::V;
   uint32_t c;
   int own;
+  bool alone;   // whether the next lane of the wave does not hold the next piece of the row
   __device__ __forceinline__ Place() {}
-  __device__ __forceinline__ Place(uint32_t at, uint32_t cols) : c(at), own(at < cols ? 0 : V) {
-    if (COLS == RAGGED && at < cols && at + V > cols) {
+  __device__ __forceinline__ Place(uint32_t at, uint32_t cols, bool last_lane = true)
+      : c(at), own(at < cols ? 0 : V), alone(last_lane || at + 2 * V > cols) {
+    if (ln_moves(COLS) && at < cols && at + V > cols) {
       c = cols - V;
       own = (int)(at + V - cols);
     }
@@ -87,6 +102,33 @@ struct Place {
       if (once) load_piece_once(row + c, x);
       else load_piece(row + c, x);
     }
+  }
+  // the same, of the walks: fetch() and, when it is used, piece() with the same row
+  __device__ __forceinline__ void fetch(const T* __restrict__ row, uint32_t cols, bool once, Raw<T, COLS>& r) const {
+    if constexpr (COLS != ODD) {
+      load(row, cols, once, r.x);
+    } else {
+      if (own >= V) return;
+      const T* p = row + c;
+      const uint32_t odd = (uint32_t)(uintptr_t)p >> 1 & 1u;
+      if (once) load_piece_once(p - odd, r.x);
+      else load_piece(p - odd, r.x);
+      // without a branch, whose end would wait for it: the others read the row's first value
+      r.end = __builtin_bit_cast(uint16_t, *(alone && odd ? p + V - 1 : row));
+    }
+  }
+  __device__ __forceinline__ Piece<T> piece(const T* row, const Raw<T, COLS>& r) const {
+    if constexpr (COLS != ODD) return r.x;
+    uint32_t q[5];
+    __builtin_memcpy(q, r.x.v, 16);
+    const uint32_t next = (uint32_t)__builtin_amdgcn_mov_dpp((int)q[0], 0x130, 0xF, 0xF, true);   // the next lane's
+    q[4] = alone ? r.end : next;
+    const uint32_t by = (uint32_t)(uintptr_t)(row + c) << 3 & 16u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = __builtin_amdgcn_alignbit(q[i + 1], q[i], by);
+    Piece<T> x;
+    __builtin_memcpy(x.v, q, 16);
+    return x;
   }
   __device__ __forceinline__ void store(T* __restrict__ row, uint32_t cols, const float* x) const {
     if (COLS == TINY) {
@@ -116,10 +158,11 @@ struct Place {
     }
   }
 };
-template <typename T>
-__device__ __forceinline__ void clear(Piece<T>& x) {
+template <typename T, int COLS>
+__device__ __forceinline__ void clear(Raw<T, COLS>& r) {
 #pragma unroll
-  for (int j = 0; j < Piece<T>::V; ++j) x.v[j] = zero_of<T>();
+  for (int j = 0; j < Piece<T>::V; ++j) r.x.v[j] = zero_of<T>();
+  r.end = 0;
 }
 
 template <int CTRL>
@@ -182,6 +225,8 @@ struct RowThreads {
   }
   static __device__ __forceinline__ uint32_t count() { return kWave ? LANES : blockDim.x; }
   static __device__ __forceinline__ uint32_t index() { return kWave ? threadIdx.x % (LANES + !LANES) : threadIdx.x; }
+  // whether the next lane of the wave, if any, holds another row
+  static __device__ __forceinline__ bool last_lane() { return (threadIdx.x + 1) % (kWave ? LANES : 64) == 0; }
   static __device__ __forceinline__ uint32_t row() { return kWave ? threadIdx.x / (LANES + !LANES) : 0; }
   // s and t summed over the row's threads. The waves' sums alternate between two places, so
   // that one barrier a sum is enough: before a place is written again, every wave has passed
@@ -211,6 +256,12 @@ constexpr uint32_t ln_forward_waves(int nv) { return nv == 8 ? 32 : 20; }
 constexpr uint32_t ln_backward_waves(int lanes, int nv) { return nv == 8 ? 20 : lanes ? 12 : 16; }
 
 constexpr uint32_t LN_MAX_COLS = 16384;   // of a row in registers
+
+// Whether some row starts at an odd 16-bit value.
+template <typename T>
+bool ln_odd(const void* p, int64_t stride) {
+  return sizeof(T) == 2 && (((uintptr_t)p >> 1 | (uintptr_t)stride) & 1);
+}
 
 // Calls f.run<LANES, NV>(threads) for the threads that hold rows of `cols` values: as few lanes
 // of a wave as do with 8 values each, a wave with 16, or a workgroup of as many waves as do with

@@ -84,6 +84,14 @@ def test_rows_apart_and_unaligned(rows, cols, dtype, offset, gap):
     check(*inputs(rows, cols, dtype, dtype, seed=1, offset=offset, gap=gap), dtype, dtype)
 
 
+@pytest.mark.parametrize("rows,cols", [(9, 1025), (7, 1536), (600, 2001), (9, 4096), (5, 8191), (4, 9001), (3, 16383)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("offset,gap", [(0, 0), (1, 0), (0, 1), (1, 2), (2, 3)])
+def test_rows_that_start_at_odd_values(rows, cols, dtype, offset, gap):
+    """Rows of several waves; the values before and after each row are NaN."""
+    check(*inputs(rows, cols, dtype, "f32", seed=12, offset=offset, gap=gap), dtype, "f32")
+
+
 @pytest.mark.parametrize("cols", [64, 1000, 8192])
 def test_without_weight_bias_or_parameter_gradients(cols):
     x, dy, w, b = inputs(37, cols, "bf16", "f32", seed=2)
