@@ -140,6 +140,26 @@ def test_a_workgroup_alone_and_two(rows, cols, dtype, wdtype):
                        tg.layer_norm_backward(dy, x, w, mean, rstd)[0])
 
 
+@pytest.mark.parametrize("rows,cols", [(5, 333), (100, 333), (2, 20000), (0, 64)])
+@pytest.mark.parametrize("dtype,wdtype", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+def test_one_of_the_parameters_gradients(rows, cols, dtype, wdtype):
+    """dweight or dbias may be NULL at the C entry; the other is the same as with both."""
+    x, dy, w, _ = inputs(rows, cols, dtype, wdtype, seed=13)
+    _, mean, rstd = tg.layer_norm_forward(x, w)
+    both = tg.layer_norm_backward(dy, x, w, mean, rstd)
+    lib, code = tg.load_library(), tg.DTYPE_CODES
+    ws = torch.empty(max(16, lib.tgrad_layer_norm_workspace(rows, cols)), dtype=torch.uint8, device="cuda")
+    for which in (0, 1):
+        dx, out = torch.empty_like(x), torch.full_like(w, float("nan"))
+        p = [None, None]
+        p[which] = out.data_ptr()
+        rc = lib.tgrad_layer_norm_backward(dy.data_ptr(), cols, x.data_ptr(), cols, w.data_ptr(), mean.data_ptr(),
+                                           rstd.data_ptr(), dx.data_ptr(), p[0], p[1], rows, cols, code[dtype],
+                                           code[wdtype], ws.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        assert torch.equal(dx, both[0]) and torch.equal(out, both[1 + which])
+
+
 @pytest.mark.parametrize("rows", [1, 300, 1705])
 @pytest.mark.parametrize("dtype,wdtype", TYPES)
 def test_one_column_has_no_gradient_of_x(rows, dtype, wdtype):
