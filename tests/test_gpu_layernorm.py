@@ -160,6 +160,26 @@ def test_one_of_the_parameters_gradients(rows, cols, dtype, wdtype):
         assert torch.equal(dx, both[0]) and torch.equal(out, both[1 + which])
 
 
+@pytest.mark.parametrize("rows,cols,dtype", [(40000, 2001, "bf16"), (20000, 4096, "f16"), (300000, 255, "bf16"), (20000, 2050, "f32")])
+def test_calls_larger_than_the_caches(rows, cols, dtype):
+    """Such calls read past the caches: rows come out as in calls on a few of them, and the sums
+    over rows within their bounds."""
+    gen = torch.Generator(device="cuda").manual_seed(14)
+    t = tg.torch_dtype(dtype)
+    x, dy = (torch.randn(rows, cols, generator=gen, device="cuda").to(t) for _ in range(2))
+    w = 1 + 0.2 * torch.randn(cols, generator=gen, device="cuda")
+    y, mean, rstd = tg.layer_norm_forward(x, w, w)
+    dx, dw, db = tg.layer_norm_backward(dy, x, w, mean, rstd)
+    for at in (0, rows // 3, rows - 64):
+        r = slice(at, at + 64)
+        part = tg.layer_norm_forward(x[r], w, w)
+        assert torch.equal(y[r], part[0]) and torch.equal(mean[r], part[1]) and torch.equal(rstd[r], part[2])
+        assert torch.equal(dx[r], tg.layer_norm_backward(dy[r], x[r], w, mean[r], rstd[r], params=False)[0])
+    n = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    for got, terms, what in ((dw, dy.double() * n, "dweight"), (db, dy.double(), "dbias")):
+        close(got, host(terms.sum(0)), L.gamma(rows + 16) * host(terms.abs().sum(0)), what)
+
+
 @pytest.mark.parametrize("rows", [1, 300, 1705])
 @pytest.mark.parametrize("dtype,wdtype", TYPES)
 def test_one_column_has_no_gradient_of_x(rows, dtype, wdtype):
