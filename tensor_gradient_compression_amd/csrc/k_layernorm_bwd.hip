@@ -12,12 +12,25 @@ namespace tg {
 
 namespace {
 
-// A value of dw or db.
-template <typename T>
-__device__ __forceinline__ void put(void* out, int wdt, uint32_t c, float x) {
+// Values of dw or db, from the place's `from`-th on.
+template <typename WT, int V>
+__device__ __forceinline__ void put(WT* out, int from, const float* x) {
+  WT v[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) v[j] = from_f32<WT>(x[j]);
+  if (from == 0) {
+    __builtin_memcpy((Unaligned<WT, V>*)out, v, sizeof v);
+    return;
+  }
+#pragma unroll
+  for (int j = 1; j < V; ++j)
+    if (j >= from) out[j] = v[j];
+}
+template <typename T, int V>
+__device__ __forceinline__ void put(void* out, int wdt, uint32_t c, int from, const float* x) {
   if (!out) return;
-  if (wdt == DT_F32) ((float*)out)[c] = x;
-  else ((T*)out)[c] = from_f32<T>(x);
+  if (sizeof(T) == 4 || wdt == DT_F32) put<float, V>((float*)out + c, from, x);
+  else put<T, V>((T*)out + c, from, x);
 }
 
 // Up to 16 values a thread their sums over rows, the weights and two rows fit the registers;
@@ -151,21 +164,24 @@ __global__ void __launch_bounds__(RowThreads<LANES>::kMost, ln_backward_waves(LA
       }
     }
   }
-  const bool alone = gridDim.x == 1;
+  void* const dw = gridDim.x == 1 ? a.dw : pw;
+  void* const db = gridDim.x == 1 ? a.db : pw + a.cols;
+  const int dt = gridDim.x == 1 ? a.wdt : DT_F32;
 #pragma unroll
-  for (int k = 0; k < K; ++k)
+  for (int k = 0; k < K; ++k) {
+    if (at[k].own >= V) continue;
+    if (COLS == TINY) {
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (at[k].own < V && at[k].mine(j, a.cols)) {
-        const uint32_t c = at[k].c + j;
-        if (alone) {
-          put<T>(a.dw, a.wdt, c, sw[k * V + j]);
-          put<T>(a.db, a.wdt, c, sb[k * V + j]);
-        } else {
-          pw[c] = sw[k * V + j];
-          pw[a.cols + c] = sb[k * V + j];
+      for (int j = 0; j < V; ++j)
+        if (j < (int)a.cols) {
+          put<T, 1>(dw, dt, j, 0, sw + j);
+          put<T, 1>(db, dt, j, 0, sb + j);
         }
-      }
+    } else {
+      put<T, V>(dw, dt, at[k].c, COLS == WHOLE ? 0 : at[k].own, sw + k * V);
+      put<T, V>(db, dt, at[k].c, COLS == WHOLE ? 0 : at[k].own, sb + k * V);
+    }
+  }
 }
 
 template <typename T>
@@ -273,7 +289,10 @@ struct Backward {
 // are sooner added up (4M values of bf16 in rows of 1024: 16 -> 13 us).
 // One alone writes dw and db itself, which saves the second launch: up to eight turns of a wave
 // with 8 values a thread (32 x 333 fp32: 8.0 -> 6.5 us a call, but 64 rows 7.9 -> 10.5), else
-// four (4 x 4952 fp32: 9.5 -> 7.2, 8 rows 9.6 -> 10.4).
+// four, of the longest rows two (2 x 16384 bf16 6.7, 8 rows in as many workgroups 9.6, four of
+// them in one 10.1). Few long rows take fewer turns: a turn costs more than their sums do
+// (16384 bf16, four turns, two and one: 16 rows 14.8, 11.5 and 10.3 us; 64 rows 15.4, 13.2 and
+// 14.1; 256 rows 19.9, 19.0 and 22.0).
 // Without dw and db there is nothing to add up, and every row that finds a place has its own
 // (512 x 8192 bf16: 8.4 -> 6.6 us; 4 rows 6.6 -> 4.5).
 struct BackwardGroups {
@@ -285,8 +304,8 @@ struct BackwardGroups {
     constexpr int kRows = RowThreads<LANES>::kRows;
     const uint32_t held = LN_CUS * (ln_backward_waves(LANES, NV) / (threads / 64)), most = held < 768 ? held : 768;
     if (!params) n = ln_walk(rows, kRows, most);
-    else if (rows <= kRows * (LANES && NV == 8 ? 8 : 4)) n = rows > 0;
-    else n = ln_walk(rows, kRows * 4, most);
+    else if (rows <= kRows * (LANES && NV == 8 ? 8 : LANES || NV == 8 ? 4 : 2)) n = rows > 0;
+    else n = ln_walk(rows, kRows * (LANES || rows > 128 ? 4 : rows > 32 ? 2 : 1), most);
   }
 };
 

@@ -140,6 +140,13 @@ def test_a_workgroup_alone_and_two(rows, cols, dtype, wdtype):
                        tg.layer_norm_backward(dy, x, w, mean, rstd)[0])
 
 
+@pytest.mark.parametrize("rows", [2, 3, 32, 33, 128, 129])
+@pytest.mark.parametrize("cols", [2050, 8192, 9001, 16384])
+@pytest.mark.parametrize("dtype,wdtype", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f32")])
+def test_few_long_rows(rows, cols, dtype, wdtype):
+    check(*inputs(rows, cols, dtype, wdtype, seed=15), dtype, wdtype)
+
+
 @pytest.mark.parametrize("rows,cols", [(5, 333), (100, 333), (2, 20000), (0, 64)])
 @pytest.mark.parametrize("dtype,wdtype", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
 def test_one_of_the_parameters_gradients(rows, cols, dtype, wdtype):
