@@ -16,9 +16,9 @@
 // writes those twice; its sums leave them out.
 //
 // Both directions are bound by memory where rows are many (rates at 67M values): forward 5.8 to
-// 6.2 TB/s in bf16 and 6.2 to 6.7 in fp32, backward 5.0 to 5.8 and 5.3 to 6.3, for whole pieces
+// 6.2 TB/s in bf16 and 6.2 to 6.7 in fp32, backward 5.2 to 5.9 and 5.5 to 6.4, for whole pieces
 // of any width; bf16 rows of several waves that start at odd values (2001 to 12001 columns) 5.5 to
-// 6.0 and 4.5 to 4.8. Held by their threads as the fewest lanes with 8 values each, since
+// 6.0 and 4.8 to 5.2. Held by their threads as the fewest lanes with 8 values each, since
 // fewer lanes with 16 leave room for fewer waves (backward, 65536 x 256 bf16: 20 us, 18.4).
 #pragma once
 #include "layernorm.h"
