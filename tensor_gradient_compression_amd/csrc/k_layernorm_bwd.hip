@@ -284,9 +284,9 @@ struct Backward {
   }
 };
 // Workgroups of the backward walk, each of which leaves one row of sums: as many as run at
-// once, so that none waits for a place (8192 columns of bf16: 80 us with 256 workgroups of 16
-// waves, 90 with 512), at most 768, and few enough that each has four turns: fewer rows of sums
-// are sooner added up (4M values of bf16 in rows of 1024: 16 -> 13 us).
+// once, so that none waits for a place (8192 columns of bf16: 72 us with 256 workgroups of 16
+// waves, 81 with 512), at most 768, and few enough that each has four turns: fewer rows of sums
+// are sooner added up (4M values of bf16 in rows of 1024: 14 -> 11.4 us).
 // One alone writes dw and db itself, which saves the second launch: up to eight turns of a wave
 // with 8 values a thread (32 x 333 fp32: 8.0 -> 6.5 us a call, but 64 rows 7.9 -> 10.5), else
 // four, of the longest rows two (2 x 16384 bf16 6.7, 8 rows in as many workgroups 9.6, four of
