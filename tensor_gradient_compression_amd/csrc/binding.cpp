@@ -297,17 +297,18 @@ Rows rows_of(const at::Tensor& t, const char* what) {
   for (int64_t i = 0; i < d - 1; ++i) r.rows *= t.size(i);
   if (r.rows == 0) return r;
   if (t.stride(d - 1) != 1 && r.cols > 1) throw Invalid{std::string(what) + ": the last axis must be contiguous"};
-  int64_t span = 0;   // of the axes from the last leading one outwards
+  // of the axes from the last leading one outwards; none yet (an expanded axis has stride and span 0)
+  int64_t span = -1;
   for (int64_t i = d - 2; i >= 0; --i) {
     if (t.size(i) == 1) continue;
-    if (!r.stride) r.stride = t.stride(i);
+    if (span < 0) r.stride = t.stride(i);
     else if (t.stride(i) != span)
       throw Invalid{std::string(what) + ": the leading axes' strides do not form one; call contiguous()"};
     span = t.stride(i) * t.size(i);
   }
   if (r.rows > 1 && r.stride < r.cols)
     throw Invalid{std::string(what) + ": the rows overlap; call contiguous()"};
-  if (!r.stride) r.stride = r.cols;
+  if (span < 0) r.stride = r.cols;
   return r;
 }
 

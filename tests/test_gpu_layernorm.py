@@ -331,3 +331,24 @@ def test_a_bias_alone_gets_a_gradient_of_its_own_precision():
     b.requires_grad_()
     tg.layer_norm(x, None, b).backward(dy)
     close(b.grad, host(dy).sum(0), L.gamma(416) * np.abs(host(dy)).sum(0), "dbias")
+
+
+@pytest.mark.parametrize("shape,to", [((4, 1, 16), (4, 8, 16)), ((1, 8, 16), (4, 8, 16)), ((1, 1, 16), (4, 8, 16)),
+                                      ((3, 1, 2, 16), (3, 8, 2, 16)), ((3, 2, 1, 16), (3, 2, 8, 16)),
+                                      ((3, 1, 1, 16), (3, 8, 1, 16)), ((4, 1, 1), (4, 8, 1))])
+def test_expanded_leading_axes_are_refused(shape, to):
+    """Such rows lie in memory once and not evenly spaced: refused before a launch, as x and as
+    dy, and taken once they are contiguous."""
+    gen = torch.Generator(device="cuda").manual_seed(16)
+    x = torch.randn(*shape, generator=gen, device="cuda").expand(*to)
+    full = x.contiguous()
+    for f in (tg.layer_norm_forward, tg.layer_norm):
+        with pytest.raises(ValueError, match="x: .*contiguous"):
+            f(x)
+    y, mean, rstd = tg.layer_norm_forward(full)
+    for args, what in (((full, x), "x"), ((x, full), "dy")):
+        with pytest.raises(ValueError, match=f"{what}: .*contiguous"):
+            tg.layer_norm_backward(*args, None, mean, rstd)
+    flat = full.view(-1, to[-1])
+    close(y.view_as(flat), L.forward(host(flat), None, None, EPS)[0],
+          L.forward_bounds(host(flat), None, None, EPS, "f32", 17)[0], "y")
