@@ -89,6 +89,11 @@ at::Tensor empty(at::IntArrayRef sizes, c10::ScalarType type, int device) {
 
 void* data_of(const at::Tensor& t) { return const_cast<void*>(t.const_data_ptr()); }
 
+// As torch's own in-place operations: what autograd saved of the tensor is out of date.
+void changed(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 struct Sequence {
   PyObject* fast;
   Sequence(PyObject* o, const char* what) : fast(PySequence_Fast(o, what)) {
@@ -227,6 +232,7 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     gradients(p, a[2]);
     const float* clip = a[3] == Py_None ? nullptr : pair_of_floats(p, a[3], "clip");
     void* out[2] = {nullptr, nullptr};
+    std::vector<at::Tensor> moments;
     if (a[4] != Py_None) {
       if (p->bits != 8) throw Invalid{"moments: only for 8-bit states (32-bit ones are in `state`)"};
       Sequence ms(a[4], "moments: expected two tensors");
@@ -237,16 +243,14 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (t.numel() != p->total || !t.is_contiguous())
           throw Invalid{named("moments", i) + ": needs " + std::to_string(p->total) + " contiguous bfloat16 values"};
         out[i] = data_of(t);
+        moments.push_back(t);
       }
       if (p->total && out[0] == out[1]) throw Invalid{"moments: the two tensors are the same"};
     }
     check_rc(tgrad_adamw_step(p->h, p->w.data(), p->g.data(), clip, out[0], out[1], pointer(a[5], p->device)),
              "tgrad_adamw_step", tgrad_adamw_last_error(p->h));
-    // as torch's own in-place operations: what autograd saved of a weight is out of date
-    for (long i = 0; i < ws.size(); ++i) {
-      const at::Tensor& t = THPVariable_Unpack(ws[i]);
-      if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
-    }
+    for (long i = 0; i < ws.size(); ++i) changed(THPVariable_Unpack(ws[i]));
+    for (const at::Tensor& t : moments) changed(t);
     Py_RETURN_NONE;
   });
 }
@@ -271,6 +275,7 @@ PyObject* adamw_grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check_rc(tgrad_adamw_grad_norm(p->h, p->g.data(), max_norm, scale, (float*)data_of(out),
                                    pointer(a[5], p->device)),
              "tgrad_adamw_grad_norm", tgrad_adamw_last_error(p->h));
+    if (a[4] != Py_None) changed(out);
     return THPVariable_Wrap(out);
   });
 }

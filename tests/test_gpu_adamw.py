@@ -434,3 +434,19 @@ def test_autograd_sees_the_change():
     c.opt.step([w], c.gradients())
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward()
+
+
+def test_autograd_sees_the_results_that_are_written_in_place():
+    """The values of the moments and the norm, which go into the caller's tensors, change as the
+    weights do."""
+    c = Case([64], "f32", bits=8)
+    mo, out = c.moment_buffers(), torch.ones(2, device="cuda")
+    for t in mo + [out]:
+        x = torch.ones_like(t).requires_grad_()
+        y = (x * t).sum()                      # saves t
+        c.opt.step(c.w, c.gradients(), clip=c.opt.grad_norm(c.gradients(), out=out), moments=mo)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    with torch.inference_mode():               # tensors that have no version
+        out, mo = torch.ones(2, device="cuda"), c.moment_buffers()
+        c.opt.step(c.w, c.gradients(), clip=c.opt.grad_norm(c.gradients(), out=out), moments=mo)
