@@ -239,25 +239,32 @@ __global__ void __launch_bounds__(256) k_ln_columns(LnBackward a) {
   a.partial[((uint64_t)blockIdx.y * 2 + 1) * a.cols + i] = t;
 }
 
-// The partial rows' sums. blockIdx.y: dw or db; 32 columns a workgroup, 32 threads a column.
+// The partial rows' sums. blockIdx.y: dw or db; 32 columns a workgroup at a time, 32 threads a
+// column. Workgroups walk over the columns of the widest rows: a launch whose threads along an
+// axis pass 32 bits is cut to the rest without an error.
+constexpr uint32_t kReduceGroups = 1 << 16;
 template <typename WT>
 __global__ void __launch_bounds__(1024) k_ln_reduce(const float* __restrict__ partial, uint32_t n, uint32_t cols,
                                                     WT* __restrict__ dw, WT* __restrict__ db) {
   __shared__ float lds[32][33];
-  const uint32_t tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
+  const uint32_t tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   WT* out = blockIdx.y ? db : dw;
   if (!out) return;
-  float s = 0.0f;
-  if (c < cols) {
-    const float* p = partial + (uint64_t)blockIdx.y * cols + c;
+  for (uint32_t first = blockIdx.x * 32; first < cols; first += kReduceGroups * 32) {
+    const uint32_t c = first + tx;
+    float s = 0.0f;
+    if (c < cols) {
+      const float* p = partial + (uint64_t)blockIdx.y * cols + c;
 #pragma unroll 8
-    for (uint32_t r = ty; r < n; r += 32) s += p[(uint64_t)r * 2 * cols];
+      for (uint32_t r = ty; r < n; r += 32) s += p[(uint64_t)r * 2 * cols];
+    }
+    lds[ty][tx] = s;
+    __syncthreads();
+    s = group_sum<32>(lds[tx][ty]);
+    const uint32_t o = first + ty;
+    if (tx == 0 && o < cols) out[o] = from_f32<WT>(s);
+    __syncthreads();   // read before it is written again
   }
-  lds[ty][tx] = s;
-  __syncthreads();
-  s = group_sum<32>(lds[tx][ty]);
-  const uint32_t o = blockIdx.x * 32 + ty;
-  if (tx == 0 && o < cols) out[o] = from_f32<WT>(s);
 }
 
 template <typename T>
@@ -328,7 +335,8 @@ hipError_t backward(LnBackward a, hipStream_t s) {
     if (params) k_ln_columns<T><<<dim3((a.cols + 255) / 256, n), 256, 0, s>>>(a);
   }
   if (params && !alone) {
-    const dim3 grid((a.cols + 31) / 32, 2);
+    const uint32_t groups = (a.cols + 31) / 32;
+    const dim3 grid(groups < kReduceGroups ? groups : kReduceGroups, 2);
     if (a.wdt == DT_F32) k_ln_reduce<float><<<grid, 1024, 0, s>>>(a.partial, n, a.cols, (float*)a.dw, (float*)a.db);
     else k_ln_reduce<T><<<grid, 1024, 0, s>>>(a.partial, n, a.cols, (T*)a.dw, (T*)a.db);
   }

@@ -352,3 +352,22 @@ def test_expanded_leading_axes_are_refused(shape, to):
     flat = full.view(-1, to[-1])
     close(y.view_as(flat), L.forward(host(flat), None, None, EPS)[0],
           L.forward_bounds(host(flat), None, None, EPS, "f32", 17)[0], "y")
+
+
+def test_more_columns_than_one_launch_has_threads_for():
+    """2^27 + 33 columns, of which 32 threads each add up the sums over rows. With x of 1 and -1,
+    a mean of 0 and a deviation of 1 every product is exact, and one row's sums are its own values."""
+    cols = (1 << 27) + 33
+    print("CASE layer norm 1 x 2^27 + 33", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    dy = torch.randn(1, cols, generator=gen, device="cuda").bfloat16()
+    x = torch.ones_like(dy)
+    x[:, ::3] = -1
+    mean, rstd = torch.zeros(1, device="cuda"), torch.ones(1, device="cuda")
+    dx, dw, db = tg.layer_norm_backward(dy, x, None, mean, rstd)
+    assert torch.equal(db, dy[0]) and torch.equal(dw, (dy * x)[0])
+    s, u, h = (float(t.sum(dtype=torch.float64)) / cols for t in (dy, dy * x, dy.abs()))
+    bound = 2 * L.gamma(cols / 1024 + 26) * h
+    for r in (slice(0, 4096), slice(cols - 4096, cols)):
+        true = host(dy[0, r]) - s - host(x[0, r]) * u
+        close(dx[0, r], true, bound + L.rounding(np.abs(true) + bound, "bf16"), "dx")
