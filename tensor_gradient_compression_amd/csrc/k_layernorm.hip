@@ -113,43 +113,44 @@ __global__ void __launch_bounds__(LN_LONG) k_ln_forward_long(LnForward a) {
   constexpr int V = Piece<T>::V;
   __shared__ float lds[RT::kLds];
   RT rt(lds);
-  const int64_t row = blockIdx.x;
-  const T* x = (const T*)a.x + row * a.x_stride;
-  float s = 0.0f, unused;
-  Piece<T> p;
-  for (uint32_t c = threadIdx.x * V; c < a.cols; c += LN_LONG * V) {
-    const Place<T, RAGGED> at(c, a.cols);
-    at.load(x, a.cols, false, p);
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* x = (const T*)a.x + row * a.x_stride;
+    float s = 0.0f, unused;
+    Piece<T> p;
+    for (uint32_t c = threadIdx.x * V; c < a.cols; c += LN_LONG * V) {
+      const Place<T, RAGGED> at(c, a.cols);
+      at.load(x, a.cols, false, p);
 #pragma unroll
-    for (int j = 0; j < V; ++j) s += at.mine(j, a.cols) ? to_f32(p.v[j]) : 0.0f;
-  }
-  rt.template sum<false>(s, unused);
-  const float mean = s / (float)a.cols;
-  s = 0.0f;
-  for (uint32_t c = threadIdx.x * V; c < a.cols; c += LN_LONG * V) {
-    const Place<T, RAGGED> at(c, a.cols);
-    at.load(x, a.cols, false, p);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float d = to_f32(p.v[j]) - mean;
-      s = __builtin_fmaf(d, at.mine(j, a.cols) ? d : 0.0f, s);
+      for (int j = 0; j < V; ++j) s += at.mine(j, a.cols) ? to_f32(p.v[j]) : 0.0f;
     }
-  }
-  rt.template sum<false>(s, unused);
-  const float rstd = 1.0f / sqrtf(s / (float)a.cols + a.eps);
-  for (uint32_t c = threadIdx.x * V; c < a.cols; c += LN_LONG * V) {
-    const Place<T, RAGGED> at(c, a.cols);
-    float w[V], b[V], o[V];
-    at.load(x, a.cols, false, p);
-    at.weights(a.w, a.wdt, a.cols, 1.0f, w);
-    at.weights(a.b, a.wdt, a.cols, 0.0f, b);
+    rt.template sum<false>(s, unused);
+    const float mean = s / (float)a.cols;
+    s = 0.0f;
+    for (uint32_t c = threadIdx.x * V; c < a.cols; c += LN_LONG * V) {
+      const Place<T, RAGGED> at(c, a.cols);
+      at.load(x, a.cols, false, p);
 #pragma unroll
-    for (int j = 0; j < V; ++j) o[j] = __builtin_fmaf((to_f32(p.v[j]) - mean) * rstd, w[j], b[j]);
-    at.store((T*)a.y + row * (int64_t)a.cols, a.cols, o);
-  }
-  if (threadIdx.x == 0) {
-    a.mean[row] = mean;
-    a.rstd[row] = rstd;
+      for (int j = 0; j < V; ++j) {
+        const float d = to_f32(p.v[j]) - mean;
+        s = __builtin_fmaf(d, at.mine(j, a.cols) ? d : 0.0f, s);
+      }
+    }
+    rt.template sum<false>(s, unused);
+    const float rstd = 1.0f / sqrtf(s / (float)a.cols + a.eps);
+    for (uint32_t c = threadIdx.x * V; c < a.cols; c += LN_LONG * V) {
+      const Place<T, RAGGED> at(c, a.cols);
+      float w[V], b[V], o[V];
+      at.load(x, a.cols, false, p);
+      at.weights(a.w, a.wdt, a.cols, 1.0f, w);
+      at.weights(a.b, a.wdt, a.cols, 0.0f, b);
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[j] = __builtin_fmaf((to_f32(p.v[j]) - mean) * rstd, w[j], b[j]);
+      at.store((T*)a.y + row * (int64_t)a.cols, a.cols, o);
+    }
+    if (threadIdx.x == 0) {
+      a.mean[row] = mean;
+      a.rstd[row] = rstd;
+    }
   }
 }
 
@@ -176,7 +177,7 @@ struct Forward {
 
 template <typename T>
 hipError_t forward(const LnForward& a, hipStream_t s) {
-  if (!ln_dispatch(a.cols, Forward<T>{a, s})) k_ln_forward_long<T><<<(uint32_t)a.rows, LN_LONG, 0, s>>>(a);
+  if (!ln_dispatch(a.cols, Forward<T>{a, s})) k_ln_forward_long<T><<<ln_walk(a.rows, 1, LN_LONG_GROUPS), LN_LONG, 0, s>>>(a);
   return hipGetLastError();
 }
 

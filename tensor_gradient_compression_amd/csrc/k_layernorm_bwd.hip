@@ -190,37 +190,38 @@ __global__ void __launch_bounds__(LN_LONG) k_ln_dx_long(LnBackward a) {
   constexpr int V = Piece<T>::V;
   __shared__ float lds[RT::kLds];
   RT rt(lds);
-  const int64_t row = blockIdx.x;
-  const T* x = (const T*)a.x + row * a.x_stride;
-  const T* dy = (const T*)a.dy + row * a.dy_stride;
-  const float mean = a.mean[row], rstd = a.rstd[row];
-  float s = 0.0f, u = 0.0f, w[V];
-  Piece<T> p, q;
-  for (uint32_t c = threadIdx.x * V; c < a.cols; c += LN_LONG * V) {
-    const Place<T, RAGGED> at(c, a.cols);
-    at.load(x, a.cols, false, p);
-    at.load(dy, a.cols, false, q);
-    at.weights(a.w, a.wdt, a.cols, 1.0f, w);
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* x = (const T*)a.x + row * a.x_stride;
+    const T* dy = (const T*)a.dy + row * a.dy_stride;
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float s = 0.0f, u = 0.0f, w[V];
+    Piece<T> p, q;
+    for (uint32_t c = threadIdx.x * V; c < a.cols; c += LN_LONG * V) {
+      const Place<T, RAGGED> at(c, a.cols);
+      at.load(x, a.cols, false, p);
+      at.load(dy, a.cols, false, q);
+      at.weights(a.w, a.wdt, a.cols, 1.0f, w);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float h = at.mine(j, a.cols) ? to_f32(q.v[j]) * w[j] : 0.0f;
-      s += h;
-      u = __builtin_fmaf(h, (to_f32(p.v[j]) - mean) * rstd, u);
+      for (int j = 0; j < V; ++j) {
+        const float h = at.mine(j, a.cols) ? to_f32(q.v[j]) * w[j] : 0.0f;
+        s += h;
+        u = __builtin_fmaf(h, (to_f32(p.v[j]) - mean) * rstd, u);
+      }
     }
-  }
-  rt.template sum<true>(s, u);
-  s /= (float)a.cols;
-  u /= (float)a.cols;
-  for (uint32_t c = threadIdx.x * V; c < a.cols; c += LN_LONG * V) {
-    const Place<T, RAGGED> at(c, a.cols);
-    float o[V];
-    at.load(x, a.cols, false, p);
-    at.load(dy, a.cols, false, q);
-    at.weights(a.w, a.wdt, a.cols, 1.0f, w);
+    rt.template sum<true>(s, u);
+    s /= (float)a.cols;
+    u /= (float)a.cols;
+    for (uint32_t c = threadIdx.x * V; c < a.cols; c += LN_LONG * V) {
+      const Place<T, RAGGED> at(c, a.cols);
+      float o[V];
+      at.load(x, a.cols, false, p);
+      at.load(dy, a.cols, false, q);
+      at.weights(a.w, a.wdt, a.cols, 1.0f, w);
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      o[j] = rstd * ((to_f32(q.v[j]) * w[j] - s) - (to_f32(p.v[j]) - mean) * rstd * u);
-    at.store((T*)a.dx + row * (int64_t)a.cols, a.cols, o);
+      for (int j = 0; j < V; ++j)
+        o[j] = rstd * ((to_f32(q.v[j]) * w[j] - s) - (to_f32(p.v[j]) - mean) * rstd * u);
+      at.store((T*)a.dx + row * (int64_t)a.cols, a.cols, o);
+    }
   }
 }
 
@@ -331,7 +332,7 @@ hipError_t backward(LnBackward a, hipStream_t s) {
   if (!params) a.partial = nullptr;
   if (a.rows && !ln_dispatch(a.cols, Backward<T>{a, n, once, s})) {
     alone = false;
-    k_ln_dx_long<T><<<(uint32_t)a.rows, LN_LONG, 0, s>>>(a);
+    k_ln_dx_long<T><<<ln_walk(a.rows, 1, LN_LONG_GROUPS), LN_LONG, 0, s>>>(a);
     if (params) k_ln_columns<T><<<dim3((a.cols + 255) / 256, n), 256, 0, s>>>(a);
   }
   if (params && !alone) {

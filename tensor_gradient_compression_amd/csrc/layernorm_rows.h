@@ -295,5 +295,8 @@ inline uint32_t ln_walk(int64_t rows, int per, uint32_t most) {
 }
 
 constexpr int LN_LONG = 1024;   // threads of a row beyond the registers
+// Workgroups that walk over such rows: a launch whose threads along an axis pass 32 bits is cut
+// to the rest without an error.
+constexpr uint32_t LN_LONG_GROUPS = 1 << 16;
 
 }  // namespace tg

@@ -371,3 +371,39 @@ def test_more_columns_than_one_launch_has_threads_for():
     for r in (slice(0, 4096), slice(cols - 4096, cols)):
         true = host(dy[0, r]) - s - host(x[0, r]) * u
         close(dx[0, r], true, bound + L.rounding(np.abs(true) + bound, "bf16"), "dx")
+
+
+@pytest.mark.parametrize("rows", [(1 << 16) + 3, (1 << 22) + 1])
+def test_many_rows_beyond_the_registers(rows):
+    """Rows of 16385 columns, a workgroup each at a time: more than one launch of them, and more
+    than one launch's threads. Rows of zeros but for some; each comes out as in a call on it alone."""
+    import gc
+    cols, dt = 16385, torch.bfloat16
+    gc.collect()
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 4 * rows * cols + (8 << 30):
+        pytest.skip("needs x and one more tensor of its size")
+    print(f"CASE layer norm {rows} x {cols}", flush=True)
+    x = torch.zeros(rows, cols, dtype=dt, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(18)
+    some = torch.tensor([0, 1, (1 << 16) - 1, 1 << 16, rows - 2, rows - 1], device="cuda")
+    x[some] = torch.randn(6, cols, generator=gen, device="cuda").to(dt)
+    w = (1 + 0.2 * torch.randn(cols, generator=gen, device="cuda"))
+    few = tg.layer_norm_forward(x[some], w, w)
+    zero = tg.layer_norm_forward(x[2:3], w, w)
+    y, mean, rstd = tg.layer_norm_forward(x, w, w)
+    mine = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    mine[some] = True
+    for got, one, none in zip((y, mean, rstd), few, zero):
+        assert torch.equal(got[some], one)
+        assert torch.equal(got[:64][~mine[:64]], none.expand_as(got[:64])[~mine[:64]])
+    assert bool((mean[~mine] == zero[1]).all()) and bool((rstd[~mine] == zero[2]).all())
+    middle = slice(rows // 2, rows // 2 + 64)
+    assert torch.equal(y[middle], zero[0].expand(64, cols))
+    del y, got, one, none
+    torch.cuda.empty_cache()
+    dx = tg.layer_norm_backward(x, x, w, mean, rstd, params=False)[0]
+    assert torch.equal(dx[some], tg.layer_norm_backward(x[some], x[some], w, mean[some], rstd[some], params=False)[0])
+    assert not dx[middle].any() and not dx[2:64].any()
+    del x, dx
+    torch.cuda.empty_cache()
