@@ -389,8 +389,8 @@ const char *tgrad_kernel_name(int id);
 /* ---------------------------------------------------------------- the other tensors.
  * AdamW over many tensors at once: the biases, norm weights and small products of a model
  * whose large tensors the calls above optimise. One handle steps n tensors in one launch
- * for every 240 of them; weights and gradients are the caller's and are passed to every
- * call. Per value, each operation rounded to fp32 (the division is a product with a
+ * for every 240 of them (and every 2^32 values); weights and gradients are the caller's and
+ * are passed to every call. Per value, each operation rounded to fp32 (the division is a product with a
  * reciprocal that is within one unit of the last place):
  *   g' = g * coefficient (see tgrad_adamw_grad_norm; g' = g without a clip)
  *   m = b1 m + (1 - b1) g';   v = b2 v + (1 - b2) g'^2

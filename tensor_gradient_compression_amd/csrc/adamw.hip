@@ -50,6 +50,10 @@ namespace {
 constexpr uint64_t kStreamBytes = 1500000000;
 constexpr uint32_t kStreamLds = 80 * 1024;
 
+// Chunks of one launch: a launch whose threads along an axis pass 32 bits, which 2^24 workgroups'
+// do, is cut to the rest without an error.
+constexpr uint32_t kLaunchChunks = 1 << 21;
+
 constexpr size_t kCountBytes = (ADAMW_COUNTS + 1) * ADAMW_COUNT_PITCH * sizeof(uint32_t);
 
 struct OnDevice {
@@ -173,14 +177,26 @@ int tgrad_adamw_init(tgrad_adamw_t** out, int n, const int64_t* numel, const int
       t.dtype = dtype[i];
       t.grad_dtype = grad_dtype[i];
       t.wd = weight_decay[i];
-      if (i % ADAMW_LAUNCH_TENSORS == 0)
+      auto new_launch = [&] {
         h->launches.push_back({i, 0, (uint32_t)chunks.size(), 0, (uint32_t)spans.size(), 0});
+      };
+      // closes a launch for now, with this tensor in it
+      auto up_to_here = [&](tgrad_adamw::Launch& l) {
+        l.tensors = i - l.first_tensor + 1;
+        l.chunks = (uint32_t)chunks.size() - l.first_chunk;
+        l.spans = (uint32_t)spans.size() - l.first_span;
+      };
+      if (i % ADAMW_LAUNCH_TENSORS == 0) new_launch();
       AdamwChunk c{};
       c.wd = t.wd;
       c.tensor = (uint32_t)i;
       c.wdt = dtype[i] == TGRAD_C64 ? DT_F32 : (uint32_t)dtype[i];
       c.gdt = grad_dtype[i] == TGRAD_C64 ? DT_F32 : (uint32_t)grad_dtype[i];
       for (uint64_t s = 0; s < t.values; s += ADAMW_CHUNK) {
+        if (chunks.size() - h->launches.back().first_chunk == kLaunchChunks) {
+          up_to_here(h->launches.back());
+          new_launch();
+        }
         c.start = s;
         c.state = at + s;
         c.n = (uint32_t)(t.values - s < ADAMW_CHUNK ? t.values - s : ADAMW_CHUNK);
@@ -193,9 +209,7 @@ int tgrad_adamw_init(tgrad_adamw_t** out, int n, const int64_t* numel, const int
         delete h;
         return TGRAD_EINVAL;
       }
-      h->launches.back().tensors++;
-      h->launches.back().chunks = (uint32_t)chunks.size() - h->launches.back().first_chunk;
-      h->launches.back().spans = (uint32_t)spans.size() - h->launches.back().first_span;
+      up_to_here(h->launches.back());
       h->tensors.push_back(t);
       bytes += t.values * (16 + (c.wdt == DT_F32 ? 8 : 4) + (c.gdt == DT_F32 ? 4 : 2));
       at += (t.values + ADAMW_GROUP - 1) / ADAMW_GROUP * ADAMW_GROUP;

@@ -450,3 +450,38 @@ def test_autograd_sees_the_results_that_are_written_in_place():
     with torch.inference_mode():               # tensors that have no version
         out, mo = torch.ones(2, device="cuda"), c.moment_buffers()
         c.opt.step(c.w, c.gradients(), clip=c.opt.grad_norm(c.gradients(), out=out), moments=mo)
+
+
+def test_more_values_than_one_launch_has_threads_for():
+    """A tensor of 2^35 + 1000 values, 2^24 workgroups' and one more: its end and a piece in its
+    middle are stepped like tensors of their own, with the same random bits at multiples of 2^32."""
+    import gc
+    tail, at = 1000, (5 << 32, 1 << 35)
+    n = at[1] + tail
+    gc.collect()
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 6.2 * n + (8 << 30):
+        pytest.skip("needs weights, gradients and state of 2^35 values")
+    print("CASE adamw 2^35 values", flush=True)
+    big = tg.AdamW([n], "bf16", state_bits=8, seed=5, **HYPER)
+    small = tg.AdamW([tail], "bf16", state_bits=8, seed=5, **HYPER)
+    w, g = (torch.zeros(n, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    wt, gt = random_tensor(tail, "bf16", gen, 0.02), random_tensor(tail, "bf16", gen, 0.01)
+    for a in at:
+        w[a:a + tail], g[a:a + tail] = wt, gt
+    for _ in range(2):
+        big.step([w], [g])
+        small.step([wt], [gt])
+    whole = tail // A.GROUP * A.GROUP
+    for a in at:
+        assert torch.equal(w[a:a + tail], wt)
+        for k in ("m", "root_v"):
+            assert torch.equal(big.state[k][a:a + whole], small.state[k][:whole])
+    norm = math.sqrt(2 * float((gt.double() ** 2).sum()))
+    assert abs(float(big.grad_norm([g])[0]) - norm) <= 1.01 * E * norm
+    assert big.t == 2
+    del w, g
+    big.close()
+    del big
+    torch.cuda.empty_cache()
