@@ -4,7 +4,9 @@ Every HIP source under csrc/ is compiled for gfx950 only, without floating-point
 contraction (the Adam and weight-update arithmetic keeps its written rounding order)
 and without packed-fp32 instructions, then linked into one shared library next to
 this file. csrc/binding.cpp, the part of the Python binding that unpacks torch tensors, is
-host code against torch's headers and becomes _tgrad_torch.so. Usage: python -m tensor_gradient_compression_amd.build
+host code against torch's headers and becomes _tgrad_torch.so (left out without torch; the
+library itself is a C library and needs hipcc alone).
+Usage: python -m tensor_gradient_compression_amd.build
 """
 from __future__ import annotations
 
@@ -51,12 +53,11 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _torch_dir() -> str:
+def _torch_dir():
+    """torch's folder, or None without torch."""
     import importlib.util
     spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.origin:
-        raise RuntimeError("torch not found: its headers are required to build the binding")
-    return os.path.dirname(spec.origin)
+    return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
 
 
 def _run(cmd, what: str) -> None:
@@ -93,16 +94,19 @@ def build(verbose: bool = True) -> str:
     srcs = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".hip"))
     jobs = min(len(srcs), max(1, min(8, os.cpu_count() or 1)))
     with cf.ThreadPoolExecutor(jobs) as ex:
-        bound = ex.submit(_compile_binding)
+        bound = ex.submit(_compile_binding) if _torch_dir() else None
         objs = list(ex.map(_compile, srcs))
-        binding_obj = bound.result()
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("link failed:\n" + res.stdout + res.stderr)
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+    # the library is there whatever the binding lacks
+    if bound is not None:
+        _link_binding(bound.result())
+    elif verbose:
+        print("torch not found: built without the torch binding")
     if verbose:
         print(f"built {LIB}")
     return LIB

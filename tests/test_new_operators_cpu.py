@@ -160,3 +160,28 @@ def test_layer_norm_refuses(lib):
         assert bwd(**kw) == tg.EINVAL, kw
     assert lib.tgrad_layer_norm_workspace(-1, 8) == -1 and lib.tgrad_layer_norm_workspace(1, 0) == -1
     assert lib.tgrad_layer_norm_workspace(5, 8) > 0
+
+
+@pytest.mark.parametrize("lacks", ["torch", "a C++ compiler"])
+def test_the_library_builds_without_what_the_binding_needs(lacks, tmp_path, monkeypatch, capsys):
+    """libtgrad.so is a C library: hipcc is enough for it."""
+    import importlib.util
+    from tensor_gradient_compression_amd import build
+    src = tmp_path / "csrc"
+    src.mkdir()
+    (src / "one.hip").write_text('extern "C" int one() { return 1; }\n')
+    for name, at in (("CSRC", src), ("BUILD", tmp_path / "_build"), ("LIB", tmp_path / "libtgrad.so"),
+                     ("BINDING", tmp_path / "_tgrad_torch.so")):
+        monkeypatch.setattr(build, name, str(at))
+    if lacks == "torch":
+        monkeypatch.setattr(importlib.util, "find_spec", lambda *a: None)
+        build.build()
+        assert "torch" in capsys.readouterr().out
+    else:
+        def fails():
+            raise RuntimeError("g++ not found")
+        monkeypatch.setattr(build, "_compile_binding", fails)
+        with pytest.raises(RuntimeError, match="g\\+\\+"):
+            build.build()
+    assert ctypes.CDLL(build.LIB).one() == 1
+    assert not os.path.exists(build.BINDING)
