@@ -485,3 +485,26 @@ def test_more_values_than_one_launch_has_threads_for():
     big.close()
     del big
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16", "c64"])
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("numels", [[9_000_011, 300_001], [130_000_003, 5]])
+def test_norm_of_spans_of_several_passes(dtype, offset, numels):
+    """Spans of 8192 to 98304 values, several passes of a workgroup, with ragged ends. fp64 sums
+    in another order differ far less than fp32's rounding."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    opt = tg.AdamW(numels, dtype, state_bits=8)
+    g = [random_tensor(n, dtype, gen, 1.0, offset) for n in numels]
+    squares = 0.0
+    for x in g:
+        v = torch.view_as_real(x).reshape(-1) if x.is_complex() else x
+        for part in v.split(1 << 26):
+            squares += float((part.double() ** 2).sum())
+    out = opt.grad_norm(g, max_norm=2.0, grad_scale=0.5)
+    norm = 0.5 * math.sqrt(squares)
+    coef = 0.5 * min(1.0, 2.0 / norm)
+    assert abs(float(out[0]) - norm) <= 1.01 * E * norm
+    assert abs(float(out[1]) - coef) <= 1.01 * E * coef
+    g[0].reshape(-1)[-1] = math.inf              # the very last value of a span
+    assert float(opt.grad_norm(g)[0]) == math.inf

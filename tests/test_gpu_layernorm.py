@@ -407,3 +407,45 @@ def test_many_rows_beyond_the_registers(rows):
     assert not dx[middle].any() and not dx[2:64].any()
     del x, dx
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("rows,cols", [(70000, 8), (300000, 5), (66000, 64), (300000, 255), (4097, 256), (1000, 333),
+                                       (2500, 1024), (40000, 2001), (20000, 4096), (8192, 8192), (3000, 9001),
+                                       (131, 16384), (2000, 16384), (513, 20000), (1, 70001)])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("gap", [0, 1])
+def test_every_row_counts_once_in_the_sums(rows, cols, dtype, gap):
+    """x at a distance of 1 / rstd from its mean, whole gradients from 1 to 7: products and sums
+    below 2^24 are exact in any order, and a row that is lost or taken twice shows."""
+    print(f"CASE layer norm sums {rows} x {cols} {dtype} gap {gap}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(19)
+    t = tg.torch_dtype(dtype)
+
+    def whole(lo, hi, *s):
+        return torch.randint(lo, hi, s, generator=gen, device="cuda", dtype=torch.int32)
+
+    sign, dy, mean, e = (whole(0, 2, rows, cols) * 2 - 1).char(), whole(1, 8, rows, cols).char(), whole(-8, 9, rows), whole(0, 3, rows)
+    x = torch.zeros(rows, cols + gap, dtype=t, device="cuda")[:, :cols]
+    g = torch.zeros(rows, cols + gap, dtype=t, device="cuda")[:, :cols]
+    x.copy_(mean[:, None] + (sign << e[:, None]))
+    g.copy_(dy)
+    w = torch.ones(cols, device="cuda")
+    dw, db = tg.layer_norm_backward(g, x, w, mean.float(), torch.exp2(-e.float()))[1:]
+    assert torch.equal(dw, (sign * dy).sum(0, dtype=torch.int64).float())
+    assert torch.equal(db, dy.sum(0, dtype=torch.int64).float())
+
+
+@pytest.mark.parametrize("rows,cols", [(70000, 8), (66000, 64), (300000, 255), (40000, 2001), (20000, 4096)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sums_over_many_rows_as_near_as_their_depth_allows(rows, cols, dtype):
+    """A thread adds at most rows / 256 of its own (a walk takes 256 rows at a time or more where
+    they are this many), then come up to 64 + 4 of its workgroup's and 768 / 32 + 32 of the
+    workgroups'."""
+    x, dy, w, _ = inputs(rows, cols, dtype, "f32", seed=20)
+    _, mean, rstd = tg.layer_norm_forward(x, w)
+    dw, db = tg.layer_norm_backward(dy, x, w, mean, rstd)[1:]
+    bound = L.gamma(rows / 256 + 68 + 56)
+    n = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    for got, terms, what in ((dw, dy.double() * n, "dweight"), (db, dy.double(), "dbias")):
+        true = host(terms.sum(0))
+        close(got, true, bound * host(terms.abs().sum(0)) + L.rounding(np.abs(true), "f32"), what)
