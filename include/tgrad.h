@@ -433,6 +433,7 @@ int64_t tgrad_adamw_state_bytes(int n, const int64_t *numel, const int *dtype, i
  *   weight_decay[n]  of each tensor, >= 0
  *   state_bits       32 or 8
  *   lr, beta1, beta2, eps   lr >= 0, beta in [0, 1), eps >= 0; lr and eps finite
+ *                    (a positive eps below 2^-126 counts as that)
  *   seed             of the 8-bit state's rounding
  *   state            the buffer above; it must outlive the handle. Its contents are neither
  *                    read nor written by this call.

@@ -1,5 +1,6 @@
 // Host side of AdamW over many tensors: the handle, its division of the tensors into
 // workgroups' chunks, and the launches. Kernels and arithmetic: k_adamw.hip.
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -327,7 +328,10 @@ int tgrad_adamw_step(tgrad_adamw_t* h, void* const* weights, const void* const* 
   a.c1 = (float)(1.0 - h->b1);
   a.b2 = (float)h->b2;
   a.c2 = (float)(1.0 - h->b2);
-  a.eps = (float)h->eps;
+  // The reciprocal of a subnormal eps, or of one that rounds to 0, is infinite, and a value
+  // without a gradient so far would become 0 * infinity. Beside any root of v above zero (2^-75
+  // and more) the least normal number is as little as those.
+  a.eps = h->eps > 0.0 && h->eps < FLT_MIN ? FLT_MIN : (float)h->eps;
   for (const auto& l : h->launches) {
     if (!l.chunks) continue;
     AdamwTable tab;

@@ -508,3 +508,16 @@ def test_norm_of_spans_of_several_passes(dtype, offset, numels):
     assert abs(float(out[1]) - coef) <= 1.01 * E * coef
     g[0].reshape(-1)[-1] = math.inf              # the very last value of a span
     assert float(opt.grad_norm(g)[0]) == math.inf
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-37, 1e-39, 1e-45, 1e-60])
+def test_eps_below_fp32s_normal_numbers(bits, eps):
+    """Any eps above zero keeps a value that has had no gradient at its decayed weight, where 0 / 0
+    would lose it, and is nothing beside the root of the others' v."""
+    c = Case([300, 5], "f32", bits=bits, hyper=dict(lr=1e-2, betas=(0.9, 0.999), eps=eps))
+    for _ in range(2):
+        g = c.gradients()
+        g[0][::3] = 0
+        c.checked_step(g)
+    assert all(bool(w.isfinite().all()) for w in c.w)
