@@ -298,9 +298,11 @@ struct Backward {
 // One alone writes dw and db itself, which saves the second launch: up to eight turns of a wave
 // with 8 values a thread (32 x 333 fp32: 8.0 -> 6.5 us a call, but 64 rows 7.9 -> 10.5), else
 // four, of the longest rows two (2 x 16384 bf16 6.7, 8 rows in as many workgroups 9.6, four of
-// them in one 10.1). Few long rows take fewer turns: a turn costs more than their sums do
-// (16384 bf16, four turns, two and one: 16 rows 14.8, 11.5 and 10.3 us; 64 rows 15.4, 13.2 and
-// 14.1; 256 rows 19.9, 19.0 and 22.0).
+// them in one 10.1). Few long rows take fewer turns: a turn costs more than their sums do, up to
+// 32 rows two turns more than one and up to 256 rows four more than two (16384 bf16, four turns,
+// two and one: 16 rows 14.8, 11.5 and 10.3 us; 64 rows 15.4, 13.2 and 14.1; four and two: 192
+// rows 19.4 and 17.6, 256 20.1 and 19.1, 384 20.1 and 22.0; 8192 bf16 11.7 and 11.4, 12.4 and
+// 12.7, 13.9 and 14.4).
 // Without dw and db there is nothing to add up, and every row that finds a place has its own
 // (512 x 8192 bf16: 8.4 -> 6.6 us; 4 rows 6.6 -> 4.5).
 struct BackwardGroups {
@@ -313,7 +315,7 @@ struct BackwardGroups {
     const uint32_t held = LN_CUS * (ln_backward_waves(LANES, NV) / (threads / 64)), most = held < 768 ? held : 768;
     if (!params) n = ln_walk(rows, kRows, most);
     else if (rows <= kRows * (LANES && NV == 8 ? 8 : LANES || NV == 8 ? 4 : 2)) n = rows > 0;
-    else n = ln_walk(rows, kRows * (LANES || rows > 128 ? 4 : rows > 32 ? 2 : 1), most);
+    else n = ln_walk(rows, kRows * (LANES || rows > 256 ? 4 : rows > 32 ? 2 : 1), most);
   }
 };
 

@@ -449,3 +449,10 @@ def test_sums_over_many_rows_as_near_as_their_depth_allows(rows, cols, dtype):
     for got, terms, what in ((dw, dy.double() * n, "dweight"), (db, dy.double(), "dbias")):
         true = host(terms.sum(0))
         close(got, true, bound * host(terms.abs().sum(0)) + L.rounding(np.abs(true), "f32"), what)
+
+
+@pytest.mark.parametrize("rows", [255, 256, 257])
+@pytest.mark.parametrize("cols", [2050, 9001, 16384])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_some_hundred_long_rows(rows, cols, dtype):
+    check(*inputs(rows, cols, dtype, "f32", seed=21), dtype, "f32")
