@@ -7,7 +7,8 @@
 // to 16384 columns are held by as many waves as they need, which meet in LDS once for each
 // sum. A workgroup walks over rows: the weight and the bias stay in registers, and the next row
 // is loaded while the sums of this one are formed. Longer rows are read again from the cache for
-// each sum.
+// each sum, by one workgroup each (3000 x 32768 bf16: forward 114 us, 3.4 TB/s of what it needs;
+// backward 319, 1.8 TB/s).
 //
 // Every access is 16 bytes wide, at the element's alignment, which the hardware takes for
 // global memory: rows start anywhere (odd column counts, strides). Where the columns do not
@@ -58,8 +59,8 @@ __device__ __forceinline__ void store_piece(T* __restrict__ p, const float* x) {
 
 // How the columns of a row divide: into whole pieces; with a last piece moved back; less than
 // one piece, which is read and written value by value; or, of rows of 16-bit values that several
-// waves hold and some of which start at odd ones, as RAGGED but read by whole words. Accesses off
-// the words cost about twice as much (33M fp16 values: 4099 columns forward 30 -> 27 us, 2001
+// waves hold and some of which start at odd ones, as RAGGED but read by whole words: loads off the
+// words make 15 to 25% of a call (33M fp16 values: 4099 columns forward 30 -> 25 us, 2001
 // backward 59 -> 50, 12001 76 -> 58; rows that a wave holds gain nothing, 255 columns 44 -> 48).
 enum Columns { WHOLE = 0, RAGGED = 1, TINY = 2, ODD = 3 };
 constexpr bool ln_moves(int columns) { return columns == RAGGED || columns == ODD; }

@@ -8,13 +8,15 @@ import tensor_gradient_compression_amd as _tg
 def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5):
     """(y, mean, rstd) of x (float32, float16 or bfloat16; the last axis contiguous, the
     leading ones evenly spaced). weight, bias: None, or one value per column in float32 or
-    x's type. mean and rstd are float32, of x's shape without the last axis."""
+    x's type. mean and rstd are float32, of x's shape without the last axis. Autograd records
+    nothing of this call, whatever its inputs require: layer_norm is the differentiable one."""
     return _tg.binding().layer_norm_forward(x, weight, bias, eps)
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, params: bool = True):
     """(dx, dweight, dbias) from forward's inputs and statistics; dweight and dbias in the
-    weight's type (x's without a weight), None where params is false."""
+    weight's type (x's without a weight), None where params is false. Autograd records nothing
+    of this call."""
     return _tg.binding().layer_norm_backward(dy, x, weight, mean, rstd, params)
 
 
@@ -50,5 +52,6 @@ def _layer_norm_function():
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
-    """y = (x - mean) / sqrt(var + eps) * weight + bias over the last axis, with gradients."""
+    """y = (x - mean) / sqrt(var + eps) * weight + bias over the last axis, with gradients (of
+    the first order, in reverse mode). Inputs as those of layer_norm_forward."""
     return _layer_norm_function().apply(x, weight, bias, eps)
