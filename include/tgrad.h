@@ -427,7 +427,7 @@ int64_t tgrad_adamw_state_bytes(int n, const int64_t *numel, const int *dtype, i
 
 /*
  * Create a handle on the current HIP device for n >= 1 tensors (synchronises the device).
- *   numel[n]         elements of each, >= 0
+ *   numel[n]         elements of each, >= 0; at most 2^27 pieces of 2048 values in all
  *   dtype[n]         enum tgrad_dtype of the weights
  *   grad_dtype[n]    of the gradients: the weight's, or TGRAD_F32 for a 16-bit weight
  *   weight_decay[n]  of each tensor, >= 0

@@ -55,6 +55,10 @@ constexpr uint32_t kStreamLds = 80 * 1024;
 // do, is cut to the rest without an error.
 constexpr uint32_t kLaunchChunks = 1 << 21;
 
+// Chunks of a handle, for each of which the host makes a record of 80 bytes: more values than any
+// card holds a state of.
+constexpr uint64_t kMostChunks = 1 << 27;
+
 constexpr size_t kCountBytes = (ADAMW_COUNTS + 1) * ADAMW_COUNT_PITCH * sizeof(uint32_t);
 
 struct OnDevice {
@@ -136,7 +140,11 @@ int tgrad_adamw_init(tgrad_adamw_t** out, int n, const int64_t* numel, const int
       !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0 && std::isfinite(eps)))
     return TGRAD_EINVAL;
   if ((total > 0 && !state) || ((uintptr_t)state & 15u) != 0) return TGRAD_EINVAL;
+  uint64_t pieces = 0;
   for (int i = 0; i < n; ++i) {
+    const uint64_t values = (uint64_t)numel[i] * (dtype[i] == TGRAD_C64 ? 2 : 1);
+    pieces += (values + ADAMW_CHUNK - 1) / ADAMW_CHUNK;
+    if (pieces > kMostChunks) return TGRAD_EINVAL;
     const bool half = dtype[i] == TGRAD_F16 || dtype[i] == TGRAD_BF16;
     if (grad_dtype[i] != dtype[i] && !(half && grad_dtype[i] == TGRAD_F32)) return TGRAD_EINVAL;
     if (!(weight_decay[i] >= 0.0 && std::isfinite(weight_decay[i]))) return TGRAD_EINVAL;
@@ -206,10 +214,6 @@ int tgrad_adamw_init(tgrad_adamw_t** out, int n, const int64_t* numel, const int
       for (uint64_t s = 0; s < t.values; s += size)
         spans.push_back({s, (uint32_t)i, (uint32_t)(t.values - s < size ? t.values - s : size), c.gdt});
       if (i == 0 && chunks.empty()) chunks.push_back(c);   // the step count needs a keeper
-      if (chunks.size() > (1u << 30)) {
-        delete h;
-        return TGRAD_EINVAL;
-      }
       up_to_here(h->launches.back());
       h->tensors.push_back(t);
       bytes += t.values * (16 + (c.wdt == DT_F32 ? 8 : 4) + (c.gdt == DT_F32 ? 4 : 2));

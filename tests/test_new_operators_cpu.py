@@ -185,3 +185,12 @@ def test_the_library_builds_without_what_the_binding_needs(lacks, tmp_path, monk
             build.build()
     assert ctypes.CDLL(build.LIB).one() == 1
     assert not os.path.exists(build.BINDING)
+
+
+@pytest.mark.parametrize("numel,dtype", [([1 << 40], 0), ([1 << 40], 3), ([1 << 38, 1], 2), ([1 << 39] * 4, 1)])
+def test_adamw_init_refuses_more_than_a_card_could_hold(lib, numel, dtype):
+    """Before tables of 80 bytes for every 2048 values take the host's memory."""
+    h, n = P(1), len(numel)
+    rc = lib.tgrad_adamw_init(ctypes.byref(h), n, arr(I64, numel), arr(INT, [dtype] * n), arr(INT, [dtype] * n),
+                              arr(DBL, [0.0] * n), 8, 1e-3, 0.9, 0.99, 1e-8, 0, P(4096))
+    assert rc == tg.EINVAL and not h.value
