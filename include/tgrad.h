@@ -511,6 +511,120 @@ int tgrad_layer_norm_backward(const void *dy, int64_t dy_stride, const void *x, 
                               void *dweight, void *dbias, int64_t rows, int64_t cols, int dtype,
                               int weight_dtype, void *workspace, void *stream);
 
+/* ---------------------------------------------------------------- matrices.
+ * The products of a model's blocks, beside the tensors above: an optimizer for matrices and
+ * the gated layer whose two weights are such matrices.
+ *
+ * Newton-Schulz orthogonalisation: with coefficients (a, b, c),
+ *   X = U / (|U| + eps), |U| the root of the sum of squares; `steps` times:
+ *   A = X X^T,  X = a X + (b A + c A A) X      (rows > cols: the same of the transpose)
+ * which brings X's singular values near 1. (3.4445, -4.7750, 2.0315) and 5 steps are usual.
+ * The products take fp16 parts of X, A and B = b A + c A A with fp32 sums, held under 2^12
+ * (X) and 2^8: matrices whose X or B leave +-16 or +-256 in some step overflow, which with the
+ * usual coefficients none do. X is carried in 22 bits between the steps. bf16 results come from
+ * products of the upper parts (11 bits), 3e-4 to 2e-3 of the result's norm off before they are
+ * rounded; fp32 and fp16 results from products of both parts, 3e-7 to 1e-5. A matrix of zeros
+ * stays one (where eps > 0); one with a value that is not finite becomes NaN.
+ *
+ * tgrad_orthogonalize: `count` matrices of rows x cols values.
+ *   x          device, matrices matrix_stride and their rows row_stride >= cols elements apart
+ *   out        device, contiguous, of x's type; may be x where that is contiguous
+ *   dtype      TGRAD_F32, TGRAD_F16 or TGRAD_BF16
+ *   steps      1 to 100;  coefficients: host, three finite values;  eps >= 0, finite
+ *   workspace  device, tgrad_orthogonalize_workspace bytes, 16-byte aligned. It may be reused
+ *              once the stream's work is done.
+ * count = 0 is valid. 1 <= rows, cols <= 2^19, and at most 2^21 workgroups' parts in a launch.
+ * Errors: TGRAD_EINVAL, TGRAD_EHIP. The workspace's size is -1 for invalid sizes (host only). */
+int64_t tgrad_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols, int dtype);
+int tgrad_orthogonalize(const void *x, int64_t matrix_stride, int64_t row_stride, void *out,
+                        int64_t count, int64_t rows, int64_t cols, int dtype, int steps,
+                        const double *coefficients, double eps, void *workspace, void *stream);
+
+/* Muon over many matrices at once. Per tensor (count matrices of rows x cols values, one after
+ * the other), with g' = g * coefficient (see tgrad_adamw_grad_norm; g' = g without a clip):
+ *   m = mu m + (1 - mu) g';   u = (1 - mu) g' + mu m  (nesterov)  or  m
+ *   w <- round(w * decay - lr * scale * orthogonalised(u))
+ * with decay = fp32(1 - lr * weight_decay), and products as for a result of w's type. The
+ * momentum is one flat fp32 buffer of the caller's (tgrad_muon_state_values floats, 16-byte
+ * aligned) in which every tensor's values start at a multiple of 128, zeroed for a new run.
+ * A step is captured and replayed as it is; one handle is used by one host thread and one
+ * stream at a time (its workspace, about 8 bytes a value and 4 or 8 min(rows, cols)^2 bytes a
+ * matrix, is its own). */
+typedef struct tgrad_muon tgrad_muon_t;
+
+/* Floats of the momentum; -1 for invalid sizes. Host only. */
+int64_t tgrad_muon_state_values(int n, const int64_t *count, const int64_t *rows, const int64_t *cols);
+
+/*
+ * Create a handle on the current HIP device for n >= 1 tensors (synchronises the device).
+ *   count, rows, cols [n]   count >= 0, 1 <= rows, cols <= 2^19
+ *   dtype[n]         TGRAD_F32, TGRAD_F16 or TGRAD_BF16 of the weights
+ *   grad_dtype[n]    of the gradients: the weight's, or TGRAD_F32
+ *   weight_decay[n], scale[n]   of each tensor, >= 0 and finite
+ *   lr >= 0, finite;  momentum in [0, 1);  nesterov: 0 or 1
+ *   steps, coefficients, eps    as above
+ *   state            the buffer above; it must outlive the handle. Neither read nor written by
+ *                    this call.
+ * Errors: TGRAD_EINVAL (also more than some 2^21 parts of 8192 values or matrices),
+ * TGRAD_ENOMEM, TGRAD_EHIP. *out is NULL on error.
+ */
+int tgrad_muon_init(tgrad_muon_t **out, int n, const int64_t *count, const int64_t *rows,
+                    const int64_t *cols, const int *dtype, const int *grad_dtype,
+                    const double *weight_decay, const double *scale, double lr, double momentum,
+                    int nesterov, int steps, const double *coefficients, double eps, float *state);
+/* Free the handle's own device memory (the momentum stays the caller's). The caller
+ * synchronises first. NULL is a no-op. */
+int tgrad_muon_destroy(tgrad_muon_t *h);
+const char *tgrad_muon_last_error(const tgrad_muon_t *h);
+/* The learning rate from the next step on (>= 0, finite); a captured step keeps its own. */
+int tgrad_muon_set_lr(tgrad_muon_t *h, double lr);
+/* One step: weights[i] (updated in place) and grads[i] (only read) are contiguous device
+ * buffers, aligned to their elements (both may be NULL where count[i] is 0). clip: NULL, or two
+ * device floats from tgrad_adamw_grad_norm; where the norm clip[0] is not finite the step is
+ * left out on the device. Errors: TGRAD_EINVAL, TGRAD_EHIP. */
+int tgrad_muon_step(tgrad_muon_t *h, void *const *weights, const void *const *grads,
+                    const float *clip, void *stream);
+
+/*
+ * Gated linear layer over `rows` rows of `in` values, to `hidden` values, and its gradients:
+ *   g = x w_gate^T + b_gate,  u = x w_up^T + b_up,  y = act(g) u
+ *   dg = dy u act'(g),  du = dy act(g),  dx = dg w_gate + du w_up
+ *   dw_gate = dg^T x,  dw_up = du^T x,  db = sums over rows of dg and du
+ * act: silu (g / (1 + e^-g)), gelu (g times the normal distribution's probability up to g),
+ * sigmoid or relu (with slope 0 at 0). Sums are fp32, y is rounded once. The gradients form g
+ * and u again from x; 16-bit dg and du are rounded to that type between the products (db comes
+ * from the values before). fp32 products are made of six products of bf16 parts, as exact as
+ * fp32 sums; a value that is not finite makes what it enters NaN there. Results do not depend
+ * on the order in which workgroups run.
+ *   x, dy           device, rows x_stride >= in (dy_stride >= hidden) elements apart
+ *   w_gate, w_up    device, contiguous, hidden rows of in values;  dw_gate, dw_up alike
+ *   b_gate, b_up, db_gate, db_up   device, hidden values;  b: NULL: 0
+ *   y, dx           device, contiguous; no result overlaps an input
+ *   dx, the dw and the db may be NULL, the latter in pairs
+ *   dtype           TGRAD_F32, TGRAD_F16 or TGRAD_BF16, of all of them
+ *   workspace       device, tgrad_gated_linear_workspace bytes, 16-byte aligned (NULL for 0).
+ *                   It may be reused once the stream's work is done.
+ * The workspace's size is that of a call with the same x, strides and weights, whose alignment
+ * matters (rows that are not 16-byte aligned or no multiple of 8 values are copied); backward: 0
+ * or 1; -1 for invalid sizes. Host only.
+ * rows = 0 is valid (the weights' gradients become 0). 1 <= in, hidden <= 2^19. Every pointer
+ * is aligned to its element. Errors: TGRAD_EINVAL, TGRAD_EHIP.
+ */
+enum tgrad_activation { TGRAD_SILU = 0, TGRAD_GELU = 1, TGRAD_SIGMOID = 2, TGRAD_RELU = 3 };
+int64_t tgrad_gated_linear_workspace(const void *x, int64_t x_stride, const void *w_gate,
+                                     const void *w_up, int64_t rows, int64_t in, int64_t hidden,
+                                     int dtype, int backward);
+int tgrad_gated_linear_forward(const void *x, int64_t x_stride, const void *w_gate,
+                               const void *w_up, const void *b_gate, const void *b_up, void *y,
+                               int64_t rows, int64_t in, int64_t hidden, int dtype,
+                               int activation, void *workspace, void *stream);
+int tgrad_gated_linear_backward(const void *dy, int64_t dy_stride, const void *x, int64_t x_stride,
+                                const void *w_gate, const void *w_up, const void *b_gate,
+                                const void *b_up, void *dx, void *dw_gate, void *dw_up,
+                                void *db_gate, void *db_up, int64_t rows, int64_t in,
+                                int64_t hidden, int dtype, int activation, void *workspace,
+                                void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -7,7 +7,9 @@ missing; there is no CPU fallback.
 
 TGrad and step_many optimise large weight tensors in a compressed space; AdamW steps all the
 other tensors of a model at once; layer_norm (and its two parts, layer_norm_forward and
-layer_norm_backward) is the normalisation whose small weights are among those.
+layer_norm_backward) is the normalisation whose small weights are among those. Muon steps a
+model's matrices by their orthogonalised momentum (orthogonalize on its own); gated_linear (and
+its parts) is the layer of two such matrices.
 """
 from __future__ import annotations
 
@@ -124,6 +126,30 @@ SIGNATURES = [
     ("tgrad_layer_norm_workspace", _I64, [_I64, _I64]),
     ("tgrad_layer_norm_backward", ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _I64,
                                                  _I64, ctypes.c_int, ctypes.c_int, _P, _P]),
+    ("tgrad_orthogonalize_workspace", _I64, [_I64, _I64, _I64, ctypes.c_int]),
+    ("tgrad_orthogonalize", ctypes.c_int, [_P, _I64, _I64, _P, _I64, _I64, _I64, ctypes.c_int,
+                                           ctypes.c_int, ctypes.POINTER(ctypes.c_double),
+                                           ctypes.c_double, _P, _P]),
+    ("tgrad_muon_state_values", _I64, [ctypes.c_int, ctypes.POINTER(_I64), ctypes.POINTER(_I64),
+                                       ctypes.POINTER(_I64)]),
+    ("tgrad_muon_init", ctypes.c_int, [ctypes.POINTER(_P), ctypes.c_int, ctypes.POINTER(_I64),
+                                       ctypes.POINTER(_I64), ctypes.POINTER(_I64),
+                                       ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int),
+                                       ctypes.POINTER(ctypes.c_double),
+                                       ctypes.POINTER(ctypes.c_double), ctypes.c_double,
+                                       ctypes.c_double, ctypes.c_int, ctypes.c_int,
+                                       ctypes.POINTER(ctypes.c_double), ctypes.c_double, _P]),
+    ("tgrad_muon_destroy", ctypes.c_int, [_P]),
+    ("tgrad_muon_last_error", ctypes.c_char_p, [_P]),
+    ("tgrad_muon_set_lr", ctypes.c_int, [_P, ctypes.c_double]),
+    ("tgrad_muon_step", ctypes.c_int, [_P, ctypes.POINTER(_P), ctypes.POINTER(_P), _P, _P]),
+    ("tgrad_gated_linear_workspace", _I64, [_P, _I64, _P, _P, _I64, _I64, _I64, ctypes.c_int,
+                                            ctypes.c_int]),
+    ("tgrad_gated_linear_forward", ctypes.c_int, [_P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I64,
+                                                  ctypes.c_int, ctypes.c_int, _P, _P]),
+    ("tgrad_gated_linear_backward", ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P,
+                                                   _P, _P, _I64, _I64, _I64, ctypes.c_int,
+                                                   ctypes.c_int, _P, _P]),
 ]
 
 
@@ -513,4 +539,6 @@ def to_host(t, dtype: str) -> np.ndarray:
 
 
 from .adamw import AdamW  # noqa: E402
+from .gated import gated_linear, gated_linear_backward, gated_linear_forward  # noqa: E402
 from .layernorm import layer_norm, layer_norm_backward, layer_norm_forward  # noqa: E402
+from .muon import Muon, orthogonalize  # noqa: E402

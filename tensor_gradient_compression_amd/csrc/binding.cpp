@@ -1,4 +1,5 @@
-// Python side of the operators on lists of tensors and of layer norm: unpacks torch tensors,
+// Python side of the operators on lists of tensors, of layer norm, the gated linear layer and
+// orthogonalisation: unpacks torch tensors,
 // checks them against what the library will read and write, and calls the C functions of
 // tgrad.h on the current stream. A step over some hundred small tensors takes the GPU less
 // time than interpreted checks of each of them would take the host, so they are made here.
@@ -11,6 +12,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
+#include <memory>
 #include <string>
 #include <vector>
 
@@ -38,6 +40,7 @@ c10::ScalarType scalar_type(int code) {
 
 struct Plan {
   tgrad_adamw_t* h = nullptr;
+  tgrad_muon_t* muon = nullptr;
   int device = 0, bits = 32;
   int64_t total = 0;
   std::vector<int64_t> numel;
@@ -47,11 +50,13 @@ struct Plan {
 };
 
 const char* kPlan = "tgrad.adamw_plan";
+const char* kMuonPlan = "tgrad.muon_plan";
 
 void free_plan(PyObject* cap) { delete (Plan*)PyCapsule_GetPointer(cap, kPlan); }
+void free_muon_plan(PyObject* cap) { delete (Plan*)PyCapsule_GetPointer(cap, kMuonPlan); }
 
-Plan* plan_of(PyObject* cap) {
-  Plan* p = (Plan*)PyCapsule_GetPointer(cap, kPlan);
+Plan* plan_of(PyObject* cap, const char* kind = kPlan) {
+  Plan* p = (Plan*)PyCapsule_GetPointer(cap, kind);
   if (!p) throw Raised{};
   return p;
 }
@@ -187,6 +192,21 @@ PyObject* adamw_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+void weights_of(Plan* p, const Sequence& ws) {
+  if (ws.size() != (long)p->numel.size())
+    throw Invalid{"weights: " + std::to_string(ws.size()) + " tensors, the handle has " +
+                  std::to_string(p->numel.size())};
+  for (long i = 0; i < ws.size(); ++i) {
+    const at::Tensor& t = tensor(ws[i], "weights", i);
+    on_gpu(t, p->wt[i], p->device, "weights", i);
+    if (t.numel() != p->numel[i])
+      throw Invalid{named("weights", i) + ": " + std::to_string(t.numel()) + " elements, expected " +
+                    std::to_string(p->numel[i])};
+    if (!t.is_contiguous()) throw Invalid{named("weights", i) + ": must be contiguous"};
+    p->w[i] = data_of(t);
+  }
+}
+
 void gradients(Plan* p, PyObject* list) {
   Sequence s(list, "grads: expected a list of tensors");
   if (s.size() != (long)p->numel.size())
@@ -217,18 +237,7 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     want(n, 6, "adamw_step");
     Plan* p = plan_of(a[0]);
     Sequence ws(a[1], "weights: expected a list of tensors");
-    if (ws.size() != (long)p->numel.size())
-      throw Invalid{"weights: " + std::to_string(ws.size()) + " tensors, the handle has " +
-                    std::to_string(p->numel.size())};
-    for (long i = 0; i < ws.size(); ++i) {
-      const at::Tensor& t = tensor(ws[i], "weights", i);
-      on_gpu(t, p->wt[i], p->device, "weights", i);
-      if (t.numel() != p->numel[i])
-        throw Invalid{named("weights", i) + ": " + std::to_string(t.numel()) + " elements, expected " +
-                      std::to_string(p->numel[i])};
-      if (!t.is_contiguous()) throw Invalid{named("weights", i) + ": must be contiguous"};
-      p->w[i] = data_of(t);
-    }
+    weights_of(p, ws);
     gradients(p, a[2]);
     const float* clip = a[3] == Py_None ? nullptr : pair_of_floats(p, a[3], "clip");
     void* out[2] = {nullptr, nullptr};
@@ -411,6 +420,188 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// muon_plan(handle, device, numels, dtype codes, gradient dtype codes)
+PyObject* muon_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want(n, 5, "muon_plan");
+    std::vector<int64_t> wt = ints(a[3], "dtypes"), gt = ints(a[4], "grad dtypes");
+    std::unique_ptr<Plan> p(new Plan());
+    p->muon = (tgrad_muon_t*)PyLong_AsVoidPtr(a[0]);
+    p->device = (int)PyLong_AsLong(a[1]);
+    if (PyErr_Occurred()) throw Raised{};
+    p->numel = ints(a[2], "numels");
+    for (int64_t c : wt) p->wt.push_back(scalar_type((int)c));
+    for (int64_t c : gt) p->gt.push_back(scalar_type((int)c));
+    p->w.resize(p->numel.size());
+    p->g.resize(p->numel.size());
+    PyObject* cap = PyCapsule_New(p.get(), kMuonPlan, free_muon_plan);
+    if (cap) (void)p.release();
+    return cap;
+  });
+}
+
+// muon_step(plan, weights, grads, clip or None, stream or None)
+PyObject* muon_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want(n, 5, "muon_step");
+    Plan* p = plan_of(a[0], kMuonPlan);
+    Sequence ws(a[1], "weights: expected a list of tensors");
+    weights_of(p, ws);
+    gradients(p, a[2]);
+    const float* clip = a[3] == Py_None ? nullptr : pair_of_floats(p, a[3], "clip");
+    check_rc(tgrad_muon_step(p->muon, p->w.data(), p->g.data(), clip, pointer(a[4], p->device)), "tgrad_muon_step",
+             tgrad_muon_last_error(p->muon));
+    for (long i = 0; i < ws.size(); ++i) changed(THPVariable_Unpack(ws[i]));
+    Py_RETURN_NONE;
+  });
+}
+
+// orthogonalize(x, steps, a, b, c, eps) -> a tensor like x
+PyObject* orthogonalize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want(n, 6, "orthogonalize");
+    const at::Tensor& x = tensor(a[0], "x");
+    const int dt = code_of(x, "x");
+    on_gpu(x, x.scalar_type(), -1, "x");
+    const int dev = (int)x.get_device();
+    const int64_t d = x.dim();
+    if (d < 2) throw Invalid{"x: needs at least two axes"};
+    const int64_t rows = x.size(d - 2), cols = x.size(d - 1);
+    int64_t count = 1, stride = 0, span = -1;
+    for (int64_t i = 0; i < d - 2; ++i) count *= x.size(i);
+    if (rows < 1 || cols < 1) throw Invalid{"x: its matrices are empty"};
+    if (count > 0) {
+      if (cols > 1 && x.stride(d - 1) != 1) throw Invalid{"x: the last axis must be contiguous"};
+      if (rows > 1 && x.stride(d - 2) < cols) throw Invalid{"x: the rows overlap; call contiguous()"};
+      for (int64_t i = d - 3; i >= 0; --i) {   // the matrices have to lie evenly
+        if (x.size(i) == 1) continue;
+        if (span < 0) stride = x.stride(i);
+        else if (x.stride(i) != span)
+          throw Invalid{"x: the leading axes' strides do not form one; call contiguous()"};
+        span = x.stride(i) * x.size(i);
+      }
+    }
+    const int64_t row = rows > 1 ? x.stride(d - 2) : cols;
+    if (count > 1 && stride < (rows - 1) * row + cols) throw Invalid{"x: the matrices overlap; call contiguous()"};
+    const long steps = PyLong_AsLong(a[1]);
+    const double co[3] = {PyFloat_AsDouble(a[2]), PyFloat_AsDouble(a[3]), PyFloat_AsDouble(a[4])};
+    const double eps = PyFloat_AsDouble(a[5]);
+    if (PyErr_Occurred()) throw Raised{};
+    if (steps < 1 || steps > 100) throw Invalid{"steps: 1 to 100"};
+    const int64_t bytes = tgrad_orthogonalize_workspace(count, rows, cols, dt);
+    if (bytes < 0) throw Invalid{"x: too many rows, columns or matrices"};
+    const c10::DeviceGuard guard(x.device());
+    at::Tensor out = empty(x.sizes(), x.scalar_type(), dev), ws = empty({bytes}, at::kByte, dev);
+    check_rc(tgrad_orthogonalize(data_of(x), stride, row, data_of(out), count, rows, cols, dt, (int)steps, co, eps,
+                                 data_of(ws), pointer(Py_None, dev)),
+             "tgrad_orthogonalize", "");
+    return THPVariable_Wrap(out);
+  });
+}
+
+// What both directions of the gated linear layer take.
+struct Gated {
+  int dt = 0, dev = 0, act = 0;
+  Rows r;
+  int64_t hidden = 0;
+  const at::Tensor *x = nullptr, *w[2] = {}, *b[2] = {};
+};
+Gated gated_of(PyObject* x, PyObject* const* weights, PyObject* const* biases, PyObject* act) {
+  Gated g;
+  g.x = &tensor(x, "x");
+  g.dt = code_of(*g.x, "x");
+  on_gpu(*g.x, g.x->scalar_type(), -1, "x");
+  g.dev = (int)g.x->get_device();
+  g.r = rows_of(*g.x, "x");
+  for (int i = 0; i < 2; ++i) {
+    const char* what = i ? "w_up" : "w_gate";
+    g.w[i] = &tensor(weights[i], what);
+    on_gpu(*g.w[i], g.x->scalar_type(), g.dev, what);
+    if (g.w[i]->dim() != 2 || g.w[i]->size(1) != g.r.cols || g.w[i]->size(0) < 1)
+      throw Invalid{std::string(what) + ": needs the shape (hidden, " + std::to_string(g.r.cols) + ")"};
+    if (!g.w[i]->is_contiguous()) throw Invalid{std::string(what) + ": must be contiguous"};
+  }
+  g.hidden = g.w[0]->size(0);
+  if (g.w[1]->size(0) != g.hidden) throw Invalid{"w_up: its shape is not w_gate's"};
+  for (int i = 0; i < 2; ++i) {
+    g.b[i] = vector_of(biases[i], g.hidden, g.dev, i ? "b_up" : "b_gate");
+    if (g.b[i] && g.b[i]->scalar_type() != g.x->scalar_type())
+      throw Invalid{std::string(i ? "b_up" : "b_gate") + ": dtype differs from x's"};
+  }
+  g.act = (int)PyLong_AsLong(act);
+  if (PyErr_Occurred()) throw Raised{};
+  return g;
+}
+const void* data_or_null(const at::Tensor* t) { return t ? data_of(*t) : nullptr; }
+
+at::Tensor gated_workspace(const Gated& g, int backward) {
+  const int64_t bytes = tgrad_gated_linear_workspace(data_of(*g.x), g.r.stride, data_of(*g.w[0]), data_of(*g.w[1]),
+                                                     g.r.rows, g.r.cols, g.hidden, g.dt, backward);
+  if (bytes < 0) throw Invalid{"x: too many rows or columns"};
+  return bytes ? empty({bytes}, at::kByte, g.dev) : at::Tensor();
+}
+
+// gated_linear_forward(x, w_gate, w_up, b_gate or None, b_up or None, activation) -> y
+PyObject* gated_linear_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want(n, 6, "gated_linear_forward");
+    const Gated g = gated_of(a[0], a + 1, a + 3, a[5]);
+    const c10::DeviceGuard guard(g.x->device());
+    std::vector<int64_t> sizes(g.x->sizes().begin(), g.x->sizes().end());
+    sizes.back() = g.hidden;
+    at::Tensor y = empty(sizes, g.x->scalar_type(), g.dev), ws = gated_workspace(g, 0);
+    check_rc(tgrad_gated_linear_forward(data_of(*g.x), g.r.stride, data_of(*g.w[0]), data_of(*g.w[1]),
+                                        data_or_null(g.b[0]), data_or_null(g.b[1]), data_of(y), g.r.rows, g.r.cols,
+                                        g.hidden, g.dt, g.act, ws.defined() ? data_of(ws) : nullptr,
+                                        pointer(Py_None, g.dev)),
+             "tgrad_gated_linear_forward", "");
+    return THPVariable_Wrap(y);
+  });
+}
+
+// gated_linear_backward(dy, x, w_gate, w_up, b_gate or None, b_up or None, activation, need dx, need the weights',
+// need the biases') -> (dx, dw_gate, dw_up, db_gate, db_up), None for what is not needed
+PyObject* gated_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want(n, 10, "gated_linear_backward");
+    const Gated g = gated_of(a[1], a + 2, a + 4, a[6]);
+    const at::Tensor& dy = tensor(a[0], "dy");
+    on_gpu(dy, g.x->scalar_type(), g.dev, "dy");
+    bool same = dy.dim() == g.x->dim();
+    for (int64_t i = 0; same && i < dy.dim(); ++i)
+      same = dy.size(i) == (i == dy.dim() - 1 ? g.hidden : g.x->size(i));
+    if (!same) throw Invalid{"dy: its shape is not y's"};
+    const Rows rd = rows_of(dy, "dy");
+    int need[3];
+    for (int i = 0; i < 3; ++i)
+      if ((need[i] = PyObject_IsTrue(a[7 + i])) < 0) throw Raised{};
+    const c10::DeviceGuard guard(g.x->device());
+    at::Tensor out[5];
+    const auto type = g.x->scalar_type();
+    if (need[0]) out[0] = empty(g.x->sizes(), type, g.dev);
+    for (int i = 0; i < 2; ++i) {
+      if (need[1]) out[1 + i] = empty({g.hidden, g.r.cols}, type, g.dev);
+      if (need[2]) out[3 + i] = empty({g.hidden}, type, g.dev);
+    }
+    at::Tensor ws = gated_workspace(g, 1);
+    void* p[5];
+    for (int i = 0; i < 5; ++i) p[i] = out[i].defined() ? data_of(out[i]) : nullptr;
+    check_rc(tgrad_gated_linear_backward(data_of(dy), rd.stride, data_of(*g.x), g.r.stride, data_of(*g.w[0]),
+                                         data_of(*g.w[1]), data_or_null(g.b[0]), data_or_null(g.b[1]), p[0], p[1], p[2],
+                                         p[3], p[4], g.r.rows, g.r.cols, g.hidden, g.dt, g.act,
+                                         ws.defined() ? data_of(ws) : nullptr, pointer(Py_None, g.dev)),
+             "tgrad_gated_linear_backward", "");
+    PyObject* t = PyTuple_New(5);
+    if (!t) throw Raised{};
+    for (int i = 0; i < 5; ++i) {
+      PyObject* o = out[i].defined() ? THPVariable_Wrap(out[i]) : Py_None;
+      if (o == Py_None) Py_INCREF(o);
+      PyTuple_SET_ITEM(t, i, o);
+    }
+    return t;
+  });
+}
+
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {{"set_error", set_error, METH_O, nullptr},
                           FAST(adamw_plan),
@@ -418,6 +609,11 @@ PyMethodDef kMethods[] = {{"set_error", set_error, METH_O, nullptr},
                           FAST(adamw_grad_norm),
                           FAST(layer_norm_forward),
                           FAST(layer_norm_backward),
+                          FAST(muon_plan),
+                          FAST(muon_step),
+                          FAST(orthogonalize),
+                          FAST(gated_linear_forward),
+                          FAST(gated_linear_backward),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_tgrad_torch", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,133 @@
+// Gated linear layer: what the host side (gated.hip) and the kernels (k_gated.hip,
+// k_gated_bwd.hip) share. gfx950 only.
+#pragma once
+#include "mm_tile.h"
+
+namespace tg {
+
+enum GatedAct { GATED_SILU = 0, GATED_GELU, GATED_SIGMOID, GATED_RELU, GATED_ACTS };
+
+// A matrix in the parts that the products take: one of its own 16-bit values, or three of bf16
+// that add up to an fp32 value, `part` values apart.
+struct GatedParts {
+  const void* p;
+  int64_t lines, part;
+  uint32_t len, stride;
+};
+// Products of parts, the smallest first: A's and B's part of segment s (of 6; the last alone
+// for 16-bit values).
+constexpr uint32_t GATED_PART_A = 0x001102, GATED_PART_B = 0x010120;
+
+__host__ __device__ inline uint32_t gated_pad(uint32_t n) { return (n + 7u) & ~7u; }
+
+// Copies of rows whose lines are not 16-byte aligned (16 bits), or their parts (fp32).
+struct GatedPack {
+  const void* src;
+  int64_t rows, stride;
+  uint32_t cols;
+  int dt;
+  void* dst;          // rows of gated_pad(cols) values, zeros behind; fp32: three times
+};
+hipError_t launch_gated_pack(const GatedPack* a, int n, hipStream_t s);
+
+struct GatedArgs {
+  GatedParts x, wg, wu;
+  const void* bg;      // may be NULL: 0
+  const void* bu;
+  int64_t rows;
+  uint32_t in, hidden;
+  int dt, act;
+  // forward
+  void* y;
+  // backward: dg and du side by side, rows of 2 gated_pad(hidden) values (fp32: three times)
+  const void* dy;
+  int64_t dy_stride;
+  void* grads;
+  float* row_sums;     // or NULL: sums of dg and du over a tile's rows, as rows of 2 gated_pad(hidden)
+};
+hipError_t launch_gated_forward(const GatedArgs& a, hipStream_t s);
+hipError_t launch_gated_grads(const GatedArgs& a, hipStream_t s);
+// rows of row_sums
+int64_t gated_sum_rows(int64_t rows, uint32_t in, uint32_t hidden);
+
+// dx = dg Wg + du Wu
+struct GatedDx {
+  GatedParts grads, wg, wu;
+  void* dx;
+  int64_t rows;
+  uint32_t in, hidden;
+  int dt;
+  float* partial;      // gated_dx_splits() sums of rows x in, if more than one
+};
+int gated_dx_splits(int64_t rows, uint32_t in, uint32_t hidden);
+hipError_t launch_gated_dx(const GatedDx& a, hipStream_t s);
+
+// dWg = dg^T x, dWu = du^T x, and the biases' gradients
+struct GatedDw {
+  GatedParts grads, x;
+  void* dwg;
+  void* dwu;
+  void* dbg;           // may be NULL, together
+  void* dbu;
+  const float* row_sums;
+  int64_t sum_rows;
+  int64_t rows;
+  uint32_t in, hidden;
+  int dt;
+  float* partial;      // gated_dw_splits() sums of 2 gated_pad(hidden) x in, if more than one
+};
+int gated_dw_splits(int64_t rows, uint32_t in, uint32_t hidden);
+hipError_t launch_gated_dw(const GatedDw& a, hipStream_t s);
+
+// The tile of a product: 0: 256 x 256, 1: 128 x 128, 2: 64 x 64.
+int gated_tile(int64_t ni, int64_t nj);
+
+template <int DT> struct GatedType;
+template <> struct GatedType<DT_F32> { using T = float; static constexpr int MM = DT_BF16, SEGS = 6; };
+template <> struct GatedType<DT_F16> { using T = _Float16; static constexpr int MM = DT_F16, SEGS = 1; };
+template <> struct GatedType<DT_BF16> { using T = bf16_t; static constexpr int MM = DT_BF16, SEGS = 1; };
+
+// Segment s of SEGS: a part of a matrix from k0 on.
+template <int SEGS>
+__device__ __forceinline__ MmOperand gated_operand(const GatedParts& m, uint32_t parts, int s, int64_t k0, bool crossed) {
+  const uint32_t part = (parts >> (4 * (SEGS == 1 ? 5 : s))) & 3u;
+  MmOperand o;
+  o.p = (const char*)m.p + (int64_t)part * m.part * 2 + (crossed ? k0 * m.stride : k0) * 2;
+  o.lines = crossed ? m.lines - k0 : m.lines;
+  o.len = crossed ? m.len : m.len - (uint32_t)k0;
+  o.stride = m.stride;
+  return o;
+}
+
+// A value as three of bf16 that add up to it: each the nearest to what is left, so that the
+// second is 2^-8 and the third 2^-16 of the value at most. The first of one that is not finite
+// holds it; one that would round to infinity is cut instead.
+__device__ __forceinline__ void three_parts(float x, bf16_t* p) {
+  p[0] = from_f32<bf16_t>(x);
+  if ((p[0].b & 0x7F80u) == 0x7F80u) {
+    const uint32_t b = __float_as_uint(x);
+    if ((b & 0x7F800000u) == 0x7F800000u) {
+      p[1].b = p[2].b = 0;
+      return;
+    }
+    p[0].b = (uint16_t)(b >> 16);
+  }
+  const float r = x - to_f32(p[0]);   // exact, as the next
+  p[1] = from_f32<bf16_t>(r);
+  p[2] = from_f32<bf16_t>(r - to_f32(p[1]));
+}
+
+// n of 4 values to p
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const T* v, int n, bool vec) {
+  if (vec) {
+    if constexpr (sizeof(T) == 4) *(f32x4*)p = *(const f32x4*)v;
+    else *(uint2*)p = *(const uint2*)v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+
+}  // namespace tg

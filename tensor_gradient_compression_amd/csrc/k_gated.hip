@@ -1,0 +1,317 @@
+// Gated linear layer, y = act(x Wg^T + bg) * (x Wu^T + bu): the forward product, and the first
+// product of the gradients.
+//
+// Both products are one: a tile's columns are 16 of the gate's and 16 of the other weight's by
+// turns, so that a lane's sums hold g and u of the same places, and the activation and the
+// product follow in registers. The backward pass keeps nothing of the forward's: the same tile
+// forms g and u again (a third of its operations, and no 4 or 8 bytes a value in memory between
+// the passes), then dg = dy u act'(g) and du = dy act(g), which leave rounded to x's type as
+// the operands of the products for dx and the weights (k_gated_bwd.hip).
+//
+// fp32 values are multiplied in three bf16 parts, which add up to them exactly, by six of the
+// nine products of parts; the three that are left out are 2^-24 of the whole and less. The
+// matrix instructions do 16 times as much in bf16 as in fp32.
+#include "gated.h"
+
+namespace tg {
+
+namespace {
+
+// Phi(-x) for x >= 0, the normal distribution's lower tail: t 2^(p(t) - x^2 log2(e) / 2) with
+// t = 1 / (1 + x / sqrt(8)) and p a polynomial fitted to log2(erfcx(x / sqrt 2) / 2t) at
+// Chebyshev points; 3.4e-7 of the value for every x (SHORT: 9.7e-7).
+template <bool SHORT>
+__device__ __forceinline__ float normal_tail(float x) {
+  const float t = __builtin_amdgcn_rcpf(1.0f + 0.353553391f * x);
+  float p;
+  if constexpr (SHORT) {
+    p = -0.273941745f;
+    p = __builtin_fmaf(p, t, 1.09719799f);
+    p = __builtin_fmaf(p, t, -1.46694501f);
+    p = __builtin_fmaf(p, t, 0.526053097f);
+    p = __builtin_fmaf(p, t, -0.0686230273f);
+    p = __builtin_fmaf(p, t, 0.571813192f);
+    p = __builtin_fmaf(p, t, 1.44010662f);
+    p = __builtin_fmaf(p, t, -2.82566219f);
+  } else {
+    p = 0.253258819f;
+    p = __builtin_fmaf(p, t, -1.21736752f);
+    p = __builtin_fmaf(p, t, 2.20788314f);
+    p = __builtin_fmaf(p, t, -1.70057641f);
+    p = __builtin_fmaf(p, t, 0.440011764f);
+    p = __builtin_fmaf(p, t, -0.281599746f);
+    p = __builtin_fmaf(p, t, 0.141806747f);
+    p = __builtin_fmaf(p, t, 0.53962246f);
+    p = __builtin_fmaf(p, t, 1.4427072f);
+    p = __builtin_fmaf(p, t, -2.82574634f);
+  }
+  return t * __builtin_amdgcn_exp2f(__builtin_fmaf(x * -0.721347520f, x, p));
+}
+
+constexpr float kLog2e = 1.44269504f;
+
+// act(g), and act'(g) for the gradients
+template <bool SHORT, bool SLOPE>
+__device__ __forceinline__ float activate(float g, int act, float& slope) {
+  if (act == GATED_RELU) {
+    // a NaN stays one
+    if (SLOPE) slope = g > 0.0f ? 1.0f : 0.0f;
+    return g < 0.0f ? 0.0f : g;
+  }
+  if (act == GATED_GELU) {
+    const float tail = normal_tail<SHORT>(__builtin_fabsf(g));
+    const float cdf = g < 0.0f ? tail : 1.0f - tail;
+    if (SLOPE) {
+      const float e = 0.398942280f * __builtin_amdgcn_exp2f(g * -0.721347520f * g);
+      slope = e == 0.0f ? cdf : __builtin_fmaf(g, e, cdf);
+    }
+    // -infinity times a tail of zero is the limit, zero
+    return tail == 0.0f ? (g < 0.0f ? 0.0f : g) : g * cdf;
+  }
+  // 1 / (1 + e^-|g|) and its counterpart e^-|g| / (1 + e^-|g|)
+  const float e = __builtin_amdgcn_exp2f(-kLog2e * __builtin_fabsf(g));
+  const float r = __builtin_amdgcn_rcpf(1.0f + e);
+  const float p = g < 0.0f ? e * r : r, q = g < 0.0f ? r : e * r;
+  if (act == GATED_SIGMOID) {
+    if (SLOPE) slope = p * q;
+    return p;
+  }
+  if (SLOPE) slope = q == 0.0f ? p : p == 0.0f ? 0.0f : p * __builtin_fmaf(g, q, 1.0f);
+  return p == 0.0f ? 0.0f : g * p;
+}
+
+template <class S, int DT>
+__device__ __forceinline__ void gate_and_up(MmSums<S>& sums, TG_LDS char* lds, const GatedArgs& a, int64_t row0, uint32_t f0) {
+  using G = GatedType<DT>;
+  mm_tile<S, G::MM, false, false, true>(
+      sums, lds,
+      [&](int s, MmOperand& x, MmOperand& g, MmOperand& u) {
+        x = gated_operand<G::SEGS>(a.x, GATED_PART_A, s, 0, false);
+        g = gated_operand<G::SEGS>(a.wg, GATED_PART_B, s, 0, false);
+        u = gated_operand<G::SEGS>(a.wu, GATED_PART_B, s, 0, false);
+      },
+      G::SEGS, a.x.len, row0, f0, a.x.stride, a.wg.stride);
+}
+
+template <typename T>
+__device__ __forceinline__ void bias4(const void* p, uint32_t f, uint32_t hidden, float* b) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b[e] = p && f + e < hidden ? to_f32(((const T*)p)[f + e]) : 0.0f;
+}
+
+template <class S, int DT>
+__global__ void __launch_bounds__(S::THREADS, 2) k_gated_forward(const GatedArgs a) {
+  using T = typename GatedType<DT>::T;
+  extern __shared__ char lds_raw[];
+  TG_LDS char* const lds = (TG_LDS char*)lds_raw;
+  const uint32_t nj = (a.hidden + S::BN / 2 - 1) / (S::BN / 2), ni = (uint32_t)((a.rows + S::BM - 1) / S::BM);
+  uint32_t ti, tj;
+  tile_at(xcd_order(blockIdx.x, gridDim.x), ni, nj, ti, tj);
+  const int64_t row0 = (int64_t)ti * S::BM;
+  const uint32_t f0 = tj * (S::BN / 2);
+  MmSums<S> sums;
+  gate_and_up<S, DT>(sums, lds, a, row0, f0);
+  const int lane = threadIdx.x & 63, wave = (int)uniform(threadIdx.x >> 6);
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  const bool aligned = (a.hidden % 4) == 0 && ((uintptr_t)a.y & (4 * sizeof(T) - 1)) == 0;
+#pragma unroll
+  for (int j = 0; j < S::FN; j += 2) {
+    const uint32_t f = f0 + (wn * S::FN + j) * 8 + (lane >> 4) * 4;
+    float bg[4], bu[4];
+    bias4<T>(a.bg, f, a.hidden, bg);
+    bias4<T>(a.bu, f, a.hidden, bu);
+#pragma unroll
+    for (int i = 0; i < S::FM; ++i) {
+      const int64_t m = row0 + (wm * S::FM + i) * 16 + (lane & 15);
+      if (m >= a.rows || f >= a.hidden) continue;
+      T y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float slope;
+        const float p = activate<DT != DT_F32, false>(sums.c[i][j][e] + bg[e], a.act, slope);
+        y[e] = from_f32<T>(p * (sums.c[i][j + 1][e] + bu[e]));
+      }
+      store4((T*)a.y + m * a.hidden + f, y, (int)(a.hidden - f < 4 ? a.hidden - f : 4), aligned);
+    }
+  }
+}
+
+template <class S, int DT>
+__global__ void __launch_bounds__(S::THREADS, 2) k_gated_grads(const GatedArgs a) {
+  using T = typename GatedType<DT>::T;
+  extern __shared__ char lds_raw[];
+  TG_LDS char* const lds = (TG_LDS char*)lds_raw;
+  const uint32_t nj = (a.hidden + S::BN / 2 - 1) / (S::BN / 2), ni = (uint32_t)((a.rows + S::BM - 1) / S::BM);
+  uint32_t ti, tj;
+  tile_at(xcd_order(blockIdx.x, gridDim.x), ni, nj, ti, tj);
+  const int64_t row0 = (int64_t)ti * S::BM;
+  const uint32_t f0 = tj * (S::BN / 2);
+  MmSums<S> sums;
+  gate_and_up<S, DT>(sums, lds, a, row0, f0);
+  const int lane = threadIdx.x & 63, wave = (int)uniform(threadIdx.x >> 6);
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  const uint32_t pad = gated_pad(a.hidden);
+  const int64_t part = a.rows * 2 * (int64_t)pad;
+  const bool aligned = (a.hidden % 4) == 0 && (a.dy_stride % 4) == 0 && ((uintptr_t)a.dy & (4 * sizeof(T) - 1)) == 0;
+#pragma unroll
+  for (int j = 0; j < S::FN; j += 2) {
+    const uint32_t f = f0 + (wn * S::FN + j) * 8 + (lane >> 4) * 4;
+    float bg[4], bu[4];
+    bias4<T>(a.bg, f, a.hidden, bg);
+    bias4<T>(a.bu, f, a.hidden, bu);
+    f32x4 sg = {0.f, 0.f, 0.f, 0.f}, su = sg;
+#pragma unroll
+    for (int i = 0; i < S::FM; ++i) {
+      const int64_t m = row0 + (wm * S::FM + i) * 16 + (lane & 15);
+      if (m >= a.rows || f >= pad) continue;
+      T dy[4] = {};
+      const T* const src = (const T*)a.dy + m * a.dy_stride + f;
+      if (aligned && f < a.hidden) {
+        __builtin_memcpy(dy, __builtin_assume_aligned(src, 4 * sizeof(T)), 4 * sizeof(T));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (f + e < a.hidden) dy[e] = src[e];
+      }
+      float dg[4], du[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float slope;
+        const float d = to_f32(dy[e]);
+        const float p = activate<DT != DT_F32, true>(sums.c[i][j][e] + bg[e], a.act, slope);
+        const bool in = f + e < a.hidden;     // zeros behind
+        dg[e] = in ? d * (sums.c[i][j + 1][e] + bu[e]) * slope : 0.0f;
+        du[e] = in ? d * p : 0.0f;
+        sg[e] += dg[e];
+        su[e] += du[e];
+      }
+      if constexpr (DT == DT_F32) {
+        bf16_t g[3][4], u[3][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          bf16_t p[3];
+          three_parts(dg[e], p);
+          for (int q = 0; q < 3; ++q) g[q][e] = p[q];
+          three_parts(du[e], p);
+          for (int q = 0; q < 3; ++q) u[q][e] = p[q];
+        }
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          bf16_t* const d = (bf16_t*)a.grads + q * part + m * 2 * (int64_t)pad + f;
+          store4(d, g[q], 4, true);
+          store4(d + pad, u[q], 4, true);
+        }
+      } else {
+        T g[4], u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[e] = from_f32<T>(dg[e]), u[e] = from_f32<T>(du[e]);
+        T* const d = (T*)a.grads + m * 2 * (int64_t)pad + f;
+        store4(d, g, 4, true);
+        store4(d + pad, u, 4, true);
+      }
+    }
+    if (a.row_sums) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) {
+          sg[e] += __shfl_xor(sg[e], o);
+          su[e] += __shfl_xor(su[e], o);
+        }
+      if ((lane & 15) == 0 && f < pad) {
+        float* const r = a.row_sums + ((int64_t)ti * S::WM + wm) * 2 * (int64_t)pad + f;
+        *(f32x4*)r = sg;
+        *(f32x4*)(r + pad) = su;
+      }
+    }
+  }
+}
+
+// One workgroup's 256 pieces of 8 values of a row-padded copy.
+struct PackArgs {
+  GatedPack m[3];
+  uint64_t first[4];    // workgroups before each
+};
+__global__ void __launch_bounds__(256) k_gated_pack(const PackArgs a) {
+  const int w = blockIdx.x >= a.first[2] ? 2 : blockIdx.x >= a.first[1] ? 1 : 0;
+  const GatedPack& m = a.m[w];
+  const uint32_t pieces = gated_pad(m.cols) / 8;
+  const uint64_t at = (blockIdx.x - a.first[w]) * 256 + threadIdx.x;
+  const uint64_t row = at / pieces;
+  if (row >= (uint64_t)m.rows) return;
+  const uint32_t c = (uint32_t)(at % pieces) * 8;
+  const int64_t part = m.rows * (int64_t)pieces * 8;
+  const uint64_t from = row * (uint64_t)m.stride + c;
+  if (m.dt == DT_F32) {
+    bf16_t out[3][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      bf16_t p[3];
+      three_parts(c + e < m.cols ? ((const float*)m.src)[from + e] : 0.0f, p);
+      for (int q = 0; q < 3; ++q) out[q][e] = p[q];
+    }
+    for (int q = 0; q < 3; ++q) *(uint4*)((bf16_t*)m.dst + q * part + at * 8) = *(const uint4*)out[q];
+  } else {
+    uint16_t out[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[e] = c + e < m.cols ? ((const uint16_t*)m.src)[from + e] : (uint16_t)0;
+    *(uint4*)((uint16_t*)m.dst + at * 8) = *(const uint4*)out;
+  }
+}
+
+template <class S, int DT>
+hipError_t launch_tiles(bool grads, const GatedArgs& a, hipStream_t s) {
+  const int64_t ni = (a.rows + S::BM - 1) / S::BM, nj = (a.hidden + S::BN / 2 - 1) / (S::BN / 2);
+  if (ni * nj > 0x7FFFFFFF / S::THREADS) return hipErrorInvalidValue;
+  auto* const k = grads ? k_gated_grads<S, DT> : k_gated_forward<S, DT>;
+  const hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS_BYTES);
+  if (e != hipSuccess) return e;
+  k<<<(uint32_t)(ni * nj), S::THREADS, S::LDS_BYTES, s>>>(a);
+  return hipGetLastError();
+}
+template <int DT>
+hipError_t launch_type(bool grads, const GatedArgs& a, hipStream_t s) {
+  switch (gated_tile(a.rows, 2 * (int64_t)a.hidden)) {
+    case 0: return launch_tiles<MmShape<256, 256, 2, 4>, DT>(grads, a, s);
+    case 1: return launch_tiles<MmShape<128, 128, 2, 2>, DT>(grads, a, s);
+    default: return launch_tiles<MmShape<64, 64, 2, 2>, DT>(grads, a, s);
+  }
+}
+hipError_t launch_any(bool grads, const GatedArgs& a, hipStream_t s) {
+  return a.dt == DT_F32 ? launch_type<DT_F32>(grads, a, s)
+         : a.dt == DT_F16 ? launch_type<DT_F16>(grads, a, s) : launch_type<DT_BF16>(grads, a, s);
+}
+
+}  // namespace
+
+int gated_tile(int64_t ni, int64_t nj) {
+  const int64_t big = ((ni + 255) / 256) * ((nj + 255) / 256), mid = ((ni + 127) / 128) * ((nj + 127) / 128);
+  return big >= 200 ? 0 : mid >= 200 ? 1 : 2;
+}
+
+int64_t gated_sum_rows(int64_t rows, uint32_t in, uint32_t hidden) {
+  const int t = gated_tile(rows, 2 * (int64_t)hidden);
+  const int64_t bm = t == 0 ? 256 : t == 1 ? 128 : 64;
+  return (rows + bm - 1) / bm * 2;
+}
+
+hipError_t launch_gated_forward(const GatedArgs& a, hipStream_t s) { return launch_any(false, a, s); }
+hipError_t launch_gated_grads(const GatedArgs& a, hipStream_t s) { return launch_any(true, a, s); }
+
+hipError_t launch_gated_pack(const GatedPack* m, int n, hipStream_t s) {
+  if (n < 1) return hipSuccess;
+  PackArgs a{};
+  uint64_t groups = 0;
+  for (int i = 0; i < 3; ++i) {
+    a.first[i] = groups;
+    if (i >= n) continue;
+    a.m[i] = m[i];
+    groups += ((uint64_t)m[i].rows * (gated_pad(m[i].cols) / 8) + 255) / 256;
+  }
+  if (groups == 0) return hipSuccess;
+  if (groups > 0x7FFFFFFF / 256) return hipErrorInvalidValue;
+  k_gated_pack<<<(uint32_t)groups, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace tg

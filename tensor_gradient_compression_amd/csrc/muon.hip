@@ -1,0 +1,398 @@
+// Host side of Newton-Schulz orthogonalisation and of the Muon step: the handle, the division
+// of the matrices into tiles and chunks, and the launches. Kernels and arithmetic: k_muon.hip.
+#include <cmath>
+#include <new>
+#include <string>
+#include <vector>
+
+#include "muon.h"
+#include "tgrad.h"
+
+using namespace tg;
+
+struct tgrad_muon {
+  struct Tensor {
+    int64_t values;
+    int dtype, grad_dtype;
+  };
+  struct First {             // a launch over the chunks of some tensors
+    uint32_t first_tensor, tensors, first_chunk, chunks;
+  };
+  struct List {              // a launch of a product over all matrices
+    uint32_t first = 0, n = 0;
+    int tile = 2;
+  };
+  int device = 0, steps = 5;
+  double lr = 0, momentum = 0, eps = 0, coef[3] = {};
+  bool nesterov = true;
+  std::vector<Tensor> tensors;
+  std::vector<First> firsts;
+  List chunks, starts, gram, poly, apply;
+  void* block = nullptr;     // device: matrices, parts, addresses, then the workspace
+  NsMat* mats = nullptr;
+  NsPart* parts = nullptr;
+  void** w = nullptr;
+  const void** g = nullptr;
+  char* ws = nullptr;
+  float* state = nullptr;    // the caller's
+  std::string err;
+};
+
+namespace {
+
+constexpr uint64_t kGroup = 128;           // every tensor's momentum starts at a multiple
+constexpr int64_t kMostSide = 1 << 19;     // tiles' offsets stay under 2^31 bytes
+constexpr uint64_t kMostParts = 1 << 21;   // of one launch
+constexpr int kMostSteps = 100;
+
+struct OnDevice {
+  int prev = -1;
+  explicit OnDevice(int dev) {
+    if (hipGetDevice(&prev) != hipSuccess) prev = -1;
+    if (prev != dev) (void)hipSetDevice(dev);
+    else prev = -1;
+  }
+  ~OnDevice() {
+    if (prev >= 0) (void)hipSetDevice(prev);
+  }
+};
+
+int fail(tgrad_muon_t* h, hipError_t e, const char* what) {
+  try {
+    h->err = std::string(what) + ": " + hipGetErrorString(e);
+  } catch (...) {
+  }
+  return TGRAD_EHIP;
+}
+
+uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
+
+bool side_ok(int64_t rows, int64_t cols) { return rows >= 1 && rows <= kMostSide && cols >= 1 && cols <= kMostSide; }
+bool type_ok(int dtype) { return dtype >= TGRAD_F32 && dtype <= TGRAD_BF16; }
+bool numbers_ok(int steps, const double* c, double eps) {
+  return steps >= 1 && steps <= kMostSteps && c && std::isfinite(c[0]) && std::isfinite(c[1]) && std::isfinite(c[2]) &&
+         eps >= 0.0 && std::isfinite(eps);
+}
+
+// Sizes of a matrix and its place in a workspace, from `at` on; returns the end.
+uint64_t lay_out(NsMat& m, int64_t rows, int64_t cols, int dtype, uint64_t at) {
+  m.rows = (uint32_t)rows;
+  m.cols = (uint32_t)cols;
+  m.ldx = (uint32_t)up(cols, 8);
+  m.m = (uint32_t)(rows < cols ? rows : cols);
+  m.ldm = (uint32_t)up(m.m, 8);
+  m.exact = dtype != TGRAD_BF16;
+  m.wdt = (uint32_t)dtype;
+  m.chunks = (uint32_t)(((uint64_t)rows * cols + MUON_CHUNK - 1) / MUON_CHUNK);
+  auto take = [&](uint64_t bytes) {
+    const uint64_t o = at;
+    at += up(bytes, 256);
+    return o;
+  };
+  const uint64_t x = (uint64_t)rows * m.ldx * 4, s = (uint64_t)m.m * m.ldm * (m.exact ? 4 : 2);
+  m.x = take(x);
+  m.y = take(x);
+  m.a = take(s);
+  m.b = take(s);
+  m.da = take(m.m * 4ull);
+  m.db = take(m.m * 4ull);
+  m.sums = take(m.chunks * 8ull);
+  return at;
+}
+// chunks of padded lines
+uint64_t start_chunks(const NsMat& m) { return ((uint64_t)m.rows * (m.ldx / 8) + MUON_CHUNK / 8 - 1) / (MUON_CHUNK / 8); }
+
+uint64_t across(uint64_t n, int tile) { return (n + ns_tile_size(tile) - 1) / ns_tile_size(tile); }
+uint64_t lower_tiles(uint64_t m, int tile) { return across(m, tile) * (across(m, tile) + 1) / 2; }
+
+// The largest tile that still gives enough workgroups.
+template <class Count>
+int choose_tile(const Count& count) {
+  return count(0) >= 200 ? 0 : count(1) >= 200 ? 1 : 2;
+}
+
+// `products` steps of the iteration, X in place
+struct Launches {
+  NsParts gram, poly, apply;
+  uint32_t ngram, npoly, napply;
+  int tgram, tpoly, tapply;
+};
+hipError_t iterate(const NsCommon& c, const Launches& l, int steps, NsLast last, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  for (int i = 0; i < steps && e == hipSuccess; ++i) {
+    const int at = i & 1;
+    e = launch_ns_gram(c, at, l.tgram, l.gram, l.ngram, s);
+    if (e == hipSuccess) e = launch_ns_poly(c, l.tpoly, l.poly, l.npoly, s);
+    last.last = i == steps - 1;
+    if (e == hipSuccess) e = launch_ns_apply(c, at, l.tapply, last, l.apply, l.napply, s);
+  }
+  return e;
+}
+
+// Values of the flat momentum, or -1.
+int64_t state_values(int n, const int64_t* count, const int64_t* rows, const int64_t* cols) {
+  if (n < 1 || !count || !rows || !cols) return -1;
+  uint64_t total = 0;
+  for (int i = 0; i < n; ++i) {
+    if (count[i] < 0 || count[i] > (int64_t(1) << 40) || !side_ok(rows[i], cols[i])) return -1;
+    const uint64_t each = (uint64_t)rows[i] * cols[i];
+    if ((uint64_t)count[i] > (1ull << 40) / each) return -1;
+    total += up(count[i] * each, kGroup);
+    if (total > (1ull << 40)) return -1;
+  }
+  return (int64_t)total;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t tgrad_muon_state_values(int n, const int64_t* count, const int64_t* rows, const int64_t* cols) {
+  return state_values(n, count, rows, cols);
+}
+
+int tgrad_muon_init(tgrad_muon_t** out, int n, const int64_t* count, const int64_t* rows, const int64_t* cols,
+                    const int* dtype, const int* grad_dtype, const double* weight_decay, const double* scale, double lr,
+                    double momentum, int nesterov, int steps, const double* coefficients, double eps, float* state) {
+  if (!out) return TGRAD_EINVAL;
+  *out = nullptr;
+  const int64_t total = state_values(n, count, rows, cols);
+  if (total < 0 || !dtype || !grad_dtype || !weight_decay || !scale || !numbers_ok(steps, coefficients, eps))
+    return TGRAD_EINVAL;
+  if (!(lr >= 0.0 && std::isfinite(lr)) || !(momentum >= 0.0 && momentum < 1.0)) return TGRAD_EINVAL;
+  if ((total > 0 && !state) || ((uintptr_t)state & 15u) != 0) return TGRAD_EINVAL;
+  uint64_t matrices = 0;
+  for (int i = 0; i < n; ++i) {
+    if (!type_ok(dtype[i]) || (grad_dtype[i] != dtype[i] && grad_dtype[i] != TGRAD_F32)) return TGRAD_EINVAL;
+    if (!(weight_decay[i] >= 0.0 && std::isfinite(weight_decay[i])) || !(scale[i] >= 0.0 && std::isfinite(scale[i])))
+      return TGRAD_EINVAL;
+    matrices += (uint64_t)count[i];
+    if (matrices > kMostParts) return TGRAD_EINVAL;
+  }
+  tgrad_muon_t* h = nullptr;
+  try {
+    h = new tgrad_muon_t();
+    if (hipGetDevice(&h->device) != hipSuccess) {
+      delete h;
+      return TGRAD_EHIP;
+    }
+    h->lr = lr;
+    h->momentum = momentum;
+    h->nesterov = nesterov != 0;
+    h->steps = steps;
+    h->eps = eps;
+    h->state = state;
+    for (int i = 0; i < 3; ++i) h->coef[i] = coefficients[i];
+    std::vector<NsMat> mats;
+    std::vector<NsPart> parts;
+    uint64_t ws = 0, at = 0, over = 0;
+    for (int i = 0; i < n; ++i) {
+      const uint64_t each = (uint64_t)rows[i] * cols[i];
+      h->tensors.push_back({(int64_t)(count[i] * each), dtype[i], grad_dtype[i]});
+      for (int64_t k = 0; k < count[i]; ++k) {
+        NsMat m{};
+        ws = lay_out(m, rows[i], cols[i], dtype[i], ws);
+        m.gdt = (uint32_t)grad_dtype[i];
+        m.elem = k * each;
+        m.state = at + k * each;
+        m.scale = scale[i];
+        m.wd = weight_decay[i];
+        m.tensor = (uint32_t)i;
+        mats.push_back(m);
+        over += m.chunks + start_chunks(m) + 1;
+        if (over > 2 * kMostParts) {
+          delete h;
+          return TGRAD_EINVAL;
+        }
+      }
+      at += up(count[i] * each, kGroup);
+    }
+    // chunks of values, in launches of the tensors whose addresses fit one
+    size_t mat = 0;
+    for (int i = 0; i < n || h->firsts.empty(); i += MUON_LAUNCH_TENSORS) {
+      const int t = n - i < MUON_LAUNCH_TENSORS ? n - i : MUON_LAUNCH_TENSORS;
+      tgrad_muon::First f{(uint32_t)i, (uint32_t)t, (uint32_t)parts.size(), 0};
+      for (; mat < mats.size() && mats[mat].tensor < (uint32_t)(i + t); ++mat)
+        for (uint32_t c = 0; c < mats[mat].chunks; ++c) parts.push_back({(uint32_t)mat, c, 0});
+      f.chunks = (uint32_t)parts.size() - f.first_chunk;
+      h->firsts.push_back(f);
+    }
+    auto list = [&](tgrad_muon::List& l, int tile, auto&& add) {
+      l.tile = tile;
+      l.first = (uint32_t)parts.size();
+      for (size_t k = 0; k < mats.size(); ++k) add((uint32_t)k, mats[k]);
+      l.n = (uint32_t)(parts.size() - l.first);
+    };
+    auto sum = [&](auto&& of) {
+      return choose_tile([&](int tile) {
+        uint64_t t = 0;
+        for (const NsMat& m : mats) t += of(m, tile);
+        return t;
+      });
+    };
+    list(h->starts, 0, [&](uint32_t k, const NsMat& m) {
+      for (uint32_t c = 0; c < start_chunks(m); ++c) parts.push_back({k, c, 0});
+    });
+    const int half = sum([](const NsMat& m, int t) { return lower_tiles(m.m, t); });
+    list(h->gram, half, [&](uint32_t k, const NsMat& m) {
+      for (uint32_t i = 0; i < across(m.m, half); ++i)
+        for (uint32_t j = 0; j <= i; ++j) parts.push_back({k, i, j});
+    });
+    h->poly = h->gram;
+    const int whole = sum([](const NsMat& m, int t) { return across(m.rows, t) * across(m.cols, t); });
+    list(h->apply, whole, [&](uint32_t k, const NsMat& m) {
+      const uint32_t ni = (uint32_t)across(m.rows, whole), nj = (uint32_t)across(m.cols, whole);
+      for (uint32_t b = 0; b < ni; b += 8)
+        for (uint32_t j = 0; j < nj; ++j)
+          for (uint32_t i = b; i < ni && i < b + 8; ++i) parts.push_back({k, i, j});
+    });
+    if (parts.size() > 4 * kMostParts) {
+      delete h;
+      return TGRAD_EINVAL;
+    }
+    const uint64_t bm = up(mats.size() * sizeof(NsMat), 256), bp = up(parts.size() * sizeof(NsPart), 256);
+    const uint64_t bt = up((uint64_t)n * 8, 256);
+    if (hipMalloc(&h->block, bm + bp + 2 * bt + ws) != hipSuccess) {
+      (void)hipGetLastError();
+      delete h;
+      return TGRAD_ENOMEM;
+    }
+    char* b = (char*)h->block;
+    h->mats = (NsMat*)b;
+    h->parts = (NsPart*)(b += bm);
+    h->w = (void**)(b += bp);
+    h->g = (const void**)(b += bt);
+    h->ws = b + bt;
+    hipError_t e = hipSuccess;
+    if (!mats.empty()) e = hipMemcpy(h->mats, mats.data(), mats.size() * sizeof(NsMat), hipMemcpyHostToDevice);
+    if (e == hipSuccess && !parts.empty())
+      e = hipMemcpy(h->parts, parts.data(), parts.size() * sizeof(NsPart), hipMemcpyHostToDevice);
+    if (e == hipSuccess) e = hipDeviceSynchronize();
+    if (e != hipSuccess) {
+      (void)hipFree(h->block);
+      delete h;
+      return TGRAD_EHIP;
+    }
+  } catch (const std::bad_alloc&) {
+    if (h && h->block) (void)hipFree(h->block);
+    delete h;
+    return TGRAD_ENOMEM;
+  }
+  *out = h;
+  return TGRAD_OK;
+}
+
+int tgrad_muon_destroy(tgrad_muon_t* h) {
+  if (!h) return TGRAD_OK;
+  {
+    OnDevice g(h->device);
+    (void)hipFree(h->block);
+  }
+  delete h;
+  return TGRAD_OK;
+}
+
+const char* tgrad_muon_last_error(const tgrad_muon_t* h) { return h ? h->err.c_str() : ""; }
+
+int tgrad_muon_set_lr(tgrad_muon_t* h, double lr) {
+  if (!h || !(lr >= 0.0 && std::isfinite(lr))) return TGRAD_EINVAL;
+  h->lr = lr;
+  return TGRAD_OK;
+}
+
+int tgrad_muon_step(tgrad_muon_t* h, void* const* weights, const void* const* grads, const float* clip, void* stream) {
+  if (!h || !weights || !grads || ((uintptr_t)clip & 3u)) return TGRAD_EINVAL;
+  for (size_t i = 0; i < h->tensors.size(); ++i) {
+    const auto& t = h->tensors[i];
+    if (!t.values) continue;
+    const uintptr_t wa = t.dtype == TGRAD_F32 ? 3 : 1, ga = t.grad_dtype == TGRAD_F32 ? 3 : 1;
+    if (!weights[i] || !grads[i] || ((uintptr_t)weights[i] & wa) || ((uintptr_t)grads[i] & ga)) return TGRAD_EINVAL;
+  }
+  OnDevice dev(h->device);
+  const hipStream_t s = (hipStream_t)stream;
+  NsCommon c{};
+  c.mats = h->mats;
+  c.ws = h->ws;
+  c.clip = clip;
+  c.ca = (float)h->coef[0];
+  c.cb = (float)h->coef[1];
+  c.cc = (float)h->coef[2];
+  MuonFirst f{};
+  f.w = h->w;
+  f.g = h->g;
+  f.momentum = h->state;
+  f.mu = (float)h->momentum;
+  f.nu = (float)(1.0 - h->momentum);
+  f.nesterov = h->nesterov;
+  hipError_t e = hipSuccess;
+  for (const auto& l : h->firsts) {
+    MuonTable t;
+    for (uint32_t i = 0; i < l.tensors; ++i) {
+      t.w[i] = weights[l.first_tensor + i];
+      t.g[i] = grads[l.first_tensor + i];
+    }
+    f.first_tensor = l.first_tensor;
+    f.tensors = l.tensors;
+    if (e == hipSuccess) e = launch_muon_first(c, f, t, {h->parts + l.first_chunk, 0, 0, false}, l.chunks, s);
+  }
+  auto parts = [&](const tgrad_muon::List& l) { return NsParts{h->parts + l.first, 0, 0, false}; };
+  if (e == hipSuccess) e = launch_muon_start(c, f, h->eps, parts(h->starts), h->starts.n, s);
+  const Launches l{parts(h->gram), parts(h->poly), parts(h->apply), h->gram.n, h->poly.n, h->apply.n,
+                   h->gram.tile,   h->poly.tile,   h->apply.tile};
+  NsLast last{};
+  last.w = h->w;
+  last.lr = h->lr;
+  if (e == hipSuccess) e = iterate(c, l, h->steps, last, s);
+  return e == hipSuccess ? TGRAD_OK : fail(h, e, "Muon step");
+}
+
+int64_t tgrad_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols, int dtype) {
+  if (count < 0 || count > (int64_t)kMostParts || !side_ok(rows, cols) || !type_ok(dtype)) return -1;
+  NsMat m{};
+  const uint64_t each = lay_out(m, rows, cols, dtype, 0);
+  if ((uint64_t)count > (1ull << 46) / each) return -1;
+  return (int64_t)(each * count);
+}
+
+int tgrad_orthogonalize(const void* x, int64_t matrix_stride, int64_t row_stride, void* out, int64_t count,
+                        int64_t rows, int64_t cols, int dtype, int steps, const double* coefficients, double eps,
+                        void* workspace, void* stream) {
+  if (tgrad_orthogonalize_workspace(count, rows, cols, dtype) < 0 || !numbers_ok(steps, coefficients, eps))
+    return TGRAD_EINVAL;
+  if ((rows > 1 && row_stride < cols) || row_stride > (int64_t(1) << 40)) return TGRAD_EINVAL;
+  if (count > 1 && (matrix_stride < (rows - 1) * (rows > 1 ? row_stride : 0) + cols || matrix_stride > (int64_t(1) << 42)))
+    return TGRAD_EINVAL;
+  if (count == 0) return TGRAD_OK;
+  const uintptr_t low = dtype == TGRAD_F32 ? 3 : 1;
+  if (!x || !out || !workspace || ((uintptr_t)x & low) || ((uintptr_t)out & low) || ((uintptr_t)workspace & 15u))
+    return TGRAD_EINVAL;
+  const hipStream_t s = (hipStream_t)stream;
+  NsCommon c{};
+  c.pitch = lay_out(c.one, rows, cols, dtype, 0);
+  c.one.gdt = (uint32_t)dtype;
+  c.ws = (char*)workspace;
+  c.ca = (float)coefficients[0];
+  c.cb = (float)coefficients[1];
+  c.cc = (float)coefficients[2];
+  const uint64_t n = (uint64_t)count, m = c.one.m;
+  Launches l{};
+  l.tgram = l.tpoly = choose_tile([&](int t) { return n * lower_tiles(m, t); });
+  l.tapply = choose_tile([&](int t) { return n * across(rows, t) * across(cols, t); });
+  const uint64_t chunks = n * c.one.chunks, starts = n * start_chunks(c.one), half = n * lower_tiles(m, l.tgram);
+  const uint64_t whole = n * across(rows, l.tapply) * across(cols, l.tapply);
+  for (uint64_t k : {chunks, starts, half, whole})
+    if (k > kMostParts) return TGRAD_EINVAL;
+  l.gram = l.poly = {nullptr, (uint32_t)across(m, l.tgram), (uint32_t)across(m, l.tgram), true};
+  l.apply = {nullptr, (uint32_t)across(rows, l.tapply), (uint32_t)across(cols, l.tapply), false};
+  l.ngram = l.npoly = (uint32_t)half;
+  l.napply = (uint32_t)whole;
+  const NsSource f{x, row_stride, matrix_stride};
+  hipError_t e = launch_ns_norm(c, f, {nullptr, c.one.chunks, 1, false}, (uint32_t)chunks, s);
+  if (e == hipSuccess) e = launch_ns_start(c, f, eps, {nullptr, (uint32_t)start_chunks(c.one), 1, false}, (uint32_t)starts, s);
+  NsLast last{};
+  last.out = out;
+  if (e == hipSuccess) e = iterate(c, l, steps, last, s);
+  return e == hipSuccess ? TGRAD_OK : TGRAD_EHIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,267 @@
+"""GPU: the gated linear layer and its gradients against the 64-bit oracle, within a priori
+bounds (oracle/gated_oracle.py)."""
+import numpy as np
+import pytest
+
+import oracle.gated_oracle as G
+import tensor_gradient_compression_amd as tg
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+TYPES = ["f32", "f16", "bf16"]
+# rows, in, hidden: single values, odd sizes, sizes around the tiles of 64, 128 and 256 and around 8 and 64 of k
+SHAPES = [(1, 1, 1), (1, 64, 128), (3, 2, 5), (7, 8, 8), (64, 64, 32), (65, 63, 33), (63, 65, 31), (130, 72, 40),
+          (257, 128, 129), (40, 333, 444), (300, 8, 600), (5, 1000, 7), (129, 136, 264)]
+
+
+def host(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def inputs(rows, width, hidden, dtype, seed, bias=True, offset=0, gap=0):
+    """x, dy, weights and biases; x and dy start `offset` elements into their allocation and have
+    `gap` unused ones (NaN) between rows."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    ty = tg.torch_dtype(dtype)
+
+    def normal(*s):
+        return torch.randn(*s, generator=gen, device="cuda")
+
+    def rows_in(t):
+        r, c = t.shape
+        buf = torch.full((r * (c + gap) + offset,), float("nan"), device="cuda").to(ty)
+        v = buf[offset:].view(r, c + gap)[:, :c]
+        v.copy_(t)
+        return v
+
+    x = rows_in(normal(rows, width) * torch.exp(0.5 * normal(rows, 1)))
+    dy = rows_in(normal(rows, hidden))
+    wg, wu = ((normal(hidden, width) / width ** 0.5).to(ty) for _ in range(2))
+    bg, bu = ((0.3 * normal(hidden)).to(ty) if bias else None for _ in range(2))
+    return dy, x, wg, wu, bg, bu
+
+
+def close(got, true, bound, what):
+    off = np.abs(host(got) - true)
+    assert np.all(off <= bound), f"{what}: {np.nanmax(off / bound):.3g} of the bound"
+
+
+def check(dy, x, wg, wu, bg, bu, act, dtype):
+    hidden, width = wg.shape
+    DY, X = host(dy).reshape(-1, hidden), host(x).reshape(-1, width)
+    W = host(wg), host(wu), host(bg), host(bu)
+    y = tg.gated_linear_forward(x, wg, wu, bg, bu, activation=act)
+    assert y.dtype == x.dtype and y.shape == x.shape[:-1] + (hidden,) and y.is_contiguous()
+    close(y.reshape(-1, hidden), G.forward(X, *W, act), G.forward_bound(X, *W, act, dtype), "y")
+    out = tg.gated_linear_backward(dy, x, wg, wu, bg, bu, activation=act)
+    true, bounds = G.backward(DY, X, *W, act), G.backward_bounds(DY, X, *W, act, dtype)
+    assert out[0].shape == x.shape
+    for k, (got, t, b, what) in enumerate(zip(out, true, bounds, ("dx", "dw_gate", "dw_up", "db_gate", "db_up"))):
+        if k > 2 and (bg, bu)[k - 3] is None:
+            assert got is None
+            continue
+        assert got.dtype == x.dtype and got.is_contiguous()
+        close(got.reshape(t.shape), t, b, what)
+    return y, out
+
+
+@pytest.mark.parametrize("rows,width,hidden", SHAPES)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_against_the_oracle(rows, width, hidden, dtype):
+    print(f"CASE gated {rows} {width} {hidden} {dtype}", flush=True)
+    act = ("silu", "gelu", "sigmoid", "relu")[(rows + width) % 4]
+    check(*inputs(rows, width, hidden, dtype, seed=rows + hidden), act, dtype)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "sigmoid", "relu"])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("bias", [True, False])
+def test_activations(act, dtype, bias):
+    check(*inputs(70, 24, 40, dtype, seed=2, bias=bias), act, dtype)
+
+
+@pytest.mark.parametrize("rows,width,hidden", [(9, 64, 24), (70, 40, 33), (33, 31, 72)])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("offset,gap", [(1, 0), (0, 1), (3, 5), (0, 8), (8, 64)])
+def test_rows_apart_and_unaligned(rows, width, hidden, dtype, offset, gap):
+    check(*inputs(rows, width, hidden, dtype, seed=3, offset=offset, gap=gap), "silu", dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_weights_that_start_anywhere(dtype):
+    dy, x, wg, wu, bg, bu = inputs(50, 32, 48, dtype, seed=4)
+
+    def moved(t, by):
+        buf = torch.full((t.numel() + by,), float("nan"), device="cuda").to(t.dtype)
+        buf[by:].copy_(t.reshape(-1))
+        return buf[by:].view(t.shape)
+
+    y, out = check(dy, x, wg, wu, bg, bu, "gelu", dtype)
+    y2, out2 = check(dy, x, moved(wg, 1), moved(wu, 4), moved(bg, 1), moved(bu, 3), "gelu", dtype)
+    assert torch.equal(y, y2) and all(torch.equal(a, b) for a, b in zip(out, out2))
+
+
+@pytest.mark.parametrize("rows,width,hidden", [(3000, 200, 520), (20000, 24, 40), (260, 264, 5000), (40000, 8, 16)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_larger_tiles_and_split_sums(rows, width, hidden, dtype):
+    check(*inputs(rows, width, hidden, dtype, seed=5), "silu", dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_leading_axes_and_some_gradients(dtype):
+    dy, x, wg, wu, bg, bu = inputs(60, 16, 24, dtype, seed=6)
+    x3, dy3 = x.view(3, 4, 5, 16), dy.view(3, 4, 5, 24)
+    y, out = check(dy3, x3, wg, wu, bg, bu, "silu", dtype)
+    some = tg.gated_linear_backward(dy3, x3, wg, wu, bg, bu, need_weights=False)
+    assert torch.equal(some[0], out[0]) and some[1:] == (None,) * 4
+    some = tg.gated_linear_backward(dy3, x3, wg, wu, bg, bu, need_dx=False)
+    assert some[0] is None and all(torch.equal(a, b) for a, b in zip(some[1:], out[1:]))
+    one = tg.gated_linear_backward(dy3, x3, wg, wu, bg, None)
+    assert one[3] is not None and one[4] is None
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_no_rows(dtype):
+    dy, x, wg, wu, bg, bu = inputs(4, 16, 24, dtype, seed=7)
+    assert tg.gated_linear_forward(x[:0], wg, wu, bg, bu).shape == (0, 24)
+    dx, *rest = tg.gated_linear_backward(dy[:0], x[:0], wg, wu, bg, bu)
+    assert dx.shape == (0, 16)
+    for t, like in zip(rest, (wg, wu, bg, bu)):
+        assert t.shape == like.shape and not t.any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_values_that_are_not_finite_stay_in_their_rows(dtype):
+    """Rows with NaN or infinities beside clean ones: forward and dx of the clean rows are those
+    without them; the odd sizes put what is read beyond a row or column beside them."""
+    dy, x, wg, wu, bg, bu = inputs(70, 33, 41, dtype, seed=8)
+    y, dx = tg.gated_linear_forward(x, wg, wu, bg, bu), tg.gated_linear_backward(dy, x, wg, wu, bg, bu)[0]
+    bad = x.clone()
+    bad[5, 3], bad[17, 0], bad[69, 32] = float("nan"), float("inf"), float("-inf")
+    y2, dx2 = tg.gated_linear_forward(bad, wg, wu, bg, bu), tg.gated_linear_backward(dy, bad, wg, wu, bg, bu)[0]
+    rows = torch.ones(70, dtype=torch.bool, device="cuda")
+    rows[[5, 17, 69]] = False
+    assert torch.equal(y[rows], y2[rows]) and torch.equal(dx[rows], dx2[rows])
+    assert y2[5].isnan().all() and not y2[17].isfinite().all() and not y2[69].isfinite().all()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "sigmoid", "relu"])
+def test_far_gates(act):
+    """Gates at the ends of fp32's range and at infinity: the activations' limits."""
+    g = torch.tensor([[-3e38, -1e4, -200.0, -90.0, 0.0, 90.0, 200.0, 1e4, 3e38]], device="cuda").T.contiguous()
+    one = torch.ones(1, 1, device="cuda")
+    zero, u = torch.zeros(1, 1, device="cuda"), torch.tensor([2.0], device="cuda")
+    y = tg.gated_linear_forward(g, one, zero, None, u, activation=act)[:, 0].double().cpu()
+    x = g[:, 0].double().cpu()
+    f = {"silu": torch.nn.functional.silu, "gelu": torch.nn.functional.gelu, "sigmoid": torch.sigmoid, "relu": torch.relu}[act]
+    want = 2 * f(x)
+    assert torch.allclose(y, want.float().double(), rtol=1e-4, atol=1e-36), (y, want)
+    d = tg.gated_linear_backward(torch.ones_like(g), g, one, zero, None, u, activation=act)[0]
+    assert d.isfinite().all()
+
+
+def test_large_fp32_values():
+    """Above bf16's largest number, where a part would round to infinity."""
+    x = torch.full((1, 8), 3.4e38, device="cuda")
+    w = torch.zeros(8, 8, device="cuda")
+    w[0, 0] = 1.0
+    y = tg.gated_linear_forward(x, w, torch.zeros_like(w), None, torch.ones(8, device="cuda"), activation="relu")
+    assert float(y[0, 0]) == float(x[0, 0]) and not y[0, 1:].any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_autograd(dtype):
+    """The differentiable call's gradients are those of the raw one, an expanded dy among them,
+    and only what is asked for."""
+    dy, x, wg, wu, bg, bu = inputs(40, 24, 56, dtype, seed=9)
+    leaves = [t.clone().requires_grad_() for t in (x, wg, wu, bg, bu)]
+    y = tg.gated_linear(*leaves, activation="gelu")
+    grads = torch.autograd.grad(y, leaves, dy.contiguous())
+    for a, b in zip(grads, tg.gated_linear_backward(dy, x, wg, wu, bg, bu, activation="gelu")):
+        assert torch.equal(a, b)
+    leaves[1].requires_grad_(False)
+    y = tg.gated_linear(*leaves[:3], activation="gelu")
+    y.sum().backward()
+    want = tg.gated_linear_backward(torch.ones_like(y), x, wg, wu, activation="gelu")
+    assert leaves[1].grad is None and torch.equal(leaves[0].grad, want[0]) and torch.equal(leaves[2].grad, want[2])
+
+
+def test_gradients_are_difference_quotients():
+    """fp32, along random directions: the loss is a sum of 30 x 20 values whose fp32 rounding is
+    1e-7 of its terms each; a step of 1e-2 leaves h^2 / 6 of a third derivative."""
+    dy, x, wg, wu, bg, bu = (t.double() for t in inputs(30, 12, 20, "f32", seed=10))
+    args = [x, wg, wu, bg, bu]
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    grads = tg.gated_linear_backward(dy.float(), *[a.float() for a in args])
+    h = 1e-2
+
+    def loss(*a):
+        return (tg.gated_linear_forward(*[t.float() for t in a]).double() * dy).sum()
+
+    for k, g in enumerate(grads):
+        d = torch.randn(args[k].shape, generator=gen, device="cuda", dtype=torch.float64)
+        up, down = list(args), list(args)
+        up[k], down[k] = args[k] + h * d, args[k] - h * d
+        quotient = float((loss(*up) - loss(*down)) / (2 * h))
+        slope = float((g.double() * d).sum())
+        terms = float((tg.gated_linear_forward(*[t.float() for t in args]).double() * dy).abs().sum())
+        # rounding of the two losses over 2h, and the third derivative against a step of twice h
+        up[k], down[k] = args[k] + 2 * h * d, args[k] - 2 * h * d
+        wide = float((loss(*up) - loss(*down)) / (4 * h))
+        assert abs(quotient - slope) <= abs(wide - quotient) + terms * 1e-5 / (2 * h)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_runs_repeat_and_replay(dtype):
+    """Two runs are bitwise the same, and so is every replay of a captured forward and backward
+    on other inputs, with eager work between the replays."""
+    args = inputs(300, 40, 64, dtype, seed=12)
+    again = inputs(300, 40, 64, dtype, seed=13)
+    static = [t.clone() for t in args]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        tg.gated_linear_forward(*static[1:])
+        tg.gated_linear_backward(*static)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = tg.gated_linear_forward(*static[1:])
+        out = tg.gated_linear_backward(*static)
+    for t in (args, again, args):
+        for s, v in zip(static, t):
+            s.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, tg.gated_linear_forward(*t[1:]))
+        for a, b in zip(out, tg.gated_linear_backward(*t)):
+            assert torch.equal(a, b)
+
+
+def test_another_stream():
+    dy, x, wg, wu, bg, bu = inputs(500, 64, 96, "bf16", seed=14)
+    want = tg.gated_linear_forward(x, wg, wu, bg, bu), *tg.gated_linear_backward(dy, x, wg, wu, bg, bu)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = tg.gated_linear_forward(x, wg, wu, bg, bu), *tg.gated_linear_backward(dy, x, wg, wu, bg, bu)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_refusals():
+    dy, x, wg, wu, bg, bu = inputs(6, 16, 24, "f32", seed=15)
+    f = tg.gated_linear_forward
+    for args, match in (((x, wg[:, :8].contiguous(), wu), "w_gate"), ((x, wg, wu[:12].contiguous()), "w_up"),
+                        ((x, wg.T, wu), "w_gate"), ((x, wg[:, ::2], wu), "w_gate"), ((x, wg.half(), wu), "w_gate"),
+                        ((x, wg, wu.cpu()), "w_up"), ((x, wg, wu, bg[:5]), "b_gate"), ((x, wg, wu, bg, bu.half()), "b_up"),
+                        ((x.double(), wg, wu), "x"), ((x.T.contiguous().T, wg, wu), "x"), ((x[0, 0], wg, wu), "x"),
+                        ((x.expand(2, 6, 16), wg, wu), "x"), ((torch.zeros(3, 0, device="cuda"), wg, wu), "x")):
+        with pytest.raises(ValueError, match=match):
+            f(*args)
+    for bad in (dy[:5], dy.half(), dy[:, :8], dy.T.contiguous().T, dy.expand(1, 6, 24)):
+        with pytest.raises(ValueError, match="dy"):
+            tg.gated_linear_backward(bad, x, wg, wu)
+    with pytest.raises(ValueError, match="activation"):
+        f(x, wg, wu, activation="swish")

@@ -1,0 +1,328 @@
+"""GPU: Newton-Schulz orthogonalisation and the Muon step against the 64-bit oracle, within
+what the kernels' formats allow (oracle/muon_oracle.py)."""
+import math
+
+import numpy as np
+import pytest
+
+import oracle.muon_oracle as M
+import tensor_gradient_compression_amd as tg
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+TYPES = ["f32", "f16", "bf16"]
+SHAPES = [(1, 1), (1, 9), (9, 1), (2, 3), (8, 8), (5, 200), (200, 5), (63, 65), (64, 64), (65, 63), (130, 72), (72, 130),
+          (257, 100), (100, 257), (128, 128)]
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def matrix(gen, rows, cols):
+    """Directions of falling size and noise, as a gradient's."""
+    k = min(rows, cols) // 4 + 1
+    x = torch.randn(rows, k, generator=gen, device="cuda") / torch.arange(1, k + 1, device="cuda")
+    return x @ torch.randn(k, cols, generator=gen, device="cuda") + 0.1 * torch.randn(rows, cols, generator=gen, device="cuda")
+
+
+def near(got, u, dtype, what, size=1.0, **ns):
+    """`got` against size times the orthogonalised u, rounded to dtype."""
+    true = M.orthogonalize(u, **ns)
+    e2, em = M.bounds(u, true, dtype, **ns)
+    off, r = host(got) - size * true, M.HALF_ULP[dtype]
+    a, b = np.linalg.norm(off), size * e2 + r * np.linalg.norm(size * true)
+    assert a <= b, f"{what}: 2-norm {a / b:.3g} of the bound"
+    a, b = np.abs(off), size * em + M.rounding(size * true, dtype) + r * size * em
+    assert np.all(a <= b), f"{what}: {np.max(a / b):.3g} of the bound"
+
+
+@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_orthogonalize(rows, cols, dtype):
+    print(f"CASE orthogonalize {rows} x {cols} {dtype}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(rows * 7 + cols)
+    x = (0.01 * matrix(gen, rows, cols)).to(tg.torch_dtype(dtype))
+    y = tg.orthogonalize(x)
+    assert y.shape == x.shape and y.dtype == x.dtype and y.is_contiguous()
+    near(y, host(x), dtype, "orthogonalize")
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(700, 530, "bf16"), (530, 700, "f16"), (1100, 260, "f32"), (300, 2050, "bf16")])
+def test_orthogonalize_over_several_tiles(rows, cols, dtype):
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = matrix(gen, rows, cols).to(tg.torch_dtype(dtype))
+    near(tg.orthogonalize(x), host(x), dtype, "orthogonalize")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("count,rows,cols", [(3, 20, 33), (300, 8, 8), (40, 64, 64), (7, 130, 70)])
+def test_stacks(dtype, count, rows, cols):
+    """Every matrix of a stack is as it is alone, bit for bit where its tiles are the same."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.stack([matrix(gen, rows, cols) for _ in range(count)]).to(tg.torch_dtype(dtype))
+    y = tg.orthogonalize(x)
+    for i in range(0, count, max(1, count // 4)):
+        near(y[i], host(x[i]), dtype, f"matrix {i}")
+    y4 = tg.orthogonalize(x.view(1, count, 1, rows, cols))
+    assert torch.equal(y4.view_as(y), y)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_strides(dtype):
+    """Rows and matrices apart, unaligned starts; what lies between is NaN."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.stack([matrix(gen, 21, 37) for _ in range(3)]).to(tg.torch_dtype(dtype))
+    y = tg.orthogonalize(x)
+    buf = torch.full((1 + 3 * 25 * 41,), float("nan"), device="cuda").to(x.dtype)
+    v = buf[1:].view(3, 25, 41)[:, :21, :37]
+    v.copy_(x)
+    assert torch.equal(tg.orthogonalize(v), y)
+    near(tg.orthogonalize(v[1]), host(x[1]), dtype, "one of them")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("steps,coefficients,eps", [(1, (1.5, -0.5, 0.0), 0.0), (8, (2.0, -1.5, 0.5), 1e-3), (3, M.COEFFICIENTS, 1.0)])
+def test_other_iterations(dtype, steps, coefficients, eps):
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x = matrix(gen, 40, 72).to(tg.torch_dtype(dtype))
+    ns = dict(steps=steps, coefficients=coefficients, eps=eps)
+    near(tg.orthogonalize(x, **ns), host(x), dtype, "orthogonalize", **ns)
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-6, 1e6, 1e30])
+def test_any_size(size):
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = matrix(gen, 30, 20) * size
+    near(tg.orthogonalize(x, eps=0.0), host(x), "f32", "orthogonalize", eps=0.0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_zeros_and_nan(dtype):
+    ty = tg.torch_dtype(dtype)
+    x = torch.zeros(3, 20, 30, device="cuda", dtype=ty)
+    assert not tg.orthogonalize(x).any()
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    x[0], x[2] = matrix(gen, 20, 30).to(ty), matrix(gen, 20, 30).to(ty)
+    clean = tg.orthogonalize(x)
+    x[1, 3, 4] = float("nan")
+    y = tg.orthogonalize(x)
+    assert y[1].isnan().all() and torch.equal(y[0], clean[0]) and torch.equal(y[2], clean[2])
+    assert tg.orthogonalize(x[:0]).shape == (0, 20, 30)
+
+
+def tensors(shapes, dtype, grad, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    w, g = [], []
+    for s in shapes:
+        n = math.prod(s[:-2])
+        w.append((0.02 * torch.randn(*s, generator=gen, device="cuda")).to(tg.torch_dtype(dtype)))
+        g.append((0.01 * torch.stack([matrix(gen, *s[-2:]) for _ in range(n)] or [torch.zeros(s[-2:], device="cuda")])
+                  [:n].reshape(s)).to(tg.torch_dtype(grad)))
+    return w, g
+
+
+def check_step(opt, w, g, m, before, clip=1.0):
+    """The weights w after a step from `before` with momentum m (flat, before)."""
+    for i, s in enumerate(opt.shapes):
+        n = math.prod(s)
+        flat = m[opt.offsets[i]:opt.offsets[i] + n]
+        new = host(opt.state["momentum"])[opt.offsets[i]:opt.offsets[i] + n]
+        gi = host(g[i]).reshape(-1) * clip
+        mom, u = M.momentum(gi, flat, opt.momentum, opt.nesterov)
+        # two products and a sum of fp32, of a gradient whose product with the coefficient is one more
+        assert np.all(np.abs(new - mom) <= 5 * 2.0 ** -24 * (np.abs(gi) + np.abs(flat)) + 1e-44)
+        u, W, B = u.reshape(-1, *s[-2:]), host(w[i]).reshape(-1, *s[-2:]), host(before[i]).reshape(-1, *s[-2:])
+        for k in range(len(u)):
+            step = opt.lr * opt.scale[i]
+            ns = dict(steps=opt.steps, coefficients=opt.coefficients, eps=opt.eps)
+            true = M.orthogonalize(u[k], **ns)
+            e2, em = M.bounds(u[k], true, opt.dtypes[i], **ns)
+            want = B[k] * (1 - opt.lr * opt.weight_decay[i]) - step * true
+            mine = 8 * 2.0 ** -24 * (np.abs(B[k]) + step * np.abs(true))
+            off = W[k] - want
+            r = M.HALF_ULP[opt.dtypes[i]]
+            a, b = np.linalg.norm(off), step * e2 + np.linalg.norm(mine) + r * np.linalg.norm(want) + 2.0 ** -25 * len(want)
+            assert a <= b, f"tensor {i} matrix {k}: 2-norm {a / b:.3g} of the bound"
+            b = step * em + mine + M.rounding(np.abs(want) + step * em, opt.dtypes[i])
+            assert np.all(np.abs(off) <= b), f"tensor {i} matrix {k}: {np.max(np.abs(off) / b):.3g} of the bound"
+
+
+@pytest.mark.parametrize("dtype,grad", [("f32", "f32"), ("f16", "f16"), ("bf16", "bf16"), ("bf16", "f32"), ("f16", "f32")])
+@pytest.mark.parametrize("nesterov,scale", [(True, "spectral"), (False, "rms")])
+def test_muon_steps(dtype, grad, nesterov, scale):
+    """Three steps over matrices of every shape, stacks and an empty stack among them."""
+    print(f"CASE muon {dtype} {grad} {nesterov} {scale}", flush=True)
+    shapes = [(1, 1), (30, 20), (3, 17, 33), (64, 64), (0, 5, 6), (5, 130), (2, 2, 9, 8), (130, 70)]
+    w, _ = tensors(shapes, dtype, grad, 1)
+    opt = tg.Muon(shapes, dtype, grad, lr=0.02, momentum=0.9, nesterov=nesterov, weight_decay=0.1, scale=scale)
+    for t in range(3):
+        _, g = tensors(shapes, dtype, grad, 10 + t)
+        before, m = [x.clone() for x in w], host(opt.state["momentum"])
+        opt.step(w, g)
+        check_step(opt, w, g, m, before)
+
+
+def test_muon_types_scales_and_decays_of_their_own():
+    shapes = [(20, 30), (40, 10), (33, 33)]
+    w, g = [], []
+    for s, d, k in zip(shapes, ("f32", "bf16", "f16"), ("f32", "f32", "f16")):
+        a, b = tensors([s], d, k, 2)
+        w += a
+        g += b
+    opt = tg.Muon(shapes, ["f32", "bf16", "f16"], ["f32", "f32", "f16"], lr=0.1, weight_decay=[0.0, 0.5, 0.1],
+                  scale=[0.3, "rms", "spectral"], steps=4)
+    before = [x.clone() for x in w]
+    opt.step(w, g)
+    check_step(opt, w, g, np.zeros(opt.state["momentum"].numel()), before)
+
+
+def test_more_tensors_than_a_launch_names():
+    shapes = [(3 + i % 5, 4 + i % 3) for i in range(500)]
+    w, g = tensors(shapes, "f32", "f32", 3)
+    opt = tg.Muon(shapes, "f32", lr=0.02)
+    before = [x.clone() for x in w]
+    opt.step(w, g)
+    check_step(opt, w, g, np.zeros(opt.state["momentum"].numel()), before)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_clipping_and_a_step_that_is_left_out(dtype):
+    shapes = [(40, 24), (24, 40), (5, 16, 16)]
+    w, g = tensors(shapes, dtype, dtype, 4)
+    opt = tg.Muon(shapes, dtype, lr=0.02)
+    norm = tg.AdamW([x.numel() for x in w], dtype)
+    clip = norm.grad_norm(g, max_norm=0.05)
+    before = [x.clone() for x in w]
+    opt.step(w, g, clip=clip)
+    check_step(opt, w, g, np.zeros(opt.state["momentum"].numel()), before, clip=float(clip[1]))
+    after, m = [x.clone() for x in w], opt.state["momentum"].clone()
+    g[1][3, 3] = float("inf")
+    opt.step(w, g, clip=norm.grad_norm(g, max_norm=0.05))
+    assert all(torch.equal(a, b) for a, b in zip(w, after)) and torch.equal(m, opt.state["momentum"])
+
+
+def test_muon_is_orthogonalize():
+    """A step from no momentum without decay moves a weight by lr * scale times what orthogonalize
+    gives for its gradient (the factor in front of u cancels but for eps)."""
+    w, g = tensors([(50, 80)], "f32", "f32", 5)
+    opt = tg.Muon([(50, 80)], "f32", lr=0.5, weight_decay=0.0, scale=1.0, eps=0.0)
+    before = w[0].clone()
+    opt.step(w, g)
+    o = tg.orthogonalize(g[0], eps=0.0)
+    assert torch.linalg.norm((before - w[0]) / 0.5 - o) <= 1e-5 * torch.linalg.norm(o)
+
+
+def test_muon_unaligned_tensors():
+    """Weights and gradients that start at any element."""
+    shapes = [(17, 13), (9, 21)]
+    w, g = tensors(shapes, "bf16", "f32", 6)
+
+    def moved(t, by):
+        buf = torch.zeros(t.numel() + by, device="cuda", dtype=t.dtype)
+        buf[by:].copy_(t.reshape(-1))
+        return buf[by:].view(t.shape)
+
+    a, b = (tg.Muon(shapes, "bf16", "f32", lr=0.02) for _ in range(2))
+    w2, g2 = [moved(x, 1) for x in w], [moved(x, 3) for x in g]
+    a.step(w, g)
+    b.step(w2, g2)
+    assert all(torch.equal(x, y) for x, y in zip(w, w2))
+
+
+def test_muon_runs_repeat_replay_and_resume():
+    shapes = [(70, 40), (3, 20, 50)]
+    grads = [tensors(shapes, "bf16", "bf16", 20 + t)[1] for t in range(4)]
+
+    def fresh():
+        return tensors(shapes, "bf16", "bf16", 7)[0], tg.Muon(shapes, "bf16", lr=0.02)
+
+    w, opt = fresh()
+    want = []
+    for g in grads:
+        opt.step(w, g)
+        want.append([x.clone() for x in w])
+    # replayed, with eager work between
+    w, opt = fresh()
+    static = [x.clone() for x in grads[0]]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        opt.step(w, static)
+    for g, v in zip(grads, want):
+        for s, x in zip(static, g):
+            s.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(w, v))
+    # stopped and resumed, on a stream of its own
+    w, opt = fresh()
+    for g in grads[:2]:
+        opt.step(w, g)
+    saved = opt.state_dict()
+    opt.close()
+    other = tg.Muon(shapes, "bf16", lr=0.02)
+    other.load_state_dict(saved)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for g in grads[2:]:
+        other.step(w, g, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(w, want[-1]))
+    with pytest.raises(ValueError, match="shapes"):
+        tg.Muon([(70, 40)], "bf16").load_state_dict(saved)
+    with pytest.raises(ValueError, match="momentum"):
+        tg.Muon(shapes, "bf16", momentum=0.5).load_state_dict(saved)
+
+
+def test_muon_set_lr():
+    w, g = tensors([(20, 20)], "f32", "f32", 8)
+    opt = tg.Muon([(20, 20)], "f32", lr=0.5)
+    opt.set_lr(0.01)
+    before = [x.clone() for x in w]
+    opt.step(w, g)
+    check_step(opt, w, g, np.zeros(opt.state["momentum"].numel()), before)
+    with pytest.raises(tg.TGradError):
+        opt.set_lr(-1.0)
+
+
+def test_orthogonalize_replays():
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    a, b = (torch.stack([matrix(gen, 70, 50) for _ in range(3)]) for _ in range(2))
+    x = a.clone()
+    tg.orthogonalize(x)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        y = tg.orthogonalize(x)
+    for v in (a, b, a):
+        x.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, tg.orthogonalize(v))
+
+
+def test_refusals():
+    x = torch.zeros(4, 6, 8, device="cuda")
+    for bad, match in ((x[..., ::2], "contiguous"), (x.transpose(1, 2), "contiguous"), (x[0, 0], "two axes"),
+                       (x[0, :1].expand(6, 8), "overlap"), (x[:1].expand(4, 6, 8), "overlap"), (x[:, :0], "empty"),
+                       (x[..., :0], "empty"), (x.to(torch.float64), "dtype"), (x.cpu(), "GPU"),
+                       (x.view(2, 2, 6, 8).transpose(0, 1), "strides")):
+        with pytest.raises(ValueError, match=match):
+            tg.orthogonalize(bad)
+    for kw in (dict(steps=0), dict(steps=101), dict(coefficients=(1.0, 2.0))):
+        with pytest.raises(ValueError):
+            tg.orthogonalize(x, **kw)
+    for kw in (dict(eps=-1.0), dict(coefficients=(1.0, float("nan"), 0.0))):
+        with pytest.raises(tg.TGradError):
+            tg.orthogonalize(x, **kw)
+    opt = tg.Muon([(6, 8)], "f32")
+    w, g = x[0].clone(), x[1].clone()
+    for ws, gs, match in (([w, w], [g], "weights"), ([w], [g, g], "grads"), ([w.half()], [g], "weights"),
+                          ([w], [g.half()], "grads"), ([w.T], [g], "weights"), ([w], [g[:5]], "grads"),
+                          ([w.cpu()], [g], "weights"), ([w], [None], "grads")):
+        with pytest.raises(ValueError, match=match):
+            opt.step(ws, gs)
+    with pytest.raises(ValueError, match="clip"):
+        opt.step([w], [g], clip=torch.zeros(3, device="cuda"))
