@@ -272,9 +272,9 @@ hipError_t launch_tiles(bool grads, const GatedArgs& a, hipStream_t s) {
 template <int DT>
 hipError_t launch_type(bool grads, const GatedArgs& a, hipStream_t s) {
   switch (gated_tile(a.rows, 2 * (int64_t)a.hidden)) {
-    case 0: return launch_tiles<MmShape<256, 256, 2, 4>, DT>(grads, a, s);
-    case 1: return launch_tiles<MmShape<128, 128, 2, 2>, DT>(grads, a, s);
-    default: return launch_tiles<MmShape<64, 64, 2, 2>, DT>(grads, a, s);
+    case 0: return launch_tiles<MmBig, DT>(grads, a, s);
+    case 1: return launch_tiles<MmMid, DT>(grads, a, s);
+    default: return launch_tiles<MmSmall, DT>(grads, a, s);
   }
 }
 hipError_t launch_any(bool grads, const GatedArgs& a, hipStream_t s) {
@@ -291,8 +291,8 @@ int gated_tile(int64_t ni, int64_t nj) {
 
 int64_t gated_sum_rows(int64_t rows, uint32_t in, uint32_t hidden) {
   const int t = gated_tile(rows, 2 * (int64_t)hidden);
-  const int64_t bm = t == 0 ? 256 : t == 1 ? 128 : 64;
-  return (rows + bm - 1) / bm * 2;
+  const int64_t bm = t == 0 ? MmBig::BM : t == 1 ? MmMid::BM : MmSmall::BM;
+  return (rows + bm - 1) / bm * (t == 0 ? MmBig::WM : t == 1 ? MmMid::WM : MmSmall::WM);
 }
 
 hipError_t launch_gated_forward(const GatedArgs& a, hipStream_t s) { return launch_any(false, a, s); }

@@ -175,9 +175,9 @@ hipError_t launch_tiles(K* k, int64_t tiles, int splits, int64_t size, const A& 
   return hipGetLastError();
 }
 
-using Big = MmShape<256, 256, 2, 4>;
-using Mid = MmShape<128, 128, 2, 2>;
-using Small = MmShape<64, 64, 2, 2>;
+using Big = MmBig;
+using Mid = MmMid;
+using Small = MmSmall;
 
 template <int DT>
 hipError_t dx_type(const GatedDx& a, hipStream_t s) {

@@ -387,9 +387,9 @@ hipError_t launch_shape(K* k, uint32_t n, hipStream_t s, const A&... a) {
   k<<<n, S::THREADS, S::LDS_BYTES, s>>>(a...);
   return hipGetLastError();
 }
-using Big = MmShape<256, 256, 2, 4>;
-using Mid = MmShape<128, 128, 2, 2>;
-using Small = MmShape<64, 64, 2, 2>;
+using Big = MmBig;
+using Mid = MmMid;
+using Small = MmSmall;
 
 }  // namespace
 

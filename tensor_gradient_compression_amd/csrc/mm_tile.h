@@ -9,7 +9,7 @@
 // read back as fragments of v_mfma_f32_16x16x32: straight ones 8 values a lane at once, crossed
 // ones by the transposing reads (ds_read_b64_tr_b16: 16 lanes name 4 rows of 16 values, each
 // lane receives its column of them). A transfer fills LDS in lane order, so bank conflicts are
-// avoided by permuting what each lane fetches: a straight row's eight 16-byte pieces by the
+// avoided by permuting what each lane fetches: a straight row's four 16-byte pieces by the
 // row's low bits, a crossed row's 32-byte pairs by those bits of k in which the 32 lanes of a
 // read differ.
 //
@@ -22,6 +22,7 @@
 namespace tg {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -48,29 +49,31 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
 }
 
-// One operand's way into LDS: ROWS rows (or columns of C) by 64 values of k, PER transfers of
+// k values of a stage: what one fragment of a matrix instruction takes.
+constexpr int MM_K = 32;
+
+// One operand's way into LDS: ROWS rows (or columns of C) by 32 values of k, PER transfers of
 // 1 KB for each of WAVES waves.
 template <int ROWS, int WAVES, bool CROSSED>
 struct MmLoader {
-  static constexpr int PER = ROWS / 8 / WAVES;
-  static constexpr int BYTES = ROWS * 128;
-  static_assert(PER * 8 * WAVES == ROWS, "the waves share the transfers evenly");
+  static constexpr int PER = ROWS / 16 / WAVES;
+  static constexpr int BYTES = ROWS * MM_K * 2;
+  static_assert(PER * 16 * WAVES == ROWS, "the waves share the transfers evenly");
   uint32_t v[PER];       // lane's byte offsets from the stage's first byte
   uint32_t k_of_lane;    // straight: the k of the lane's piece within the stage
   uint64_t at;           // the stage's first byte
-  int64_t left;          // bytes from there to the operand's end
+  uint64_t left;         // bytes from there to the operand's end, more than none
 
-  // The row of the tile that transfer i of a wave begins at (straight).
-  __device__ static int row0(int wave, int i) { return (wave * PER + i) * 8; }
-
+  // BY_TURNS: the operand holds every other 16 of the tile's rows
+  template <bool BY_TURNS = false>
   __device__ __forceinline__ void init(int wave, int lane, uint32_t stride) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int q = wave * PER + i;
       if constexpr (!CROSSED) {
-        const int r = lane >> 3;
-        k_of_lane = (uint32_t)(((lane & 7) ^ r) * 8);
-        v[i] = (uint32_t)(q * 8 + r) * (stride * 2) + k_of_lane * 2;
+        const int r = lane >> 2;
+        k_of_lane = (uint32_t)(((lane & 3) ^ ((r >> 1) & 3)) * 8);
+        v[i] = (uint32_t)((BY_TURNS ? q >> 1 : q) * 16 + r) * (stride * 2) + k_of_lane * 2;
       } else {
         constexpr int LANES = ROWS / 8;   // of one k
         const int k = q * (64 / LANES) + lane / LANES, c = lane % LANES;
@@ -82,28 +85,38 @@ struct MmLoader {
   // crossed: how a k's pairs are permuted
   __device__ static constexpr int turn(int k) { return ((k & 3) | (((k >> 3) & 1) << 2)) & (ROWS / 16 - 1); }
 
-  // from row `row` and k = 0 on
-  __device__ __forceinline__ void start(const MmOperand& o, int64_t row) {
-    const uint64_t skip = CROSSED ? (uint64_t)row * 2 : (uint64_t)row * o.stride * 2;
-    at = (uint64_t)o.p + skip;
-    left = ((o.lines - 1) * (int64_t)o.stride + o.len) * 2 - (int64_t)skip;
+  // from row `row` and value `k` of k on
+  __device__ __forceinline__ void start(const MmOperand& o, int64_t row, int64_t k) {
+    const int64_t skip = (CROSSED ? row + k * o.stride : row * o.stride + k) * 2;
+    at = (uint64_t)o.p + (uint64_t)skip;
+    left = (uint64_t)(((o.lines - 1) * (int64_t)o.stride + o.len) * 2 - skip);
   }
-  // past 64 values of k
   __device__ __forceinline__ void next(uint32_t stride) {
-    const uint32_t step = CROSSED ? stride * 128 : 128;
+    const uint32_t step = (CROSSED ? stride : 1) * (MM_K * 2);
     at += step;
     left -= step;
   }
-  // `rem`: values of k from the stage's first one on; `i0`, `n`: which transfers
-  template <int I0 = 0, int N = PER>
-  __device__ __forceinline__ void issue(TG_LDS char* lds, int wave, uint32_t rem) const {
-    const int64_t l = left < 0 ? 0 : left;
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)at, 0, (int)(l > 0xFFFFFFF0ll ? 0xFFFFFFF0u : (uint32_t)l), 0x00020000);
+  // Transfers I0, I0 + STEP, ...; `rem`: values of k from the stage's first one on. Written as
+  // instructions: the compiler would wait for all transfers before any read of LDS.
+  template <int I0 = 0, int STEP = 1>
+  __device__ __forceinline__ void issue(uint32_t lds, int wave, int rem) const {
+    u32x4 rs;
+    rs[0] = (uint32_t)at;
+    rs[1] = (uint32_t)(at >> 32) & 0xFFFFu;
+    rs[2] = (uint32_t)(left >> 32) ? 0xFFFFFFF0u : (uint32_t)left;
+    rs[3] = 0x00020000u;
 #pragma unroll
-    for (int i = I0; i < I0 + N; ++i) {
-      const uint32_t o = CROSSED || k_of_lane < rem ? v[i] : 0xFFFFFFF0u;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (TG_LDS void*)(lds + (wave * PER + i) * 1024), 16, (int)o, 0, 0, 0);
+    for (int i = I0; i < PER; i += STEP) {
+      const uint32_t o = CROSSED || (int)k_of_lane < rem ? v[i] : 0xFFFFFFF0u;
+      // a scalar register that the vector unit wrote takes five states to reach a transfer
+      if (i == I0)
+        __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                         ::"s"(lds + (uint32_t)(wave * PER + i) * 1024u), "v"(o), "s"(rs)
+                         : "memory");
+      else
+        __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                         ::"s"(lds + (uint32_t)(wave * PER + i) * 1024u), "v"(o), "s"(rs)
+                         : "memory");
     }
   }
 };
@@ -111,13 +124,12 @@ struct MmLoader {
 // One operand's fragments: a wave's N blocks of 16 rows from `row` (a multiple of 16 N) on.
 template <int ROWS, int N, bool CROSSED>
 struct MmReader {
-  uint32_t at[CROSSED ? N : 2];
+  uint32_t at[CROSSED ? N : 1];
 
   __device__ __forceinline__ void init(int row, int lane) {
     const int r = lane & 15, kg = lane >> 4;
     if constexpr (!CROSSED) {
-      at[0] = (uint32_t)((row + r) * 128 + ((kg ^ (r & 7)) * 16));
-      at[1] = at[0] ^ 64;
+      at[0] = (uint32_t)((row + r) * 64 + ((kg ^ ((r >> 1) & 3)) * 16));
     } else {
       const int k = kg * 8 + (r >> 2);
 #pragma unroll
@@ -125,12 +137,11 @@ struct MmReader {
         at[i] = (uint32_t)(k * (ROWS * 2) + (((row >> 4) + i) ^ MmLoader<ROWS, 1, true>::turn(k)) * 32 + (r & 3) * 8);
     }
   }
-  // block i, the 32 values of k from 32 half on
-  __device__ __forceinline__ s16x8 get(const TG_LDS char* lds, int i, int half) const {
+  __device__ __forceinline__ s16x8 get(const TG_LDS char* lds, int i) const {
     if constexpr (!CROSSED) {
-      return *(const TG_LDS s16x8*)(lds + at[half] + i * 2048);
+      return *(const TG_LDS s16x8*)(lds + at[0] + i * 1024);
     } else {
-      const TG_LDS char* const a = lds + at[i] + half * (ROWS * 64);
+      const TG_LDS char* const a = lds + at[i];
       const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TG_LDS s16x4*)a);
       const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TG_LDS s16x4*)(a + ROWS * 8));
       return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -146,14 +157,29 @@ __device__ __forceinline__ f32x4 mm_mfma(s16x8 a, s16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// A tile of BM x BN by WM x WN waves.
-template <int BM_, int BN_, int WM_, int WN_>
+// How the waves of a workgroup share a tile.
+//   MM_TURNS  eight waves, each a part of the tile over all of k, in two groups that read
+//             fragments and multiply by turns: one wave of either group is on each SIMD, so the
+//             matrix instructions of one run while the other waits for LDS.
+//   MM_EVEN   four waves, each a part of the tile over all of k; two workgroups fit a CU and
+//             overlap by themselves.
+//   MM_ALONE  four waves, each the whole tile over a quarter of k, from stages of its own and
+//             without a barrier; their sums are added at the end. For few tiles and long sums.
+enum MmMode { MM_TURNS, MM_EVEN, MM_ALONE };
+
+// A tile of BM x BN by WM x WN waves. FM x FN: a wave's blocks of 16 x 16, as it ends with them.
+template <int BM_, int BN_, int WM_, int WN_, MmMode MODE_>
 struct MmShape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr MmMode MODE = MODE_;
   static constexpr int WAVES = WM * WN, THREADS = WAVES * 64;
   static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
-  static constexpr int STAGE = (BM + BN) * 128, LDS_BYTES = 2 * STAGE;
+  static constexpr int STAGE = (BM + BN) * MM_K * 2, STAGES = 4;
+  static constexpr int LDS_BYTES = STAGES * STAGE * (MODE == MM_ALONE ? WAVES : 1);
 };
+using MmBig = MmShape<256, 256, 2, 4, MM_TURNS>;
+using MmMid = MmShape<128, 128, 2, 2, MM_EVEN>;
+using MmSmall = MmShape<64, 64, 4, 1, MM_ALONE>;
 
 // The sums of a wave: c[i][j] holds, in lane l, row 16 i + (l & 15) and columns
 // 16 j + 4 (l >> 4) + 0..3 of the wave's part.
@@ -162,99 +188,195 @@ struct MmSums {
   f32x4 c[S::FM][S::FN];
 };
 
-// `source(s, a, b)` names the operands of segment s; all straight (crossed) As have the stride
-// sa, all Bs sb. k values in each of nseg segments. B's rows may come from two matrices, one
-// for every other 16 (DUAL: source(s, a, b, b2), tile row 32 q + r < 16 from b, 16 more from b2, both
-// at row 16 q + r of them; bj counts in rows of either).
+// `source(s, a, b, b2)` names the operands of segment s; all straight (crossed) As have the
+// stride sa, all Bs sb. k values in each of nseg segments. B's rows may come from two matrices
+// (DUAL): tile row 32 q + r < 16 from b, the 16 after from b2, both at row 16 q + r of them; bj
+// counts in rows of either.
 template <class S, int DT, bool CA, bool CB, bool DUAL, class Source>
 __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const Source& source, int nseg, int64_t k,
                                         int64_t ai, int64_t bj, uint32_t sa, uint32_t sb) {
   static_assert(!DUAL || !CB, "two matrices by turns: straight ones");
+  constexpr bool ALONE = S::MODE == MM_ALONE;
+  constexpr int LOADERS = ALONE ? 1 : S::WAVES;
+  constexpr int FM = ALONE ? S::BM / 16 : S::FM, FN = ALONE ? S::BN / 16 : S::FN;   // while summing
+  constexpr int STAGES = S::STAGES;
   const int tid = threadIdx.x, lane = tid & 63, wave = (int)uniform(tid >> 6);
-  using LA = MmLoader<S::BM, S::WAVES, CA>;
-  using LB = MmLoader<S::BN, S::WAVES, CB>;
+  const int loader = ALONE ? 0 : wave;
+  using LA = MmLoader<S::BM, LOADERS, CA>;
+  using LB = MmLoader<S::BN, LOADERS, CB>;
+  constexpr int LOADS = LA::PER + LB::PER;
   LA la;
   LB lb, lb2;
-  la.init(wave, lane, sa);
-  lb.init(wave, lane, sb);
-  if constexpr (DUAL) {
-    // tile row 8 q + lane / 8 of transfer q: matrix (q >> 1) & 1, its row 16 (q >> 2) + 8 (q & 1) + lane / 8
+  la.init(loader, lane, sa);
+  lb.template init<DUAL>(loader, lane, sb);
+  if constexpr (DUAL) lb2 = lb;
+  MmReader<S::BM, FM, CA> ra;
+  MmReader<S::BN, FN, CB> rb;
+  const int wm = ALONE ? 0 : wave / S::WN, wn = ALONE ? 0 : wave % S::WN;
+  ra.init(wm * FM * 16, lane);
+  rb.init(wn * FN * 16, lane);
+  f32x4 c[FM][FN];
 #pragma unroll
-    for (int i = 0; i < LB::PER; ++i) {
-      const int q = wave * LB::PER + i;
-      lb.v[i] -= (uint32_t)(q * 8 - (16 * (q >> 2) + 8 * (q & 1))) * (sb * 2);
-    }
-  }
-  MmReader<S::BM, S::FM, CA> ra;
-  MmReader<S::BN, S::FN, CB> rb;
-  const int wm = wave / S::WN, wn = wave % S::WN;
-  ra.init(wm * S::FM * 16, lane);
-  rb.init(wn * S::FN * 16, lane);
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
-  for (int i = 0; i < S::FM; ++i)
-#pragma unroll
-    for (int j = 0; j < S::FN; ++j) sums.c[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < FN; ++j) c[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int64_t per_seg = (k + 63) >> 6, total = per_seg * nseg;
-  if (total <= 0) return;
-  int seg = 0;
-  int64_t rem = 0;
+  // this wave's k of every segment
+  int64_t from = 0, many = k;
+  if constexpr (ALONE) {
+    const int64_t quarter = ((k + MM_K * S::WAVES - 1) / (MM_K * S::WAVES)) * MM_K;
+    from = wave * quarter;
+    many = k - from < quarter ? k - from : quarter;
+    lds += wave * (STAGES * S::STAGE);
+  }
+  const int total = many > 0 ? (int)((many + MM_K - 1) / MM_K) * nseg : 0;
+  const uint32_t lds0 = uniform((uint32_t)(uintptr_t)lds);
+  int seg = 0, issued = 0, rem = 0;
+  uint32_t into = 0;       // where the next stage goes
   auto begin = [&](int s) {
     MmOperand a, b, b2;
     source(s, a, b, b2);
-    la.start(a, ai);
-    if constexpr (DUAL && LB::PER == 2) lb.start(wave & 1 ? b2 : b, bj);
-    else lb.start(b, bj);
-    if constexpr (DUAL && LB::PER == 4) lb2.start(b2, bj);
-    rem = k;
+    la.start(a, ai, from);
+    lb.start(b, bj, from);
+    if constexpr (DUAL) lb2.start(b2, bj, from);
+    rem = (int)many;
   };
-  constexpr int LOADS = LA::PER + LB::PER;
-  auto issue = [&](int buf) {
-    TG_LDS char* const l = lds + buf * S::STAGE;
-    const uint32_t r = (uint32_t)(rem < 64 ? rem : 64);
-    la.issue(l, wave, r);
-    if constexpr (!DUAL || LB::PER == 2) {
-      lb.issue(l + LA::BYTES, wave, r);
+  auto after = [&](uint32_t at) { return at == (STAGES - 1) * S::STAGE ? 0u : at + S::STAGE; };
+  auto issue = [&]() {
+    const uint32_t l = lds0 + into;
+    into = after(into);
+    la.issue(l, loader, rem);
+    if constexpr (!DUAL) {
+      lb.issue(l + LA::BYTES, loader, rem);
     } else {
-      // a wave's four transfers: two from either matrix (of two, every other wave's from one)
-      static_assert(LB::PER == 4, "a wave's transfers end where the matrices change");
-#pragma unroll
-      for (int i = 0; i < 4; ++i) lb2.v[i] = lb.v[i];
-      lb2.k_of_lane = lb.k_of_lane;
-      lb.template issue<0, 2>(l + LA::BYTES, wave, r);
-      lb2.template issue<2, 2>(l + LA::BYTES, wave, r);
+      static_assert(LB::PER % 2 == 0, "a wave's transfers: from either matrix by turns");
+      lb.template issue<0, 2>(l + LA::BYTES, loader, rem);
+      lb2.template issue<1, 2>(l + LA::BYTES, loader, rem);
     }
-    rem -= 64;
+    ++issued;
+    rem -= MM_K;
     if (rem > 0) {
       la.next(sa);
       lb.next(sb);
-      if constexpr (DUAL && LB::PER == 4) lb2.next(sb);
+      if constexpr (DUAL) lb2.next(sb);
     } else if (++seg < nseg) {
       begin(seg);
     }
   };
-  begin(0);
-  issue(0);
-  if (total > 1) issue(1);
-  for (int64_t t = 0; t < total; ++t) {
-    if (t + 1 < total) wait_vm<LOADS>();
+  // waits until stage t has arrived
+  auto arrived = [&](int t) {
+    const int behind = issued - 1 - t;
+    if (ALONE && behind >= 3) wait_vm<3 * LOADS>();
+    else if (behind >= 2) wait_vm<2 * LOADS>();
+    else if (behind == 1) wait_vm<LOADS>();
     else wait_vm<0>();
+  };
+  static_assert(STAGES == 4, "two stages behind the one that is awaited, three of a wave alone");
+  auto fragments = [&](uint32_t at, s16x8 (&fa)[FM], s16x8 (&fb)[FN]) {
+    const TG_LDS char* const l = lds + at;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) fb[j] = rb.get(l + LA::BYTES, j);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) fa[i] = ra.get(l, i);
+  };
+  auto multiply = [&](const s16x8 (&fa)[FM], const s16x8 (&fb)[FN]) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) c[i][j] = mm_mfma<DT>(fb[j], fa[i], c[i][j]);
+  };
+  if (total > 0) {
+    begin(0);
+    issue();
+    if (total > 1) issue();
+    if (total > 2) issue();
+    if (ALONE && total > 3) issue();
+  }
+  int t = 0;
+  uint32_t at = 0;
+  if constexpr (S::MODE == MM_TURNS) {
+    const int group = wave >> 2;
+    if (total > 0) arrived(0);
     lds_barrier();
-    const TG_LDS char* const l = lds + (t & 1) * S::STAGE;
-    s16x8 fa[S::FM], fb[S::FN];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int j = 0; j < S::FN; ++j) fb[j] = rb.get(l + LA::BYTES, j, h);
-#pragma unroll
-      for (int i = 0; i < S::FM; ++i) fa[i] = ra.get(l, i, h);
-#pragma unroll
-      for (int i = 0; i < S::FM; ++i)
-#pragma unroll
-        for (int j = 0; j < S::FN; ++j) sums.c[i][j] = mm_mfma<DT>(fb[j], fa[i], sums.c[i][j]);
+    if (group) lds_barrier();
+    auto product = [&](const s16x8 (&fa)[FM], const s16x8 (&fb)[FN]) {
+      lds_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_setprio(1);
+      multiply(fa, fb);
+      __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_sched_barrier(0);
+      lds_barrier();
+    };
+    for (; t + 3 < total; ++t, at = after(at)) {
+      s16x8 fa[FM], fb[FN];
+      fragments(at, fa, fb);
+      // into the stage before this one: both groups' reads of it ended at a barrier since
+      issue();
+      wait_vm<2 * LOADS>();
+      product(fa, fb);
     }
+    for (; t < total; ++t, at = after(at)) {
+      s16x8 fa[FM], fb[FN];
+      fragments(at, fa, fb);
+      if (t + 1 < total) arrived(t + 1);
+      product(fa, fb);
+    }
+    if (!group) lds_barrier();
+  } else if constexpr (S::MODE == MM_EVEN) {
+    for (; t < total; ++t, at = after(at)) {
+      arrived(t);
+      lds_barrier();       // every wave's part of this stage is there, and the one before is read
+      s16x8 fa[FM], fb[FN];
+      fragments(at, fa, fb);
+      if (issued < total) issue();
+      multiply(fa, fb);
+    }
+  } else {
+    // a stage's fragments are read while the one before is multiplied
+    s16x8 fa[2][FM], fb[2][FN];
+    if (total > 0) {
+      arrived(0);
+      fragments(at, fa[0], fb[0]);
+    }
+    for (; t < total; t += 2) {
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        if (t + o >= total) break;
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // this stage's fragments are read and its place is free
+        if (issued < total) issue();
+        at = after(at);
+        if (t + o + 1 < total) {
+          arrived(t + o + 1);
+          fragments(at, fa[o ^ 1], fb[o ^ 1]);
+        }
+        multiply(fa[o], fb[o]);
+      }
+    }
+  }
+  if constexpr (!ALONE) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) sums.c[i][j] = c[i][j];
+  } else {
+    // every wave's sums to LDS; wave w then adds those of its row of blocks, in the waves' order
+    lds -= wave * (STAGES * S::STAGE);
     lds_barrier();
-    if (t + 2 < total) issue((int)(t & 1));
+    TG_LDS f32x4* const all = (TG_LDS f32x4*)lds;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) all[((wave * FM + i) * FN + j) * 64 + lane] = c[i][j];
+    lds_barrier();
+    static_assert(S::FM * S::WAVES == FM && S::FN == FN, "a row of blocks for each wave");
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      f32x4 s = all[(wave * FN + j) * 64 + lane];
+#pragma unroll
+      for (int w = 1; w < S::WAVES; ++w) s += all[((w * FM + wave) * FN + j) * 64 + lane];
+      sums.c[0][j] = s;
+    }
   }
 }
 
