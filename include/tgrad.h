@@ -531,8 +531,8 @@ int tgrad_layer_norm_backward(const void *dy, int64_t dy_stride, const void *x, 
  *   out        device, contiguous, of x's type; may be x where that is contiguous
  *   dtype      TGRAD_F32, TGRAD_F16 or TGRAD_BF16
  *   steps      1 to 100;  coefficients: host, three finite values;  eps >= 0, finite
- *   workspace  device, tgrad_orthogonalize_workspace bytes, 16-byte aligned. It may be reused
- *              once the stream's work is done.
+ *   workspace  device, tgrad_orthogonalize_workspace bytes, 16-byte aligned (NULL for 0). It may
+ *              be reused once the stream's work is done.
  * count = 0 is valid. 1 <= rows, cols <= 2^19, and at most 2^21 workgroups' parts in a launch.
  * Errors: TGRAD_EINVAL, TGRAD_EHIP. The workspace's size is -1 for invalid sizes (host only). */
 int64_t tgrad_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols, int dtype);

@@ -491,9 +491,10 @@ PyObject* orthogonalize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t bytes = tgrad_orthogonalize_workspace(count, rows, cols, dt);
     if (bytes < 0) throw Invalid{"x: too many rows, columns or matrices"};
     const c10::DeviceGuard guard(x.device());
-    at::Tensor out = empty(x.sizes(), x.scalar_type(), dev), ws = empty({bytes}, at::kByte, dev);
+    at::Tensor out = empty(x.sizes(), x.scalar_type(), dev), ws;
+    if (bytes) ws = empty({bytes}, at::kByte, dev);
     check_rc(tgrad_orthogonalize(data_of(x), stride, row, data_of(out), count, rows, cols, dt, (int)steps, co, eps,
-                                 data_of(ws), pointer(Py_None, dev)),
+                                 bytes ? data_of(ws) : nullptr, pointer(Py_None, dev)),
              "tgrad_orthogonalize", "");
     return THPVariable_Wrap(out);
   });

@@ -11,6 +11,8 @@
 // fp32 values are multiplied in three bf16 parts, which add up to them exactly, by six of the
 // nine products of parts; the three that are left out are 2^-24 of the whole and less. The
 // matrix instructions do 16 times as much in bf16 as in fp32.
+#include <type_traits>
+
 #include "gated.h"
 
 namespace tg {
@@ -19,47 +21,55 @@ namespace {
 
 // Phi(-x) for x >= 0, the normal distribution's lower tail: t 2^(p(t) - x^2 log2(e) / 2) with
 // t = 1 / (1 + x / sqrt(8)) and p a polynomial fitted to log2(erfcx(x / sqrt 2) / 2t) at
-// Chebyshev points; 3.4e-7 of the value for every x (SHORT: 9.7e-7).
-template <bool SHORT>
+// Chebyshev points; 3.4e-7 of the value for every x.
 __device__ __forceinline__ float normal_tail(float x) {
   const float t = __builtin_amdgcn_rcpf(1.0f + 0.353553391f * x);
-  float p;
-  if constexpr (SHORT) {
-    p = -0.273941745f;
-    p = __builtin_fmaf(p, t, 1.09719799f);
-    p = __builtin_fmaf(p, t, -1.46694501f);
-    p = __builtin_fmaf(p, t, 0.526053097f);
-    p = __builtin_fmaf(p, t, -0.0686230273f);
-    p = __builtin_fmaf(p, t, 0.571813192f);
-    p = __builtin_fmaf(p, t, 1.44010662f);
-    p = __builtin_fmaf(p, t, -2.82566219f);
-  } else {
-    p = 0.253258819f;
-    p = __builtin_fmaf(p, t, -1.21736752f);
-    p = __builtin_fmaf(p, t, 2.20788314f);
-    p = __builtin_fmaf(p, t, -1.70057641f);
-    p = __builtin_fmaf(p, t, 0.440011764f);
-    p = __builtin_fmaf(p, t, -0.281599746f);
-    p = __builtin_fmaf(p, t, 0.141806747f);
-    p = __builtin_fmaf(p, t, 0.53962246f);
-    p = __builtin_fmaf(p, t, 1.4427072f);
-    p = __builtin_fmaf(p, t, -2.82574634f);
-  }
+  float p = 0.253258819f;
+  p = __builtin_fmaf(p, t, -1.21736752f);
+  p = __builtin_fmaf(p, t, 2.20788314f);
+  p = __builtin_fmaf(p, t, -1.70057641f);
+  p = __builtin_fmaf(p, t, 0.440011764f);
+  p = __builtin_fmaf(p, t, -0.281599746f);
+  p = __builtin_fmaf(p, t, 0.141806747f);
+  p = __builtin_fmaf(p, t, 0.53962246f);
+  p = __builtin_fmaf(p, t, 1.4427072f);
+  p = __builtin_fmaf(p, t, -2.82574634f);
   return t * __builtin_amdgcn_exp2f(__builtin_fmaf(x * -0.721347520f, x, p));
+}
+// The same for 16-bit results: a polynomial fitted to log2 Phi(-x) for x up to 6.5 (7.4e-6 of
+// the value; Phi(-6.5) is 4e-11) that falls ever faster beyond.
+__device__ __forceinline__ float short_normal_tail(float x) {
+  float p = -1.76984737e-6f;
+  p = __builtin_fmaf(p, x, 6.02403488e-5f);
+  p = __builtin_fmaf(p, x, -9.19429847e-4f);
+  p = __builtin_fmaf(p, x, 8.46320244e-3f);
+  p = __builtin_fmaf(p, x, -5.38683020e-2f);
+  p = __builtin_fmaf(p, x, -4.58553402e-1f);
+  p = __builtin_fmaf(p, x, -1.15121899f);
+  p = __builtin_fmaf(p, x, -0.999997157f);
+  return __builtin_amdgcn_exp2f(p);
 }
 
 constexpr float kLog2e = 1.44269504f;
 
-// act(g), and act'(g) for the gradients
-template <bool SHORT, bool SLOPE>
-__device__ __forceinline__ float activate(float g, int act, float& slope) {
-  if (act == GATED_RELU) {
-    // a NaN stays one
+// act(g), and act'(g) for the gradients. SHORT: for 16-bit results, in fewer instructions: an
+// epilogue of 67M GELUs is bound by them. A NaN stays one, and infinities give the limits.
+template <int ACT, bool SHORT, bool SLOPE>
+__device__ __forceinline__ float activate(float g, float& slope) {
+  const float x = __builtin_fabsf(g);
+  if constexpr (ACT == GATED_RELU) {
     if (SLOPE) slope = g > 0.0f ? 1.0f : 0.0f;
     return g < 0.0f ? 0.0f : g;
-  }
-  if (act == GATED_GELU) {
-    const float tail = normal_tail<SHORT>(__builtin_fabsf(g));
+  } else if constexpr (ACT == GATED_GELU && SHORT) {
+    // g Phi(g) = max(g, 0) - |g| Phi(-|g|);  its slope 1/2 +- (1/2 - Phi(-|g|) + |g| phi(g))
+    const float tail = short_normal_tail(x), near = __builtin_fminf(x, 30.0f);
+    if (SLOPE) {
+      const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(g * -0.721347520f, g, -1.32574806f));
+      slope = 0.5f + __builtin_copysignf(__builtin_fmaf(near, e, 0.5f - tail), g);
+    }
+    return __builtin_fmaf(0.5f, g + x, -near * tail);
+  } else if constexpr (ACT == GATED_GELU) {
+    const float tail = normal_tail(x);
     const float cdf = g < 0.0f ? tail : 1.0f - tail;
     if (SLOPE) {
       const float e = 0.398942280f * __builtin_amdgcn_exp2f(g * -0.721347520f * g);
@@ -67,17 +77,36 @@ __device__ __forceinline__ float activate(float g, int act, float& slope) {
     }
     // -infinity times a tail of zero is the limit, zero
     return tail == 0.0f ? (g < 0.0f ? 0.0f : g) : g * cdf;
+  } else if constexpr (SHORT) {
+    const float r = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * g));
+    if constexpr (ACT == GATED_SIGMOID) {
+      if (SLOPE) slope = __builtin_fmaf(-r, r, r);
+      return r;
+    }
+    const float low = __builtin_fmaxf(g, -200.0f);
+    if (SLOPE) slope = __builtin_fmaf(__builtin_fminf(low, 200.0f) * r, 1.0f - r, r);
+    return low * r;
+  } else {
+    // 1 / (1 + e^-|g|) and its counterpart e^-|g| / (1 + e^-|g|)
+    const float e = __builtin_amdgcn_exp2f(-kLog2e * x);
+    const float r = __builtin_amdgcn_rcpf(1.0f + e);
+    const float p = g < 0.0f ? e * r : r, q = g < 0.0f ? r : e * r;
+    if constexpr (ACT == GATED_SIGMOID) {
+      if (SLOPE) slope = p * q;
+      return p;
+    }
+    if (SLOPE) slope = q == 0.0f ? p : p == 0.0f ? 0.0f : p * __builtin_fmaf(g, q, 1.0f);
+    return p == 0.0f ? 0.0f : g * p;
   }
-  // 1 / (1 + e^-|g|) and its counterpart e^-|g| / (1 + e^-|g|)
-  const float e = __builtin_amdgcn_exp2f(-kLog2e * __builtin_fabsf(g));
-  const float r = __builtin_amdgcn_rcpf(1.0f + e);
-  const float p = g < 0.0f ? e * r : r, q = g < 0.0f ? r : e * r;
-  if (act == GATED_SIGMOID) {
-    if (SLOPE) slope = p * q;
-    return p;
-  }
-  if (SLOPE) slope = q == 0.0f ? p : p == 0.0f ? 0.0f : p * __builtin_fmaf(g, q, 1.0f);
-  return p == 0.0f ? 0.0f : g * p;
+}
+
+// f with the activation as a constant
+template <class F>
+__device__ __forceinline__ void with_activation(int act, const F& f) {
+  if (act == GATED_SILU) f(std::integral_constant<int, GATED_SILU>{});
+  else if (act == GATED_GELU) f(std::integral_constant<int, GATED_GELU>{});
+  else if (act == GATED_SIGMOID) f(std::integral_constant<int, GATED_SIGMOID>{});
+  else f(std::integral_constant<int, GATED_RELU>{});
 }
 
 template <class S, int DT>
@@ -114,26 +143,29 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_forward(const GatedArgs
   const int lane = threadIdx.x & 63, wave = (int)uniform(threadIdx.x >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
   const bool aligned = (a.hidden % 4) == 0 && ((uintptr_t)a.y & (4 * sizeof(T) - 1)) == 0;
+  with_activation(a.act, [&](auto act) {
+    constexpr int ACT = decltype(act)::value;
 #pragma unroll
-  for (int j = 0; j < S::FN; j += 2) {
-    const uint32_t f = f0 + (wn * S::FN + j) * 8 + (lane >> 4) * 4;
-    float bg[4], bu[4];
-    bias4<T>(a.bg, f, a.hidden, bg);
-    bias4<T>(a.bu, f, a.hidden, bu);
+    for (int j = 0; j < S::FN; j += 2) {
+      const uint32_t f = f0 + (wn * S::FN + j) * 8 + (lane >> 4) * 4;
+      float bg[4], bu[4];
+      bias4<T>(a.bg, f, a.hidden, bg);
+      bias4<T>(a.bu, f, a.hidden, bu);
 #pragma unroll
-    for (int i = 0; i < S::FM; ++i) {
-      const int64_t m = row0 + (wm * S::FM + i) * 16 + (lane & 15);
-      if (m >= a.rows || f >= a.hidden) continue;
-      T y[4];
+      for (int i = 0; i < S::FM; ++i) {
+        const int64_t m = row0 + (wm * S::FM + i) * 16 + (lane & 15);
+        if (m >= a.rows || f >= a.hidden) continue;
+        T y[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float slope;
-        const float p = activate<DT != DT_F32, false>(sums.c[i][j][e] + bg[e], a.act, slope);
-        y[e] = from_f32<T>(p * (sums.c[i][j + 1][e] + bu[e]));
+        for (int e = 0; e < 4; ++e) {
+          float slope;
+          const float p = activate<ACT, DT != DT_F32, false>(sums.c[i][j][e] + bg[e], slope);
+          y[e] = from_f32<T>(p * (sums.c[i][j + 1][e] + bu[e]));
+        }
+        store4((T*)a.y + m * a.hidden + f, y, (int)(a.hidden - f < 4 ? a.hidden - f : 4), aligned);
       }
-      store4((T*)a.y + m * a.hidden + f, y, (int)(a.hidden - f < 4 ? a.hidden - f : 4), aligned);
     }
-  }
+  });
 }
 
 template <class S, int DT>
@@ -153,78 +185,81 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_grads(const GatedArgs a
   const uint32_t pad = gated_pad(a.hidden);
   const int64_t part = a.rows * 2 * (int64_t)pad;
   const bool aligned = (a.hidden % 4) == 0 && (a.dy_stride % 4) == 0 && ((uintptr_t)a.dy & (4 * sizeof(T) - 1)) == 0;
+  with_activation(a.act, [&](auto act) {
+    constexpr int ACT = decltype(act)::value;
 #pragma unroll
-  for (int j = 0; j < S::FN; j += 2) {
-    const uint32_t f = f0 + (wn * S::FN + j) * 8 + (lane >> 4) * 4;
-    float bg[4], bu[4];
-    bias4<T>(a.bg, f, a.hidden, bg);
-    bias4<T>(a.bu, f, a.hidden, bu);
-    f32x4 sg = {0.f, 0.f, 0.f, 0.f}, su = sg;
+    for (int j = 0; j < S::FN; j += 2) {
+      const uint32_t f = f0 + (wn * S::FN + j) * 8 + (lane >> 4) * 4;
+      float bg[4], bu[4];
+      bias4<T>(a.bg, f, a.hidden, bg);
+      bias4<T>(a.bu, f, a.hidden, bu);
+      f32x4 sg = {0.f, 0.f, 0.f, 0.f}, su = sg;
 #pragma unroll
-    for (int i = 0; i < S::FM; ++i) {
-      const int64_t m = row0 + (wm * S::FM + i) * 16 + (lane & 15);
-      if (m >= a.rows || f >= pad) continue;
-      T dy[4] = {};
-      const T* const src = (const T*)a.dy + m * a.dy_stride + f;
-      if (aligned && f < a.hidden) {
-        __builtin_memcpy(dy, __builtin_assume_aligned(src, 4 * sizeof(T)), 4 * sizeof(T));
-      } else {
+      for (int i = 0; i < S::FM; ++i) {
+        const int64_t m = row0 + (wm * S::FM + i) * 16 + (lane & 15);
+        if (m >= a.rows || f >= pad) continue;
+        T dy[4] = {};
+        const T* const src = (const T*)a.dy + m * a.dy_stride + f;
+        if (aligned && f < a.hidden) {
+          __builtin_memcpy(dy, __builtin_assume_aligned(src, 4 * sizeof(T)), 4 * sizeof(T));
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (f + e < a.hidden) dy[e] = src[e];
-      }
-      float dg[4], du[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float slope;
-        const float d = to_f32(dy[e]);
-        const float p = activate<DT != DT_F32, true>(sums.c[i][j][e] + bg[e], a.act, slope);
-        const bool in = f + e < a.hidden;     // zeros behind
-        dg[e] = in ? d * (sums.c[i][j + 1][e] + bu[e]) * slope : 0.0f;
-        du[e] = in ? d * p : 0.0f;
-        sg[e] += dg[e];
-        su[e] += du[e];
-      }
-      if constexpr (DT == DT_F32) {
-        bf16_t g[3][4], u[3][4];
+          for (int e = 0; e < 4; ++e)
+            if (f + e < a.hidden) dy[e] = src[e];
+        }
+        float dg[4], du[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          bf16_t p[3];
-          three_parts(dg[e], p);
-          for (int q = 0; q < 3; ++q) g[q][e] = p[q];
-          three_parts(du[e], p);
-          for (int q = 0; q < 3; ++q) u[q][e] = p[q];
+          float slope;
+          const float d = to_f32(dy[e]);
+          const float p = activate<ACT, DT != DT_F32, true>(sums.c[i][j][e] + bg[e], slope);
+          const bool in = f + e < a.hidden;     // zeros behind
+          dg[e] = in ? d * (sums.c[i][j + 1][e] + bu[e]) * slope : 0.0f;
+          du[e] = in ? d * p : 0.0f;
+          sg[e] += dg[e];
+          su[e] += du[e];
         }
+        if constexpr (DT == DT_F32) {
+          bf16_t g[3][4], u[3][4];
 #pragma unroll
-        for (int q = 0; q < 3; ++q) {
-          bf16_t* const d = (bf16_t*)a.grads + q * part + m * 2 * (int64_t)pad + f;
-          store4(d, g[q], 4, true);
-          store4(d + pad, u[q], 4, true);
+          for (int e = 0; e < 4; ++e) {
+            bf16_t p[3];
+            three_parts(dg[e], p);
+            for (int q = 0; q < 3; ++q) g[q][e] = p[q];
+            three_parts(du[e], p);
+            for (int q = 0; q < 3; ++q) u[q][e] = p[q];
+          }
+#pragma unroll
+          for (int q = 0; q < 3; ++q) {
+            bf16_t* const d = (bf16_t*)a.grads + q * part + m * 2 * (int64_t)pad + f;
+            store4(d, g[q], 4, true);
+            store4(d + pad, u[q], 4, true);
+          }
+        } else {
+          T g[4], u[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) g[e] = from_f32<T>(dg[e]), u[e] = from_f32<T>(du[e]);
+          T* const d = (T*)a.grads + m * 2 * (int64_t)pad + f;
+          store4(d, g, 4, true);
+          store4(d + pad, u, 4, true);
         }
-      } else {
-        T g[4], u[4];
+      }
+      if (a.row_sums) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) g[e] = from_f32<T>(dg[e]), u[e] = from_f32<T>(du[e]);
-        T* const d = (T*)a.grads + m * 2 * (int64_t)pad + f;
-        store4(d, g, 4, true);
-        store4(d + pad, u, 4, true);
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int o = 1; o < 16; o <<= 1) {
+            sg[e] += __shfl_xor(sg[e], o);
+            su[e] += __shfl_xor(su[e], o);
+          }
+        if ((lane & 15) == 0 && f < pad) {
+          float* const r = a.row_sums + ((int64_t)ti * S::WM + wm) * 2 * (int64_t)pad + f;
+          *(f32x4*)r = sg;
+          *(f32x4*)(r + pad) = su;
+        }
       }
     }
-    if (a.row_sums) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) {
-          sg[e] += __shfl_xor(sg[e], o);
-          su[e] += __shfl_xor(su[e], o);
-        }
-      if ((lane & 15) == 0 && f < pad) {
-        float* const r = a.row_sums + ((int64_t)ti * S::WM + wm) * 2 * (int64_t)pad + f;
-        *(f32x4*)r = sg;
-        *(f32x4*)(r + pad) = su;
-      }
-    }
-  }
+  });
 }
 
 // One workgroup's 256 pieces of 8 values of a row-padded copy.
@@ -271,7 +306,7 @@ hipError_t launch_tiles(bool grads, const GatedArgs& a, hipStream_t s) {
 }
 template <int DT>
 hipError_t launch_type(bool grads, const GatedArgs& a, hipStream_t s) {
-  switch (gated_tile(a.rows, 2 * (int64_t)a.hidden)) {
+  switch (gated_tile(a.rows, 2 * (int64_t)a.hidden, a.in)) {
     case 0: return launch_tiles<MmBig, DT>(grads, a, s);
     case 1: return launch_tiles<MmMid, DT>(grads, a, s);
     default: return launch_tiles<MmSmall, DT>(grads, a, s);
@@ -284,13 +319,13 @@ hipError_t launch_any(bool grads, const GatedArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int gated_tile(int64_t ni, int64_t nj) {
+int gated_tile(int64_t ni, int64_t nj, int64_t k) {
   const int64_t big = ((ni + 255) / 256) * ((nj + 255) / 256), mid = ((ni + 127) / 128) * ((nj + 127) / 128);
-  return big >= 200 ? 0 : mid >= 200 ? 1 : 2;
+  return big >= 200 && k > 512 ? 0 : mid >= 200 ? 1 : 2;
 }
 
 int64_t gated_sum_rows(int64_t rows, uint32_t in, uint32_t hidden) {
-  const int t = gated_tile(rows, 2 * (int64_t)hidden);
+  const int t = gated_tile(rows, 2 * (int64_t)hidden, in);
   const int64_t bm = t == 0 ? MmBig::BM : t == 1 ? MmMid::BM : MmSmall::BM;
   return (rows + bm - 1) / bm * (t == 0 ? MmBig::WM : t == 1 ? MmMid::WM : MmSmall::WM);
 }

@@ -19,10 +19,12 @@
 // 1.7e-3); most of it is the lower part of X that B X leaves out. For fp32 and fp16 results the products take both parts of X, A and B
 // (three products of parts; 3e-7 to 1e-5), which is `exact` here.
 //
-// What bounds it. 4 m^2 n + ... operations: matrix instructions for large matrices, launches
-// (two, and three for every step) for small ones. All matrices of a handle share every launch.
+// What bounds it: matrix instructions for large matrices, launches (two, and three for every
+// step) for middle ones; small ones are k_muon_small.hip's. All matrices of a handle share every
+// launch.
 // Of the symmetric products only the tiles on and below the diagonal are formed.
 #include "muon.h"
+#include "muon_common.h"
 
 namespace tg {
 
@@ -32,51 +34,6 @@ namespace {
 
 constexpr uint32_t kPartsA = 0x001, kPartsB = 0x010;   // lower upper, upper lower, upper upper
 
-__device__ __forceinline__ bool left_out(const NsCommon& c) {
-  return c.clip && !(__builtin_fabsf(c.clip[0]) <= 3.40282347e38f);
-}
-
-// this workgroup's matrix (its offsets those of its own) and part
-__device__ __forceinline__ uint32_t my_part(const NsCommon& c, const NsParts& p, uint32_t b, NsMat& m, uint32_t& i,
-                                            uint32_t& j) {
-  if (p.list) {
-    const NsPart q = p.list[b];
-    m = c.mats[q.mat];
-    i = q.i;
-    j = q.j;
-    return q.mat;
-  }
-  const uint32_t each = p.lower ? p.ni * (p.ni + 1) / 2 : p.ni * p.nj, mat = b / each, t = b - mat * each;
-  if (p.lower) {
-    i = (uint32_t)((__builtin_sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
-    while (i * (i + 1) / 2 > t) --i;
-    while ((i + 1) * (i + 2) / 2 <= t) ++i;
-    j = t - i * (i + 1) / 2;
-  } else {
-    tile_at(t, p.ni, p.nj, i, j);
-  }
-  m = c.one;
-  const uint64_t o = mat * c.pitch;
-  m.x += o;
-  m.y += o;
-  m.a += o;
-  m.b += o;
-  m.da += o;
-  m.db += o;
-  m.sums += o;
-  return mat;
-}
-
-__device__ __forceinline__ float load_as(const void* p, uint32_t dt, uint64_t i) {
-  return dt == DT_F32 ? ((const float*)p)[i] : dt == DT_F16 ? to_f32(((const _Float16*)p)[i]) : to_f32(((const bf16_t*)p)[i]);
-}
-
-// v as two fp16 parts
-__device__ __forceinline__ void two_parts(float v, _Float16& hi, _Float16& lo) {
-  hi = (_Float16)v;
-  lo = (_Float16)(v - (float)hi);
-}
-
 __device__ __forceinline__ void workgroup_sum(double s, double* out) {
   __shared__ double w[4];
 #pragma unroll
@@ -85,8 +42,6 @@ __device__ __forceinline__ void workgroup_sum(double s, double* out) {
   __syncthreads();
   if (threadIdx.x == 0) *out = (w[0] + w[1]) + (w[2] + w[3]);
 }
-
-__device__ __forceinline__ float updated(float g, float m, const MuonFirst& f) { return f.nesterov ? f.nu * g + f.mu * m : m; }
 
 __global__ void __launch_bounds__(256) k_muon_first(const NsCommon c, const MuonFirst f, const MuonTable t,
                                                     const NsParts p) {
@@ -371,9 +326,7 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_ns_apply(const NsCommon c, co
       if (j + e >= m.cols) continue;
       float y = r[e] * (1.0f / NS_X);
       if (last.w) y = load_as(out, m.wdt, to + e) * decay - step * y;
-      if (m.wdt == DT_F32) ((float*)out)[to + e] = y;
-      else if (m.wdt == DT_F16) ((_Float16*)out)[to + e] = from_f32<_Float16>(y);
-      else ((bf16_t*)out)[to + e] = from_f32<bf16_t>(y);
+      store_as(out, m.wdt, to + e, y);
     }
   });
 }

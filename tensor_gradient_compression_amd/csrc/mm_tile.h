@@ -9,8 +9,8 @@
 // read back as fragments of v_mfma_f32_16x16x32: straight ones 8 values a lane at once, crossed
 // ones by the transposing reads (ds_read_b64_tr_b16: 16 lanes name 4 rows of 16 values, each
 // lane receives its column of them). A transfer fills LDS in lane order, so bank conflicts are
-// avoided by permuting what each lane fetches: a straight row's four 16-byte pieces by the
-// row's low bits, a crossed row's 32-byte pairs by those bits of k in which the 32 lanes of a
+// avoided by permuting what each lane fetches: a straight row's 16-byte pieces by the row's
+// low bits, a crossed row's 32-byte pairs by those bits of k in which the 32 lanes of a
 // read differ.
 //
 // k may run over several segments, each with operands of its own: a value held in two or three
@@ -49,16 +49,14 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
 }
 
-// k values of a stage: what one fragment of a matrix instruction takes.
-constexpr int MM_K = 32;
-
-// One operand's way into LDS: ROWS rows (or columns of C) by 32 values of k, PER transfers of
+// One operand's way into LDS: ROWS rows (or columns of C) by K values of k, PER transfers of
 // 1 KB for each of WAVES waves.
-template <int ROWS, int WAVES, bool CROSSED>
+template <int ROWS, int K, int WAVES, bool CROSSED>
 struct MmLoader {
-  static constexpr int PER = ROWS / 16 / WAVES;
-  static constexpr int BYTES = ROWS * MM_K * 2;
-  static_assert(PER * 16 * WAVES == ROWS, "the waves share the transfers evenly");
+  static constexpr int BYTES = ROWS * K * 2;
+  static constexpr int PER = BYTES / 1024 / WAVES;
+  static constexpr int PIECES = K / 8;   // of a straight row
+  static_assert(PER * 1024 * WAVES == BYTES, "the waves share the transfers evenly");
   uint32_t v[PER];       // lane's byte offsets from the stage's first byte
   uint32_t k_of_lane;    // straight: the k of the lane's piece within the stage
   uint64_t at;           // the stage's first byte
@@ -71,9 +69,11 @@ struct MmLoader {
     for (int i = 0; i < PER; ++i) {
       const int q = wave * PER + i;
       if constexpr (!CROSSED) {
-        const int r = lane >> 2;
-        k_of_lane = (uint32_t)(((lane & 3) ^ ((r >> 1) & 3)) * 8);
-        v[i] = (uint32_t)((BY_TURNS ? q >> 1 : q) * 16 + r) * (stride * 2) + k_of_lane * 2;
+        constexpr int LINES = 64 / PIECES;   // of a transfer
+        const int r = lane / PIECES;
+        k_of_lane = (uint32_t)(((lane % PIECES) ^ turn_row(r)) * 8);
+        const int row = q * LINES + r;
+        v[i] = (uint32_t)(BY_TURNS ? (row >> 5) * 16 + (row & 15) : row) * (stride * 2) + k_of_lane * 2;
       } else {
         constexpr int LANES = ROWS / 8;   // of one k
         const int k = q * (64 / LANES) + lane / LANES, c = lane % LANES;
@@ -82,7 +82,8 @@ struct MmLoader {
       }
     }
   }
-  // crossed: how a k's pairs are permuted
+  // straight: how a row's pieces are permuted; crossed: how a k's pairs are
+  __device__ static constexpr int turn_row(int r) { return K == 64 ? r & 7 : (r >> 1) & 3; }
   __device__ static constexpr int turn(int k) { return ((k & 3) | (((k >> 3) & 1) << 2)) & (ROWS / 16 - 1); }
 
   // from row `row` and value `k` of k on
@@ -92,13 +93,16 @@ struct MmLoader {
     left = (uint64_t)(((o.lines - 1) * (int64_t)o.stride + o.len) * 2 - skip);
   }
   __device__ __forceinline__ void next(uint32_t stride) {
-    const uint32_t step = (CROSSED ? stride : 1) * (MM_K * 2);
+    const uint32_t step = (CROSSED ? stride : 1) * (K * 2);
     at += step;
     left -= step;
   }
-  // Transfers I0, I0 + STEP, ...; `rem`: values of k from the stage's first one on. Written as
-  // instructions: the compiler would wait for all transfers before any read of LDS.
-  template <int I0 = 0, int STEP = 1>
+  // Whether transfer i is of the second matrix of two that alternate.
+  __device__ static constexpr bool second(int i) { return ((i * (64 / PIECES)) >> 4) & 1; }
+
+  // The transfers (BY_TURNS: those of one matrix); `rem`: values of k from the stage's first one
+  // on. Written as instructions: the compiler would wait for all transfers before any read of LDS.
+  template <bool BY_TURNS = false, bool SECOND = false>
   __device__ __forceinline__ void issue(uint32_t lds, int wave, int rem) const {
     u32x4 rs;
     rs[0] = (uint32_t)at;
@@ -106,10 +110,11 @@ struct MmLoader {
     rs[2] = (uint32_t)(left >> 32) ? 0xFFFFFFF0u : (uint32_t)left;
     rs[3] = 0x00020000u;
 #pragma unroll
-    for (int i = I0; i < PER; i += STEP) {
+    for (int i = 0; i < PER; ++i) {
+      if (BY_TURNS && second(i) != SECOND) continue;
       const uint32_t o = CROSSED || (int)k_of_lane < rem ? v[i] : 0xFFFFFFF0u;
       // a scalar register that the vector unit wrote takes five states to reach a transfer
-      if (i == I0)
+      if (i == 0 || (BY_TURNS && SECOND && !second(i - 1)))
         __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                          ::"s"(lds + (uint32_t)(wave * PER + i) * 1024u), "v"(o), "s"(rs)
                          : "memory");
@@ -122,26 +127,29 @@ struct MmLoader {
 };
 
 // One operand's fragments: a wave's N blocks of 16 rows from `row` (a multiple of 16 N) on.
-template <int ROWS, int N, bool CROSSED>
+template <int ROWS, int K, int N, bool CROSSED>
 struct MmReader {
-  uint32_t at[CROSSED ? N : 1];
+  uint32_t at[CROSSED ? N : K / 32];
 
   __device__ __forceinline__ void init(int row, int lane) {
+    using L = MmLoader<ROWS, K, 1, CROSSED>;
     const int r = lane & 15, kg = lane >> 4;
     if constexpr (!CROSSED) {
-      at[0] = (uint32_t)((row + r) * 64 + ((kg ^ ((r >> 1) & 3)) * 16));
+      at[0] = (uint32_t)((row + r) * (K * 2) + ((kg ^ L::turn_row(r)) * 16));
+      if constexpr (K == 64) at[1] = at[0] ^ 64;
     } else {
       const int k = kg * 8 + (r >> 2);
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        at[i] = (uint32_t)(k * (ROWS * 2) + (((row >> 4) + i) ^ MmLoader<ROWS, 1, true>::turn(k)) * 32 + (r & 3) * 8);
+        at[i] = (uint32_t)(k * (ROWS * 2) + (((row >> 4) + i) ^ L::turn(k)) * 32 + (r & 3) * 8);
     }
   }
-  __device__ __forceinline__ s16x8 get(const TG_LDS char* lds, int i) const {
+  // block i, the 32 values of k from 32 part on
+  __device__ __forceinline__ s16x8 get(const TG_LDS char* lds, int i, int part) const {
     if constexpr (!CROSSED) {
-      return *(const TG_LDS s16x8*)(lds + at[0] + i * 1024);
+      return *(const TG_LDS s16x8*)(lds + at[part] + i * (K * 32));
     } else {
-      const TG_LDS char* const a = lds + at[i];
+      const TG_LDS char* const a = lds + at[i] + part * (ROWS * 64);
       const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TG_LDS s16x4*)a);
       const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TG_LDS s16x4*)(a + ROWS * 8));
       return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -167,14 +175,19 @@ __device__ __forceinline__ f32x4 mm_mfma(s16x8 a, s16x8 b, f32x4 c) {
 //             without a barrier; their sums are added at the end. For few tiles and long sums.
 enum MmMode { MM_TURNS, MM_EVEN, MM_ALONE };
 
-// A tile of BM x BN by WM x WN waves. FM x FN: a wave's blocks of 16 x 16, as it ends with them.
+// A tile of BM x BN by WM x WN waves, in stages of K values of k of which STAGES fit. FM x FN: a
+// wave's blocks of 16 x 16, as it ends with them.
+// Four stages of 32 keep a transfer in flight for two stages' products; two of 64 fetch straight
+// rows by whole cache lines and have half the barriers (MM_TURNS, 8192 x 8192 x 8192: 1014 us with
+// four of 32, 1032 with two of 64; MM_EVEN, 18 Grams of 1024 x 4096: 148 and 136).
 template <int BM_, int BN_, int WM_, int WN_, MmMode MODE_>
 struct MmShape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
   static constexpr MmMode MODE = MODE_;
   static constexpr int WAVES = WM * WN, THREADS = WAVES * 64;
   static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
-  static constexpr int STAGE = (BM + BN) * MM_K * 2, STAGES = 4;
+  static constexpr int K = MODE == MM_EVEN ? 64 : 32, STAGES = MODE == MM_EVEN ? 2 : 4;
+  static constexpr int STAGE = (BM + BN) * K * 2;
   static constexpr int LDS_BYTES = STAGES * STAGE * (MODE == MM_ALONE ? WAVES : 1);
 };
 using MmBig = MmShape<256, 256, 2, 4, MM_TURNS>;
@@ -199,19 +212,19 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
   constexpr bool ALONE = S::MODE == MM_ALONE;
   constexpr int LOADERS = ALONE ? 1 : S::WAVES;
   constexpr int FM = ALONE ? S::BM / 16 : S::FM, FN = ALONE ? S::BN / 16 : S::FN;   // while summing
-  constexpr int STAGES = S::STAGES;
+  constexpr int STAGES = S::STAGES, K = S::K;
   const int tid = threadIdx.x, lane = tid & 63, wave = (int)uniform(tid >> 6);
   const int loader = ALONE ? 0 : wave;
-  using LA = MmLoader<S::BM, LOADERS, CA>;
-  using LB = MmLoader<S::BN, LOADERS, CB>;
+  using LA = MmLoader<S::BM, K, LOADERS, CA>;
+  using LB = MmLoader<S::BN, K, LOADERS, CB>;
   constexpr int LOADS = LA::PER + LB::PER;
   LA la;
   LB lb, lb2;
   la.init(loader, lane, sa);
   lb.template init<DUAL>(loader, lane, sb);
   if constexpr (DUAL) lb2 = lb;
-  MmReader<S::BM, FM, CA> ra;
-  MmReader<S::BN, FN, CB> rb;
+  MmReader<S::BM, K, FM, CA> ra;
+  MmReader<S::BN, K, FN, CB> rb;
   const int wm = ALONE ? 0 : wave / S::WN, wn = ALONE ? 0 : wave % S::WN;
   ra.init(wm * FM * 16, lane);
   rb.init(wn * FN * 16, lane);
@@ -224,12 +237,12 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
   // this wave's k of every segment
   int64_t from = 0, many = k;
   if constexpr (ALONE) {
-    const int64_t quarter = ((k + MM_K * S::WAVES - 1) / (MM_K * S::WAVES)) * MM_K;
+    const int64_t quarter = ((k + K * S::WAVES - 1) / (K * S::WAVES)) * K;
     from = wave * quarter;
     many = k - from < quarter ? k - from : quarter;
     lds += wave * (STAGES * S::STAGE);
   }
-  const int total = many > 0 ? (int)((many + MM_K - 1) / MM_K) * nseg : 0;
+  const int total = many > 0 ? (int)((many + K - 1) / K) * nseg : 0;
   const uint32_t lds0 = uniform((uint32_t)(uintptr_t)lds);
   int seg = 0, issued = 0, rem = 0;
   uint32_t into = 0;       // where the next stage goes
@@ -249,12 +262,12 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
     if constexpr (!DUAL) {
       lb.issue(l + LA::BYTES, loader, rem);
     } else {
-      static_assert(LB::PER % 2 == 0, "a wave's transfers: from either matrix by turns");
-      lb.template issue<0, 2>(l + LA::BYTES, loader, rem);
-      lb2.template issue<1, 2>(l + LA::BYTES, loader, rem);
+      static_assert(LB::PER * (64 / LB::PIECES) % 32 == 0, "a wave's transfers: whole pairs of blocks");
+      lb.template issue<true, false>(l + LA::BYTES, loader, rem);
+      lb2.template issue<true, true>(l + LA::BYTES, loader, rem);
     }
     ++issued;
-    rem -= MM_K;
+    rem -= K;
     if (rem > 0) {
       la.next(sa);
       lb.next(sb);
@@ -263,21 +276,12 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
       begin(seg);
     }
   };
-  // waits until stage t has arrived
-  auto arrived = [&](int t) {
-    const int behind = issued - 1 - t;
-    if (ALONE && behind >= 3) wait_vm<3 * LOADS>();
-    else if (behind >= 2) wait_vm<2 * LOADS>();
-    else if (behind == 1) wait_vm<LOADS>();
-    else wait_vm<0>();
-  };
-  static_assert(STAGES == 4, "two stages behind the one that is awaited, three of a wave alone");
-  auto fragments = [&](uint32_t at, s16x8 (&fa)[FM], s16x8 (&fb)[FN]) {
+  auto fragments = [&](uint32_t at, int part, s16x8 (&fa)[FM], s16x8 (&fb)[FN]) {
     const TG_LDS char* const l = lds + at;
 #pragma unroll
-    for (int j = 0; j < FN; ++j) fb[j] = rb.get(l + LA::BYTES, j);
+    for (int j = 0; j < FN; ++j) fb[j] = rb.get(l + LA::BYTES, j, part);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) fa[i] = ra.get(l, i);
+    for (int i = 0; i < FM; ++i) fa[i] = ra.get(l, i, part);
   };
   auto multiply = [&](const s16x8 (&fa)[FM], const s16x8 (&fb)[FN]) {
 #pragma unroll
@@ -285,18 +289,26 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
 #pragma unroll
       for (int j = 0; j < FN; ++j) c[i][j] = mm_mfma<DT>(fb[j], fa[i], c[i][j]);
   };
-  if (total > 0) {
-    begin(0);
-    issue();
-    if (total > 1) issue();
-    if (total > 2) issue();
-    if (ALONE && total > 3) issue();
-  }
+  // waits until stage t has arrived
+  auto arrived = [&](int t) {
+    const int behind = issued - 1 - t;
+    if (behind >= 3) wait_vm<3 * LOADS>();
+    else if (behind == 2) wait_vm<2 * LOADS>();
+    else if (behind == 1) wait_vm<LOADS>();
+    else wait_vm<0>();
+  };
+  if (total > 0) begin(0);
   int t = 0;
   uint32_t at = 0;
   if constexpr (S::MODE == MM_TURNS) {
+    // Phases between barriers:  group 0: read t    multiply  read t + 1  multiply
+    //                           group 1:           read t    multiply    read t + 1  multiply
+    // Stage t + 3 goes where t - 1 was, whose reads by both groups ended at a barrier before either
+    // reads t; what a group reads in its next phase both have awaited before the barrier there.
     const int group = wave >> 2;
-    if (total > 0) arrived(0);
+    for (int i = 0; i < 3; ++i)
+      if (i < total) issue();
+    arrived(0);
     lds_barrier();
     if (group) lds_barrier();
     auto product = [&](const s16x8 (&fa)[FM], const s16x8 (&fb)[FN]) {
@@ -310,34 +322,40 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
     };
     for (; t + 3 < total; ++t, at = after(at)) {
       s16x8 fa[FM], fb[FN];
-      fragments(at, fa, fb);
-      // into the stage before this one: both groups' reads of it ended at a barrier since
+      fragments(at, 0, fa, fb);
       issue();
       wait_vm<2 * LOADS>();
       product(fa, fb);
     }
     for (; t < total; ++t, at = after(at)) {
       s16x8 fa[FM], fb[FN];
-      fragments(at, fa, fb);
-      if (t + 1 < total) arrived(t + 1);
+      fragments(at, 0, fa, fb);
+      arrived(t + 1);
       product(fa, fb);
     }
     if (!group) lds_barrier();
   } else if constexpr (S::MODE == MM_EVEN) {
+    if (total > 0) issue();
     for (; t < total; ++t, at = after(at)) {
-      arrived(t);
+      wait_vm<0>();
       lds_barrier();       // every wave's part of this stage is there, and the one before is read
-      s16x8 fa[FM], fb[FN];
-      fragments(at, fa, fb);
       if (issued < total) issue();
-      multiply(fa, fb);
+#pragma unroll
+      for (int part = 0; part < K / 32; ++part) {
+        s16x8 fa[FM], fb[FN];
+        fragments(at, part, fa, fb);
+        multiply(fa, fb);
+      }
     }
   } else {
     // a stage's fragments are read while the one before is multiplied
+    static_assert(!ALONE || (STAGES == 4 && K == 32), "at most three stages behind the one that is awaited");
+    for (int i = 0; i < STAGES; ++i)
+      if (i < total) issue();
     s16x8 fa[2][FM], fb[2][FN];
     if (total > 0) {
       arrived(0);
-      fragments(at, fa[0], fb[0]);
+      fragments(at, 0, fa[0], fb[0]);
     }
     for (; t < total; t += 2) {
 #pragma unroll
@@ -348,7 +366,7 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
         at = after(at);
         if (t + o + 1 < total) {
           arrived(t + o + 1);
-          fragments(at, fa[o ^ 1], fb[o ^ 1]);
+          fragments(at, 0, fa[o ^ 1], fb[o ^ 1]);
         }
         multiply(fa[o], fb[o]);
       }

@@ -1,5 +1,6 @@
 // Host side of Newton-Schulz orthogonalisation and of the Muon step: the handle, the division
 // of the matrices into tiles and chunks, and the launches. Kernels and arithmetic: k_muon.hip.
+#include <algorithm>
 #include <cmath>
 #include <new>
 #include <string>
@@ -15,8 +16,13 @@ struct tgrad_muon {
     int64_t values;
     int dtype, grad_dtype;
   };
-  struct First {             // a launch over the chunks of some tensors
+  struct Small {             // a launch over matrices that a workgroup holds
+    uint32_t first = 0, n = 0, lds = 0;
+    int slots = 0;
+  };
+  struct First {             // launches over some tensors, whose addresses their arguments carry
     uint32_t first_tensor, tensors, first_chunk, chunks;
+    Small small[2];          // bf16, and those whose products take both parts
   };
   struct List {              // a launch of a product over all matrices
     uint32_t first = 0, n = 0;
@@ -191,7 +197,8 @@ int tgrad_muon_init(tgrad_muon_t** out, int n, const int64_t* count, const int64
       h->tensors.push_back({(int64_t)(count[i] * each), dtype[i], grad_dtype[i]});
       for (int64_t k = 0; k < count[i]; ++k) {
         NsMat m{};
-        ws = lay_out(m, rows[i], cols[i], dtype[i], ws);
+        const uint64_t end = lay_out(m, rows[i], cols[i], dtype[i], ws);
+        if (!ns_small_slots(m.rows, m.cols, m.exact != 0)) ws = end;   // others need none of it
         m.gdt = (uint32_t)grad_dtype[i];
         m.elem = k * each;
         m.state = at + k * each;
@@ -207,26 +214,44 @@ int tgrad_muon_init(tgrad_muon_t** out, int n, const int64_t* count, const int64
       }
       at += up(count[i] * each, kGroup);
     }
-    // chunks of values, in launches of the tensors whose addresses fit one
+    auto small = [](const NsMat& m) { return ns_small_slots(m.rows, m.cols, m.exact != 0); };
+    // matrices that a workgroup holds, and chunks of the others' values, in launches of the
+    // tensors whose addresses fit one
     size_t mat = 0;
     for (int i = 0; i < n || h->firsts.empty(); i += MUON_LAUNCH_TENSORS) {
       const int t = n - i < MUON_LAUNCH_TENSORS ? n - i : MUON_LAUNCH_TENSORS;
-      tgrad_muon::First f{(uint32_t)i, (uint32_t)t, (uint32_t)parts.size(), 0};
-      for (; mat < mats.size() && mats[mat].tensor < (uint32_t)(i + t); ++mat)
-        for (uint32_t c = 0; c < mats[mat].chunks; ++c) parts.push_back({(uint32_t)mat, c, 0});
+      tgrad_muon::First f{(uint32_t)i, (uint32_t)t, 0, 0, {}};
+      size_t end = mat;
+      while (end < mats.size() && mats[end].tensor < (uint32_t)(i + t)) ++end;
+      for (int exact = 0; exact < 2; ++exact) {
+        auto& l = f.small[exact];
+        l.first = (uint32_t)parts.size();
+        for (size_t k = mat; k < end; ++k) {
+          const int slots = small(mats[k]);
+          if (!slots || mats[k].exact != (uint32_t)exact) continue;
+          parts.push_back({(uint32_t)k, 0, 0});
+          l.slots = std::max(l.slots, slots);
+          l.lds = std::max(l.lds, ns_small_lds(mats[k].rows, mats[k].cols, exact != 0));
+        }
+        l.n = (uint32_t)parts.size() - l.first;
+      }
+      f.first_chunk = (uint32_t)parts.size();
+      for (; mat < end; ++mat)
+        for (uint32_t c = 0; !small(mats[mat]) && c < mats[mat].chunks; ++c) parts.push_back({(uint32_t)mat, c, 0});
       f.chunks = (uint32_t)parts.size() - f.first_chunk;
       h->firsts.push_back(f);
     }
     auto list = [&](tgrad_muon::List& l, int tile, auto&& add) {
       l.tile = tile;
       l.first = (uint32_t)parts.size();
-      for (size_t k = 0; k < mats.size(); ++k) add((uint32_t)k, mats[k]);
+      for (size_t k = 0; k < mats.size(); ++k)
+        if (!small(mats[k])) add((uint32_t)k, mats[k]);
       l.n = (uint32_t)(parts.size() - l.first);
     };
     auto sum = [&](auto&& of) {
       return choose_tile([&](int tile) {
         uint64_t t = 0;
-        for (const NsMat& m : mats) t += of(m, tile);
+        for (const NsMat& m : mats) t += small(m) ? 0 : of(m, tile);
         return t;
       });
     };
@@ -333,9 +358,15 @@ int tgrad_muon_step(tgrad_muon_t* h, void* const* weights, const void* const* gr
     }
     f.first_tensor = l.first_tensor;
     f.tensors = l.tensors;
+    for (int exact = 0; exact < 2; ++exact) {
+      const auto& q = l.small[exact];
+      const NsSmall k{h->steps, q.slots, exact != 0, q.lds, h->eps, h->lr, nullptr};
+      if (e == hipSuccess) e = launch_ns_small(c, k, f, &t, NsSource{}, {h->parts + q.first, 0, 0, false}, q.n, s);
+    }
     if (e == hipSuccess) e = launch_muon_first(c, f, t, {h->parts + l.first_chunk, 0, 0, false}, l.chunks, s);
   }
   auto parts = [&](const tgrad_muon::List& l) { return NsParts{h->parts + l.first, 0, 0, false}; };
+  if (!h->starts.n) return e == hipSuccess ? TGRAD_OK : fail(h, e, "Muon step");
   if (e == hipSuccess) e = launch_muon_start(c, f, h->eps, parts(h->starts), h->starts.n, s);
   const Launches l{parts(h->gram), parts(h->poly), parts(h->apply), h->gram.n, h->poly.n, h->apply.n,
                    h->gram.tile,   h->poly.tile,   h->apply.tile};
@@ -350,6 +381,7 @@ int64_t tgrad_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols,
   if (count < 0 || count > (int64_t)kMostParts || !side_ok(rows, cols) || !type_ok(dtype)) return -1;
   NsMat m{};
   const uint64_t each = lay_out(m, rows, cols, dtype, 0);
+  if (ns_small_slots(m.rows, m.cols, m.exact != 0)) return 0;
   if ((uint64_t)count > (1ull << 46) / each) return -1;
   return (int64_t)(each * count);
 }
@@ -357,14 +389,14 @@ int64_t tgrad_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols,
 int tgrad_orthogonalize(const void* x, int64_t matrix_stride, int64_t row_stride, void* out, int64_t count,
                         int64_t rows, int64_t cols, int dtype, int steps, const double* coefficients, double eps,
                         void* workspace, void* stream) {
-  if (tgrad_orthogonalize_workspace(count, rows, cols, dtype) < 0 || !numbers_ok(steps, coefficients, eps))
-    return TGRAD_EINVAL;
+  const int64_t bytes = tgrad_orthogonalize_workspace(count, rows, cols, dtype);
+  if (bytes < 0 || !numbers_ok(steps, coefficients, eps)) return TGRAD_EINVAL;
   if ((rows > 1 && row_stride < cols) || row_stride > (int64_t(1) << 40)) return TGRAD_EINVAL;
   if (count > 1 && (matrix_stride < (rows - 1) * (rows > 1 ? row_stride : 0) + cols || matrix_stride > (int64_t(1) << 42)))
     return TGRAD_EINVAL;
   if (count == 0) return TGRAD_OK;
   const uintptr_t low = dtype == TGRAD_F32 ? 3 : 1;
-  if (!x || !out || !workspace || ((uintptr_t)x & low) || ((uintptr_t)out & low) || ((uintptr_t)workspace & 15u))
+  if (!x || !out || (bytes && !workspace) || ((uintptr_t)x & low) || ((uintptr_t)out & low) || ((uintptr_t)workspace & 15u))
     return TGRAD_EINVAL;
   const hipStream_t s = (hipStream_t)stream;
   NsCommon c{};
@@ -374,6 +406,13 @@ int tgrad_orthogonalize(const void* x, int64_t matrix_stride, int64_t row_stride
   c.ca = (float)coefficients[0];
   c.cb = (float)coefficients[1];
   c.cc = (float)coefficients[2];
+  const NsSource f{x, row_stride, matrix_stride};
+  if (const int slots = ns_small_slots(c.one.rows, c.one.cols, c.one.exact != 0)) {
+    c.pitch = 0;
+    const NsSmall k{steps, slots, c.one.exact != 0, ns_small_lds(c.one.rows, c.one.cols, c.one.exact != 0), eps, 0.0, out};
+    const hipError_t e = launch_ns_small(c, k, MuonFirst{}, nullptr, f, {nullptr, 1, 1, false}, (uint32_t)count, s);
+    return e == hipSuccess ? TGRAD_OK : TGRAD_EHIP;
+  }
   const uint64_t n = (uint64_t)count, m = c.one.m;
   Launches l{};
   l.tgram = l.tpoly = choose_tile([&](int t) { return n * lower_tiles(m, t); });
@@ -386,7 +425,6 @@ int tgrad_orthogonalize(const void* x, int64_t matrix_stride, int64_t row_stride
   l.apply = {nullptr, (uint32_t)across(rows, l.tapply), (uint32_t)across(cols, l.tapply), false};
   l.ngram = l.npoly = (uint32_t)half;
   l.napply = (uint32_t)whole;
-  const NsSource f{x, row_stride, matrix_stride};
   hipError_t e = launch_ns_norm(c, f, {nullptr, c.one.chunks, 1, false}, (uint32_t)chunks, s);
   if (e == hipSuccess) e = launch_ns_start(c, f, eps, {nullptr, (uint32_t)start_chunks(c.one), 1, false}, (uint32_t)starts, s);
   NsLast last{};

@@ -120,13 +120,14 @@ def test_orthogonalize_refuses(lib):
         return lib.tgrad_orthogonalize(P(x), mstr, rstr, P(out), n, rows, cols, dt, steps, co, eps, P(ws), None)
 
     inf = (DBL * 3)(1.0, float("inf"), 0.0)
-    for kw in (dict(x=None), dict(out=None), dict(ws=None), dict(ws=4104), dict(x=4098), dict(out=4097), dict(n=-1),
+    for kw in (dict(x=None), dict(out=None), dict(ws=4104), dict(x=4098), dict(out=4097), dict(n=-1),
                dict(rows=0), dict(cols=0), dict(rows=(1 << 19) + 1), dict(cols=1 << 20), dict(dt=3), dict(dt=-1),
                dict(steps=0), dict(steps=101), dict(co=None), dict(co=inf), dict(eps=-1.0), dict(eps=float("nan")),
                dict(rstr=3), dict(mstr=11), dict(n=1 << 22, mstr=12)):
         assert call(**kw) == tg.EINVAL, kw
+    assert call(ws=None, rows=300, cols=400, rstr=400, mstr=120000) == tg.EINVAL
     assert call(n=0, x=None, out=None, ws=None) == tg.OK
-    assert lib.tgrad_orthogonalize_workspace(2, 3, 4, 0) > 0
+    assert lib.tgrad_orthogonalize_workspace(2, 300, 400, 0) > 0
     for bad in ((-1, 3, 4, 0), (1, 0, 4, 0), (1, 3, 0, 0), (1, 3, 4, 3), (1 << 40, 3, 4, 0), (1 << 20, 1 << 19, 1 << 19, 0)):
         assert lib.tgrad_orthogonalize_workspace(*bad) == -1
 
