@@ -1,11 +1,12 @@
 // Newton-Schulz orthogonalisation and the Muon step (see k_muon.hip for the iteration and its
 // formats) of matrices that a workgroup holds: one workgroup a matrix, one launch for all of it.
 //
-// Eight waves. A wave owns parts of 16 x 32 values of X, whose values it keeps in registers as
+// Eight or 16 waves. A wave owns parts of 16 or 32 x 32 values of X, which it keeps in registers as
 // fp32 from the first pass over the gradient to the last over the weights; LDS holds what the
 // products read, the fp16 parts of X and of A, which B replaces. A launch of its own for each
 // product of a 64 x 64 matrix takes 5 us, nearly all of it latency; here a step's three products
 // are four barriers apart.
+#include <algorithm>
 #include <type_traits>
 
 #include "muon_common.h"
@@ -13,8 +14,6 @@
 namespace tg {
 
 namespace {
-
-constexpr int kWaves = 8, kThreads = kWaves * 64;
 
 // The places of a matrix in LDS, in 16-bit values: lines are padded to whole k of a matrix
 // instruction and 8 more, so that eight lines' 16-byte pieces lie in eight different banks.
@@ -44,35 +43,44 @@ template <bool CROSSED>
 __device__ __forceinline__ s16x8 fragment(const lds_f16* p, uint32_t ld, uint32_t line, uint32_t k, uint32_t lane) {
   const uint32_t r = lane & 15, kg = lane >> 4;
   if constexpr (!CROSSED) {
-    return *(const TG_LDS s16x8*)(p + (line + r) * ld + k + kg * 8);
+    return *(const TG_LDS s16x8*)(p + __umul24(line + r, ld) + k + kg * 8);
   } else {
-    const lds_f16* const a = p + (k + kg * 8 + (r >> 2)) * ld + line + (r & 3) * 4;
+    const lds_f16* const a = p + __umul24(k + kg * 8 + (r >> 2), ld) + line + (r & 3) * 4;
     const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TG_LDS s16x4*)a);
     const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TG_LDS s16x4*)(a + 4 * ld));
     return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
   }
 }
 
-// 16 x 32 sums over kk values of k of the products of the parts of a and b
-template <bool EXACT, bool CA, bool CB>
-__device__ __forceinline__ void product(f32x4 (&c)[2], const lds_f16* a, uint32_t lda, uint32_t pa, uint32_t i,
+// 16 RB x 32 sums over kk values of k of the products of the parts of a and b
+template <int RB, bool EXACT, bool CA, bool CB>
+__device__ __forceinline__ void product(f32x4 (&c)[RB][2], const lds_f16* a, uint32_t lda, uint32_t pa, uint32_t i,
                                         const lds_f16* b, uint32_t ldb, uint32_t pb, uint32_t j, uint32_t kk, uint32_t lane) {
-  c[0] = c[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int g = 0; g < RB; ++g) c[g][0] = c[g][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
   for (uint32_t k = 0; k < kk; k += 32) {
-    const s16x8 ah = fragment<CA>(a, lda, i, k, lane);
-    s16x8 al = {};
-    if (EXACT) al = fragment<CA>(a + pa, lda, i, k, lane);
+    s16x8 ah[RB], al[RB], bh[2], bl[2];
+#pragma unroll
+    for (int g = 0; g < RB; ++g) {
+      ah[g] = fragment<CA>(a, lda, i + 16 * g, k, lane);
+      if (EXACT) al[g] = fragment<CA>(a + pa, lda, i + 16 * g, k, lane);
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const s16x8 bh = fragment<CB>(b, ldb, j + 16 * h, k, lane);
-      if (EXACT) {
-        const s16x8 bl = fragment<CB>(b + pb, ldb, j + 16 * h, k, lane);
-        c[h] = mm_mfma<DT_F16>(bh, al, c[h]);
-        c[h] = mm_mfma<DT_F16>(bl, ah, c[h]);
-      }
-      c[h] = mm_mfma<DT_F16>(bh, ah, c[h]);
+      bh[h] = fragment<CB>(b, ldb, j + 16 * h, k, lane);
+      if (EXACT) bl[h] = fragment<CB>(b + pb, ldb, j + 16 * h, k, lane);
     }
+#pragma unroll
+    for (int g = 0; g < RB; ++g)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (EXACT) {
+          c[g][h] = mm_mfma<DT_F16>(bh[h], al[g], c[g][h]);
+          c[g][h] = mm_mfma<DT_F16>(bl[h], ah[g], c[g][h]);
+        }
+        c[g][h] = mm_mfma<DT_F16>(bh[h], ah[g], c[g][h]);
+      }
   }
 }
 
@@ -88,11 +96,12 @@ __device__ __forceinline__ void put4(lds_f16* p, uint32_t part, const float* v) 
 
 struct NoTable {};
 
-// SLOTS: parts of X that a wave owns at most. Table: MuonTable for a step, else matrices given as
+// SLOTS: parts of 16 RB x 32 values of X that a wave owns at most (of A: one). Table: MuonTable for a step, else matrices given as
 // they are.
-template <int SLOTS, bool EXACT, class Table>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int WAVES, int RB, int SLOTS, bool EXACT, class Table>
+__global__ void __launch_bounds__(WAVES * 64, WAVES / 4)
     k_ns_small(const NsCommon c, const NsSmall k, const MuonFirst f, const Table table, const NsSource src, const NsParts p) {
+  constexpr uint32_t kWaves = WAVES, kThreads = WAVES * 64;
   constexpr bool MUON = std::is_same<Table, MuonTable>::value;
   extern __shared__ char lds_raw[];
   __shared__ double sums[kWaves];
@@ -105,52 +114,67 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, c4 = (lane >> 4) * 4;
   const uint32_t across = (m.cols + 31) / 32, sacross = (m.m + 31) / 32;
   // the first row and column of this wave's parts of X, and of A
-  uint32_t xi[SLOTS], xj[SLOTS], si[4], sj[4];
+  uint32_t xi[SLOTS], xj[SLOTS], si[1], sj[1];
   auto places = [&](uint32_t wide, uint32_t* i, uint32_t* j, int n) {
     uint32_t a = wave / wide, b = wave % wide;
 #pragma unroll
     for (int s = 0; s < n; ++s) {
-      i[s] = uniform(a * 16);
+      i[s] = uniform(a * 16 * RB);
       j[s] = uniform(b * 32);
       for (b += kWaves; b >= wide; b -= wide) ++a;
     }
   };
   places(across, xi, xj, SLOTS);
-  places(sacross, si, sj, 4);
+  places(sacross, si, sj, 1);
   for (uint32_t i = threadIdx.x; i < (at.bytes + 15) / 16; i += kThreads) ((TG_LDS u32x4*)x16)[i] = u32x4{0, 0, 0, 0};
 
   // this wave's values: the gradient and momentum, or the matrix
   const float coef = c.clip ? c.clip[1] : 1.0f;
   const void* from = src.x;
   if constexpr (MUON) from = table.g[m.tensor - f.first_tensor];
-  float x[SLOTS][2][4];
+  float x[SLOTS][RB][2][4];
   double square = 0.0;
   with_type(m.gdt, [&](auto zero) {
     using T = decltype(zero);
     const T* const g = (const T*)from + (MUON ? m.elem : mat * src.matrix_stride);
     const int64_t pitch = MUON ? (int64_t)m.cols : src.row_stride;
+    float* const mom = MUON ? f.momentum + m.state : nullptr;
+    // all of a part's loads at once: those outside the matrix take its first value
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-      const uint32_t i = xi[s] + r;
+      T raw[2 * RB][4];
+      float old[2 * RB][4];
+      auto inside = [&](int gh, int e, uint32_t& i, uint32_t& j) {
+        i = xi[s] + (gh >> 1) * 16 + r;
+        j = xj[s] + (gh & 1) * 16 + c4 + e;
+        return i < m.rows && j < m.cols;
+      };
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t j = xj[s] + h * 16 + c4;
+      for (int gh = 0; gh < 2 * RB; ++gh)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float u = 0.0f;
-          if (i < m.rows && j + e < m.cols) {
-            u = to_f32(g[i * pitch + j + e]);
-            if (MUON) {
-              float* const mom = f.momentum + m.state + (uint64_t)i * m.cols + j + e;
-              const float v = u * coef, w = f.mu * *mom + f.nu * v;
-              *mom = w;
-              u = updated(v, w, f);
-            }
+          uint32_t i, j;
+          const bool in = inside(gh, e, i, j);
+          raw[gh][e] = g[in ? i * pitch + j : 0];
+          if (MUON) old[gh][e] = mom[in ? (uint64_t)i * m.cols + j : 0];
+        }
+#pragma unroll
+      for (int gh = 0; gh < 2 * RB; ++gh)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t i, j;
+          const bool in = inside(gh, e, i, j);
+          float u = to_f32(raw[gh][e]);
+          if (MUON) {
+            const float v = u * coef, w = f.mu * old[gh][e] + f.nu * v;
+            if (in) mom[(uint64_t)i * m.cols + j] = w;
+            u = updated(v, w, f);
           }
-          x[s][h][e] = u;
+          u = in ? u : 0.0f;
+          x[s][gh >> 1][gh & 1][e] = u;
           square += (double)u * u;
         }
-      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   });
 #pragma unroll
@@ -164,9 +188,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
   for (int s = 0; s < SLOTS; ++s)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int gh = 0; gh < 2 * RB; ++gh)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[s][h][e] *= scale;
+      for (int e = 0; e < 4; ++e) x[s][gh >> 1][gh & 1][e] *= scale;
 
   const bool wide = m.rows <= m.cols;
 #pragma unroll 1
@@ -184,83 +208,78 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int s = 0; s < SLOTS; ++s) {
       if (xi[s] >= m.rows) continue;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) put4<EXACT>(x16 + (xi[s] + r) * at.ldx + xj[s] + h * 16 + c4, at.xpart, x[s][h]);
+      for (int gh = 0; gh < 2 * RB; ++gh)
+        put4<EXACT>(x16 + __umul24(xi[s] + (gh >> 1) * 16 + r, at.ldx) + xj[s] + (gh & 1) * 16 + c4, at.xpart,
+                    x[s][gh >> 1][gh & 1]);
     }
     __syncthreads();
+    const uint32_t i0 = si[0], j0 = sj[0];
+    const bool mine = i0 < m.m;
+    f32x4 q[RB][2];
+    if (mine) {                                                    // A
+      if (wide) product<RB, EXACT, false, false>(q, x16, at.ldx, at.xpart, i0, x16, at.ldx, at.xpart, j0, m.cols, lane);
+      else product<RB, EXACT, true, true>(q, x16, at.ldx, at.xpart, i0, x16, at.ldx, at.xpart, j0, m.rows, lane);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {                                  // A
-      const uint32_t i = si[s], j = sj[s];
-      if (i >= m.m) continue;
-      f32x4 q[2];
-      if (wide) product<EXACT, false, false>(q, x16, at.ldx, at.xpart, i, x16, at.ldx, at.xpart, j, m.cols, lane);
-      else product<EXACT, true, true>(q, x16, at.ldx, at.xpart, i, x16, at.ldx, at.xpart, j, m.rows, lane);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t on = i + r - (j + h * 16 + c4);     // which of the four lies on the diagonal
+      for (int gh = 0; gh < 2 * RB; ++gh) {
+        const uint32_t i = i0 + (gh >> 1) * 16 + r, j = j0 + (gh & 1) * 16 + c4, on = i - j;   // on: which lies on the diagonal
         float o[4], d = 0.0f;
 #pragma unroll
         for (uint32_t e = 0; e < 4; ++e) {
-          const float v = q[h][e] * (1.0f / (NS_X * NS_X));
+          const float v = q[gh >> 1][gh & 1][e] * (1.0f / (NS_X * NS_X));
           d = on == e ? v : d;
           o[e] = on == e ? 0.0f : v * NS_M;
         }
-        if (on < 4) da[i + r] = d;
-        put4<EXACT>(s16 + (i + r) * at.lds + j + h * 16 + c4, at.spart, o);
+        if (on < 4) da[i] = d;
+        put4<EXACT>(s16 + __umul24(i, at.lds) + j, at.spart, o);
       }
     }
     __syncthreads();
-    float b[4][2][4], d[4] = {};                                    // B
+    float b[2 * RB][4], db0[RB] = {};                              // B
+    if (mine) {
+      product<RB, EXACT, false, false>(q, s16, at.lds, at.spart, i0, s16, at.lds, at.spart, j0, m.m, lane);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const uint32_t i = si[s], j = sj[s];
-      if (i >= m.m) continue;
-      f32x4 q[2];
-      product<EXACT, false, false>(q, s16, at.lds, at.spart, i, s16, at.lds, at.spart, j, m.m, lane);
-      const float di = da[i + r];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t o = (i + r) * at.lds + j + h * 16 + c4;
+      for (int gh = 0; gh < 2 * RB; ++gh) {
+        const uint32_t i = i0 + (gh >> 1) * 16 + r, j = j0 + (gh & 1) * 16 + c4, on = i - j, o = __umul24(i, at.lds) + j;
         const f16x4 oh = *(const TG_LDS f16x4*)(s16 + o);
         f16x4 ol = {};
         if (EXACT) ol = *(const TG_LDS f16x4*)(s16 + at.spart + o);
-        const f32x4 dj = *(const TG_LDS f32x4*)(da + j + h * 16 + c4);
-        const uint32_t on = i + r - (j + h * 16 + c4);
+        const f32x4 dj = *(const TG_LDS f32x4*)(da + j);
+        const float di = da[i];
 #pragma unroll
         for (uint32_t e = 0; e < 4; ++e) {
-          const float q2 = q[h][e] * (1.0f / (NS_M * NS_M));
+          const float q2 = q[gh >> 1][gh & 1][e] * (1.0f / (NS_M * NS_M));
           const float v = ((float)oh[e] + (float)ol[e]) * (1.0f / NS_M);
           const float w = c.cb * v + c.cc * (q2 + (di + dj[e]) * v);
-          d[s] = on == e ? c.cb * di + c.cc * (di * di + q2) : d[s];
-          b[s][h][e] = on == e ? 0.0f : w * NS_M;
+          db0[gh >> 1] = on == e ? c.cb * di + c.cc * (di * di + q2) : db0[gh >> 1];
+          b[gh][e] = on == e ? 0.0f : w * NS_M;
         }
       }
     }
     __syncthreads();
+    if (mine) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const uint32_t i = si[s], j = sj[s];
-      if (i >= m.m) continue;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        put4<EXACT>(s16 + (i + r) * at.lds + j + h * 16 + c4, at.spart, b[s][h]);
-        const uint32_t first = j + h * 16 + c4;
-        if (i + r >= first && i + r < first + 4) db[i + r] = d[s];
+      for (int gh = 0; gh < 2 * RB; ++gh) {
+        const uint32_t i = i0 + (gh >> 1) * 16 + r, j = j0 + (gh & 1) * 16 + c4;
+        put4<EXACT>(s16 + __umul24(i, at.lds) + j, at.spart, b[gh]);
+        if (i - j < 4) db[i] = db0[gh >> 1];
       }
     }
     __syncthreads();
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {                              // X
-      const uint32_t i = xi[s], j = xj[s];
-      if (i >= m.rows) continue;
-      f32x4 q[2];
-      if (wide) product<EXACT, false, true>(q, s16, at.lds, at.spart, i, x16, at.ldx, at.xpart, j, m.rows, lane);
-      else product<EXACT, false, false>(q, x16, at.ldx, at.xpart, i, s16, at.lds, at.spart, j, m.cols, lane);
+      if (xi[s] >= m.rows) continue;
+      f32x4 v[RB][2];
+      if (wide) product<RB, EXACT, false, true>(v, s16, at.lds, at.spart, xi[s], x16, at.ldx, at.xpart, xj[s], m.rows, lane);
+      else product<RB, EXACT, false, false>(v, x16, at.ldx, at.xpart, xi[s], s16, at.lds, at.spart, xj[s], m.cols, lane);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const f32x4 dj = *(const TG_LDS f32x4*)(wide ? db + (i + r) / 4 * 4 : db + j + h * 16 + c4);
-        const float di = db[wide ? i + r : 0];
+      for (int gh = 0; gh < 2 * RB; ++gh) {
+        const uint32_t i = xi[s] + (gh >> 1) * 16 + r, j = xj[s] + (gh & 1) * 16 + c4;
+        const f32x4 dj = *(const TG_LDS f32x4*)(wide ? db + i / 4 * 4 : db + j);
+        const float di = db[wide ? i : 0];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[s][h][e] = (c.ca + (wide ? di : dj[e])) * x[s][h][e] + q[h][e] * (1.0f / NS_M);
+        for (int e = 0; e < 4; ++e)
+          x[s][gh >> 1][gh & 1][e] =
+              (c.ca + (wide ? di : dj[e])) * x[s][gh >> 1][gh & 1][e] + v[gh >> 1][gh & 1][e] * (1.0f / NS_M);
       }
     }
     __syncthreads();
@@ -274,57 +293,76 @@ __global__ void __launch_bounds__(kThreads, 2)
     T* const out = (T*)to + (MUON ? m.elem : (uint64_t)mat * m.rows * m.cols);
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-      const uint32_t i = xi[s] + r;
+      T old[2 * RB][4];
+      auto inside = [&](int gh, int e, uint64_t& o) {
+        const uint32_t i = xi[s] + (gh >> 1) * 16 + r, j = xj[s] + (gh & 1) * 16 + c4 + e;
+        const bool in = i < m.rows && j < m.cols;
+        o = in ? (uint64_t)i * m.cols + j : 0;
+        return in;
+      };
+      if (MUON)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int gh = 0; gh < 2 * RB; ++gh)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint64_t o;
+            (void)inside(gh, e, o);
+            old[gh][e] = out[o];
+          }
+#pragma unroll
+      for (int gh = 0; gh < 2 * RB; ++gh)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t j = xj[s] + h * 16 + c4 + e;
-          if (i >= m.rows || j >= m.cols) continue;
-          T* const o = out + (uint64_t)i * m.cols + j;
-          const float y = x[s][h][e] * (1.0f / NS_X);
-          *o = from_f32<T>(MUON ? to_f32(*o) * decay - step * y : y);
+          uint64_t o;
+          const bool in = inside(gh, e, o);
+          const float y = x[s][gh >> 1][gh & 1][e] * (1.0f / NS_X);
+          if (in) out[o] = from_f32<T>(MUON ? to_f32(old[gh][e]) * decay - step * y : y);
         }
+      __builtin_amdgcn_sched_barrier(0);
     }
   });
 }
 
-template <int SLOTS, bool EXACT, class Table>
+template <int WAVES, int RB, int SLOTS, bool EXACT, class Table>
 hipError_t launch(const NsCommon& c, const NsSmall& k, const MuonFirst& f, const Table& t, const NsSource& src,
                   const NsParts& p, uint32_t n, hipStream_t s) {
-  auto* const kernel = k_ns_small<SLOTS, EXACT, Table>;
+  if (n > 0x7FFFFFFFu / (WAVES * 64)) return hipErrorInvalidValue;
+  auto* const kernel = k_ns_small<WAVES, RB, SLOTS, EXACT, Table>;
   const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, NS_SMALL_LDS);
   if (e != hipSuccess) return e;
-  kernel<<<n, kThreads, k.lds, s>>>(c, k, f, t, src, p);
+  kernel<<<n, WAVES * 64, k.lds, s>>>(c, k, f, t, src, p);
   return hipGetLastError();
 }
-template <class Table>
+// Matrices of up to eight parts of 16 x 32 have a wave for each; others parts of 32 x 32, which
+// take two thirds of the reads of LDS that set their pace (113 x 156 fp32: 105 us in parts of
+// 16 x 32).
+template <bool EXACT, class Table>
 hipError_t launch_any(const NsCommon& c, const NsSmall& k, const MuonFirst& f, const Table& t, const NsSource& src,
                       const NsParts& p, uint32_t n, hipStream_t s) {
-  if (k.exact)
-    return k.slots <= 2   ? launch<2, true>(c, k, f, t, src, p, n, s)
-           : k.slots <= 6 ? launch<6, true>(c, k, f, t, src, p, n, s) : launch<12, true>(c, k, f, t, src, p, n, s);
-  return k.slots <= 2   ? launch<2, false>(c, k, f, t, src, p, n, s)
-         : k.slots <= 6 ? launch<6, false>(c, k, f, t, src, p, n, s) : launch<12, false>(c, k, f, t, src, p, n, s);
+  return k.parts == 1   ? launch<8, 1, 1, EXACT>(c, k, f, t, src, p, n, s)
+         : k.parts <= 32 ? launch<16, 2, 2, EXACT>(c, k, f, t, src, p, n, s) : launch<16, 2, 4, EXACT>(c, k, f, t, src, p, n, s);
 }
 static_assert(sizeof(NsCommon) + sizeof(NsSmall) + sizeof(MuonFirst) + sizeof(MuonTable) + sizeof(NsSource) + sizeof(NsParts) <=
                   4096, "kernel arguments");
 
 }  // namespace
 
-int ns_small_slots(uint32_t rows, uint32_t cols, bool exact) {
-  if ((rows < cols ? rows : cols) > 128 || rows > 65536 || cols > 65536) return 0;
-  const uint32_t parts = ((rows + 15) / 16) * ((cols + 31) / 32);
-  if (parts > 12 * kWaves || ns_small_lds(rows, cols, exact) > NS_SMALL_LDS) return 0;
-  return (int)((parts + kWaves - 1) / kWaves);
+uint32_t ns_small_parts(uint32_t rows, uint32_t cols, bool exact) {
+  const uint32_t m = rows < cols ? rows : cols;
+  if (m > 128 || rows > 65536 || cols > 65536) return 0;
+  if (ns_small_lds(rows, cols, exact) > NS_SMALL_LDS) return 0;
+  const uint32_t wide = (cols + 31) / 32;
+  if (((rows + 15) / 16) * wide <= 8 && ((m + 15) / 16) * ((m + 31) / 32) <= 8) return 1;
+  const uint32_t parts = ((rows + 31) / 32) * wide;
+  return parts <= 64 ? std::max(parts, 2u) : 0;
 }
 uint32_t ns_small_lds(uint32_t rows, uint32_t cols, bool exact) { return (places_of(rows, cols, exact).bytes + 15) & ~15u; }
 
 hipError_t launch_ns_small(const NsCommon& c, const NsSmall& k, const MuonFirst& f, const MuonTable* t, const NsSource& src,
                            const NsParts& p, uint32_t n, hipStream_t s) {
   if (n == 0) return hipSuccess;
-  if (n > 0x7FFFFFFFu / kThreads) return hipErrorInvalidValue;
-  return t ? launch_any(c, k, f, *t, src, p, n, s) : launch_any(c, k, f, NoTable{}, src, p, n, s);
+  if (t) return k.exact ? launch_any<true>(c, k, f, *t, src, p, n, s) : launch_any<false>(c, k, f, *t, src, p, n, s);
+  return k.exact ? launch_any<true>(c, k, f, NoTable{}, src, p, n, s) : launch_any<false>(c, k, f, NoTable{}, src, p, n, s);
 }
 
 }  // namespace tg

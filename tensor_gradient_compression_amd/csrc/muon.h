@@ -84,16 +84,16 @@ struct NsLast {
 hipError_t launch_ns_apply(const NsCommon& c, int at, int tile, const NsLast& l, const NsParts& p, uint32_t n,
                            hipStream_t s);
 
-// All of a step or an orthogonalisation, a workgroup a matrix: for those with ns_small_slots()
-// above zero. slots, lds: the largest of the launch's ns_small_slots() and ns_small_lds(); exact:
+// All of a step or an orthogonalisation, a workgroup a matrix: for those with ns_small_parts()
+// above zero (1: eight parts of 16 x 32 at most; others: parts of 32 x 32). parts, lds: the largest of the launch's ns_small_parts() and ns_small_lds(); exact:
 // theirs. With t a step, whose addresses it has, else of src.
 constexpr uint32_t NS_SMALL_LDS = 160 * 1024 - 512;
-int ns_small_slots(uint32_t rows, uint32_t cols, bool exact);
+uint32_t ns_small_parts(uint32_t rows, uint32_t cols, bool exact);
 uint32_t ns_small_lds(uint32_t rows, uint32_t cols, bool exact);
 struct NsSmall {
-  int steps, slots;
+  int steps;
   bool exact;
-  uint32_t lds;
+  uint32_t parts, lds;
   double eps, lr;
   void* out;           // without t: contiguous matrices
 };

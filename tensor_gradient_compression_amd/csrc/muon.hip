@@ -17,8 +17,7 @@ struct tgrad_muon {
     int dtype, grad_dtype;
   };
   struct Small {             // a launch over matrices that a workgroup holds
-    uint32_t first = 0, n = 0, lds = 0;
-    int slots = 0;
+    uint32_t first = 0, n = 0, parts = 0, lds = 0;
   };
   struct First {             // launches over some tensors, whose addresses their arguments carry
     uint32_t first_tensor, tensors, first_chunk, chunks;
@@ -198,7 +197,7 @@ int tgrad_muon_init(tgrad_muon_t** out, int n, const int64_t* count, const int64
       for (int64_t k = 0; k < count[i]; ++k) {
         NsMat m{};
         const uint64_t end = lay_out(m, rows[i], cols[i], dtype[i], ws);
-        if (!ns_small_slots(m.rows, m.cols, m.exact != 0)) ws = end;   // others need none of it
+        if (!ns_small_parts(m.rows, m.cols, m.exact != 0)) ws = end;   // others need none of it
         m.gdt = (uint32_t)grad_dtype[i];
         m.elem = k * each;
         m.state = at + k * each;
@@ -214,7 +213,7 @@ int tgrad_muon_init(tgrad_muon_t** out, int n, const int64_t* count, const int64
       }
       at += up(count[i] * each, kGroup);
     }
-    auto small = [](const NsMat& m) { return ns_small_slots(m.rows, m.cols, m.exact != 0); };
+    auto small = [](const NsMat& m) { return ns_small_parts(m.rows, m.cols, m.exact != 0); };
     // matrices that a workgroup holds, and chunks of the others' values, in launches of the
     // tensors whose addresses fit one
     size_t mat = 0;
@@ -227,10 +226,10 @@ int tgrad_muon_init(tgrad_muon_t** out, int n, const int64_t* count, const int64
         auto& l = f.small[exact];
         l.first = (uint32_t)parts.size();
         for (size_t k = mat; k < end; ++k) {
-          const int slots = small(mats[k]);
-          if (!slots || mats[k].exact != (uint32_t)exact) continue;
+          const uint32_t n = small(mats[k]);
+          if (!n || mats[k].exact != (uint32_t)exact) continue;
           parts.push_back({(uint32_t)k, 0, 0});
-          l.slots = std::max(l.slots, slots);
+          l.parts = std::max(l.parts, n);
           l.lds = std::max(l.lds, ns_small_lds(mats[k].rows, mats[k].cols, exact != 0));
         }
         l.n = (uint32_t)parts.size() - l.first;
@@ -360,7 +359,7 @@ int tgrad_muon_step(tgrad_muon_t* h, void* const* weights, const void* const* gr
     f.tensors = l.tensors;
     for (int exact = 0; exact < 2; ++exact) {
       const auto& q = l.small[exact];
-      const NsSmall k{h->steps, q.slots, exact != 0, q.lds, h->eps, h->lr, nullptr};
+      const NsSmall k{h->steps, exact != 0, q.parts, q.lds, h->eps, h->lr, nullptr};
       if (e == hipSuccess) e = launch_ns_small(c, k, f, &t, NsSource{}, {h->parts + q.first, 0, 0, false}, q.n, s);
     }
     if (e == hipSuccess) e = launch_muon_first(c, f, t, {h->parts + l.first_chunk, 0, 0, false}, l.chunks, s);
@@ -381,7 +380,7 @@ int64_t tgrad_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols,
   if (count < 0 || count > (int64_t)kMostParts || !side_ok(rows, cols) || !type_ok(dtype)) return -1;
   NsMat m{};
   const uint64_t each = lay_out(m, rows, cols, dtype, 0);
-  if (ns_small_slots(m.rows, m.cols, m.exact != 0)) return 0;
+  if (ns_small_parts(m.rows, m.cols, m.exact != 0)) return 0;
   if ((uint64_t)count > (1ull << 46) / each) return -1;
   return (int64_t)(each * count);
 }
@@ -407,9 +406,9 @@ int tgrad_orthogonalize(const void* x, int64_t matrix_stride, int64_t row_stride
   c.cb = (float)coefficients[1];
   c.cc = (float)coefficients[2];
   const NsSource f{x, row_stride, matrix_stride};
-  if (const int slots = ns_small_slots(c.one.rows, c.one.cols, c.one.exact != 0)) {
+  if (const uint32_t most = ns_small_parts(c.one.rows, c.one.cols, c.one.exact != 0)) {
     c.pitch = 0;
-    const NsSmall k{steps, slots, c.one.exact != 0, ns_small_lds(c.one.rows, c.one.cols, c.one.exact != 0), eps, 0.0, out};
+    const NsSmall k{steps, c.one.exact != 0, most, ns_small_lds(c.one.rows, c.one.cols, c.one.exact != 0), eps, 0.0, out};
     const hipError_t e = launch_ns_small(c, k, MuonFirst{}, nullptr, f, {nullptr, 1, 1, false}, (uint32_t)count, s);
     return e == hipSuccess ? TGRAD_OK : TGRAD_EHIP;
   }
