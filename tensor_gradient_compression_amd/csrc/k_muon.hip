@@ -43,6 +43,34 @@ __device__ __forceinline__ void workgroup_sum(double s, double* out) {
   if (threadIdx.x == 0) *out = (w[0] + w[1]) + (w[2] + w[3]);
 }
 
+// A chunk of a matrix: f(row, column, n) for pieces of 8 values of a line, n of them inside.
+template <class F>
+__device__ __forceinline__ void each_piece(const NsMat& m, uint32_t chunk, const F& f) {
+  const uint32_t pieces = m.ldx / 8;
+  const uint64_t first = (uint64_t)chunk * (MUON_CHUNK / 8), row0 = first / pieces;
+  const uint32_t skip = (uint32_t)(first - row0 * pieces);
+#pragma unroll
+  for (uint32_t q = 0; q < MUON_CHUNK / 8 / 256; ++q) {
+    const uint32_t at = skip + q * 256 + threadIdx.x, down = at / pieces, k = (at - down * pieces) * 8;
+    const uint64_t row = row0 + down;
+    if (row < m.rows) f((uint32_t)row, k, m.cols - k < 8 ? m.cols - k : 8);
+  }
+}
+// 8 values from p on, of which n are there (zeros behind)
+template <typename T>
+__device__ __forceinline__ void load_piece(const T* p, uint32_t n, float* v) {
+  T raw[8] = {};
+  if (n == 8) {
+    load_values<8>(p, raw);
+  } else {
+#pragma unroll
+    for (uint32_t e = 0; e < 7; ++e)
+      if (e < n) raw[e] = p[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = to_f32(raw[e]);
+}
+
 __global__ void __launch_bounds__(256) k_muon_first(const NsCommon c, const MuonFirst f, const MuonTable t,
                                                     const NsParts p) {
   if (blockIdx.x == 0 && threadIdx.x < f.tensors) {
@@ -54,17 +82,32 @@ __global__ void __launch_bounds__(256) k_muon_first(const NsCommon c, const Muon
   NsMat m;
   uint32_t chunk, none;
   my_part(c, p, blockIdx.x, m, chunk, none);
-  const void* const g = t.g[m.tensor - f.first_tensor];
-  const uint64_t n = (uint64_t)m.rows * m.cols, from = (uint64_t)chunk * MUON_CHUNK;
-  const uint64_t end = from + MUON_CHUNK < n ? from + MUON_CHUNK : n;
-  float* const mom = f.momentum + m.state;
   double s = 0.0;
-  for (uint64_t e = from + threadIdx.x; e < end; e += 256) {
-    const float v = load_as(g, m.gdt, m.elem + e) * coef, w = f.mu * mom[e] + f.nu * v;
-    mom[e] = w;
-    const double u = updated(v, w, f);
-    s += u * u;
-  }
+  with_type(m.gdt, [&](auto zero) {
+    using T = decltype(zero);
+    const T* const g = (const T*)t.g[m.tensor - f.first_tensor] + m.elem;
+    float* const mom = f.momentum + m.state;
+    each_piece(m, chunk, [&](uint32_t r, uint32_t k, uint32_t n) {
+      const uint64_t o = (uint64_t)r * m.cols + k;
+      float v[8], w[8];
+      load_piece(g + o, n, v);
+      load_piece(mom + o, n, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] *= coef;
+        w[e] = f.mu * w[e] + f.nu * v[e];
+        const double u = updated(v[e], w[e], f);
+        s += u * u;
+      }
+      if (n == 8) {
+        store_values<8>(mom + o, w);
+      } else {
+#pragma unroll
+        for (uint32_t e = 0; e < 7; ++e)
+          if (e < n) mom[o + e] = w[e];
+      }
+    });
+  });
   workgroup_sum(s, (double*)(c.ws + m.sums) + chunk);
 }
 
@@ -72,14 +115,17 @@ __global__ void __launch_bounds__(256) k_ns_norm(const NsCommon c, const NsSourc
   NsMat m;
   uint32_t chunk, none;
   const uint32_t mat = my_part(c, p, blockIdx.x, m, chunk, none);
-  const uint64_t n = (uint64_t)m.rows * m.cols, from = (uint64_t)chunk * MUON_CHUNK;
-  const uint64_t end = from + MUON_CHUNK < n ? from + MUON_CHUNK : n;
   double s = 0.0;
-  for (uint64_t e = from + threadIdx.x; e < end; e += 256) {
-    const uint64_t r = e / m.cols, k = e - r * m.cols;
-    const double u = load_as(f.x, m.gdt, mat * f.matrix_stride + r * f.row_stride + k);
-    s += u * u;
-  }
+  with_type(m.gdt, [&](auto zero) {
+    using T = decltype(zero);
+    const T* const x = (const T*)f.x + mat * f.matrix_stride;
+    each_piece(m, chunk, [&](uint32_t r, uint32_t k, uint32_t n) {
+      float v[8];
+      load_piece(x + r * f.row_stride + k, n, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += (double)v[e] * v[e];
+    });
+  });
   workgroup_sum(s, (double*)(c.ws + m.sums) + chunk);
 }
 
@@ -94,25 +140,14 @@ __device__ __forceinline__ float start_scale(const NsCommon& c, const NsMat& m, 
   return (float)((double)NS_X / (__builtin_sqrt(total) + eps));
 }
 
-// a chunk of X: 8 values of a padded line a thread
-template <class Value>
-__device__ __forceinline__ void write_x(const NsCommon& c, const NsMat& m, uint32_t chunk, float scale, const Value& value) {
-  const uint32_t pieces = m.ldx / 8;
-  const uint64_t all = (uint64_t)m.rows * pieces;
-  _Float16* const hi = (_Float16*)(c.ws + m.x);
-  _Float16* const lo = hi + (uint64_t)m.rows * m.ldx;
+// 8 values of a line of X in their parts
+__device__ __forceinline__ void write_x(const NsCommon& c, const NsMat& m, uint32_t r, uint32_t k, const float* v, float scale) {
+  _Float16* const hi = (_Float16*)(c.ws + m.x) + (uint64_t)r * m.ldx + k;
+  _Float16 h[8], l[8];
 #pragma unroll
-  for (uint32_t q = 0; q < MUON_CHUNK / 8 / 256; ++q) {
-    const uint64_t at = (uint64_t)chunk * (MUON_CHUNK / 8) + q * 256 + threadIdx.x;
-    if (at >= all) return;
-    const uint64_t r = at / pieces;
-    const uint32_t k = (uint32_t)(at - r * pieces) * 8;
-    _Float16 h[8], l[8];
-#pragma unroll
-    for (uint32_t e = 0; e < 8; ++e) two_parts(k + e < m.cols ? value(r, k + e) * scale : 0.0f, h[e], l[e]);
-    *(uint4*)(hi + at * 8) = *(const uint4*)h;
-    *(uint4*)(lo + at * 8) = *(const uint4*)l;
-  }
+  for (int e = 0; e < 8; ++e) two_parts(v[e] * scale, h[e], l[e]);
+  *(uint4*)hi = *(const uint4*)h;
+  *(uint4*)(hi + (uint64_t)m.rows * m.ldx) = *(const uint4*)l;
 }
 
 __global__ void __launch_bounds__(256) k_muon_start(const NsCommon c, const MuonFirst f, const double eps, const NsParts p) {
@@ -122,11 +157,21 @@ __global__ void __launch_bounds__(256) k_muon_start(const NsCommon c, const Muon
   uint32_t chunk, none;
   my_part(c, p, blockIdx.x, m, chunk, none);
   const float scale = start_scale(c, m, eps);
-  const void* const g = f.g[m.tensor];
-  const float* const mom = f.momentum + m.state;
-  write_x(c, m, chunk, scale, [&](uint64_t r, uint32_t k) {
-    const uint64_t e = r * m.cols + k;
-    return updated(load_as(g, m.gdt, m.elem + e) * coef, mom[e], f);
+  with_type(m.gdt, [&](auto zero) {
+    using T = decltype(zero);
+    const T* const g = (const T*)f.g[m.tensor] + m.elem;
+    const float* const mom = f.momentum + m.state;
+    each_piece(m, chunk, [&](uint32_t r, uint32_t k, uint32_t n) {
+      const uint64_t o = (uint64_t)r * m.cols + k;
+      float v[8], w[8];
+      load_piece(mom + o, n, w);
+      if (f.nesterov) {
+        load_piece(g + o, n, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = updated(v[e] * coef, w[e], f);
+      }
+      write_x(c, m, r, k, w, scale);
+    });
   });
 }
 
@@ -135,8 +180,14 @@ __global__ void __launch_bounds__(256) k_ns_start(const NsCommon c, const NsSour
   uint32_t chunk, none;
   const uint32_t mat = my_part(c, p, blockIdx.x, m, chunk, none);
   const float scale = start_scale(c, m, eps);
-  write_x(c, m, chunk, scale, [&](uint64_t r, uint32_t k) {
-    return load_as(f.x, m.gdt, mat * f.matrix_stride + r * f.row_stride + k);
+  with_type(m.gdt, [&](auto zero) {
+    using T = decltype(zero);
+    const T* const x = (const T*)f.x + mat * f.matrix_stride;
+    each_piece(m, chunk, [&](uint32_t r, uint32_t k, uint32_t n) {
+      float v[8];
+      load_piece(x + r * f.row_stride + k, n, v);
+      write_x(c, m, r, k, v, scale);
+    });
   });
 }
 
@@ -321,13 +372,27 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_ns_apply(const NsCommon c, co
     }
     const uint64_t to = (last.w ? m.elem : (uint64_t)mat * m.rows * m.cols) + (uint64_t)i * m.cols + j;
     void* const out = last.w ? last.w[m.tensor] : last.out;
+    with_type(m.wdt, [&](auto zero) {
+      using T = decltype(zero);
+      T* const o = (T*)out + to;
+      T y[4] = {};
+      if (j + 4 <= m.cols) {
+        if (last.w) load_values<4>(o, y);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (j + e >= m.cols) continue;
-      float y = r[e] * (1.0f / NS_X);
-      if (last.w) y = load_as(out, m.wdt, to + e) * decay - step * y;
-      store_as(out, m.wdt, to + e, y);
-    }
+        for (int e = 0; e < 4; ++e) {
+          const float v = r[e] * (1.0f / NS_X);
+          y[e] = from_f32<T>(last.w ? to_f32(y[e]) * decay - step * v : v);
+        }
+        store_values<4>(o, y);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+          if (j + e >= m.cols) continue;
+          const float v = r[e] * (1.0f / NS_X);
+          o[e] = from_f32<T>(last.w ? to_f32(o[e]) * decay - step * v : v);
+        }
+      }
+    });
   });
 }
 

@@ -94,6 +94,52 @@ __device__ __forceinline__ void put4(lds_f16* p, uint32_t part, const float* v) 
   if (EXACT) *(TG_LDS f16x4*)(p + part) = f16x4{l[0], l[1], l[2], l[3]};
 }
 
+// Four values of a line from column j on, without a branch where the line has four at all.
+template <typename T>
+struct Four {
+  typedef uint32_t V __attribute__((ext_vector_type(sizeof(T))));   // four values' bits
+  V v;
+  __device__ __forceinline__ void load(const T* line, uint32_t j, uint32_t cols) {
+    if (cols >= 4) {
+      __builtin_memcpy(&v, line + (j + 4 <= cols ? j : cols - 4), sizeof(V));
+    } else {
+      T t[4];
+#pragma unroll
+      for (uint32_t e = 0; e < 4; ++e) t[e] = line[e < cols ? e : 0];
+      __builtin_memcpy(&v, t, sizeof(V));
+    }
+  }
+  __device__ __forceinline__ float one(int e) const {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(v[e]);
+    } else {
+      const uint16_t b = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+      T t;
+      __builtin_memcpy(&t, &b, 2);
+      return to_f32(t);
+    }
+  }
+  // value j + e, anything past the line
+  __device__ __forceinline__ float value(int e, uint32_t j, uint32_t cols) const {
+    const uint32_t turn = cols >= 4 && j + 4 > cols ? j + 4 - cols : 0;
+    float x = one(e);
+    if (e < 3) x = turn == 1 ? one(e < 3 ? e + 1 : 3) : x;
+    if (e < 2) x = turn == 2 ? one(e < 2 ? e + 2 : 3) : x;
+    if (e < 1) x = turn == 3 ? one(3) : x;
+    return x;
+  }
+};
+template <typename T>
+__device__ __forceinline__ void store_four(T* line, uint32_t j, uint32_t cols, const T* v) {
+  if (j + 4 <= cols) {
+    store_values<4>(line + j, v);
+  } else {
+#pragma unroll
+    for (uint32_t e = 0; e < 3; ++e)
+      if (j + e < cols) line[j + e] = v[e];
+  }
+}
+
 struct NoTable {};
 
 // SLOTS: parts of 16 RB x 32 values of X that a wave owns at most (of A: one). Table: MuonTable for a step, else matrices given as
@@ -139,41 +185,36 @@ __global__ void __launch_bounds__(WAVES * 64, WAVES / 4)
     const T* const g = (const T*)from + (MUON ? m.elem : mat * src.matrix_stride);
     const int64_t pitch = MUON ? (int64_t)m.cols : src.row_stride;
     float* const mom = MUON ? f.momentum + m.state : nullptr;
-    // all of a part's loads at once: those outside the matrix take its first value
+    // all of a part's loads at once, four values each: those that would pass a line's end begin
+    // four before it and are turned, those outside the matrix take its first line
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-      T raw[2 * RB][4];
-      float old[2 * RB][4];
-      auto inside = [&](int gh, int e, uint32_t& i, uint32_t& j) {
-        i = xi[s] + (gh >> 1) * 16 + r;
-        j = xj[s] + (gh & 1) * 16 + c4 + e;
-        return i < m.rows && j < m.cols;
-      };
+      Four<T> raw[2 * RB];
+      Four<float> old[2 * RB];
 #pragma unroll
-      for (int gh = 0; gh < 2 * RB; ++gh)
+      for (int gh = 0; gh < 2 * RB; ++gh) {
+        const uint32_t i = xi[s] + (gh >> 1) * 16 + r, j = xj[s] + (gh & 1) * 16 + c4, row = i < m.rows ? i : 0;
+        raw[gh].load(g + row * pitch, j, m.cols);
+        if (MUON) old[gh].load(mom + (uint64_t)row * m.cols, j, m.cols);
+      }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t i, j;
-          const bool in = inside(gh, e, i, j);
-          raw[gh][e] = g[in ? i * pitch + j : 0];
-          if (MUON) old[gh][e] = mom[in ? (uint64_t)i * m.cols + j : 0];
-        }
-#pragma unroll
-      for (int gh = 0; gh < 2 * RB; ++gh)
+      for (int gh = 0; gh < 2 * RB; ++gh) {
+        const uint32_t i = xi[s] + (gh >> 1) * 16 + r, j = xj[s] + (gh & 1) * 16 + c4;
+        float w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          uint32_t i, j;
-          const bool in = inside(gh, e, i, j);
-          float u = to_f32(raw[gh][e]);
+          float u = raw[gh].value(e, j, m.cols);
           if (MUON) {
-            const float v = u * coef, w = f.mu * old[gh][e] + f.nu * v;
-            if (in) mom[(uint64_t)i * m.cols + j] = w;
-            u = updated(v, w, f);
+            const float v = u * coef;
+            w[e] = f.mu * old[gh].value(e, j, m.cols) + f.nu * v;
+            u = updated(v, w[e], f);
           }
-          u = in ? u : 0.0f;
+          u = i < m.rows && j + e < m.cols ? u : 0.0f;
           x[s][gh >> 1][gh & 1][e] = u;
           square += (double)u * u;
         }
+        if (MUON && i < m.rows) store_four(mom + (uint64_t)i * m.cols, j, m.cols, w);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   });
@@ -293,31 +334,24 @@ __global__ void __launch_bounds__(WAVES * 64, WAVES / 4)
     T* const out = (T*)to + (MUON ? m.elem : (uint64_t)mat * m.rows * m.cols);
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-      T old[2 * RB][4];
-      auto inside = [&](int gh, int e, uint64_t& o) {
-        const uint32_t i = xi[s] + (gh >> 1) * 16 + r, j = xj[s] + (gh & 1) * 16 + c4 + e;
-        const bool in = i < m.rows && j < m.cols;
-        o = in ? (uint64_t)i * m.cols + j : 0;
-        return in;
-      };
+      Four<T> old[2 * RB];
       if (MUON)
 #pragma unroll
-        for (int gh = 0; gh < 2 * RB; ++gh)
+        for (int gh = 0; gh < 2 * RB; ++gh) {
+          const uint32_t i = xi[s] + (gh >> 1) * 16 + r;
+          old[gh].load(out + (uint64_t)(i < m.rows ? i : 0) * m.cols, xj[s] + (gh & 1) * 16 + c4, m.cols);
+        }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint64_t o;
-            (void)inside(gh, e, o);
-            old[gh][e] = out[o];
-          }
-#pragma unroll
-      for (int gh = 0; gh < 2 * RB; ++gh)
+      for (int gh = 0; gh < 2 * RB; ++gh) {
+        const uint32_t i = xi[s] + (gh >> 1) * 16 + r, j = xj[s] + (gh & 1) * 16 + c4;
+        T y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          uint64_t o;
-          const bool in = inside(gh, e, o);
-          const float y = x[s][gh >> 1][gh & 1][e] * (1.0f / NS_X);
-          if (in) out[o] = from_f32<T>(MUON ? to_f32(old[gh][e]) * decay - step * y : y);
+          const float v = x[s][gh >> 1][gh & 1][e] * (1.0f / NS_X);
+          y[e] = from_f32<T>(MUON ? old[gh].value(e, j, m.cols) * decay - step * v : v);
         }
+        if (i < m.rows) store_four(out + (uint64_t)i * m.cols, j, m.cols, y);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   });

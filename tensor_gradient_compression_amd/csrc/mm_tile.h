@@ -44,9 +44,13 @@ constexpr int64_t MM_MOST_STRIDE = 1 << 21;
 
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
 
+// Waits until at most N of this wave's transfers are under way. The compiler knows nothing of
+// them: no read of LDS may move across.
 template <int N>
 __device__ __forceinline__ void wait_vm() {
+  __asm__ volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+  __asm__ volatile("" ::: "memory");
 }
 
 // One operand's way into LDS: ROWS rows (or columns of C) by K values of k, PER transfers of

@@ -88,7 +88,7 @@ uint64_t lay_out(NsMat& m, int64_t rows, int64_t cols, int dtype, uint64_t at) {
   m.ldm = (uint32_t)up(m.m, 8);
   m.exact = dtype != TGRAD_BF16;
   m.wdt = (uint32_t)dtype;
-  m.chunks = (uint32_t)(((uint64_t)rows * cols + MUON_CHUNK - 1) / MUON_CHUNK);
+  m.chunks = (uint32_t)(((uint64_t)rows * (m.ldx / 8) + MUON_CHUNK / 8 - 1) / (MUON_CHUNK / 8));
   auto take = [&](uint64_t bytes) {
     const uint64_t o = at;
     at += up(bytes, 256);
@@ -104,9 +104,6 @@ uint64_t lay_out(NsMat& m, int64_t rows, int64_t cols, int dtype, uint64_t at) {
   m.sums = take(m.chunks * 8ull);
   return at;
 }
-// chunks of padded lines
-uint64_t start_chunks(const NsMat& m) { return ((uint64_t)m.rows * (m.ldx / 8) + MUON_CHUNK / 8 - 1) / (MUON_CHUNK / 8); }
-
 uint64_t across(uint64_t n, int tile) { return (n + ns_tile_size(tile) - 1) / ns_tile_size(tile); }
 uint64_t lower_tiles(uint64_t m, int tile) { return across(m, tile) * (across(m, tile) + 1) / 2; }
 
@@ -205,7 +202,7 @@ int tgrad_muon_init(tgrad_muon_t** out, int n, const int64_t* count, const int64
         m.wd = weight_decay[i];
         m.tensor = (uint32_t)i;
         mats.push_back(m);
-        over += m.chunks + start_chunks(m) + 1;
+        over += 2 * m.chunks + 1;
         if (over > 2 * kMostParts) {
           delete h;
           return TGRAD_EINVAL;
@@ -255,7 +252,7 @@ int tgrad_muon_init(tgrad_muon_t** out, int n, const int64_t* count, const int64
       });
     };
     list(h->starts, 0, [&](uint32_t k, const NsMat& m) {
-      for (uint32_t c = 0; c < start_chunks(m); ++c) parts.push_back({k, c, 0});
+      for (uint32_t c = 0; c < m.chunks; ++c) parts.push_back({k, c, 0});
     });
     const int half = sum([](const NsMat& m, int t) { return lower_tiles(m.m, t); });
     list(h->gram, half, [&](uint32_t k, const NsMat& m) {
@@ -416,16 +413,16 @@ int tgrad_orthogonalize(const void* x, int64_t matrix_stride, int64_t row_stride
   Launches l{};
   l.tgram = l.tpoly = choose_tile([&](int t) { return n * lower_tiles(m, t); });
   l.tapply = choose_tile([&](int t) { return n * across(rows, t) * across(cols, t); });
-  const uint64_t chunks = n * c.one.chunks, starts = n * start_chunks(c.one), half = n * lower_tiles(m, l.tgram);
+  const uint64_t chunks = n * c.one.chunks, half = n * lower_tiles(m, l.tgram);
   const uint64_t whole = n * across(rows, l.tapply) * across(cols, l.tapply);
-  for (uint64_t k : {chunks, starts, half, whole})
+  for (uint64_t k : {chunks, half, whole})
     if (k > kMostParts) return TGRAD_EINVAL;
   l.gram = l.poly = {nullptr, (uint32_t)across(m, l.tgram), (uint32_t)across(m, l.tgram), true};
   l.apply = {nullptr, (uint32_t)across(rows, l.tapply), (uint32_t)across(cols, l.tapply), false};
   l.ngram = l.npoly = (uint32_t)half;
   l.napply = (uint32_t)whole;
   hipError_t e = launch_ns_norm(c, f, {nullptr, c.one.chunks, 1, false}, (uint32_t)chunks, s);
-  if (e == hipSuccess) e = launch_ns_start(c, f, eps, {nullptr, (uint32_t)start_chunks(c.one), 1, false}, (uint32_t)starts, s);
+  if (e == hipSuccess) e = launch_ns_start(c, f, eps, {nullptr, c.one.chunks, 1, false}, (uint32_t)chunks, s);
   NsLast last{};
   last.out = out;
   if (e == hipSuccess) e = iterate(c, l, steps, last, s);

@@ -39,10 +39,6 @@ __device__ __forceinline__ uint32_t my_part(const NsCommon& c, const NsParts& p,
   return mat;
 }
 
-__device__ __forceinline__ float load_as(const void* p, uint32_t dt, uint64_t i) {
-  return dt == DT_F32 ? ((const float*)p)[i] : dt == DT_F16 ? to_f32(((const _Float16*)p)[i]) : to_f32(((const bf16_t*)p)[i]);
-}
-
 // f with a zero of the type
 template <class F>
 __device__ __forceinline__ void with_type(uint32_t dt, const F& f) {
@@ -51,16 +47,19 @@ __device__ __forceinline__ void with_type(uint32_t dt, const F& f) {
   else f(bf16_t{0});
 }
 
-// v as two fp16 parts
+// N values at p, which is aligned to one of them (16 bytes at a time all the same)
+template <int N, typename T>
+__device__ __forceinline__ void load_values(const T* p, T* v) { __builtin_memcpy(v, p, N * sizeof(T)); }
+template <int N, typename T>
+__device__ __forceinline__ void store_values(T* p, const T* v) { __builtin_memcpy(p, v, N * sizeof(T)); }
+
+// v as two fp16 parts. (Without the empty statement the compiler rounds a product that v is twice,
+// once from its exact value and once from its fp32 one, and where these differ the lower part
+// belongs to another upper part than the one that is stored.)
 __device__ __forceinline__ void two_parts(float v, _Float16& hi, _Float16& lo) {
+  __asm__("" : "+v"(v));
   hi = (_Float16)v;
   lo = (_Float16)(v - (float)hi);
-}
-
-__device__ __forceinline__ void store_as(void* p, uint32_t dt, uint64_t i, float y) {
-  if (dt == DT_F32) ((float*)p)[i] = y;
-  else if (dt == DT_F16) ((_Float16*)p)[i] = from_f32<_Float16>(y);
-  else ((bf16_t*)p)[i] = from_f32<bf16_t>(y);
 }
 
 __device__ __forceinline__ float updated(float g, float m, const MuonFirst& f) { return f.nesterov ? f.nu * g + f.mu * m : m; }
