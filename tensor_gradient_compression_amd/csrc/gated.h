@@ -79,7 +79,7 @@ struct GatedDw {
 int gated_dw_splits(int64_t rows, uint32_t in, uint32_t hidden);
 hipError_t launch_gated_dw(const GatedDw& a, hipStream_t s);
 
-// The tile of a product: 0: 256 x 256, 1: 128 x 128, 2: 64 x 64.
+// The tile of the products of g and u: 0: 256 x 256, 1: 128 x 128, 2: 64 x 64, 3: 128 x 256.
 int gated_tile(int64_t ni, int64_t nj, int64_t k);
 
 template <int DT> struct GatedType;

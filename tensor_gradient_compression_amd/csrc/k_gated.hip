@@ -309,6 +309,7 @@ hipError_t launch_type(bool grads, const GatedArgs& a, hipStream_t s) {
   switch (gated_tile(a.rows, 2 * (int64_t)a.hidden, a.in)) {
     case 0: return launch_tiles<MmBig, DT>(grads, a, s);
     case 1: return launch_tiles<MmMid, DT>(grads, a, s);
+    case 3: return launch_tiles<MmHalf, DT>(grads, a, s);
     default: return launch_tiles<MmSmall, DT>(grads, a, s);
   }
 }
@@ -321,13 +322,13 @@ hipError_t launch_any(bool grads, const GatedArgs& a, hipStream_t s) {
 
 int gated_tile(int64_t ni, int64_t nj, int64_t k) {
   const int64_t big = ((ni + 255) / 256) * ((nj + 255) / 256), mid = ((ni + 127) / 128) * ((nj + 127) / 128);
-  return big >= 200 && k > 512 ? 0 : mid >= 200 ? 1 : 2;
+  return big >= 200 ? (k <= 1024 ? 3 : 0) : mid >= 200 ? 1 : 2;
 }
 
 int64_t gated_sum_rows(int64_t rows, uint32_t in, uint32_t hidden) {
   const int t = gated_tile(rows, 2 * (int64_t)hidden, in);
-  const int64_t bm = t == 0 ? MmBig::BM : t == 1 ? MmMid::BM : MmSmall::BM;
-  return (rows + bm - 1) / bm * (t == 0 ? MmBig::WM : t == 1 ? MmMid::WM : MmSmall::WM);
+  auto sums = [&](auto shape) { return (rows + shape.BM - 1) / shape.BM * shape.WM; };
+  return t == 0 ? sums(MmBig{}) : t == 1 ? sums(MmMid{}) : t == 2 ? sums(MmSmall{}) : sums(MmHalf{});
 }
 
 hipError_t launch_gated_forward(const GatedArgs& a, hipStream_t s) { return launch_any(false, a, s); }

@@ -17,6 +17,8 @@
 // 16-bit parts is multiplied by naming its parts' products one after another (the smallest
 // first), and [dg du] [Wg; Wu] without laying the weights together.
 #pragma once
+#include <type_traits>
+
 #include "tg_common.h"
 
 namespace tg {
@@ -53,6 +55,13 @@ __device__ __forceinline__ void wait_vm() {
   __asm__ volatile("" ::: "memory");
 }
 
+// Waits for this wave's reads and writes of LDS.
+__device__ __forceinline__ void wait_lds() {
+  __asm__ volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  __asm__ volatile("" ::: "memory");
+}
+
 // One operand's way into LDS: ROWS rows (or columns of C) by K values of k, PER transfers of
 // 1 KB for each of WAVES waves.
 template <int ROWS, int K, int WAVES, bool CROSSED>
@@ -62,9 +71,9 @@ struct MmLoader {
   static constexpr int PIECES = K / 8;   // of a straight row
   static_assert(PER * 1024 * WAVES == BYTES, "the waves share the transfers evenly");
   uint32_t v[PER];       // lane's byte offsets from the stage's first byte
-  uint32_t k_of_lane;    // straight: the k of the lane's piece within the stage
-  uint64_t at;           // the stage's first byte
-  uint64_t left;         // bytes from there to the operand's end, more than none
+  uint32_t k_of_lane;    // of the lane's piece within the stage (crossed: of the first transfer)
+  u32x4 rs;              // buffer resource from the segment's first byte (or a later one) to the operand's end
+  uint32_t at;           // the stage's first byte there
 
   // BY_TURNS: the operand holds every other 16 of the tile's rows
   template <bool BY_TURNS = false>
@@ -82,7 +91,7 @@ struct MmLoader {
         constexpr int LANES = ROWS / 8;   // of one k
         const int k = q * (64 / LANES) + lane / LANES, c = lane % LANES;
         v[i] = (uint32_t)k * (stride * 2) + (uint32_t)(c ^ (turn(k) << 1)) * 16;
-        k_of_lane = 0;
+        if (i == 0) k_of_lane = (uint32_t)k;
       }
     }
   }
@@ -93,39 +102,48 @@ struct MmLoader {
   // from row `row` and value `k` of k on
   __device__ __forceinline__ void start(const MmOperand& o, int64_t row, int64_t k) {
     const int64_t skip = (CROSSED ? row + k * o.stride : row * o.stride + k) * 2;
-    at = (uint64_t)o.p + (uint64_t)skip;
-    left = (uint64_t)(((o.lines - 1) * (int64_t)o.stride + o.len) * 2 - skip);
+    resource((uint64_t)o.p + (uint64_t)skip, (uint64_t)(((o.lines - 1) * (int64_t)o.stride + o.len) * 2 - skip));
   }
-  __device__ __forceinline__ void next(uint32_t stride) {
-    const uint32_t step = (CROSSED ? stride : 1) * (K * 2);
-    at += step;
-    left -= step;
+  __device__ __forceinline__ void resource(uint64_t from, uint64_t left) {
+    rs[0] = (uint32_t)from;
+    rs[1] = (uint32_t)(from >> 32) & 0xFFFFu;
+    rs[2] = (uint32_t)(left >> 32) ? 0xFFFFFFF0u : (uint32_t)left;
+    rs[3] = 0x00020000u;
+    at = 0;
+  }
+  __device__ __forceinline__ void next(const MmOperand& o, uint32_t stride) {
+    at += (CROSSED ? stride : 1) * (K * 2);
+    if (CROSSED && at >= 0x40000000u) {   // 32 bits do not reach through a long operand
+      const uint64_t from = (((uint64_t)rs[1] << 32) | rs[0]) + at;
+      resource(from, (uint64_t)o.p + (uint64_t)(((o.lines - 1) * (int64_t)o.stride + o.len) * 2) - from);
+    }
   }
   // Whether transfer i is of the second matrix of two that alternate.
   __device__ static constexpr bool second(int i) { return ((i * (64 / PIECES)) >> 4) & 1; }
 
-  // The transfers (BY_TURNS: those of one matrix); `rem`: values of k from the stage's first one
-  // on. Written as instructions: the compiler would wait for all transfers before any read of LDS.
-  template <bool BY_TURNS = false, bool SECOND = false>
+  // The transfers (BY_TURNS: those of one matrix) of a stage; PART: only `rem` values of k of it are
+  // there. (Whether the stage's offset counts in the resource's check or not: rows past the end
+  // are behind it by their own offsets, and k past the end is left out here.) Written as
+  // instructions: the compiler would wait for all transfers before any read of LDS.
+  template <bool PART, bool BY_TURNS = false, bool SECOND = false>
   __device__ __forceinline__ void issue(uint32_t lds, int wave, int rem) const {
-    u32x4 rs;
-    rs[0] = (uint32_t)at;
-    rs[1] = (uint32_t)(at >> 32) & 0xFFFFu;
-    rs[2] = (uint32_t)(left >> 32) ? 0xFFFFFFF0u : (uint32_t)left;
-    rs[3] = 0x00020000u;
+    bool first = true;
+    lds += (uint32_t)(wave * PER) * 1024u;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       if (BY_TURNS && second(i) != SECOND) continue;
-      const uint32_t o = CROSSED || (int)k_of_lane < rem ? v[i] : 0xFFFFFFF0u;
+      uint32_t o = v[i];
+      if (PART) o = (int)k_of_lane + (CROSSED ? i * (512 / ROWS) : 0) < rem ? o : 0xFFFFFFF0u;
       // a scalar register that the vector unit wrote takes five states to reach a transfer
-      if (i == 0 || (BY_TURNS && SECOND && !second(i - 1)))
-        __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                         ::"s"(lds + (uint32_t)(wave * PER + i) * 1024u), "v"(o), "s"(rs)
-                         : "memory");
+      if (first)
+        __asm__ volatile("s_add_u32 m0, %0, %4\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                         ::"s"(lds), "v"(o), "s"(rs), "s"(at), "i"(i * 1024)
+                         : "memory", "scc");
       else
-        __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                         ::"s"(lds + (uint32_t)(wave * PER + i) * 1024u), "v"(o), "s"(rs)
-                         : "memory");
+        __asm__ volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                         ::"s"(lds), "v"(o), "s"(rs), "s"(at), "i"(i * 1024)
+                         : "memory", "scc");
+      first = false;
     }
   }
 };
@@ -184,19 +202,20 @@ enum MmMode { MM_TURNS, MM_EVEN, MM_ALONE };
 // Four stages of 32 keep a transfer in flight for two stages' products; two of 64 fetch straight
 // rows by whole cache lines and have half the barriers (MM_TURNS, 8192 x 8192 x 8192: 1014 us with
 // four of 32, 1032 with two of 64; MM_EVEN, 18 Grams of 1024 x 4096: 148 and 136).
-template <int BM_, int BN_, int WM_, int WN_, MmMode MODE_>
+template <int BM_, int BN_, int WM_, int WN_, MmMode MODE_, int K_, int STAGES_>
 struct MmShape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
   static constexpr MmMode MODE = MODE_;
   static constexpr int WAVES = WM * WN, THREADS = WAVES * 64;
   static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
-  static constexpr int K = MODE == MM_EVEN ? 64 : 32, STAGES = MODE == MM_EVEN ? 2 : 4;
+  static constexpr int K = K_, STAGES = STAGES_;
   static constexpr int STAGE = (BM + BN) * K * 2;
   static constexpr int LDS_BYTES = STAGES * STAGE * (MODE == MM_ALONE ? WAVES : 1);
 };
-using MmBig = MmShape<256, 256, 2, 4, MM_TURNS>;
-using MmMid = MmShape<128, 128, 2, 2, MM_EVEN>;
-using MmSmall = MmShape<64, 64, 4, 1, MM_ALONE>;
+using MmBig = MmShape<256, 256, 2, 4, MM_TURNS, 32, 4>;
+using MmHalf = MmShape<128, 256, 1, 4, MM_EVEN, 32, 3>;
+using MmMid = MmShape<128, 128, 2, 2, MM_EVEN, 64, 2>;
+using MmSmall = MmShape<64, 64, 4, 1, MM_ALONE, 32, 4>;
 
 // The sums of a wave: c[i][j] holds, in lane l, row 16 i + (l & 15) and columns
 // 16 j + 4 (l >> 4) + 0..3 of the wave's part.
@@ -250,32 +269,37 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
   const uint32_t lds0 = uniform((uint32_t)(uintptr_t)lds);
   int seg = 0, issued = 0, rem = 0;
   uint32_t into = 0;       // where the next stage goes
+  MmOperand oa, ob, ob2;
   auto begin = [&](int s) {
-    MmOperand a, b, b2;
-    source(s, a, b, b2);
-    la.start(a, ai, from);
-    lb.start(b, bj, from);
-    if constexpr (DUAL) lb2.start(b2, bj, from);
+    source(s, oa, ob, ob2);
+    la.start(oa, ai, from);
+    lb.start(ob, bj, from);
+    if constexpr (DUAL) lb2.start(ob2, bj, from);
     rem = (int)many;
   };
   auto after = [&](uint32_t at) { return at == (STAGES - 1) * S::STAGE ? 0u : at + S::STAGE; };
+  auto transfers = [&](auto part, uint32_t l) {
+    constexpr bool PART = decltype(part)::value;
+    la.template issue<PART>(l, loader, rem);
+    if constexpr (!DUAL) {
+      lb.template issue<PART>(l + LA::BYTES, loader, rem);
+    } else {
+      static_assert(LB::PER * (64 / LB::PIECES) % 32 == 0, "a wave's transfers: whole pairs of blocks");
+      lb.template issue<PART, true, false>(l + LA::BYTES, loader, rem);
+      lb2.template issue<PART, true, true>(l + LA::BYTES, loader, rem);
+    }
+  };
   auto issue = [&]() {
     const uint32_t l = lds0 + into;
     into = after(into);
-    la.issue(l, loader, rem);
-    if constexpr (!DUAL) {
-      lb.issue(l + LA::BYTES, loader, rem);
-    } else {
-      static_assert(LB::PER * (64 / LB::PIECES) % 32 == 0, "a wave's transfers: whole pairs of blocks");
-      lb.template issue<true, false>(l + LA::BYTES, loader, rem);
-      lb2.template issue<true, true>(l + LA::BYTES, loader, rem);
-    }
     ++issued;
+    if (rem >= K) transfers(std::false_type{}, l);
+    else transfers(std::true_type{}, l);
     rem -= K;
     if (rem > 0) {
-      la.next(sa);
-      lb.next(sb);
-      if constexpr (DUAL) lb2.next(sb);
+      la.next(oa, sa);
+      lb.next(ob, sb);
+      if constexpr (DUAL) lb2.next(ob2, sb);
     } else if (++seg < nseg) {
       begin(seg);
     }
@@ -325,9 +349,12 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
       lds_barrier();
     };
     for (; t + 3 < total; ++t, at = after(at)) {
+      // (crossed reads take longer than straight ones: transfers that wait for them come late;
+      // 8192 x 8192 x 8192 with both operands crossed 1048 -> 990 us, straight 975 -> 993)
       s16x8 fa[FM], fb[FN];
+      if (CA) issue();
       fragments(at, 0, fa, fb);
-      issue();
+      if (!CA) issue();
       wait_vm<2 * LOADS>();
       product(fa, fb);
     }
@@ -339,9 +366,10 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
     }
     if (!group) lds_barrier();
   } else if constexpr (S::MODE == MM_EVEN) {
-    if (total > 0) issue();
+    for (int i = 0; i < STAGES - 1; ++i)
+      if (i < total) issue();
     for (; t < total; ++t, at = after(at)) {
-      wait_vm<0>();
+      arrived(t);
       lds_barrier();       // every wave's part of this stage is there, and the one before is read
       if (issued < total) issue();
 #pragma unroll
@@ -352,7 +380,8 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
       }
     }
   } else {
-    // a stage's fragments are read while the one before is multiplied
+    // a stage's fragments are read while the one before is multiplied, and its place filled again
+    // once they are there
     static_assert(!ALONE || (STAGES == 4 && K == 32), "at most three stages behind the one that is awaited");
     for (int i = 0; i < STAGES; ++i)
       if (i < total) issue();
@@ -361,19 +390,28 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
       arrived(0);
       fragments(at, 0, fa[0], fb[0]);
     }
-    for (; t < total; t += 2) {
+    for (; t + STAGES + 1 < total; t += 2) {
 #pragma unroll
       for (int o = 0; o < 2; ++o) {
-        if (t + o >= total) break;
-        __builtin_amdgcn_s_waitcnt(0xC07F);   // this stage's fragments are read and its place is free
-        if (issued < total) issue();
+        wait_lds();
+        issue();
         at = after(at);
-        if (t + o + 1 < total) {
-          arrived(t + o + 1);
-          fragments(at, 0, fa[o ^ 1], fb[o ^ 1]);
-        }
+        wait_vm<3 * LOADS>();
+        fragments(at, 0, fa[o ^ 1], fb[o ^ 1]);
         multiply(fa[o], fb[o]);
       }
+    }
+    for (; t < total; ++t) {
+      wait_lds();
+      if (issued < total) issue();
+      at = after(at);
+      if (t + 1 < total) arrived(t + 1);
+      fragments(at, 0, fa[1], fb[1]);      // behind the last: not used
+      multiply(fa[0], fb[0]);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) fa[0][i] = fa[1][i];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) fb[0][j] = fb[1][j];
     }
   }
   if constexpr (!ALONE) {
