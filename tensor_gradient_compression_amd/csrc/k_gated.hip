@@ -122,10 +122,17 @@ __device__ __forceinline__ void gate_and_up(MmSums<S>& sums, TG_LDS char* lds, c
       G::SEGS, a.x.len, row0, f0, a.x.stride, a.wg.stride);
 }
 
-template <typename T>
-__device__ __forceinline__ void bias4(const void* p, uint32_t f, uint32_t hidden, float* b) {
+// The biases of a lane's columns, gate and up by turns. (All loads of an epilogue go out before its
+// first store, which the compiler would not let them pass.)
+template <class S, typename T>
+__device__ __forceinline__ void load_biases(const GatedArgs& a, uint32_t f, float (&b)[S::FN][4]) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) b[e] = p && f + e < hidden ? to_f32(((const T*)p)[f + e]) : 0.0f;
+  for (int j = 0; j < S::FN; ++j) {
+    const T* const p = (const T*)(j & 1 ? a.bu : a.bg);
+    const uint32_t at = f + (j >> 1) * 16;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b[j][e] = p && at + e < a.hidden ? to_f32(p[at + e]) : 0.0f;
+  }
 }
 
 template <class S, int DT>
@@ -143,14 +150,16 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_forward(const GatedArgs
   const int lane = threadIdx.x & 63, wave = (int)uniform(threadIdx.x >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
   const bool aligned = (a.hidden % 4) == 0 && ((uintptr_t)a.y & (4 * sizeof(T) - 1)) == 0;
+  const uint32_t f_of_lane = f0 + wn * S::FN * 8 + (lane >> 4) * 4;
+  float bias[S::FN][4];
+  load_biases<S, T>(a, f_of_lane, bias);
   with_activation(a.act, [&](auto act) {
     constexpr int ACT = decltype(act)::value;
 #pragma unroll
     for (int j = 0; j < S::FN; j += 2) {
-      const uint32_t f = f0 + (wn * S::FN + j) * 8 + (lane >> 4) * 4;
-      float bg[4], bu[4];
-      bias4<T>(a.bg, f, a.hidden, bg);
-      bias4<T>(a.bu, f, a.hidden, bu);
+      const uint32_t f = f_of_lane + j * 8;
+      const float* const bg = bias[j];
+      const float* const bu = bias[j + 1];
 #pragma unroll
       for (int i = 0; i < S::FM; ++i) {
         const int64_t m = row0 + (wm * S::FM + i) * 16 + (lane & 15);
@@ -185,28 +194,45 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_grads(const GatedArgs a
   const uint32_t pad = gated_pad(a.hidden);
   const int64_t part = a.rows * 2 * (int64_t)pad;
   const bool aligned = (a.hidden % 4) == 0 && (a.dy_stride % 4) == 0 && ((uintptr_t)a.dy & (4 * sizeof(T) - 1)) == 0;
+  const uint32_t f_of_lane = f0 + wn * S::FN * 8 + (lane >> 4) * 4;
+  float bias[S::FN][4];
+  load_biases<S, T>(a, f_of_lane, bias);
+  T all[S::FN / 2][S::FM][4];
+  auto load = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < S::FM; ++i) {
+      const int64_t m = row0 + (wm * S::FM + i) * 16 + (lane & 15);
+      const uint32_t f = f_of_lane + j * 16;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) all[j][i][e] = T{};
+      if (m >= a.rows || f >= a.hidden) continue;
+      const T* const src = (const T*)a.dy + m * a.dy_stride + f;
+      if (aligned) {
+        __builtin_memcpy(all[j][i], __builtin_assume_aligned(src, 4 * sizeof(T)), 4 * sizeof(T));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (f + e < a.hidden) all[j][i][e] = src[e];
+      }
+    }
+  };
+  constexpr bool ALL = sizeof(T) == 2 || S::FM < 8;   // registers for all of it
+#pragma unroll
+  for (int j = 0; j < (ALL ? S::FN / 2 : 1); ++j) load(j);
   with_activation(a.act, [&](auto act) {
     constexpr int ACT = decltype(act)::value;
 #pragma unroll
     for (int j = 0; j < S::FN; j += 2) {
-      const uint32_t f = f0 + (wn * S::FN + j) * 8 + (lane >> 4) * 4;
-      float bg[4], bu[4];
-      bias4<T>(a.bg, f, a.hidden, bg);
-      bias4<T>(a.bu, f, a.hidden, bu);
+      const uint32_t f = f_of_lane + j * 8;
+      const float* const bg = bias[j];
+      const float* const bu = bias[j + 1];
+      if (!ALL && j) load(j / 2);
       f32x4 sg = {0.f, 0.f, 0.f, 0.f}, su = sg;
 #pragma unroll
       for (int i = 0; i < S::FM; ++i) {
         const int64_t m = row0 + (wm * S::FM + i) * 16 + (lane & 15);
         if (m >= a.rows || f >= pad) continue;
-        T dy[4] = {};
-        const T* const src = (const T*)a.dy + m * a.dy_stride + f;
-        if (aligned && f < a.hidden) {
-          __builtin_memcpy(dy, __builtin_assume_aligned(src, 4 * sizeof(T)), 4 * sizeof(T));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (f + e < a.hidden) dy[e] = src[e];
-        }
+        const T* const dy = all[j / 2][i];
         float dg[4], du[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {

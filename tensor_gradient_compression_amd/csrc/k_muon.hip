@@ -32,6 +32,7 @@ static_assert(sizeof(NsCommon) + sizeof(MuonFirst) + sizeof(MuonTable) + sizeof(
 
 namespace {
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 constexpr uint32_t kPartsA = 0x001, kPartsB = 0x010;   // lower upper, upper lower, upper upper
 
 __device__ __forceinline__ void workgroup_sum(double s, double* out) {
@@ -43,7 +44,8 @@ __device__ __forceinline__ void workgroup_sum(double s, double* out) {
   if (threadIdx.x == 0) *out = (w[0] + w[1]) + (w[2] + w[3]);
 }
 
-// A chunk of a matrix: f(row, column, n) for pieces of 8 values of a line, n of them inside.
+// A chunk of a matrix: f(row, column, n) for pieces of 8 values of a line, n of them inside (zeros are
+// what lines are padded with).
 template <class F>
 __device__ __forceinline__ void each_piece(const NsMat& m, uint32_t chunk, const F& f) {
   const uint32_t pieces = m.ldx / 8;
@@ -53,7 +55,7 @@ __device__ __forceinline__ void each_piece(const NsMat& m, uint32_t chunk, const
   for (uint32_t q = 0; q < MUON_CHUNK / 8 / 256; ++q) {
     const uint32_t at = skip + q * 256 + threadIdx.x, down = at / pieces, k = (at - down * pieces) * 8;
     const uint64_t row = row0 + down;
-    if (row < m.rows) f((uint32_t)row, k, m.cols - k < 8 ? m.cols - k : 8);
+    if (row < m.rows) f((uint32_t)row, k, k >= m.cols ? 0 : m.cols - k < 8 ? m.cols - k : 8);
   }
 }
 // 8 values from p on, of which n are there (zeros behind)
@@ -129,6 +131,12 @@ __global__ void __launch_bounds__(256) k_ns_norm(const NsCommon c, const NsSourc
   workgroup_sum(s, (double*)(c.ws + m.sums) + chunk);
 }
 
+// counters for whole_sums()
+__device__ __forceinline__ void clear_counters(const NsCommon& c) {
+  if (blockIdx.x || !c.counters) return;
+  for (uint32_t i = threadIdx.x; i < NS_MOST_SPLIT; i += 256) c.counters[i] = 0;
+}
+
 // 2^12 / (|U| + eps), by every workgroup from all sums of the matrix in their order
 __device__ __forceinline__ float start_scale(const NsCommon& c, const NsMat& m, double eps) {
   __shared__ double total;
@@ -152,6 +160,7 @@ __device__ __forceinline__ void write_x(const NsCommon& c, const NsMat& m, uint3
 
 __global__ void __launch_bounds__(256) k_muon_start(const NsCommon c, const MuonFirst f, const double eps, const NsParts p) {
   if (left_out(c)) return;
+  clear_counters(c);
   const float coef = c.clip ? c.clip[1] : 1.0f;
   NsMat m;
   uint32_t chunk, none;
@@ -176,6 +185,7 @@ __global__ void __launch_bounds__(256) k_muon_start(const NsCommon c, const Muon
 }
 
 __global__ void __launch_bounds__(256) k_ns_start(const NsCommon c, const NsSource f, const double eps, const NsParts p) {
+  clear_counters(c);
   NsMat m;
   uint32_t chunk, none;
   const uint32_t mat = my_part(c, p, blockIdx.x, m, chunk, none);
@@ -202,72 +212,189 @@ __device__ __forceinline__ MmOperand ns_operand(const NsCommon& c, const NsMat& 
   return o;
 }
 
-// the four columns that a lane holds of block (i, j)
-template <class S, class F>
-__device__ __forceinline__ void each_four(const MmSums<S>& sums, uint32_t i0, uint32_t j0, const F& f) {
-  const int lane = threadIdx.x & 63, wave = (int)uniform(threadIdx.x >> 6);
-  const int wm = wave / S::WN, wn = wave % S::WN;
+// The tile and the split of this workgroup: a tile's are neighbours.
+__device__ __forceinline__ void my_split(const NsParts& p, uint32_t& tile, uint32_t& split) {
+  const uint32_t t = xcd_order(blockIdx.x, gridDim.x);
+  tile = t / p.splits;
+  split = t - tile * p.splits;
+}
+
+// Leaves this workgroup's sums to the last of its tile, which adds all in their order: true for that
+// one, and its sums are the whole. The counter is zero again when it ends. The sums pass the L2s,
+// which the XCDs do not share, by accesses of agent scope; every wave waits until its own are
+// there before the workgroup is counted. (A release and an acquire around plain accesses write back
+// and empty an XCD's L2 for all its workgroups: 777 x 2051 in fp16 took 1057 us with them.)
+template <class S>
+__device__ __forceinline__ bool whole_sums(const NsCommon& c, const NsParts& p, uint32_t tile, uint32_t split, TG_LDS char* lds,
+                                           MmSums<S>& sums) {
+  if (p.splits == 1) return true;
+  TG_LDS uint32_t* const before = (TG_LDS uint32_t*)lds;   // what was there has been read
+  constexpr uint32_t EACH = S::FM * S::FN * S::THREADS * 2;
+  uint64_t* const all = (uint64_t*)(c.counters + NS_MOST_SPLIT) + (uint64_t)tile * p.splits * EACH + threadIdx.x;
 #pragma unroll
   for (int i = 0; i < S::FM; ++i)
 #pragma unroll
     for (int j = 0; j < S::FN; ++j)
-      f(i0 + (wm * S::FM + i) * 16 + (lane & 15), j0 + (wn * S::FN + j) * 16 + (lane >> 4) * 4, sums.c[i][j]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x2 v = {sums.c[i][j][2 * h], sums.c[i][j][2 * h + 1]};
+        __hip_atomic_store(all + split * EACH + ((i * S::FN + j) * 2 + h) * S::THREADS, __builtin_bit_cast(uint64_t, v),
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+  wait_vm<0>();
+  __syncthreads();
+  if (threadIdx.x == 0) *before = __hip_atomic_fetch_add(c.counters + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (*before != p.splits - 1) return false;
+  if (threadIdx.x == 0) __hip_atomic_store(c.counters + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int i = 0; i < S::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < S::FN; ++j) sums.c[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (uint32_t q = 0; q < p.splits; ++q)
+#pragma unroll
+    for (int i = 0; i < S::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f32x2 v = __builtin_bit_cast(f32x2, __hip_atomic_load(all + q * EACH + ((i * S::FN + j) * 2 + h) * S::THREADS,
+                                                                      __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+          sums.c[i][j][2 * h] += v[0];
+          sums.c[i][j][2 * h + 1] += v[1];
+        }
+  return true;
 }
 
-// v (four columns of row i, under NS_M) to a symmetric matrix, and to its other half. The rows
-// from m to ldm are only the other half's padding.
-__device__ __forceinline__ void write_symmetric(const NsCommon& c, const NsMat& m, uint64_t at, uint32_t i, uint32_t j,
-                                                bool mirror, const float* v) {
-  _Float16* const hi = (_Float16*)(c.ws + at);
-  const uint64_t part = (uint64_t)m.m * m.ldm;
+__device__ __forceinline__ uint32_t whole8(uint32_t n) { return (n + 7u) & ~7u; }
+
+// Where this lane's sums are: four columns of a row in each block.
+template <class S>
+struct Place {
+  uint32_t r, c;                    // of the first block, in the tile
+  int wi, wj;                       // its wave's first block
+  __device__ __forceinline__ Place() {
+    const int lane = threadIdx.x & 63, wave = (int)uniform(threadIdx.x >> 6);
+    wi = wave / S::WN * S::FM;
+    wj = wave % S::WN * S::FN;
+    r = wi * 16 + (lane & 15);
+    c = wj * 16 + (lane >> 4) * 4;
+  }
+};
+
+// f(i, j, what load(i, j) gave) for all blocks. Some blocks' loads go out before the first of
+// their stores, which the compiler would not let them pass: waits for memory one after another, and
+// branches around every access, were most of an epilogue (a sum over 768 by 128 x 128 tiles: 9 of 19 us).
+template <class S, class V, class Load, class F>
+__device__ __forceinline__ void each_block(const Load& load, const F& f) {
+  constexpr int BLOCKS = sizeof(V) > 32 ? 4 : sizeof(V) > 16 ? 8 : 16;
+  constexpr int ROWS = S::FM * S::FN > BLOCKS ? BLOCKS / S::FN : S::FM;
+  static_assert(S::FM % ROWS == 0, "whole groups");
+#pragma unroll
+  for (int g = 0; g < S::FM; g += ROWS) {
+    V v[ROWS][S::FN];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j) v[i][j] = load(g + i, j);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j) f(g + i, j, v[i][j]);
+  }
+}
+struct Nothing {};
+// four values in their parts
+struct Four {
+  u32x2 h, l;
+  __device__ __forceinline__ void get(float* v) const {
+    _Float16 a[4], b[4];
+    __builtin_memcpy(a, &h, 8);
+    __builtin_memcpy(b, &l, 8);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (float)a[e] + (float)b[e];
+  }
+};
+
+// A symmetric matrix around the tile at (i0, j0), and its other half.
+struct Symmetric {
+  MmWindow hi, lo, mirrored_hi, mirrored_lo;
+  __device__ __forceinline__ Symmetric(const NsCommon& c, const NsMat& m, uint64_t at, uint32_t i0, uint32_t j0)
+      : hi(c.ws + at + ((uint64_t)i0 * m.ldm + j0) * 2), lo(c.ws + at + ((uint64_t)m.m * m.ldm + (uint64_t)i0 * m.ldm + j0) * 2),
+        mirrored_hi(c.ws + at + ((uint64_t)j0 * m.ldm + i0) * 2),
+        mirrored_lo(c.ws + at + ((uint64_t)m.m * m.ldm + (uint64_t)j0 * m.ldm + i0) * 2) {}
+};
+
+// v (four columns under NS_M, of block (bi, bj)) to a symmetric matrix, and to its other half. The
+// rows from m to ldm are only the other half's padding.
+template <class S>
+__device__ __forceinline__ void write_symmetric(const NsMat& m, const Symmetric& to, const Place<S>& at, uint32_t i0,
+                                                uint32_t j0, int bi, int bj, const float* v) {
   _Float16 h[4], l[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) two_parts(v[e], h[e], l[e]);
-  if (i < m.m && j < m.ldm) {
-    *(uint2*)(hi + (uint64_t)i * m.ldm + j) = *(const uint2*)h;
-    if (m.exact) *(uint2*)(hi + part + (uint64_t)i * m.ldm + j) = *(const uint2*)l;
-  }
-  if (mirror) {
+  const uint32_t i = i0 + at.r + bi * 16, j = j0 + at.c + bj * 16;
+  const bool in = i < m.m && j < m.ldm;
+  const uint32_t lane = (at.r * m.ldm + at.c) * 2, all = (bi * 16 * m.ldm + bj * 16) * 2;
+  to.hi.store8(*(const u32x2*)h, in, lane, all);
+  if (m.exact) to.lo.store8(*(const u32x2*)l, in, lane, all);
+  if (i0 == j0) return;
+  const uint32_t mlane = (at.c * m.ldm + at.r) * 2, mall = (bj * 16 * m.ldm + bi * 16) * 2;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (j + e < m.m) {
-        hi[(uint64_t)(j + e) * m.ldm + i] = h[e];
-        if (m.exact) hi[part + (uint64_t)(j + e) * m.ldm + i] = l[e];
-      }
+  for (int e = 0; e < 4; ++e) {
+    const bool min = i < m.ldm && j + e < m.m;
+    to.mirrored_hi.store2(__builtin_bit_cast(uint16_t, h[e]), min, mlane + e * m.ldm * 2, mall);
+    if (m.exact) to.mirrored_lo.store2(__builtin_bit_cast(uint16_t, l[e]), min, mlane + e * m.ldm * 2, mall);
   }
 }
+
+// The entries of block (bi, bj) on the diagonal: f(row, e) in the lanes that hold one.
+template <class S, class F>
+__device__ __forceinline__ void on_diagonal(const NsMat& m, const Place<S>& at, uint32_t i0, uint32_t j0, int bi, int bj, const F& f) {
+  if (i0 != j0 || at.wi + bi != at.wj + bj) return;   // all lanes alike
+  const uint32_t i = i0 + at.r + bi * 16, e = (at.r & 15) - (at.c & 15);
+  if (e < 4 && i < m.m) f(i, e);
+}
+__device__ __forceinline__ float pick(const float* v, uint32_t e) { return e == 0 ? v[0] : e == 1 ? v[1] : e == 2 ? v[2] : v[3]; }
 
 template <class S>
 __global__ void __launch_bounds__(S::THREADS, 2) k_ns_gram(const NsCommon c, const int at, const NsParts p) {
   extern __shared__ char lds_raw[];
   if (left_out(c)) return;
   NsMat m;
-  uint32_t ti, tj;
-  my_part(c, p, xcd_order(blockIdx.x, gridDim.x), m, ti, tj);
+  uint32_t ti, tj, tile, split;
+  my_split(p, tile, split);
+  my_part(c, p, tile, m, ti, tj);
   const uint32_t i0 = ti * S::BM, j0 = tj * S::BN;
   const uint64_t from = at ? m.y : m.x;
   MmSums<S> sums;
+  const uint32_t splits = S::MODE == MM_TURNS ? 1 : p.splits;
   auto source = [&](int s, MmOperand& a, MmOperand& b, MmOperand&) {
     a = ns_operand(c, m, from, m.rows, m.ldx, kPartsA, s);
     b = ns_operand(c, m, from, m.rows, m.ldx, kPartsB, s);
   };
   const int nseg = m.exact ? 3 : 1;
   if (m.rows <= m.cols)
-    mm_tile<S, DT_F16, false, false, false>(sums, (TG_LDS char*)lds_raw, source, nseg, m.ldx, i0, j0, m.ldx, m.ldx);
+    mm_tile<S, DT_F16, false, false, false>(sums, (TG_LDS char*)lds_raw, source, nseg, whole8(m.cols), i0, j0, m.ldx, m.ldx, split,
+                                           splits);
   else
-    mm_tile<S, DT_F16, true, true, false>(sums, (TG_LDS char*)lds_raw, source, nseg, m.rows, i0, j0, m.ldx, m.ldx);
+    mm_tile<S, DT_F16, true, true, false>(sums, (TG_LDS char*)lds_raw, source, nseg, m.rows, i0, j0, m.ldx, m.ldx, split, splits);
+  if (S::MODE != MM_TURNS && !whole_sums<S>(c, p, tile, split, (TG_LDS char*)lds_raw, sums)) return;
   float* const diag = (float*)(c.ws + m.da);
-  each_four(sums, i0, j0, [&](uint32_t i, uint32_t j, f32x4 v) {
-    if (i >= m.ldm) return;
+  const Place<S> at_tile;
+  const Symmetric to(c, m, m.a, i0, j0);
+  each_block<S, Nothing>([](int, int) { return Nothing{}; }, [&](int bi, int bj, Nothing) {
+    const f32x4 v = sums.c[bi][bj];
     float o[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x = v[e] * (1.0f / (NS_X * NS_X));
-      const bool in = i < m.m && j + e < m.m;
-      if (in && i == j + e) diag[i] = x;
-      o[e] = in && i != j + e ? x * NS_M : 0.0f;
-    }
-    write_symmetric(c, m, m.a, i, j, ti != tj, o);
+    for (int e = 0; e < 4; ++e)
+      o[e] = i0 + at_tile.r + bi * 16 < m.m && j0 + at_tile.c + bj * 16 + e < m.m ? v[e] * (NS_M / (NS_X * NS_X)) : 0.0f;
+    on_diagonal(m, at_tile, i0, j0, bi, bj, [&](uint32_t i, uint32_t d) {
+      diag[i] = pick(o, d) * (1.0f / NS_M);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = d == (uint32_t)e ? 0.0f : o[e];
+    });
+    write_symmetric(m, to, at_tile, i0, j0, bi, bj, o);
   });
 }
 
@@ -276,45 +403,55 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_ns_poly(const NsCommon c, con
   extern __shared__ char lds_raw[];
   if (left_out(c)) return;
   NsMat m;
-  uint32_t ti, tj;
-  my_part(c, p, xcd_order(blockIdx.x, gridDim.x), m, ti, tj);
+  uint32_t ti, tj, tile, split;
+  my_split(p, tile, split);
+  my_part(c, p, tile, m, ti, tj);
   const uint32_t i0 = ti * S::BM, j0 = tj * S::BN;
   MmSums<S> sums;
+  const uint32_t splits = S::MODE == MM_TURNS ? 1 : p.splits;
   mm_tile<S, DT_F16, false, false, false>(
       sums, (TG_LDS char*)lds_raw,
       [&](int s, MmOperand& a, MmOperand& b, MmOperand&) {
         a = ns_operand(c, m, m.a, m.m, m.ldm, kPartsA, s);
         b = ns_operand(c, m, m.a, m.m, m.ldm, kPartsB, s);
       },
-      m.exact ? 3 : 1, m.ldm, i0, j0, m.ldm, m.ldm);
-  const float* const da = (const float*)(c.ws + m.da);
+      m.exact ? 3 : 1, whole8(m.m), i0, j0, m.ldm, m.ldm, split, splits);
+  if (S::MODE != MM_TURNS && !whole_sums<S>(c, p, tile, split, (TG_LDS char*)lds_raw, sums)) return;
   float* const db = (float*)(c.ws + m.db);
-  const _Float16* const oh = (const _Float16*)(c.ws + m.a);
-  const uint64_t part = (uint64_t)m.m * m.ldm;
-  each_four(sums, i0, j0, [&](uint32_t i, uint32_t j, f32x4 v) {
-    if (i >= m.ldm || j >= m.ldm) return;
-    _Float16 h[4] = {}, l[4] = {};
-    float di = 0.0f;
-    if (i < m.m) {
-      *(uint2*)h = *(const uint2*)(oh + (uint64_t)i * m.ldm + j);
-      if (m.exact) *(uint2*)l = *(const uint2*)(oh + part + (uint64_t)i * m.ldm + j);
-      di = da[i];
-    }
-    float o[4];
+  const Place<S> at;
+  const Symmetric from(c, m, m.a, i0, j0), to(c, m, m.b, i0, j0);
+  const MmWindow da_i((const float*)(c.ws + m.da) + i0), da_j((const float*)(c.ws + m.da) + j0);
+  float di[S::FM];
+  f32x4 dj[S::FN];                      // behind the m-th anything
+#pragma unroll
+  for (int i = 0; i < S::FM; ++i) di[i] = __uint_as_float(da_i.load4(i0 + at.r + i * 16 < m.m, at.r * 4, i * 64));
+#pragma unroll
+  for (int j = 0; j < S::FN; ++j) dj[j] = __builtin_bit_cast(f32x4, da_j.load16(j0 + at.c + j * 16 < m.ldm, at.c * 4, j * 64));
+  auto load = [&](int bi, int bj) {
+    const bool in = i0 + at.r + bi * 16 < m.m && j0 + at.c + bj * 16 < m.ldm;
+    const uint32_t lane = (at.r * m.ldm + at.c) * 2, all = (bi * 16 * m.ldm + bj * 16) * 2;
+    Four x = {};
+    x.h = from.hi.load8(in, lane, all);
+    if (m.exact) x.l = from.lo.load8(in, lane, all);
+    return x;
+  };
+  each_block<S, Four>(load, [&](int bi, int bj, const Four& old) {
+    const f32x4 v = sums.c[bi][bj];
+    float x[4], o[4];
+    old.get(x);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float q = v[e] * (1.0f / (NS_M * NS_M));
-      if (i >= m.m || j + e >= m.m) {
-        o[e] = 0.0f;
-      } else if (i == j + e) {
-        db[i] = c.cb * di + c.cc * (di * di + q);
-        o[e] = 0.0f;
-      } else {
-        const float x = ((float)h[e] + (float)l[e]) * (1.0f / NS_M);
-        o[e] = (c.cb * x + c.cc * (q + (di + da[j + e]) * x)) * NS_M;
-      }
+      const float q = v[e] * (1.0f / (NS_M * NS_M)), y = x[e] * (1.0f / NS_M);
+      const float b = (c.cb * y + c.cc * (q + (di[bi] + dj[bj][e]) * y)) * NS_M;
+      o[e] = i0 + at.r + bi * 16 < m.m && j0 + at.c + bj * 16 + e < m.m ? b : 0.0f;
     }
-    write_symmetric(c, m, m.b, i, j, ti != tj, o);
+    on_diagonal(m, at, i0, j0, bi, bj, [&](uint32_t i, uint32_t d) {
+      const float q[4] = {v[0], v[1], v[2], v[3]};
+      db[i] = c.cb * di[bi] + c.cc * (di[bi] * di[bi] + pick(q, d) * (1.0f / (NS_M * NS_M)));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = d == (uint32_t)e ? 0.0f : o[e];
+    });
+    write_symmetric(m, to, at, i0, j0, bi, bj, o);
   });
 }
 
@@ -323,12 +460,14 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_ns_apply(const NsCommon c, co
   extern __shared__ char lds_raw[];
   if (left_out(c)) return;
   NsMat m;
-  uint32_t ti, tj;
-  const uint32_t mat = my_part(c, p, xcd_order(blockIdx.x, gridDim.x), m, ti, tj);
+  uint32_t ti, tj, tile, split;
+  my_split(p, tile, split);
+  const uint32_t mat = my_part(c, p, tile, m, ti, tj);
   const uint32_t i0 = ti * S::BM, j0 = tj * S::BN;
   const uint64_t from = at ? m.y : m.x;
   const bool wide = m.rows <= m.cols;
   MmSums<S> sums;
+  const uint32_t splits = S::MODE == MM_TURNS ? 1 : p.splits;
   const int nseg = m.exact ? 3 : 1;
   if (wide)
     mm_tile<S, DT_F16, false, true, false>(
@@ -337,7 +476,7 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_ns_apply(const NsCommon c, co
           a = ns_operand(c, m, m.b, m.m, m.ldm, kPartsA, s);
           b = ns_operand(c, m, from, m.rows, m.ldx, kPartsB, s);
         },
-        nseg, m.ldm, i0, j0, m.ldm, m.ldx);
+        nseg, whole8(m.m), i0, j0, m.ldm, m.ldx, split, splits);
   else
     mm_tile<S, DT_F16, false, false, false>(
         sums, (TG_LDS char*)lds_raw,
@@ -345,60 +484,102 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_ns_apply(const NsCommon c, co
           a = ns_operand(c, m, from, m.rows, m.ldx, kPartsA, s);
           b = ns_operand(c, m, m.b, m.m, m.ldm, kPartsB, s);
         },
-        nseg, m.ldx, i0, j0, m.ldx, m.ldm);
-  const float* const db = (const float*)(c.ws + m.db);
-  const _Float16* const xh = (const _Float16*)(c.ws + from);
-  _Float16* const nh = (_Float16*)(c.ws + (at ? m.x : m.y));
-  const uint64_t part = (uint64_t)m.rows * m.ldx;
+        nseg, whole8(m.cols), i0, j0, m.ldx, m.ldm, split, splits);
+  if (S::MODE != MM_TURNS && !whole_sums<S>(c, p, tile, split, (TG_LDS char*)lds_raw, sums)) return;
   const float step = (float)(last.lr * m.scale), decay = (float)(1.0 - last.lr * m.wd);
-  each_four(sums, i0, j0, [&](uint32_t i, uint32_t j, f32x4 v) {
-    if (i >= m.rows || j >= m.ldx) return;
-    const uint64_t o = (uint64_t)i * m.ldx + j;
-    _Float16 h[4], l[4];
-    *(uint2*)h = *(const uint2*)(xh + o);
-    *(uint2*)l = *(const uint2*)(xh + part + o);
-    float r[4];
+  const Place<S> place;
+  const uint64_t first = ((uint64_t)i0 * m.ldx + j0) * 2, part = (uint64_t)m.rows * m.ldx * 2;
+  const MmWindow xh(c.ws + from + first), xl(c.ws + from + part + first);
+  // diag(B) of a row, or of the columns (behind the m-th anything)
+  const MmWindow db((const float*)(c.ws + m.db) + (wide ? i0 : j0));
+  float di[S::FM];
+  f32x4 dj[S::FN];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float d = c.ca + (wide ? db[i] : j + e < m.m ? db[j + e] : 0.0f);
-      r[e] = d * ((float)h[e] + (float)l[e]) + v[e] * (1.0f / NS_M);   // under NS_X
-    }
-    if (!last.last) {
+  for (int i = 0; i < S::FM; ++i)
+    di[i] = c.ca + __uint_as_float(db.load4(wide && i0 + place.r + i * 16 < m.m, place.r * 4, i * 64));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) two_parts(j + e < m.cols ? r[e] : 0.0f, h[e], l[e]);
-      *(uint2*)(nh + o) = *(const uint2*)h;
-      *(uint2*)(nh + part + o) = *(const uint2*)l;
-      return;
-    }
-    const uint64_t to = (last.w ? m.elem : (uint64_t)mat * m.rows * m.cols) + (uint64_t)i * m.cols + j;
-    void* const out = last.w ? last.w[m.tensor] : last.out;
-    with_type(m.wdt, [&](auto zero) {
-      using T = decltype(zero);
-      T* const o = (T*)out + to;
-      T y[4] = {};
+  for (int j = 0; j < S::FN; ++j)
+    dj[j] = __builtin_bit_cast(f32x4, db.load16(!wide && j0 + place.c + j * 16 < m.ldm, place.c * 4, j * 64));
+  auto row = [&](int bi) { return i0 + place.r + bi * 16; };
+  auto col = [&](int bj) { return j0 + place.c + bj * 16; };
+  const uint32_t lane = (place.r * m.ldx + place.c) * 2;
+  auto all = [&](int bi, int bj) { return (bi * 16 * m.ldx + bj * 16) * 2; };
+  auto load = [&](int bi, int bj) {
+    const bool in = row(bi) < m.rows && col(bj) < m.ldx;
+    return Four{xh.load8(in, lane, all(bi, bj)), xl.load8(in, lane, all(bi, bj))};
+  };
+  auto next = [&](int bi, int bj, const Four& old, float* r) {   // under NS_X
+    float was[4];
+    old.get(was);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      r[e] = col(bj) + e < m.cols ? (di[bi] + dj[bj][e]) * was[e] + sums.c[bi][bj][e] * (1.0f / NS_M) : 0.0f;
+  };
+  if (!last.last) {
+    char* const to = c.ws + (at ? m.x : m.y) + first;
+    const MmWindow nh(to), nl(to + part);
+    each_block<S, Four>(load, [&](int bi, int bj, const Four& old) {
+      float r[4];
+      next(bi, bj, old, r);
+      _Float16 h[4], l[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) two_parts(r[e], h[e], l[e]);
+      const bool in = row(bi) < m.rows && col(bj) < m.ldx;
+      nh.store8(*(const u32x2*)h, in, lane, all(bi, bj));
+      nl.store8(*(const u32x2*)l, in, lane, all(bi, bj));
+    });
+    return;
+  }
+  void* const out = last.w ? last.w[m.tensor] : last.out;
+  const uint64_t elem = last.w ? m.elem : (uint64_t)mat * m.rows * m.cols;
+  with_type(m.wdt, [&](auto zero) {
+    using T = decltype(zero);
+    struct Weight {
+      Four old;
+      T y[4];
+    };
+    T* const to = (T*)out + elem;
+    auto both = [&](int bi, int bj) {
+      Weight w{load(bi, bj), {}};
+      const uint32_t i = row(bi), j = col(bj);
+      if (!last.w || i >= m.rows || j >= m.cols) return w;
+      const T* const y = to + (uint64_t)i * m.cols + j;
       if (j + 4 <= m.cols) {
-        if (last.w) load_values<4>(o, y);
+        load_values<4>(y, w.y);
+      } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float v = r[e] * (1.0f / NS_X);
-          y[e] = from_f32<T>(last.w ? to_f32(y[e]) * decay - step * v : v);
-        }
+        for (int e = 0; e < 3; ++e)
+          if (j + e < m.cols) w.y[e] = y[e];
+      }
+      return w;
+    };
+    each_block<S, Weight>(both, [&](int bi, int bj, const Weight& w) {
+      const uint32_t i = row(bi), j = col(bj);
+      if (i >= m.rows || j >= m.cols) return;
+      T* const o = to + (uint64_t)i * m.cols + j;
+      float r[4];
+      next(bi, bj, w.old, r);
+      T y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = r[e] * (1.0f / NS_X);
+        y[e] = from_f32<T>(last.w ? to_f32(w.y[e]) * decay - step * x : x);
+      }
+      if (j + 4 <= m.cols) {
         store_values<4>(o, y);
       } else {
 #pragma unroll
-        for (int e = 0; e < 3; ++e) {
-          if (j + e >= m.cols) continue;
-          const float v = r[e] * (1.0f / NS_X);
-          o[e] = from_f32<T>(last.w ? to_f32(o[e]) * decay - step * v : v);
-        }
+        for (int e = 0; e < 3; ++e)
+          if (j + e < m.cols) o[e] = y[e];
       }
     });
   });
 }
 
 template <class S, class K, class... A>
-hipError_t launch_shape(K* k, uint32_t n, hipStream_t s, const A&... a) {
+hipError_t launch_shape(K* k, uint32_t n, uint32_t splits, hipStream_t s, const A&... a) {
   if (n == 0) return hipSuccess;
+  n *= splits;
   if (n > 0x7FFFFFFFu / S::THREADS) return hipErrorInvalidValue;
   const hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS_BYTES);
   if (e != hipSuccess) return e;
@@ -407,6 +588,7 @@ hipError_t launch_shape(K* k, uint32_t n, hipStream_t s, const A&... a) {
 }
 using Big = MmBig;
 using Mid = MmMid;
+using Deep = MmDeep;
 using Small = MmSmall;
 
 }  // namespace
@@ -433,20 +615,23 @@ hipError_t launch_ns_start(const NsCommon& c, const NsSource& f, double eps, con
   return hipGetLastError();
 }
 hipError_t launch_ns_gram(const NsCommon& c, int at, int tile, const NsParts& p, uint32_t n, hipStream_t s) {
-  return tile == 0   ? launch_shape<Big>(k_ns_gram<Big>, n, s, c, at, p)
-         : tile == 1 ? launch_shape<Mid>(k_ns_gram<Mid>, n, s, c, at, p)
-                     : launch_shape<Small>(k_ns_gram<Small>, n, s, c, at, p);
+  return tile == 0   ? launch_shape<Big>(k_ns_gram<Big>, n, p.splits, s, c, at, p)
+         : tile == 1 ? launch_shape<Mid>(k_ns_gram<Mid>, n, p.splits, s, c, at, p)
+         : tile == 3 ? launch_shape<Deep>(k_ns_gram<Deep>, n, p.splits, s, c, at, p)
+                     : launch_shape<Small>(k_ns_gram<Small>, n, p.splits, s, c, at, p);
 }
 hipError_t launch_ns_poly(const NsCommon& c, int tile, const NsParts& p, uint32_t n, hipStream_t s) {
-  return tile == 0   ? launch_shape<Big>(k_ns_poly<Big>, n, s, c, p)
-         : tile == 1 ? launch_shape<Mid>(k_ns_poly<Mid>, n, s, c, p)
-                     : launch_shape<Small>(k_ns_poly<Small>, n, s, c, p);
+  return tile == 0   ? launch_shape<Big>(k_ns_poly<Big>, n, p.splits, s, c, p)
+         : tile == 1 ? launch_shape<Mid>(k_ns_poly<Mid>, n, p.splits, s, c, p)
+         : tile == 3 ? launch_shape<Deep>(k_ns_poly<Deep>, n, p.splits, s, c, p)
+                     : launch_shape<Small>(k_ns_poly<Small>, n, p.splits, s, c, p);
 }
 hipError_t launch_ns_apply(const NsCommon& c, int at, int tile, const NsLast& l, const NsParts& p, uint32_t n,
                            hipStream_t s) {
-  return tile == 0   ? launch_shape<Big>(k_ns_apply<Big>, n, s, c, at, l, p)
-         : tile == 1 ? launch_shape<Mid>(k_ns_apply<Mid>, n, s, c, at, l, p)
-                     : launch_shape<Small>(k_ns_apply<Small>, n, s, c, at, l, p);
+  return tile == 0   ? launch_shape<Big>(k_ns_apply<Big>, n, p.splits, s, c, at, l, p)
+         : tile == 1 ? launch_shape<Mid>(k_ns_apply<Mid>, n, p.splits, s, c, at, l, p)
+         : tile == 3 ? launch_shape<Deep>(k_ns_apply<Deep>, n, p.splits, s, c, at, l, p)
+                     : launch_shape<Small>(k_ns_apply<Small>, n, p.splits, s, c, at, l, p);
 }
 
 }  // namespace tg

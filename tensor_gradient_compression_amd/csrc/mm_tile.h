@@ -24,6 +24,7 @@
 namespace tg {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -105,14 +106,14 @@ struct MmLoader {
     resource((uint64_t)o.p + (uint64_t)skip, (uint64_t)(((o.lines - 1) * (int64_t)o.stride + o.len) * 2 - skip));
   }
   __device__ __forceinline__ void resource(uint64_t from, uint64_t left) {
-    rs[0] = (uint32_t)from;
-    rs[1] = (uint32_t)(from >> 32) & 0xFFFFu;
-    rs[2] = (uint32_t)(left >> 32) ? 0xFFFFFFF0u : (uint32_t)left;
+    rs[0] = uniform((uint32_t)from);
+    rs[1] = uniform((uint32_t)(from >> 32)) & 0xFFFFu;
+    rs[2] = uniform((uint32_t)(left >> 32) ? 0xFFFFFFF0u : (uint32_t)left);
     rs[3] = 0x00020000u;
     at = 0;
   }
   __device__ __forceinline__ void next(const MmOperand& o, uint32_t stride) {
-    at += (CROSSED ? stride : 1) * (K * 2);
+    at += (CROSSED ? uniform(stride) : 1) * (K * 2);
     if (CROSSED && at >= 0x40000000u) {   // 32 bits do not reach through a long operand
       const uint64_t from = (((uint64_t)rs[1] << 32) | rs[0]) + at;
       resource(from, (uint64_t)o.p + (uint64_t)(((o.lines - 1) * (int64_t)o.stride + o.len) * 2) - from);
@@ -215,6 +216,7 @@ struct MmShape {
 using MmBig = MmShape<256, 256, 2, 4, MM_TURNS, 32, 4>;
 using MmHalf = MmShape<128, 256, 1, 4, MM_EVEN, 32, 3>;
 using MmMid = MmShape<128, 128, 2, 2, MM_EVEN, 64, 2>;
+using MmDeep = MmShape<128, 128, 2, 2, MM_EVEN, 64, 4>;
 using MmSmall = MmShape<64, 64, 4, 1, MM_ALONE, 32, 4>;
 
 // The sums of a wave: c[i][j] holds, in lane l, row 16 i + (l & 15) and columns
@@ -227,10 +229,11 @@ struct MmSums {
 // `source(s, a, b, b2)` names the operands of segment s; all straight (crossed) As have the
 // stride sa, all Bs sb. k values in each of nseg segments. B's rows may come from two matrices
 // (DUAL): tile row 32 q + r < 16 from b, the 16 after from b2, both at row 16 q + r of them; bj
-// counts in rows of either.
+// counts in rows of either. Of `splits` parts of every segment's k only part `split` is summed.
 template <class S, int DT, bool CA, bool CB, bool DUAL, class Source>
 __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const Source& source, int nseg, int64_t k,
-                                        int64_t ai, int64_t bj, uint32_t sa, uint32_t sb) {
+                                        int64_t ai, int64_t bj, uint32_t sa, uint32_t sb, uint32_t split = 0,
+                                        uint32_t splits = 1) {
   static_assert(!DUAL || !CB, "two matrices by turns: straight ones");
   constexpr bool ALONE = S::MODE == MM_ALONE;
   constexpr int LOADERS = ALONE ? 1 : S::WAVES;
@@ -258,13 +261,11 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
     for (int j = 0; j < FN; ++j) c[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   // this wave's k of every segment
-  int64_t from = 0, many = k;
-  if constexpr (ALONE) {
-    const int64_t quarter = ((k + K * S::WAVES - 1) / (K * S::WAVES)) * K;
-    from = wave * quarter;
-    many = k - from < quarter ? k - from : quarter;
-    lds += wave * (STAGES * S::STAGE);
-  }
+  const uint32_t pieces = splits * (ALONE ? S::WAVES : 1);
+  const int64_t piece = (k + K * pieces - 1) / (K * pieces) * K;
+  const int64_t from = (ALONE ? split * S::WAVES + wave : split) * piece;
+  const int64_t many = k - from < piece ? k - from : piece;
+  if constexpr (ALONE) lds += wave * (STAGES * S::STAGE);
   const int total = many > 0 ? (int)((many + K - 1) / K) * nseg : 0;
   const uint32_t lds0 = uniform((uint32_t)(uintptr_t)lds);
   int seg = 0, issued = 0, rem = 0;
@@ -439,6 +440,36 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
     }
   }
 }
+
+// A matrix around a tile, for what follows a product. Loads and stores at byte offsets from `first`
+// (of one lane, and of all together) happen where `in` holds; loads give zeros elsewhere. Through a
+// buffer resource that takes no branch, and the loads of many blocks go out together.
+struct MmWindow {
+  __amdgpu_buffer_rsrc_t rs;
+  __device__ __forceinline__ explicit MmWindow(const void* first)
+      : rs(__builtin_amdgcn_make_buffer_rsrc(
+            (void*)((uint64_t)uniform((uint32_t)((uint64_t)first >> 32)) << 32 | uniform((uint32_t)(uint64_t)first)), 0,
+            0x80000000u, 0x20000)) {}
+  __device__ static __forceinline__ uint32_t at(bool in, uint32_t lane) { return in ? lane : 0xFFFFFFF0u; }
+  __device__ __forceinline__ uint32_t load4(bool in, uint32_t lane, uint32_t all) const {
+    return __builtin_amdgcn_raw_buffer_load_b32(rs, at(in, lane), all, 0);
+  }
+  __device__ __forceinline__ u32x2 load8(bool in, uint32_t lane, uint32_t all) const {
+    return __builtin_amdgcn_raw_buffer_load_b64(rs, at(in, lane), all, 0);
+  }
+  __device__ __forceinline__ u32x4 load16(bool in, uint32_t lane, uint32_t all) const {
+    return __builtin_amdgcn_raw_buffer_load_b128(rs, at(in, lane), all, 0);
+  }
+  __device__ __forceinline__ void store2(uint16_t v, bool in, uint32_t lane, uint32_t all) const {
+    __builtin_amdgcn_raw_buffer_store_b16(v, rs, at(in, lane), all, 0);
+  }
+  __device__ __forceinline__ void store8(u32x2 v, bool in, uint32_t lane, uint32_t all) const {
+    __builtin_amdgcn_raw_buffer_store_b64(v, rs, at(in, lane), all, 0);
+  }
+  __device__ __forceinline__ void store16(u32x4 v, bool in, uint32_t lane, uint32_t all) const {
+    __builtin_amdgcn_raw_buffer_store_b128(v, rs, at(in, lane), all, 0);
+  }
+};
 
 // Workgroup b of n to a place in the order of tiles, so that each of the eight XCDs (workgroups
 // go to them by turns) walks a run of neighbours, which share operands in its L2.

@@ -34,13 +34,17 @@ struct NsParts {
   const NsPart* list;
   uint32_t ni, nj;
   bool lower;          // alike: only those with j <= i, ni = nj
+  uint32_t splits;     // products: workgroups to a tile, each over a part of the sum
 };
+// Products that are split leave their sums behind the counters, a tile's one after another.
+constexpr uint32_t NS_MOST_SPLIT = 512, NS_MOST_SPLITS = 8;
 
 struct NsCommon {
   const NsMat* mats;   // or NULL: all like `one`, `pitch` bytes of the workspace apart
   NsMat one;
   uint64_t pitch;
   char* ws;
+  uint32_t* counters;  // NS_MOST_SPLIT, or NULL if no product is split
   const float* clip;   // NULL, or {norm, coefficient}: nothing happens where the norm is not finite
   float ca, cb, cc;
 };
@@ -71,7 +75,8 @@ struct NsSource {
 hipError_t launch_ns_norm(const NsCommon& c, const NsSource& f, const NsParts& p, uint32_t n, hipStream_t s);
 hipError_t launch_ns_start(const NsCommon& c, const NsSource& f, double eps, const NsParts& p, uint32_t n, hipStream_t s);
 
-// The products. `tile`: 0: 256 x 256, 1: 128 x 128, 2: 64 x 64; `at`: which X is read.
+// The products. `tile`: 0: 256 x 256, 1: 128 x 128, 2: 64 x 64, 3: 128 x 128 of a
+// workgroup alone on its compute unit; n: tiles; `at`: which X is read.
 hipError_t launch_ns_gram(const NsCommon& c, int at, int tile, const NsParts& p, uint32_t n, hipStream_t s);
 hipError_t launch_ns_poly(const NsCommon& c, int tile, const NsParts& p, uint32_t n, hipStream_t s);
 // X to the other X, or at the end to the weights or a result
@@ -100,6 +105,6 @@ struct NsSmall {
 hipError_t launch_ns_small(const NsCommon& c, const NsSmall& k, const MuonFirst& f, const MuonTable* t, const NsSource& src,
                            const NsParts& p, uint32_t n, hipStream_t s);
 
-constexpr uint32_t ns_tile_size(int tile) { return tile == 0 ? 256 : tile == 1 ? 128 : 64; }
+constexpr uint32_t ns_tile_size(int tile) { return tile == 0 ? 256 : tile == 2 ? 64 : 128; }
 
 }  // namespace tg

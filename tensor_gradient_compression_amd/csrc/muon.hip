@@ -24,7 +24,7 @@ struct tgrad_muon {
     Small small[2];          // bf16, and those whose products take both parts
   };
   struct List {              // a launch of a product over all matrices
-    uint32_t first = 0, n = 0;
+    uint32_t first = 0, n = 0, splits = 1;
     int tile = 2;
   };
   int device = 0, steps = 5;
@@ -39,6 +39,7 @@ struct tgrad_muon {
   void** w = nullptr;
   const void** g = nullptr;
   char* ws = nullptr;
+  uint32_t* counters = nullptr;
   float* state = nullptr;    // the caller's
   std::string err;
 };
@@ -79,13 +80,17 @@ bool numbers_ok(int steps, const double* c, double eps) {
          eps >= 0.0 && std::isfinite(eps);
 }
 
+// A line's values with its padding: long ones are whole cache lines, which the tiles' transfers
+// take in halves (2048 x 2048 x 2048 in lines of 2056: 60 us, of 2048: 48).
+uint32_t line(uint64_t n) { return (uint32_t)up(n, n >= 256 ? 64 : 8); }
+
 // Sizes of a matrix and its place in a workspace, from `at` on; returns the end.
 uint64_t lay_out(NsMat& m, int64_t rows, int64_t cols, int dtype, uint64_t at) {
   m.rows = (uint32_t)rows;
   m.cols = (uint32_t)cols;
-  m.ldx = (uint32_t)up(cols, 8);
+  m.ldx = line(cols);
   m.m = (uint32_t)(rows < cols ? rows : cols);
-  m.ldm = (uint32_t)up(m.m, 8);
+  m.ldm = line(m.m);
   m.exact = dtype != TGRAD_BF16;
   m.wdt = (uint32_t)dtype;
   m.chunks = (uint32_t)(((uint64_t)rows * (m.ldx / 8) + MUON_CHUNK / 8 - 1) / (MUON_CHUNK / 8));
@@ -104,14 +109,61 @@ uint64_t lay_out(NsMat& m, int64_t rows, int64_t cols, int dtype, uint64_t at) {
   m.sums = take(m.chunks * 8ull);
   return at;
 }
+// what a product that is split needs besides
+uint64_t counters_bytes(uint64_t sums) { return sums ? NS_MOST_SPLIT * 4 + sums : 0; }
 uint64_t across(uint64_t n, int tile) { return (n + ns_tile_size(tile) - 1) / ns_tile_size(tile); }
 uint64_t lower_tiles(uint64_t m, int tile) { return across(m, tile) * (across(m, tile) + 1) / 2; }
 
-// The largest tile that still gives enough workgroups.
-template <class Count>
-int choose_tile(const Count& count) {
-  return count(0) >= 200 ? 0 : count(1) >= 200 ? 1 : 2;
+// A tile, and how many workgroups share each.
+struct Way {
+  int tile = 2;
+  uint32_t splits = 1;
+  uint64_t tiles = 0;
+  uint64_t sums() const {   // bytes of those that are split
+    return splits > 1 ? tiles * splits * ns_tile_size(tile) * ns_tile_size(tile) * 4 : 0;
+  }
+};
+// The one after which the compute unit with most to do ends first. What one takes is counted in
+// bytes that it brings to LDS (at most 50 a ns; the matrix instructions of 256 x 256 tiles take
+// a sixth longer than that), with the sums that a split writes and the last one of a tile reads.
+template <class Each>
+Way choose(const Each& each) {
+  Way best;
+  double least = 0;
+  for (int tile = 0; tile < 3; ++tile) {
+    const double side = ns_tile_size(tile);
+    uint64_t tiles = 0, longest = 0;
+    double total = 0;
+    each(tile, [&](uint64_t n, uint64_t k) {   // n tiles with sums over k
+      tiles += n;
+      longest = std::max(longest, k);
+      total += (double)n * k;
+    });
+    if (!tiles) return best;
+    for (uint32_t splits = 1; splits <= (tile ? NS_MOST_SPLITS : 1); ++splits) {
+      if (splits > 1 && (tiles * splits > NS_MOST_SPLIT || longest < splits * 256)) break;
+      const double one = (double)longest / splits, cost = one * std::ceil(total / 256 / one - 1e-6) * side * (tile ? 4 : 4.7) +
+                         (splits > 1 ? side * side * 4 * (1 + splits) : 0);
+      if (!(tile == 0 && splits == 1) && cost >= least) continue;
+      least = cost;
+      best = {tile, splits, tiles};
+    }
+  }
+  if (best.tile == 1 && best.tiles * best.splits <= 256) best.tile = 3;
+  return best;
 }
+
+// Those of `count` matrices alike.
+struct Ways {
+  Way gram, poly, apply;
+  Ways(const NsMat& m, uint64_t count) {
+    const uint64_t parts = m.exact ? 3 : 1;
+    gram = choose([&](int t, auto&& add) { add(count * lower_tiles(m.m, t), parts * std::max(m.rows, m.cols)); });
+    poly = choose([&](int t, auto&& add) { add(count * lower_tiles(m.m, t), parts * m.m); });
+    apply = choose([&](int t, auto&& add) { add(count * across(m.rows, t) * across(m.cols, t), parts * m.m); });
+  }
+  uint64_t sums() const { return std::max({gram.sums(), poly.sums(), apply.sums()}); }
+};
 
 // `products` steps of the iteration, X in place
 struct Launches {
@@ -237,32 +289,38 @@ int tgrad_muon_init(tgrad_muon_t** out, int n, const int64_t* count, const int64
       f.chunks = (uint32_t)parts.size() - f.first_chunk;
       h->firsts.push_back(f);
     }
-    auto list = [&](tgrad_muon::List& l, int tile, auto&& add) {
-      l.tile = tile;
+    auto list = [&](tgrad_muon::List& l, Way way, auto&& add) {
+      l.tile = way.tile;
+      l.splits = way.splits;
       l.first = (uint32_t)parts.size();
       for (size_t k = 0; k < mats.size(); ++k)
         if (!small(mats[k])) add((uint32_t)k, mats[k]);
       l.n = (uint32_t)(parts.size() - l.first);
     };
-    auto sum = [&](auto&& of) {
-      return choose_tile([&](int tile) {
-        uint64_t t = 0;
-        for (const NsMat& m : mats) t += small(m) ? 0 : of(m, tile);
-        return t;
+    uint64_t sums = 0;
+    auto way = [&](auto&& tiles, auto&& length) {
+      const Way w = choose([&](int tile, auto&& add) {
+        for (const NsMat& m : mats)
+          if (!small(m)) add(tiles(m, tile), (uint64_t)length(m) * (m.exact ? 3 : 1));
       });
+      sums = std::max(sums, w.sums());
+      return w;
     };
-    list(h->starts, 0, [&](uint32_t k, const NsMat& m) {
+    list(h->starts, Way{}, [&](uint32_t k, const NsMat& m) {
       for (uint32_t c = 0; c < m.chunks; ++c) parts.push_back({k, c, 0});
     });
-    const int half = sum([](const NsMat& m, int t) { return lower_tiles(m.m, t); });
-    list(h->gram, half, [&](uint32_t k, const NsMat& m) {
-      for (uint32_t i = 0; i < across(m.m, half); ++i)
-        for (uint32_t j = 0; j <= i; ++j) parts.push_back({k, i, j});
-    });
-    h->poly = h->gram;
-    const int whole = sum([](const NsMat& m, int t) { return across(m.rows, t) * across(m.cols, t); });
+    auto lower = [](const NsMat& m, int tile) { return lower_tiles(m.m, tile); };
+    const Way ways[2] = {way(lower, [](const NsMat& m) { return std::max(m.rows, m.cols); }),
+                         way(lower, [](const NsMat& m) { return m.m; })};
+    for (int o = 0; o < 2; ++o)
+      list(o ? h->poly : h->gram, ways[o], [&](uint32_t k, const NsMat& m) {
+        for (uint32_t i = 0; i < across(m.m, ways[o].tile); ++i)
+          for (uint32_t j = 0; j <= i; ++j) parts.push_back({k, i, j});
+      });
+    const Way whole = way([](const NsMat& m, int t) { return across(m.rows, t) * across(m.cols, t); },
+                          [](const NsMat& m) { return m.m; });
     list(h->apply, whole, [&](uint32_t k, const NsMat& m) {
-      const uint32_t ni = (uint32_t)across(m.rows, whole), nj = (uint32_t)across(m.cols, whole);
+      const uint32_t ni = (uint32_t)across(m.rows, whole.tile), nj = (uint32_t)across(m.cols, whole.tile);
       for (uint32_t b = 0; b < ni; b += 8)
         for (uint32_t j = 0; j < nj; ++j)
           for (uint32_t i = b; i < ni && i < b + 8; ++i) parts.push_back({k, i, j});
@@ -273,7 +331,7 @@ int tgrad_muon_init(tgrad_muon_t** out, int n, const int64_t* count, const int64
     }
     const uint64_t bm = up(mats.size() * sizeof(NsMat), 256), bp = up(parts.size() * sizeof(NsPart), 256);
     const uint64_t bt = up((uint64_t)n * 8, 256);
-    if (hipMalloc(&h->block, bm + bp + 2 * bt + ws) != hipSuccess) {
+    if (hipMalloc(&h->block, bm + bp + 2 * bt + ws + counters_bytes(sums)) != hipSuccess) {
       (void)hipGetLastError();
       delete h;
       return TGRAD_ENOMEM;
@@ -284,6 +342,7 @@ int tgrad_muon_init(tgrad_muon_t** out, int n, const int64_t* count, const int64
     h->w = (void**)(b += bp);
     h->g = (const void**)(b += bt);
     h->ws = b + bt;
+    if (sums) h->counters = (uint32_t*)(h->ws + ws);
     hipError_t e = hipSuccess;
     if (!mats.empty()) e = hipMemcpy(h->mats, mats.data(), mats.size() * sizeof(NsMat), hipMemcpyHostToDevice);
     if (e == hipSuccess && !parts.empty())
@@ -334,6 +393,7 @@ int tgrad_muon_step(tgrad_muon_t* h, void* const* weights, const void* const* gr
   NsCommon c{};
   c.mats = h->mats;
   c.ws = h->ws;
+  c.counters = h->counters;
   c.clip = clip;
   c.ca = (float)h->coef[0];
   c.cb = (float)h->coef[1];
@@ -357,11 +417,11 @@ int tgrad_muon_step(tgrad_muon_t* h, void* const* weights, const void* const* gr
     for (int exact = 0; exact < 2; ++exact) {
       const auto& q = l.small[exact];
       const NsSmall k{h->steps, exact != 0, q.parts, q.lds, h->eps, h->lr, nullptr};
-      if (e == hipSuccess) e = launch_ns_small(c, k, f, &t, NsSource{}, {h->parts + q.first, 0, 0, false}, q.n, s);
+      if (e == hipSuccess) e = launch_ns_small(c, k, f, &t, NsSource{}, {h->parts + q.first, 0, 0, false, 1}, q.n, s);
     }
-    if (e == hipSuccess) e = launch_muon_first(c, f, t, {h->parts + l.first_chunk, 0, 0, false}, l.chunks, s);
+    if (e == hipSuccess) e = launch_muon_first(c, f, t, {h->parts + l.first_chunk, 0, 0, false, 1}, l.chunks, s);
   }
-  auto parts = [&](const tgrad_muon::List& l) { return NsParts{h->parts + l.first, 0, 0, false}; };
+  auto parts = [&](const tgrad_muon::List& l) { return NsParts{h->parts + l.first, 0, 0, false, l.splits}; };
   if (!h->starts.n) return e == hipSuccess ? TGRAD_OK : fail(h, e, "Muon step");
   if (e == hipSuccess) e = launch_muon_start(c, f, h->eps, parts(h->starts), h->starts.n, s);
   const Launches l{parts(h->gram), parts(h->poly), parts(h->apply), h->gram.n, h->poly.n, h->apply.n,
@@ -379,7 +439,7 @@ int64_t tgrad_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols,
   const uint64_t each = lay_out(m, rows, cols, dtype, 0);
   if (ns_small_parts(m.rows, m.cols, m.exact != 0)) return 0;
   if ((uint64_t)count > (1ull << 46) / each) return -1;
-  return (int64_t)(each * count);
+  return (int64_t)(each * count + counters_bytes(count ? Ways(m, count).sums() : 0));
 }
 
 int tgrad_orthogonalize(const void* x, int64_t matrix_stride, int64_t row_stride, void* out, int64_t count,
@@ -406,23 +466,23 @@ int tgrad_orthogonalize(const void* x, int64_t matrix_stride, int64_t row_stride
   if (const uint32_t most = ns_small_parts(c.one.rows, c.one.cols, c.one.exact != 0)) {
     c.pitch = 0;
     const NsSmall k{steps, c.one.exact != 0, most, ns_small_lds(c.one.rows, c.one.cols, c.one.exact != 0), eps, 0.0, out};
-    const hipError_t e = launch_ns_small(c, k, MuonFirst{}, nullptr, f, {nullptr, 1, 1, false}, (uint32_t)count, s);
+    const hipError_t e = launch_ns_small(c, k, MuonFirst{}, nullptr, f, {nullptr, 1, 1, false, 1}, (uint32_t)count, s);
     return e == hipSuccess ? TGRAD_OK : TGRAD_EHIP;
   }
   const uint64_t n = (uint64_t)count, m = c.one.m;
-  Launches l{};
-  l.tgram = l.tpoly = choose_tile([&](int t) { return n * lower_tiles(m, t); });
-  l.tapply = choose_tile([&](int t) { return n * across(rows, t) * across(cols, t); });
-  const uint64_t chunks = n * c.one.chunks, half = n * lower_tiles(m, l.tgram);
-  const uint64_t whole = n * across(rows, l.tapply) * across(cols, l.tapply);
-  for (uint64_t k : {chunks, half, whole})
+  const Ways w(c.one, n);
+  const uint64_t chunks = n * c.one.chunks;
+  for (uint64_t k : {chunks, w.gram.tiles, w.poly.tiles, w.apply.tiles})
     if (k > kMostParts) return TGRAD_EINVAL;
-  l.gram = l.poly = {nullptr, (uint32_t)across(m, l.tgram), (uint32_t)across(m, l.tgram), true};
-  l.apply = {nullptr, (uint32_t)across(rows, l.tapply), (uint32_t)across(cols, l.tapply), false};
-  l.ngram = l.npoly = (uint32_t)half;
-  l.napply = (uint32_t)whole;
-  hipError_t e = launch_ns_norm(c, f, {nullptr, c.one.chunks, 1, false}, (uint32_t)chunks, s);
-  if (e == hipSuccess) e = launch_ns_start(c, f, eps, {nullptr, c.one.chunks, 1, false}, (uint32_t)chunks, s);
+  if (w.sums()) c.counters = (uint32_t*)(c.ws + c.pitch * n);
+  auto parts = [&](const Way& y, uint64_t r, uint64_t k, bool lower) {
+    return NsParts{nullptr, (uint32_t)across(r, y.tile), (uint32_t)across(k, y.tile), lower, y.splits};
+  };
+  const Launches l{parts(w.gram, m, m, true), parts(w.poly, m, m, true), parts(w.apply, rows, cols, false),
+                   (uint32_t)w.gram.tiles,    (uint32_t)w.poly.tiles,    (uint32_t)w.apply.tiles,
+                   w.gram.tile,               w.poly.tile,               w.apply.tile};
+  hipError_t e = launch_ns_norm(c, f, {nullptr, c.one.chunks, 1, false, 1}, (uint32_t)chunks, s);
+  if (e == hipSuccess) e = launch_ns_start(c, f, eps, {nullptr, c.one.chunks, 1, false, 1}, (uint32_t)chunks, s);
   NsLast last{};
   last.out = out;
   if (e == hipSuccess) e = iterate(c, l, steps, last, s);
