@@ -589,7 +589,7 @@ hipError_t launch_shape(K* k, uint32_t n, uint32_t splits, hipStream_t s, const 
 using Big = MmBig;
 using Mid = MmMid;
 using Deep = MmDeep;
-using Small = MmSmall;
+using Small = MmNear;
 
 }  // namespace
 

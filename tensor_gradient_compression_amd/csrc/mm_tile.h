@@ -196,7 +196,11 @@ __device__ __forceinline__ f32x4 mm_mfma(s16x8 a, s16x8 b, f32x4 c) {
 //             overlap by themselves.
 //   MM_ALONE  four waves, each the whole tile over a quarter of k, from stages of its own and
 //             without a barrier; their sums are added at the end. For few tiles and long sums.
-enum MmMode { MM_TURNS, MM_EVEN, MM_ALONE };
+//   MM_AHEAD  each wave a part of the tile over all of k; it reads the fragments of one half of a
+//             stage while it multiplies the other's, the next stage's among them. For tiles whose
+//             workgroups have a CU to themselves or share it with one (2048 x 2048 x 2048 by 128 x 128:
+//             27.6 us MM_EVEN, 25.9 so; by 64 x 64: 47.9 MM_ALONE, 34.4 so).
+enum MmMode { MM_TURNS, MM_EVEN, MM_ALONE, MM_AHEAD };
 
 // A tile of BM x BN by WM x WN waves, in stages of K values of k of which STAGES fit. FM x FN: a
 // wave's blocks of 16 x 16, as it ends with them.
@@ -216,7 +220,8 @@ struct MmShape {
 using MmBig = MmShape<256, 256, 2, 4, MM_TURNS, 32, 4>;
 using MmHalf = MmShape<128, 256, 1, 4, MM_EVEN, 32, 3>;
 using MmMid = MmShape<128, 128, 2, 2, MM_EVEN, 64, 2>;
-using MmDeep = MmShape<128, 128, 2, 2, MM_EVEN, 64, 4>;
+using MmDeep = MmShape<128, 128, 2, 4, MM_AHEAD, 64, 4>;
+using MmNear = MmShape<64, 64, 2, 2, MM_AHEAD, 64, 4>;
 using MmSmall = MmShape<64, 64, 4, 1, MM_ALONE, 32, 4>;
 
 // The sums of a wave: c[i][j] holds, in lane l, row 16 i + (l & 15) and columns
@@ -379,6 +384,28 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
         fragments(at, part, fa, fb);
         multiply(fa, fb);
       }
+    }
+  } else if constexpr (S::MODE == MM_AHEAD) {
+    // Between the two halves of a stage a barrier: all waves have read it, and what each has awaited
+    // of the next is there for all.
+    static_assert(S::MODE != MM_AHEAD || K == 64, "two halves of a stage");
+    for (int i = 0; i < STAGES; ++i)
+      if (i < total) issue();
+    s16x8 fa[2][FM], fb[2][FN];
+    if (total > 0) {
+      arrived(0);
+      lds_barrier();
+      fragments(at, 0, fa[0], fb[0]);
+    }
+    for (; t < total; ++t) {
+      fragments(at, 1, fa[1], fb[1]);
+      multiply(fa[0], fb[0]);
+      if (t + 1 < total) arrived(t + 1);
+      lds_barrier();
+      if (issued < total) issue();
+      at = after(at);
+      fragments(at, 0, fa[0], fb[0]);      // behind the last: not used
+      multiply(fa[1], fb[1]);
     }
   } else {
     // a stage's fragments are read while the one before is multiplied, and its place filled again

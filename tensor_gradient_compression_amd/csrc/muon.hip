@@ -123,9 +123,13 @@ struct Way {
     return splits > 1 ? tiles * splits * ns_tile_size(tile) * ns_tile_size(tile) * 4 : 0;
   }
 };
-// The one after which the compute unit with most to do ends first. What one takes is counted in
-// bytes that it brings to LDS (at most 50 a ns; the matrix instructions of 256 x 256 tiles take
-// a sixth longer than that), with the sums that a split writes and the last one of a tile reads.
+// The one after which the compute unit with most to do ends first, in ns, by what was measured:
+// 256 x 256 tiles bring 36 bytes a ns of their operands to LDS (matrix instructions bind them),
+// 128 x 128 ones 50, smaller ones 68 where two workgroups share a unit and 52 where one is alone;
+// what follows the product takes 0.5 ns a place, and the sums of a split pass memory at 4 TB/s after
+// 2 us of waiting. (1536 x 1536 in fp16: Gram of 128 x 128 tiles in three splits 34 us, in six 42;
+// 18 of 1024 x 4096 in bf16: 256 x 256 tiles 123, 128 x 128 141; 777 x 2051 in fp16, B X: 128 x 128
+// in four splits 41, in two 32, 64 x 64 unsplit 25.)
 template <class Each>
 Way choose(const Each& each) {
   Way best;
@@ -142,8 +146,10 @@ Way choose(const Each& each) {
     if (!tiles) return best;
     for (uint32_t splits = 1; splits <= (tile ? NS_MOST_SPLITS : 1); ++splits) {
       if (splits > 1 && (tiles * splits > NS_MOST_SPLIT || longest < splits * 256)) break;
-      const double one = (double)longest / splits, cost = one * std::ceil(total / 256 / one - 1e-6) * side * (tile ? 4 : 4.7) +
-                         (splits > 1 ? side * side * 4 * (1 + splits) : 0);
+      const double one = (double)longest / splits, loads = std::ceil(total / 256 / one - 1e-6);
+      const double rate = tile == 0 ? 36 : tile == 1 ? 50 : loads > 1 ? 68 : 52;
+      const double cost = loads * (one * side * 4 / rate + side * side / 2) +
+                          (splits > 1 ? 2000 + tiles * splits * side * side * 8 / 4000 : 0);
       if (!(tile == 0 && splits == 1) && cost >= least) continue;
       least = cost;
       best = {tile, splits, tiles};
