@@ -135,6 +135,18 @@ __device__ __forceinline__ void load_biases(const GatedArgs& a, uint32_t f, floa
   }
 }
 
+// four values of T through a window
+template <typename T>
+__device__ __forceinline__ void window_store(const MmWindow& w, const T* v, bool in, uint32_t lane, uint32_t all) {
+  if constexpr (sizeof(T) == 4) w.store16(*(const u32x4*)v, in, lane, all);
+  else w.store8(*(const u32x2*)v, in, lane, all);
+}
+template <typename T>
+__device__ __forceinline__ void window_load(const MmWindow& w, T* v, bool in, uint32_t lane, uint32_t all) {
+  if constexpr (sizeof(T) == 4) *(u32x4*)v = w.load16(in, lane, all);
+  else *(u32x2*)v = w.load8(in, lane, all);
+}
+
 template <class S, int DT>
 __global__ void __launch_bounds__(S::THREADS, 2) k_gated_forward(const GatedArgs a) {
   using T = typename GatedType<DT>::T;
@@ -150,9 +162,10 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_forward(const GatedArgs
   const int lane = threadIdx.x & 63, wave = (int)uniform(threadIdx.x >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
   const bool aligned = (a.hidden % 4) == 0 && ((uintptr_t)a.y & (4 * sizeof(T) - 1)) == 0;
-  const uint32_t f_of_lane = f0 + wn * S::FN * 8 + (lane >> 4) * 4;
+  const uint32_t r = wm * S::FM * 16 + (lane & 15), c = wn * S::FN * 8 + (lane >> 4) * 4, f_of_lane = f0 + c;
   float bias[S::FN][4];
   load_biases<S, T>(a, f_of_lane, bias);
+  const MmWindow out((T*)a.y + row0 * a.hidden + f0);
   with_activation(a.act, [&](auto act) {
     constexpr int ACT = decltype(act)::value;
 #pragma unroll
@@ -162,16 +175,19 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_forward(const GatedArgs
       const float* const bu = bias[j + 1];
 #pragma unroll
       for (int i = 0; i < S::FM; ++i) {
-        const int64_t m = row0 + (wm * S::FM + i) * 16 + (lane & 15);
-        if (m >= a.rows || f >= a.hidden) continue;
-        T y[4];
+        const int64_t m = row0 + r + i * 16;
+        alignas(16) T y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float slope;
           const float p = activate<ACT, DT != DT_F32, false>(sums.c[i][j][e] + bg[e], slope);
           y[e] = from_f32<T>(p * (sums.c[i][j + 1][e] + bu[e]));
         }
-        store4((T*)a.y + m * a.hidden + f, y, (int)(a.hidden - f < 4 ? a.hidden - f : 4), aligned);
+        const bool in = m < a.rows && f < a.hidden;
+        if (aligned)
+          window_store<T>(out, y, in, (r * a.hidden + c) * sizeof(T), (i * 16 * a.hidden + j * 8) * sizeof(T));
+        else if (in)
+          store4((T*)a.y + m * a.hidden + f, y, (int)(a.hidden - f < 4 ? a.hidden - f : 4), false);
       }
     }
   });
@@ -193,30 +209,29 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_grads(const GatedArgs a
   const int wm = wave / S::WN, wn = wave % S::WN;
   const uint32_t pad = gated_pad(a.hidden);
   const int64_t part = a.rows * 2 * (int64_t)pad;
-  const bool aligned = (a.hidden % 4) == 0 && (a.dy_stride % 4) == 0 && ((uintptr_t)a.dy & (4 * sizeof(T) - 1)) == 0;
-  const uint32_t f_of_lane = f0 + wn * S::FN * 8 + (lane >> 4) * 4;
+  const bool aligned = (a.hidden % 4) == 0 && (a.dy_stride % 4) == 0 && ((uintptr_t)a.dy & (4 * sizeof(T) - 1)) == 0 &&
+                       a.dy_stride <= 1 << 20;   // a window's offsets are 31 bits
+  const uint32_t r = wm * S::FM * 16 + (lane & 15), c = wn * S::FN * 8 + (lane >> 4) * 4, f_of_lane = f0 + c;
   float bias[S::FN][4];
   load_biases<S, T>(a, f_of_lane, bias);
-  T all[S::FN / 2][S::FM][4];
+  alignas(16) T all[S::FN / 2][S::FM][4];
+  const MmWindow in((const T*)a.dy + row0 * a.dy_stride + f0);
   auto load = [&](int j) {
+    const uint32_t f = f_of_lane + j * 16;
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
-      const int64_t m = row0 + (wm * S::FM + i) * 16 + (lane & 15);
-      const uint32_t f = f_of_lane + j * 16;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) all[j][i][e] = T{};
-      if (m >= a.rows || f >= a.hidden) continue;
-      const T* const src = (const T*)a.dy + m * a.dy_stride + f;
+      const int64_t m = row0 + r + i * 16;
       if (aligned) {
-        __builtin_memcpy(all[j][i], __builtin_assume_aligned(src, 4 * sizeof(T)), 4 * sizeof(T));
+        window_load<T>(in, all[j][i], m < a.rows && f < a.hidden, (r * (uint32_t)a.dy_stride + c) * sizeof(T),
+                       (i * 16 * (uint32_t)a.dy_stride + j * 16) * sizeof(T));
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (f + e < a.hidden) all[j][i][e] = src[e];
+          all[j][i][e] = m < a.rows && f + e < a.hidden ? ((const T*)a.dy)[m * a.dy_stride + f + e] : T{};
       }
     }
   };
-  constexpr bool ALL = sizeof(T) == 2 || S::FM < 8;   // registers for all of it
+  constexpr bool ALL = S::FM < 8;   // registers for all of it
 #pragma unroll
   for (int j = 0; j < (ALL ? S::FN / 2 : 1); ++j) load(j);
   with_activation(a.act, [&](auto act) {
@@ -230,23 +245,23 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_grads(const GatedArgs a
       f32x4 sg = {0.f, 0.f, 0.f, 0.f}, su = sg;
 #pragma unroll
       for (int i = 0; i < S::FM; ++i) {
-        const int64_t m = row0 + (wm * S::FM + i) * 16 + (lane & 15);
-        if (m >= a.rows || f >= pad) continue;
+        const bool there = row0 + r + i * 16 < a.rows && f < pad;
         const T* const dy = all[j / 2][i];
+        const uint32_t to_lane = (r * 2 * pad + c) * 2, to_all = (i * 32 * pad + j * 8) * 2;
         float dg[4], du[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float slope;
           const float d = to_f32(dy[e]);
           const float p = activate<ACT, DT != DT_F32, true>(sums.c[i][j][e] + bg[e], slope);
-          const bool in = f + e < a.hidden;     // zeros behind
-          dg[e] = in ? d * (sums.c[i][j + 1][e] + bu[e]) * slope : 0.0f;
-          du[e] = in ? d * p : 0.0f;
+          const bool real = f + e < a.hidden;     // zeros behind
+          dg[e] = real ? d * (sums.c[i][j + 1][e] + bu[e]) * slope : 0.0f;
+          du[e] = real ? d * p : 0.0f;
           sg[e] += dg[e];
           su[e] += du[e];
         }
         if constexpr (DT == DT_F32) {
-          bf16_t g[3][4], u[3][4];
+          alignas(8) bf16_t g[3][4], u[3][4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             bf16_t p[3];
@@ -257,17 +272,17 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_grads(const GatedArgs a
           }
 #pragma unroll
           for (int q = 0; q < 3; ++q) {
-            bf16_t* const d = (bf16_t*)a.grads + q * part + m * 2 * (int64_t)pad + f;
-            store4(d, g[q], 4, true);
-            store4(d + pad, u[q], 4, true);
+            const MmWindow to((bf16_t*)a.grads + q * part + row0 * 2 * (int64_t)pad + f0);
+            window_store<bf16_t>(to, g[q], there, to_lane, to_all);
+            window_store<bf16_t>(to, u[q], there, to_lane, to_all + pad * 2);
           }
         } else {
-          T g[4], u[4];
+          alignas(8) T g[4], u[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) g[e] = from_f32<T>(dg[e]), u[e] = from_f32<T>(du[e]);
-          T* const d = (T*)a.grads + m * 2 * (int64_t)pad + f;
-          store4(d, g, 4, true);
-          store4(d + pad, u, 4, true);
+          const MmWindow to((T*)a.grads + row0 * 2 * (int64_t)pad + f0);
+          window_store<T>(to, g, there, to_lane, to_all);
+          window_store<T>(to, u, there, to_lane, to_all + pad * 2);
         }
       }
       if (a.row_sums) {

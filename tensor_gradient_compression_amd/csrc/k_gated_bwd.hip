@@ -155,8 +155,17 @@ __global__ void __launch_bounds__(256) k_gated_join_rows(const float* p, int64_t
   const int64_t v = (int64_t)blockIdx.x * 16 + c;
   const int64_t at = v < half ? v : v - half + half_at;
   float s = 0.0f;
-  if (v < n)
-    for (int64_t r = q; r < rows; r += 16) s += p[r * pitch + at];
+  if (v < n) {
+    int64_t r = q;
+    for (; r + 7 * 16 < rows; r += 8 * 16) {   // eight loads under way
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = p[(r + e * 16) * pitch + at];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += x[e];
+    }
+    for (; r < rows; r += 16) s += p[r * pitch + at];
+  }
   sums[q][c] = s;
   __syncthreads();
   if (q == 0 && v < n) {
