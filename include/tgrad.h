@@ -596,7 +596,7 @@ int tgrad_muon_step(tgrad_muon_t *h, void *const *weights, const void *const *gr
  * from the values before). fp32 products are made of six products of bf16 parts, as exact as
  * fp32 sums; a value that is not finite makes what it enters NaN there. Results do not depend
  * on the order in which workgroups run.
- *   x, dy           device, rows x_stride >= in (dy_stride >= hidden) elements apart
+ *   x, dy           device, rows x_stride >= in (dy_stride >= hidden, <= 2^20) elements apart
  *   w_gate, w_up    device, contiguous, hidden rows of in values;  dw_gate, dw_up alike
  *   b_gate, b_up, db_gate, db_up   device, hidden values;  b: NULL: 0
  *   y, dx           device, contiguous; no result overlaps an input

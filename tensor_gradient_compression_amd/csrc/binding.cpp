@@ -573,6 +573,7 @@ PyObject* gated_linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       same = dy.size(i) == (i == dy.dim() - 1 ? g.hidden : g.x->size(i));
     if (!same) throw Invalid{"dy: its shape is not y's"};
     const Rows rd = rows_of(dy, "dy");
+    if (rd.rows > 1 && rd.stride > (1 << 20)) throw Invalid{"dy: its rows are more than 2^20 values apart; call contiguous()"};
     int need[3];
     for (int i = 0; i < 3; ++i)
       if ((need[i] = PyObject_IsTrue(a[7 + i])) < 0) throw Raised{};

@@ -18,7 +18,8 @@ struct GatedParts {
 // for 16-bit values).
 constexpr uint32_t GATED_PART_A = 0x001102, GATED_PART_B = 0x010120;
 
-__host__ __device__ inline uint32_t gated_pad(uint32_t n) { return (n + 7u) & ~7u; }
+// (long lines are whole cache lines, which the tiles' transfers take in halves)
+__host__ __device__ inline uint32_t gated_pad(uint32_t n) { return n >= 256 ? (n + 63u) & ~63u : (n + 7u) & ~7u; }
 
 // Copies of rows whose lines are not 16-byte aligned (16 bits), or their parts (fp32).
 struct GatedPack {

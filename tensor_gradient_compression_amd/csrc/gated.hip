@@ -9,6 +9,7 @@ namespace {
 
 // sizes that the kernels' indexes and tiles' offsets hold
 constexpr int64_t kMostSide = 1 << 19;
+constexpr int64_t kMostDyStride = 1 << 20;   // 256 rows of a tile stay under 2^31 bytes
 
 bool shape_ok(int64_t rows, int64_t in, int64_t hidden, int dtype, int act) {
   return rows >= 0 && rows <= 0x7FFFFFFF - 65536 && in >= 1 && in <= kMostSide && hidden >= 1 && hidden <= kMostSide &&
@@ -122,7 +123,7 @@ int tgrad_gated_linear_backward(const void* dy, int64_t dy_stride, const void* x
                                 void* dw_gate, void* dw_up, void* db_gate, void* db_up, int64_t rows, int64_t in,
                                 int64_t hidden, int dtype, int activation, void* workspace, void* stream) {
   if (!shape_ok(rows, in, hidden, dtype, activation) || !stride_ok(x_stride, rows, in) ||
-      !stride_ok(dy_stride, rows, hidden))
+      !stride_ok(dy_stride, rows, hidden) || (rows > 1 && dy_stride > kMostDyStride))
     return TGRAD_EINVAL;
   for (const void* q : {dy, x, w_gate, w_up, b_gate, b_up, (const void*)dx, (const void*)dw_gate, (const void*)dw_up,
                         (const void*)db_gate, (const void*)db_up})
@@ -152,7 +153,7 @@ int tgrad_gated_linear_backward(const void* dy, int64_t dy_stride, const void* x
     a.dt = dtype;
     a.act = activation;
     a.dy = dy;
-    a.dy_stride = dy_stride;
+    a.dy_stride = rows > 1 ? dy_stride : hidden;
     a.grads = ws + b.grads;
     a.row_sums = db_gate ? (float*)(ws + b.sums) : nullptr;
     e = launch_gated_grads(a, s);

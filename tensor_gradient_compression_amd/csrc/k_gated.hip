@@ -142,6 +142,16 @@ __device__ __forceinline__ void window_store(const MmWindow& w, const T* v, bool
   else w.store8(*(const u32x2*)v, in, lane, all);
 }
 template <typename T>
+__device__ __forceinline__ void window_store_one(const MmWindow& w, T v, bool in, uint32_t lane, uint32_t all) {
+  if constexpr (sizeof(T) == 4) w.store4(__builtin_bit_cast(uint32_t, v), in, lane, all);
+  else w.store2(__builtin_bit_cast(uint16_t, v), in, lane, all);
+}
+template <typename T>
+__device__ __forceinline__ void window_load_one(const MmWindow& w, T& v, bool in, uint32_t lane, uint32_t all) {
+  if constexpr (sizeof(T) == 4) v = __builtin_bit_cast(T, w.load4(in, lane, all));
+  else v = __builtin_bit_cast(T, w.load2(in, lane, all));
+}
+template <typename T>
 __device__ __forceinline__ void window_load(const MmWindow& w, T* v, bool in, uint32_t lane, uint32_t all) {
   if constexpr (sizeof(T) == 4) *(u32x4*)v = w.load16(in, lane, all);
   else *(u32x2*)v = w.load8(in, lane, all);
@@ -183,11 +193,13 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_forward(const GatedArgs
           const float p = activate<ACT, DT != DT_F32, false>(sums.c[i][j][e] + bg[e], slope);
           y[e] = from_f32<T>(p * (sums.c[i][j + 1][e] + bu[e]));
         }
-        const bool in = m < a.rows && f < a.hidden;
-        if (aligned)
-          window_store<T>(out, y, in, (r * a.hidden + c) * sizeof(T), (i * 16 * a.hidden + j * 8) * sizeof(T));
-        else if (in)
-          store4((T*)a.y + m * a.hidden + f, y, (int)(a.hidden - f < 4 ? a.hidden - f : 4), false);
+        const uint32_t at = (r * a.hidden + c) * sizeof(T), all = (i * 16 * a.hidden + j * 8) * sizeof(T);
+        if (aligned) {
+          window_store<T>(out, y, m < a.rows && f < a.hidden, at, all);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) window_store_one<T>(out, y[e], m < a.rows && f + e < a.hidden, at + e * sizeof(T), all);
+        }
       }
     }
   });
@@ -198,7 +210,7 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_grads(const GatedArgs a
   using T = typename GatedType<DT>::T;
   extern __shared__ char lds_raw[];
   TG_LDS char* const lds = (TG_LDS char*)lds_raw;
-  const uint32_t nj = (a.hidden + S::BN / 2 - 1) / (S::BN / 2), ni = (uint32_t)((a.rows + S::BM - 1) / S::BM);
+  const uint32_t nj = (gated_pad(a.hidden) + S::BN / 2 - 1) / (S::BN / 2), ni = (uint32_t)((a.rows + S::BM - 1) / S::BM);
   uint32_t ti, tj;
   tile_at(xcd_order(blockIdx.x, gridDim.x), ni, nj, ti, tj);
   const int64_t row0 = (int64_t)ti * S::BM;
@@ -209,31 +221,29 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_grads(const GatedArgs a
   const int wm = wave / S::WN, wn = wave % S::WN;
   const uint32_t pad = gated_pad(a.hidden);
   const int64_t part = a.rows * 2 * (int64_t)pad;
-  const bool aligned = (a.hidden % 4) == 0 && (a.dy_stride % 4) == 0 && ((uintptr_t)a.dy & (4 * sizeof(T) - 1)) == 0 &&
-                       a.dy_stride <= 1 << 20;   // a window's offsets are 31 bits
+  const bool aligned = (a.hidden % 4) == 0 && (a.dy_stride % 4) == 0 && ((uintptr_t)a.dy & (4 * sizeof(T) - 1)) == 0;
   const uint32_t r = wm * S::FM * 16 + (lane & 15), c = wn * S::FN * 8 + (lane >> 4) * 4, f_of_lane = f0 + c;
   float bias[S::FN][4];
   load_biases<S, T>(a, f_of_lane, bias);
-  alignas(16) T all[S::FN / 2][S::FM][4];
+  // dy of some rows' blocks of a column, as many as there are registers for
+  constexpr int ROWS = S::FM < 4 ? S::FM : 4;
+  alignas(16) T some[ROWS][4];
   const MmWindow in((const T*)a.dy + row0 * a.dy_stride + f0);
-  auto load = [&](int j) {
-    const uint32_t f = f_of_lane + j * 16;
+  auto load = [&](int j, int i0) {
+    const uint32_t f = f_of_lane + j * 8;
 #pragma unroll
-    for (int i = 0; i < S::FM; ++i) {
-      const int64_t m = row0 + r + i * 16;
+    for (int i = 0; i < ROWS; ++i) {
+      const int64_t m = row0 + r + (i0 + i) * 16;
+      const uint32_t at = (r * (uint32_t)a.dy_stride + c) * sizeof(T);
+      const uint32_t more = ((i0 + i) * 16 * (uint32_t)a.dy_stride + j * 8) * sizeof(T);
       if (aligned) {
-        window_load<T>(in, all[j][i], m < a.rows && f < a.hidden, (r * (uint32_t)a.dy_stride + c) * sizeof(T),
-                       (i * 16 * (uint32_t)a.dy_stride + j * 16) * sizeof(T));
+        window_load<T>(in, some[i], m < a.rows && f < a.hidden, at, more);
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          all[j][i][e] = m < a.rows && f + e < a.hidden ? ((const T*)a.dy)[m * a.dy_stride + f + e] : T{};
+        for (int e = 0; e < 4; ++e) window_load_one<T>(in, some[i][e], m < a.rows && f + e < a.hidden, at + e * sizeof(T), more);
       }
     }
   };
-  constexpr bool ALL = S::FM < 8;   // registers for all of it
-#pragma unroll
-  for (int j = 0; j < (ALL ? S::FN / 2 : 1); ++j) load(j);
   with_activation(a.act, [&](auto act) {
     constexpr int ACT = decltype(act)::value;
 #pragma unroll
@@ -241,12 +251,12 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_grads(const GatedArgs a
       const uint32_t f = f_of_lane + j * 8;
       const float* const bg = bias[j];
       const float* const bu = bias[j + 1];
-      if (!ALL && j) load(j / 2);
       f32x4 sg = {0.f, 0.f, 0.f, 0.f}, su = sg;
 #pragma unroll
       for (int i = 0; i < S::FM; ++i) {
         const bool there = row0 + r + i * 16 < a.rows && f < pad;
-        const T* const dy = all[j / 2][i];
+        if (i % ROWS == 0) load(j, i);
+        const T* const dy = some[i % ROWS];
         const uint32_t to_lane = (r * 2 * pad + c) * 2, to_all = (i * 32 * pad + j * 8) * 2;
         float dg[4], du[4];
 #pragma unroll
@@ -337,7 +347,8 @@ __global__ void __launch_bounds__(256) k_gated_pack(const PackArgs a) {
 
 template <class S, int DT>
 hipError_t launch_tiles(bool grads, const GatedArgs& a, hipStream_t s) {
-  const int64_t ni = (a.rows + S::BM - 1) / S::BM, nj = (a.hidden + S::BN / 2 - 1) / (S::BN / 2);
+  const int64_t ni = (a.rows + S::BM - 1) / S::BM;
+  const int64_t nj = ((grads ? gated_pad(a.hidden) : a.hidden) + S::BN / 2 - 1) / (S::BN / 2);
   if (ni * nj > 0x7FFFFFFF / S::THREADS) return hipErrorInvalidValue;
   auto* const k = grads ? k_gated_grads<S, DT> : k_gated_forward<S, DT>;
   const hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS_BYTES);

@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_dx(const GatedDx a, con
   tile_at(xcd_order(blockIdx.x, gridDim.x), ni, nj, ti, tj);
   const int64_t row0 = (int64_t)ti * S::BM, k0 = (int64_t)blockIdx.y * size;
   const uint32_t n0 = tj * S::BN, pad = gated_pad(a.hidden);
-  const int64_t k = (int64_t)pad - k0 < size ? (int64_t)pad - k0 : size;
+  const int64_t k = (int64_t)a.hidden - k0 < size ? (int64_t)a.hidden - k0 : size;   // zeros behind in dg and du
   MmSums<S> sums;
   mm_tile<S, G::MM, false, true, false>(
       sums, lds,
@@ -191,7 +191,7 @@ using Small = MmSmall;
 template <int DT>
 hipError_t dx_type(const GatedDx& a, hipStream_t s) {
   const int t = tile_of(a.rows, a.in, a.hidden), n = gated_dx_splits(a.rows, a.in, a.hidden);
-  const int64_t tiles = tiles_of(a.rows, a.in, t), size = split_size(gated_pad(a.hidden), n);
+  const int64_t tiles = tiles_of(a.rows, a.in, t), size = split_size(a.hidden, n);
   hipError_t e = t == 0   ? launch_tiles<Big>(k_gated_dx<Big, DT>, tiles, n, size, a, s)
                  : t == 1 ? launch_tiles<Mid>(k_gated_dx<Mid, DT>, tiles, n, size, a, s)
                           : launch_tiles<Small>(k_gated_dx<Small, DT>, tiles, n, size, a, s);
@@ -209,10 +209,11 @@ hipError_t dw_type(const GatedDw& a, hipStream_t s) {
   const uint32_t pad = gated_pad(a.hidden);
   const int t = tile_of(2 * (int64_t)pad, a.in, a.rows), n = gated_dw_splits(a.rows, a.in, a.hidden);
   const int64_t tiles = tiles_of(2 * (int64_t)pad, a.in, t), size = split_size(a.rows, n);
-  hipError_t e = t == 0   ? launch_tiles<Big>(k_gated_dw<Big, DT>, tiles, n, size, a, s)
+  hipError_t e = !a.dwg   ? hipSuccess
+                 : t == 0 ? launch_tiles<Big>(k_gated_dw<Big, DT>, tiles, n, size, a, s)
                  : t == 1 ? launch_tiles<Mid>(k_gated_dw<Mid, DT>, tiles, n, size, a, s)
                           : launch_tiles<Small>(k_gated_dw<Small, DT>, tiles, n, size, a, s);
-  if (e == hipSuccess && n > 1) {
+  if (e == hipSuccess && a.dwg && n > 1) {
     const int64_t v = 2 * (int64_t)a.hidden * a.in;
     if ((v + 255) / 256 > 0x7FFFFFFF / 256) return hipErrorInvalidValue;
     k_gated_join<T><<<(uint32_t)((v + 255) / 256), 256, 0, s>>>(a.partial, n, v, v, (T*)a.dwg, (T*)a.dwu, v / 2, v / 2);
@@ -233,7 +234,7 @@ int gated_dx_splits(int64_t rows, uint32_t in, uint32_t hidden) {
   const int t = tile_of(rows, in, hidden);
   const int n = splits_of(tiles_of(rows, in, t), hidden, t);
   // none of them empty
-  return (int)((gated_pad(hidden) + split_size(gated_pad(hidden), n) - 1) / split_size(gated_pad(hidden), n));
+  return (int)((hidden + split_size(hidden, n) - 1) / split_size(hidden, n));
 }
 int gated_dw_splits(int64_t rows, uint32_t in, uint32_t hidden) {
   const int64_t f = 2 * (int64_t)gated_pad(hidden);

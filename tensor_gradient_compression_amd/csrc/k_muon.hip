@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_ns_apply(const NsCommon c, co
           a = ns_operand(c, m, m.b, m.m, m.ldm, kPartsA, s);
           b = ns_operand(c, m, from, m.rows, m.ldx, kPartsB, s);
         },
-        nseg, whole8(m.m), i0, j0, m.ldm, m.ldx, split, splits);
+        nseg, m.m, i0, j0, m.ldm, m.ldx, split, splits);
   else
     mm_tile<S, DT_F16, false, false, false>(
         sums, (TG_LDS char*)lds_raw,

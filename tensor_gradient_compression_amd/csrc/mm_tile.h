@@ -103,12 +103,13 @@ struct MmLoader {
   // from row `row` and value `k` of k on
   __device__ __forceinline__ void start(const MmOperand& o, int64_t row, int64_t k) {
     const int64_t skip = (CROSSED ? row + k * o.stride : row * o.stride + k) * 2;
-    resource((uint64_t)o.p + (uint64_t)skip, (uint64_t)(((o.lines - 1) * (int64_t)o.stride + o.len) * 2 - skip));
+    resource((uint64_t)o.p + (uint64_t)skip, ((o.lines - 1) * (int64_t)o.stride + o.len) * 2 - skip);
   }
-  __device__ __forceinline__ void resource(uint64_t from, uint64_t left) {
+  // (what lies behind the operand is none of it; the check takes the stage's offset off the size)
+  __device__ __forceinline__ void resource(uint64_t from, int64_t left) {
     rs[0] = uniform((uint32_t)from);
     rs[1] = uniform((uint32_t)(from >> 32)) & 0xFFFFu;
-    rs[2] = uniform((uint32_t)(left >> 32) ? 0xFFFFFFF0u : (uint32_t)left);
+    rs[2] = uniform(left <= 0 ? 0u : left >> 32 ? 0xFFFFFFF0u : (uint32_t)left);
     rs[3] = 0x00020000u;
     at = 0;
   }
@@ -116,16 +117,14 @@ struct MmLoader {
     at += (CROSSED ? uniform(stride) : 1) * (K * 2);
     if (CROSSED && at >= 0x40000000u) {   // 32 bits do not reach through a long operand
       const uint64_t from = (((uint64_t)rs[1] << 32) | rs[0]) + at;
-      resource(from, (uint64_t)o.p + (uint64_t)(((o.lines - 1) * (int64_t)o.stride + o.len) * 2) - from);
+      resource(from, (int64_t)((uint64_t)o.p + (uint64_t)(((o.lines - 1) * (int64_t)o.stride + o.len) * 2) - from));
     }
   }
   // Whether transfer i is of the second matrix of two that alternate.
   __device__ static constexpr bool second(int i) { return ((i * (64 / PIECES)) >> 4) & 1; }
 
   // The transfers (BY_TURNS: those of one matrix) of a stage; PART: only `rem` values of k of it are
-  // there. (Whether the stage's offset counts in the resource's check or not: rows past the end
-  // are behind it by their own offsets, and k past the end is left out here.) Written as
-  // instructions: the compiler would wait for all transfers before any read of LDS.
+  // there. Written as instructions: the compiler would wait for all transfers before any read of LDS.
   template <bool PART, bool BY_TURNS = false, bool SECOND = false>
   __device__ __forceinline__ void issue(uint32_t lds, int wave, int rem) const {
     bool first = true;
@@ -478,6 +477,9 @@ struct MmWindow {
             (void*)((uint64_t)uniform((uint32_t)((uint64_t)first >> 32)) << 32 | uniform((uint32_t)(uint64_t)first)), 0,
             0x80000000u, 0x20000)) {}
   __device__ static __forceinline__ uint32_t at(bool in, uint32_t lane) { return in ? lane : 0xFFFFFFF0u; }
+  __device__ __forceinline__ uint16_t load2(bool in, uint32_t lane, uint32_t all) const {
+    return __builtin_amdgcn_raw_buffer_load_b16(rs, at(in, lane), all, 0);
+  }
   __device__ __forceinline__ uint32_t load4(bool in, uint32_t lane, uint32_t all) const {
     return __builtin_amdgcn_raw_buffer_load_b32(rs, at(in, lane), all, 0);
   }
@@ -489,6 +491,9 @@ struct MmWindow {
   }
   __device__ __forceinline__ void store2(uint16_t v, bool in, uint32_t lane, uint32_t all) const {
     __builtin_amdgcn_raw_buffer_store_b16(v, rs, at(in, lane), all, 0);
+  }
+  __device__ __forceinline__ void store4(uint32_t v, bool in, uint32_t lane, uint32_t all) const {
+    __builtin_amdgcn_raw_buffer_store_b32(v, rs, at(in, lane), all, 0);
   }
   __device__ __forceinline__ void store8(u32x2 v, bool in, uint32_t lane, uint32_t all) const {
     __builtin_amdgcn_raw_buffer_store_b64(v, rs, at(in, lane), all, 0);
