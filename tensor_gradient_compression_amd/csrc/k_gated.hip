@@ -122,39 +122,62 @@ __device__ __forceinline__ void gate_and_up(MmSums<S>& sums, TG_LDS char* lds, c
       G::SEGS, a.x.len, row0, f0, a.x.stride, a.wg.stride);
 }
 
-// The biases of a lane's columns, gate and up by turns. (All loads of an epilogue go out before its
-// first store, which the compiler would not let them pass.)
-template <class S, typename T>
-__device__ __forceinline__ void load_biases(const GatedArgs& a, uint32_t f, float (&b)[S::FN][4]) {
+// The biases of eight columns of a lane, gate and up. (All loads of an epilogue go out before its first
+// store, which the compiler would not let them pass.)
+template <typename T>
+__device__ __forceinline__ void load_biases(const GatedArgs& a, uint32_t f, float (&b)[2][8]) {
 #pragma unroll
-  for (int j = 0; j < S::FN; ++j) {
-    const T* const p = (const T*)(j & 1 ? a.bu : a.bg);
-    const uint32_t at = f + (j >> 1) * 16;
+  for (int h = 0; h < 2; ++h) {
+    const T* const p = (const T*)(h ? a.bu : a.bg);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) b[j][e] = p && at + e < a.hidden ? to_f32(p[at + e]) : 0.0f;
+    for (int e = 0; e < 8; ++e) b[h][e] = p && f + e < a.hidden ? to_f32(p[f + e]) : 0.0f;
   }
 }
 
-// four values of T through a window
+// Eight values of T on end through a window, `n` of them in the matrix; wide: by 16 bytes.
 template <typename T>
-__device__ __forceinline__ void window_store(const MmWindow& w, const T* v, bool in, uint32_t lane, uint32_t all) {
-  if constexpr (sizeof(T) == 4) w.store16(*(const u32x4*)v, in, lane, all);
-  else w.store8(*(const u32x2*)v, in, lane, all);
+__device__ __forceinline__ void window_store(const MmWindow& w, const T* v, int n, bool wide, uint32_t lane, uint32_t all) {
+  constexpr int E = 16 / sizeof(T);
+  if (wide) {
+#pragma unroll
+    for (int e = 0; e < 8; e += E) w.store16(*(const u32x4*)(v + e), e < n, lane + e * sizeof(T), all);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (sizeof(T) == 4) w.store4(__builtin_bit_cast(uint32_t, v[e]), e < n, lane + e * 4, all);
+      else w.store2(__builtin_bit_cast(uint16_t, v[e]), e < n, lane + e * 2, all);
+    }
+  }
 }
 template <typename T>
-__device__ __forceinline__ void window_store_one(const MmWindow& w, T v, bool in, uint32_t lane, uint32_t all) {
-  if constexpr (sizeof(T) == 4) w.store4(__builtin_bit_cast(uint32_t, v), in, lane, all);
-  else w.store2(__builtin_bit_cast(uint16_t, v), in, lane, all);
+__device__ __forceinline__ void window_load(const MmWindow& w, T* v, int n, bool wide, uint32_t lane, uint32_t all) {
+  constexpr int E = 16 / sizeof(T);
+  if (wide) {
+#pragma unroll
+    for (int e = 0; e < 8; e += E) *(u32x4*)(v + e) = w.load16(e < n, lane + e * sizeof(T), all);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (sizeof(T) == 4) v[e] = __builtin_bit_cast(T, w.load4(e < n, lane + e * 4, all));
+      else v[e] = __builtin_bit_cast(T, w.load2(e < n, lane + e * 2, all));
+    }
+  }
 }
+// whether a row's pieces of 16 bytes are whole and aligned
 template <typename T>
-__device__ __forceinline__ void window_load_one(const MmWindow& w, T& v, bool in, uint32_t lane, uint32_t all) {
-  if constexpr (sizeof(T) == 4) v = __builtin_bit_cast(T, w.load4(in, lane, all));
-  else v = __builtin_bit_cast(T, w.load2(in, lane, all));
+__device__ __forceinline__ bool wide_rows(const void* p, uint32_t cols, int64_t stride) {
+  constexpr uint32_t E = 16 / sizeof(T);
+  return cols % E == 0 && stride % E == 0 && ((uintptr_t)p & 15u) == 0;
 }
-template <typename T>
-__device__ __forceinline__ void window_load(const MmWindow& w, T* v, bool in, uint32_t lane, uint32_t all) {
-  if constexpr (sizeof(T) == 4) *(u32x4*)v = w.load16(in, lane, all);
-  else *(u32x2*)v = w.load8(in, lane, all);
+
+// A lane's eight columns of a row: g in two blocks, u in the two between them.
+template <class S>
+__device__ __forceinline__ void eight(const MmSums<S>& sums, int i, int j, float (&g)[8], float (&u)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    g[e] = sums.c[i][j + (e >> 2) * 2][e & 3];
+    u[e] = sums.c[i][j + (e >> 2) * 2 + 1][e & 3];
+  }
 }
 
 template <class S, int DT>
@@ -171,35 +194,29 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_forward(const GatedArgs
   gate_and_up<S, DT>(sums, lds, a, row0, f0);
   const int lane = threadIdx.x & 63, wave = (int)uniform(threadIdx.x >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
-  const bool aligned = (a.hidden % 4) == 0 && ((uintptr_t)a.y & (4 * sizeof(T) - 1)) == 0;
-  const uint32_t r = wm * S::FM * 16 + (lane & 15), c = wn * S::FN * 8 + (lane >> 4) * 4, f_of_lane = f0 + c;
-  float bias[S::FN][4];
-  load_biases<S, T>(a, f_of_lane, bias);
+  const bool wide = wide_rows<T>(a.y, a.hidden, a.hidden);
+  const uint32_t r = wm * S::FM * 16 + (lane & 15), c = wn * S::FN * 8 + (lane >> 4) * 8;
   const MmWindow out((T*)a.y + row0 * a.hidden + f0);
   with_activation(a.act, [&](auto act) {
     constexpr int ACT = decltype(act)::value;
 #pragma unroll
-    for (int j = 0; j < S::FN; j += 2) {
-      const uint32_t f = f_of_lane + j * 8;
-      const float* const bg = bias[j];
-      const float* const bu = bias[j + 1];
+    for (int j = 0; j < S::FN; j += 4) {
+      const uint32_t f = f0 + c + j * 8;
+      float bias[2][8];
+      load_biases<T>(a, f, bias);
 #pragma unroll
       for (int i = 0; i < S::FM; ++i) {
-        const int64_t m = row0 + r + i * 16;
-        alignas(16) T y[4];
+        float g[8], u[8];
+        eight(sums, i, j, g, u);
+        alignas(16) T y[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 8; ++e) {
           float slope;
-          const float p = activate<ACT, DT != DT_F32, false>(sums.c[i][j][e] + bg[e], slope);
-          y[e] = from_f32<T>(p * (sums.c[i][j + 1][e] + bu[e]));
+          const float p = activate<ACT, DT != DT_F32, false>(g[e] + bias[0][e], slope);
+          y[e] = from_f32<T>(p * (u[e] + bias[1][e]));
         }
-        const uint32_t at = (r * a.hidden + c) * sizeof(T), all = (i * 16 * a.hidden + j * 8) * sizeof(T);
-        if (aligned) {
-          window_store<T>(out, y, m < a.rows && f < a.hidden, at, all);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) window_store_one<T>(out, y[e], m < a.rows && f + e < a.hidden, at + e * sizeof(T), all);
-        }
+        const int n = row0 + r + i * 16 < a.rows ? (int)a.hidden - (int)f : 0;
+        window_store<T>(out, y, n, wide, (r * a.hidden + c) * sizeof(T), (i * 16 * a.hidden + j * 8) * sizeof(T));
       }
     }
   });
@@ -210,7 +227,8 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_grads(const GatedArgs a
   using T = typename GatedType<DT>::T;
   extern __shared__ char lds_raw[];
   TG_LDS char* const lds = (TG_LDS char*)lds_raw;
-  const uint32_t nj = (gated_pad(a.hidden) + S::BN / 2 - 1) / (S::BN / 2), ni = (uint32_t)((a.rows + S::BM - 1) / S::BM);
+  const uint32_t pad = gated_pad(a.hidden);
+  const uint32_t nj = (pad + S::BN / 2 - 1) / (S::BN / 2), ni = (uint32_t)((a.rows + S::BM - 1) / S::BM);
   uint32_t ti, tj;
   tile_at(xcd_order(blockIdx.x, gridDim.x), ni, nj, ti, tj);
   const int64_t row0 = (int64_t)ti * S::BM;
@@ -219,61 +237,52 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_grads(const GatedArgs a
   gate_and_up<S, DT>(sums, lds, a, row0, f0);
   const int lane = threadIdx.x & 63, wave = (int)uniform(threadIdx.x >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
-  const uint32_t pad = gated_pad(a.hidden);
   const int64_t part = a.rows * 2 * (int64_t)pad;
-  const bool aligned = (a.hidden % 4) == 0 && (a.dy_stride % 4) == 0 && ((uintptr_t)a.dy & (4 * sizeof(T) - 1)) == 0;
-  const uint32_t r = wm * S::FM * 16 + (lane & 15), c = wn * S::FN * 8 + (lane >> 4) * 4, f_of_lane = f0 + c;
-  float bias[S::FN][4];
-  load_biases<S, T>(a, f_of_lane, bias);
-  // dy of some rows' blocks of a column, as many as there are registers for
-  constexpr int ROWS = S::FM < 4 ? S::FM : 4;
-  alignas(16) T some[ROWS][4];
+  const bool wide = wide_rows<T>(a.dy, a.hidden, a.dy_stride);
+  const uint32_t r0 = wm * S::FM * 16 + (lane & 15), c0 = wn * S::FN * 8 + (lane >> 4) * 8;
+  const uint32_t dy_stride = (uint32_t)a.dy_stride;
   const MmWindow in((const T*)a.dy + row0 * a.dy_stride + f0);
-  auto load = [&](int j, int i0) {
-    const uint32_t f = f_of_lane + j * 8;
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const int64_t m = row0 + r + (i0 + i) * 16;
-      const uint32_t at = (r * (uint32_t)a.dy_stride + c) * sizeof(T);
-      const uint32_t more = ((i0 + i) * 16 * (uint32_t)a.dy_stride + j * 8) * sizeof(T);
-      if (aligned) {
-        window_load<T>(in, some[i], m < a.rows && f < a.hidden, at, more);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) window_load_one<T>(in, some[i][e], m < a.rows && f + e < a.hidden, at + e * sizeof(T), more);
-      }
-    }
-  };
   with_activation(a.act, [&](auto act) {
     constexpr int ACT = decltype(act)::value;
+    // (what is alike for all activations would be computed before them, into more registers than are there)
+    uint32_t r = r0, c = c0;
+    __asm__ volatile("" : "+v"(r), "+v"(c));
 #pragma unroll
-    for (int j = 0; j < S::FN; j += 2) {
-      const uint32_t f = f_of_lane + j * 8;
-      const float* const bg = bias[j];
-      const float* const bu = bias[j + 1];
-      f32x4 sg = {0.f, 0.f, 0.f, 0.f}, su = sg;
+    for (int j = 0; j < S::FN; j += 4) {
+      const uint32_t f = f0 + c + j * 8;
+      float bias[2][8];
+      load_biases<T>(a, f, bias);
+      float sg[8] = {}, su[8] = {};
+      // dy of some rows' blocks, as many as there are registers for
+      constexpr int ROWS = S::FM < 4 ? S::FM : 4;
+      alignas(16) T dy[ROWS][8];
 #pragma unroll
       for (int i = 0; i < S::FM; ++i) {
-        const bool there = row0 + r + i * 16 < a.rows && f < pad;
-        if (i % ROWS == 0) load(j, i);
-        const T* const dy = some[i % ROWS];
-        const uint32_t to_lane = (r * 2 * pad + c) * 2, to_all = (i * 32 * pad + j * 8) * 2;
-        float dg[4], du[4];
+        if (i % ROWS == 0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+          for (int k = 0; k < ROWS; ++k)
+            window_load<T>(in, dy[k], row0 + r + (i + k) * 16 < a.rows ? (int)a.hidden - (int)f : 0, wide,
+                           (r * dy_stride + c) * sizeof(T), ((i + k) * 16 * dy_stride + j * 8) * sizeof(T));
+        }
+        float g[8], u[8], dg[8], du[8];
+        eight(sums, i, j, g, u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
           float slope;
-          const float d = to_f32(dy[e]);
-          const float p = activate<ACT, DT != DT_F32, true>(sums.c[i][j][e] + bg[e], slope);
+          const float d = to_f32(dy[i % ROWS][e]);
+          const float p = activate<ACT, DT != DT_F32, true>(g[e] + bias[0][e], slope);
           const bool real = f + e < a.hidden;     // zeros behind
-          dg[e] = real ? d * (sums.c[i][j + 1][e] + bu[e]) * slope : 0.0f;
+          dg[e] = real ? d * (u[e] + bias[1][e]) * slope : 0.0f;
           du[e] = real ? d * p : 0.0f;
           sg[e] += dg[e];
           su[e] += du[e];
         }
+        const int n = row0 + r + i * 16 < a.rows && f < pad ? 8 : 0;
+        const uint32_t to_lane = (r * 2 * pad + c) * 2, to_all = (i * 32 * pad + j * 8) * 2;
         if constexpr (DT == DT_F32) {
-          alignas(8) bf16_t g[3][4], u[3][4];
+          alignas(16) bf16_t g[3][8], u[3][8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < 8; ++e) {
             bf16_t p[3];
             three_parts(dg[e], p);
             for (int q = 0; q < 3; ++q) g[q][e] = p[q];
@@ -283,30 +292,34 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_grads(const GatedArgs a
 #pragma unroll
           for (int q = 0; q < 3; ++q) {
             const MmWindow to((bf16_t*)a.grads + q * part + row0 * 2 * (int64_t)pad + f0);
-            window_store<bf16_t>(to, g[q], there, to_lane, to_all);
-            window_store<bf16_t>(to, u[q], there, to_lane, to_all + pad * 2);
+            window_store<bf16_t>(to, g[q], n, true, to_lane, to_all);
+            window_store<bf16_t>(to, u[q], n, true, to_lane, to_all + pad * 2);
           }
         } else {
-          alignas(8) T g[4], u[4];
+          alignas(16) T g[8], u[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) g[e] = from_f32<T>(dg[e]), u[e] = from_f32<T>(du[e]);
+          for (int e = 0; e < 8; ++e) g[e] = from_f32<T>(dg[e]), u[e] = from_f32<T>(du[e]);
           const MmWindow to((T*)a.grads + row0 * 2 * (int64_t)pad + f0);
-          window_store<T>(to, g, there, to_lane, to_all);
-          window_store<T>(to, u, there, to_lane, to_all + pad * 2);
+          window_store<T>(to, g, n, true, to_lane, to_all);
+          window_store<T>(to, u, n, true, to_lane, to_all + pad * 2);
         }
+        __builtin_amdgcn_sched_barrier(0);   // a row after the other: registers for few at a time
       }
       if (a.row_sums) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 8; ++e)
 #pragma unroll
           for (int o = 1; o < 16; o <<= 1) {
             sg[e] += __shfl_xor(sg[e], o);
             su[e] += __shfl_xor(su[e], o);
           }
         if ((lane & 15) == 0 && f < pad) {
-          float* const r = a.row_sums + ((int64_t)ti * S::WM + wm) * 2 * (int64_t)pad + f;
-          *(f32x4*)r = sg;
-          *(f32x4*)(r + pad) = su;
+          float* const s = a.row_sums + ((int64_t)ti * S::WM + wm) * 2 * (int64_t)pad + f;
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            *(f32x4*)(s + e) = f32x4{sg[e], sg[e + 1], sg[e + 2], sg[e + 3]};
+            *(f32x4*)(s + pad + e) = f32x4{su[e], su[e + 1], su[e + 2], su[e + 3]};
+          }
         }
       }
     }

@@ -76,7 +76,9 @@ struct MmLoader {
   u32x4 rs;              // buffer resource from the segment's first byte (or a later one) to the operand's end
   uint32_t at;           // the stage's first byte there
 
-  // BY_TURNS: the operand holds every other 16 of the tile's rows
+  // BY_TURNS: the operand holds every other 16 of the tile's rows; of 32 of its rows 0..3, 8..11, ..
+  // are in the first 16 that it holds of 64, the others in the second: a lane's sums of the
+  // two blocks are those of eight rows on end
   template <bool BY_TURNS = false>
   __device__ __forceinline__ void init(int wave, int lane, uint32_t stride) {
 #pragma unroll
@@ -87,7 +89,8 @@ struct MmLoader {
         const int r = lane / PIECES;
         k_of_lane = (uint32_t)(((lane % PIECES) ^ turn_row(r)) * 8);
         const int row = q * LINES + r;
-        v[i] = (uint32_t)(BY_TURNS ? (row >> 5) * 16 + (row & 15) : row) * (stride * 2) + k_of_lane * 2;
+        const int of = (row >> 6) * 32 + ((row >> 2) & 3) * 8 + ((row >> 5) & 1) * 4 + (row & 3);
+        v[i] = (uint32_t)(BY_TURNS ? of : row) * (stride * 2) + k_of_lane * 2;
       } else {
         constexpr int LANES = ROWS / 8;   // of one k
         const int k = q * (64 / LANES) + lane / LANES, c = lane % LANES;
@@ -232,8 +235,7 @@ struct MmSums {
 
 // `source(s, a, b, b2)` names the operands of segment s; all straight (crossed) As have the
 // stride sa, all Bs sb. k values in each of nseg segments. B's rows may come from two matrices
-// (DUAL): tile row 32 q + r < 16 from b, the 16 after from b2, both at row 16 q + r of them; bj
-// counts in rows of either. Of `splits` parts of every segment's k only part `split` is summed.
+// (DUAL): 16 by turns, as MmLoader's init has them; bj counts in rows of either. Of `splits` parts of every segment's k only part `split` is summed.
 template <class S, int DT, bool CA, bool CB, bool DUAL, class Source>
 __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const Source& source, int nseg, int64_t k,
                                         int64_t ai, int64_t bj, uint32_t sa, uint32_t sb, uint32_t split = 0,
@@ -498,8 +500,10 @@ struct MmWindow {
   __device__ __forceinline__ void store8(u32x2 v, bool in, uint32_t lane, uint32_t all) const {
     __builtin_amdgcn_raw_buffer_store_b64(v, rs, at(in, lane), all, 0);
   }
+  // (The offset is one register: with a scalar one beside it the compiler lets the next instruction
+  // write the stored registers, and the store then takes some of the new values.)
   __device__ __forceinline__ void store16(u32x4 v, bool in, uint32_t lane, uint32_t all) const {
-    __builtin_amdgcn_raw_buffer_store_b128(v, rs, at(in, lane), all, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(v, rs, at(in, lane + all), 0, 0);
   }
 };
 
