@@ -81,7 +81,7 @@ int gated_dw_splits(int64_t rows, uint32_t in, uint32_t hidden);
 hipError_t launch_gated_dw(const GatedDw& a, hipStream_t s);
 
 // The tile of the products of g and u: 0: 256 x 256, 1: 128 x 128, 2: 64 x 64, 3: 128 x 256.
-int gated_tile(int64_t ni, int64_t nj, int64_t k);
+int gated_tile(int64_t rows, int64_t hidden, int64_t in, bool grads);
 
 template <int DT> struct GatedType;
 template <> struct GatedType<DT_F32> { using T = float; static constexpr int MM = DT_BF16, SEGS = 6; };

@@ -363,7 +363,9 @@ hipError_t launch_tiles(bool grads, const GatedArgs& a, hipStream_t s) {
   const int64_t ni = (a.rows + S::BM - 1) / S::BM;
   const int64_t nj = ((grads ? gated_pad(a.hidden) : a.hidden) + S::BN / 2 - 1) / (S::BN / 2);
   if (ni * nj > 0x7FFFFFFF / S::THREADS) return hipErrorInvalidValue;
-  auto* const k = grads ? k_gated_grads<S, DT> : k_gated_forward<S, DT>;
+  void (*k)(GatedArgs) = k_gated_forward<S, DT>;
+  if constexpr (S::MODE != MM_EVEN || S::BN == 128)   // those of gated_tile()
+    if (grads) k = k_gated_grads<S, DT>;
   const hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS_BYTES);
   if (e != hipSuccess) return e;
   k<<<(uint32_t)(ni * nj), S::THREADS, S::LDS_BYTES, s>>>(a);
@@ -371,10 +373,10 @@ hipError_t launch_tiles(bool grads, const GatedArgs& a, hipStream_t s) {
 }
 template <int DT>
 hipError_t launch_type(bool grads, const GatedArgs& a, hipStream_t s) {
-  switch (gated_tile(a.rows, 2 * (int64_t)a.hidden, a.in)) {
+  switch (gated_tile(a.rows, a.hidden, a.in, grads)) {
     case 0: return launch_tiles<MmBig, DT>(grads, a, s);
     case 1: return launch_tiles<MmMid, DT>(grads, a, s);
-    case 3: return launch_tiles<MmHalf, DT>(grads, a, s);
+    case 3: return launch_tiles<MmHalf, DT>(false, a, s);   // the forward pass alone
     default: return launch_tiles<MmSmall, DT>(grads, a, s);
   }
 }
@@ -385,15 +387,20 @@ hipError_t launch_any(bool grads, const GatedArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int gated_tile(int64_t ni, int64_t nj, int64_t k) {
-  const int64_t big = ((ni + 255) / 256) * ((nj + 255) / 256), mid = ((ni + 127) / 128) * ((nj + 127) / 128);
-  return big >= 200 ? (k <= 1024 ? 3 : 0) : mid >= 200 ? 1 : 2;
+// 256 x 256 where its tiles fill the chip, smaller ones for short sums, whose epilogue is most of the
+// time: two workgroups of a CU overlap theirs (65536 x 256 x 1024 in bf16, the epilogue alike in both:
+// forward 170 us by 128 x 256, 183 by 128 x 128; the gradients, which need more registers, 283 and 221).
+// 64 x 64 for few tiles.
+int gated_tile(int64_t rows, int64_t hidden, int64_t in, bool grads) {
+  auto tiles = [&](int64_t t) { return ((rows + t - 1) / t) * ((2 * hidden + t - 1) / t); };
+  if (tiles(256) >= 200) return in > 1024 ? 0 : grads ? 1 : 3;
+  return tiles(128) >= 200 ? 1 : 2;
 }
 
 int64_t gated_sum_rows(int64_t rows, uint32_t in, uint32_t hidden) {
-  const int t = gated_tile(rows, 2 * (int64_t)hidden, in);
+  const int t = gated_tile(rows, hidden, in, true);
   auto sums = [&](auto shape) { return (rows + shape.BM - 1) / shape.BM * shape.WM; };
-  return t == 0 ? sums(MmBig{}) : t == 1 ? sums(MmMid{}) : t == 2 ? sums(MmSmall{}) : sums(MmHalf{});
+  return t == 0 ? sums(MmBig{}) : t == 1 ? sums(MmMid{}) : sums(MmSmall{});
 }
 
 hipError_t launch_gated_forward(const GatedArgs& a, hipStream_t s) { return launch_any(false, a, s); }
