@@ -265,3 +265,70 @@ def test_refusals():
             tg.gated_linear_backward(bad, x, wg, wu)
     with pytest.raises(ValueError, match="activation"):
         f(x, wg, wu, activation="swish")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "sigmoid", "relu"])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width,hidden", [(26000, 16, 256), (26000, 8, 120)])
+def test_activations_in_larger_tiles(act, dtype, rows, width, hidden):
+    """Epilogues of many rows, where a store's registers are soon used again."""
+    if dtype == "f32" and act == "relu":
+        act = "silu"      # which side of zero is the last bit's
+    check(*inputs(rows, width, hidden, dtype, seed=16), act, dtype)
+
+
+@pytest.mark.parametrize("dtype,bias", [("bf16", True), ("f16", False)])
+def test_long_sums_in_the_largest_tiles(dtype, bias):
+    check(*inputs(3000, 1032, 2100, dtype, seed=17, bias=bias), "silu", dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width,hidden", [(65, 136, 261), (33, 264, 300), (700, 24, 1001), (130, 520, 72)])
+def test_nothing_behind_the_operands_is_read(dtype, rows, width, hidden):
+    """Every operand between NaNs, as it lies and copied."""
+    args = inputs(rows, width, hidden, dtype, seed=18)
+
+    def between(t):
+        buf = torch.full((t.numel() + 2048,), float("nan"), device="cuda").to(t.dtype)
+        v = buf[1024:1024 + t.numel()].view(t.shape)
+        v.copy_(t)
+        return v
+
+    y, out = check(*args, "silu", dtype)
+    there = [between(t) for t in args]
+    assert torch.equal(y, tg.gated_linear_forward(*there[1:]))
+    assert all(torch.equal(a, b) for a, b in zip(out, tg.gated_linear_backward(*there)))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_the_biases_gradients_alone(dtype):
+    """The C call's dw may be NULL where its db is not."""
+    dy, x, wg, wu, bg, bu = inputs(70, 24, 40, dtype, seed=19)
+    want = tg.gated_linear_backward(dy, x, wg, wu, bg, bu)
+    got = tg.binding().gated_linear_backward(dy, x, wg, wu, bg, bu, 0, False, False, True)
+    assert got[:3] == (None,) * 3 and torch.equal(got[3], want[3]) and torch.equal(got[4], want[4])
+
+
+def test_rows_of_dy_too_far_apart():
+    x, w = torch.zeros(2, 8, device="cuda"), torch.zeros(16, 8, device="cuda")
+    far = torch.zeros(2, (1 << 20) + 8, device="cuda")[:, :16]
+    with pytest.raises(ValueError, match="dy"):
+        tg.gated_linear_backward(far, x, w, w)
+    one = tg.gated_linear_backward(far[:1], x[:1], w, w)
+    assert not one[0].any()
+
+
+def test_two_streams_at_once():
+    args = [inputs(900, 64, 200, "bf16", seed=20 + i) for i in range(2)]
+    want = [(tg.gated_linear_forward(*a[1:]), *tg.gated_linear_backward(*a)) for a in args]
+    sides = [torch.cuda.Stream() for _ in args]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for i, s in enumerate(sides):
+            with torch.cuda.stream(s):
+                got[i].append((tg.gated_linear_forward(*args[i][1:]), *tg.gated_linear_backward(*args[i])))
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        for r in runs:
+            assert all(torch.equal(a, b) for a, b in zip(w, r))

@@ -326,3 +326,73 @@ def test_refusals():
             opt.step(ws, gs)
     with pytest.raises(ValueError, match="clip"):
         opt.step([w], [g], clip=torch.zeros(3, device="cuda"))
+
+
+SPLIT = [(1, 300, 3000, "f32"), (1, 3000, 200, "f16"), (1, 260, 5000, "bf16"), (1, 900, 900, "f16"), (3, 300, 1500, "bf16"),
+         (2, 1500, 260, "f32")]
+
+
+@pytest.mark.parametrize("count,rows,cols,dtype", SPLIT)
+def test_sums_that_workgroups_share(count, rows, cols, dtype):
+    """Long sums of few tiles: against the oracle, again, and replayed with other work between."""
+    print(f"CASE split {count} {rows} {cols} {dtype}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(rows + cols)
+    a, b = (torch.stack([matrix(gen, rows, cols) for _ in range(count)]).to(tg.torch_dtype(dtype)) for _ in range(2))
+    y = tg.orthogonalize(a)
+    near(y[-1], host(a[-1]), dtype, "orthogonalize")
+    z = tg.orthogonalize(b)
+    x = a.clone()
+    tg.orthogonalize(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = tg.orthogonalize(x)
+    for v, w in ((b, z), (a, y), (a, y), (b, z)):
+        x.copy_(v)
+        graph.replay()
+        assert torch.equal(tg.orthogonalize(v), w)
+        torch.cuda.synchronize()
+        assert torch.equal(out, w)
+
+
+def test_split_sums_on_two_streams():
+    gen = torch.Generator(device="cuda").manual_seed(21)
+    xs = [matrix(gen, 300, 2000).half(), matrix(gen, 2000, 280)]
+    want = [tg.orthogonalize(x) for x in xs]
+    sides, got = [torch.cuda.Stream() for _ in xs], [[], []]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for i, s in enumerate(sides):
+            with torch.cuda.stream(s):
+                got[i].append(tg.orthogonalize(xs[i]))
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        assert all(torch.equal(r, w) for r in runs)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_muon_steps_of_split_sums(dtype):
+    """Matrices that a workgroup holds beside larger ones whose sums are split, twice."""
+    shapes = [(300, 2500), (20, 30), (2, 400, 260), (1030, 130)]
+    w, _ = tensors(shapes, dtype, dtype, 22)
+    opt = tg.Muon(shapes, dtype, lr=0.05, weight_decay=0.1)
+    for t in range(2):
+        _, g = tensors(shapes, dtype, dtype, 23 + t)
+        before, m = [x.clone() for x in w], host(opt.state["momentum"])
+        opt.step(w, g)
+        check_step(opt, w, g, m, before)
+
+
+@pytest.mark.parametrize("rows,cols", [(261, 520), (520, 261), (700, 300), (257, 257)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_nothing_around_a_matrix_is_read(rows, cols, dtype):
+    """A matrix between NaNs, after its workspace's memory held NaNs."""
+    gen = torch.Generator(device="cuda").manual_seed(24)
+    x = matrix(gen, rows, cols).to(tg.torch_dtype(dtype))
+    want = tg.orthogonalize(x)
+    buf = torch.full((rows + 8, cols + 40), float("nan"), device="cuda").to(x.dtype)
+    v = buf[3:3 + rows, 17:17 + cols]
+    v.copy_(x)
+    fill = [torch.full((1 << 22,), float("nan"), device="cuda") for _ in range(8)]
+    del fill
+    assert torch.equal(tg.orthogonalize(v), want)
