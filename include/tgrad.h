@@ -548,8 +548,8 @@ int tgrad_orthogonalize(const void *x, int64_t matrix_stride, int64_t row_stride
  * momentum is one flat fp32 buffer of the caller's (tgrad_muon_state_values floats, 16-byte
  * aligned) in which every tensor's values start at a multiple of 128, zeroed for a new run.
  * A step is captured and replayed as it is; one handle is used by one host thread and one
- * stream at a time (its workspace, about 8 bytes a value and 4 or 8 min(rows, cols)^2 bytes a
- * matrix, is its own). */
+ * stream at a time (its workspace, about 8 bytes a value, 4 or 8 min(rows, cols)^2 bytes a
+ * matrix and up to 34 MB of shared sums, is its own). */
 typedef struct tgrad_muon tgrad_muon_t;
 
 /* Floats of the momentum; -1 for invalid sizes. Host only. */
@@ -579,7 +579,8 @@ const char *tgrad_muon_last_error(const tgrad_muon_t *h);
 /* The learning rate from the next step on (>= 0, finite); a captured step keeps its own. */
 int tgrad_muon_set_lr(tgrad_muon_t *h, double lr);
 /* One step: weights[i] (updated in place) and grads[i] (only read) are contiguous device
- * buffers, aligned to their elements (both may be NULL where count[i] is 0). clip: NULL, or two
+ * buffers, aligned to their elements (both may be NULL where count[i] is 0). No weight overlaps
+ * another (TGRAD_EINVAL) or a gradient. clip: NULL, or two
  * device floats from tgrad_adamw_grad_norm; where the norm clip[0] is not finite the step is
  * left out on the device. Errors: TGRAD_EINVAL, TGRAD_EHIP. */
 int tgrad_muon_step(tgrad_muon_t *h, void *const *weights, const void *const *grads,

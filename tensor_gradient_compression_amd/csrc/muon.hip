@@ -4,6 +4,7 @@
 #include <cmath>
 #include <new>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "muon.h"
@@ -41,6 +42,7 @@ struct tgrad_muon {
   char* ws = nullptr;
   uint32_t* counters = nullptr;
   float* state = nullptr;    // the caller's
+  std::vector<std::pair<uintptr_t, uintptr_t>> spans;   // of a step's weights
   std::string err;
 };
 
@@ -242,6 +244,7 @@ int tgrad_muon_init(tgrad_muon_t** out, int n, const int64_t* count, const int64
     h->steps = steps;
     h->eps = eps;
     h->state = state;
+    h->spans.reserve(n);
     for (int i = 0; i < 3; ++i) h->coef[i] = coefficients[i];
     std::vector<NsMat> mats;
     std::vector<NsPart> parts;
@@ -394,6 +397,15 @@ int tgrad_muon_step(tgrad_muon_t* h, void* const* weights, const void* const* gr
     const uintptr_t wa = t.dtype == TGRAD_F32 ? 3 : 1, ga = t.grad_dtype == TGRAD_F32 ? 3 : 1;
     if (!weights[i] || !grads[i] || ((uintptr_t)weights[i] & wa) || ((uintptr_t)grads[i] & ga)) return TGRAD_EINVAL;
   }
+  h->spans.clear();          // within what was reserved
+  for (size_t i = 0; i < h->tensors.size(); ++i) {
+    const auto& t = h->tensors[i];
+    const uintptr_t at = (uintptr_t)weights[i];
+    if (t.values) h->spans.emplace_back(at, at + (uintptr_t)t.values * (t.dtype == TGRAD_F32 ? 4 : 2));
+  }
+  std::sort(h->spans.begin(), h->spans.end());
+  for (size_t i = 1; i < h->spans.size(); ++i)
+    if (h->spans[i].first < h->spans[i - 1].second) return TGRAD_EINVAL;   // two workgroups' at once
   OnDevice dev(h->device);
   const hipStream_t s = (hipStream_t)stream;
   NsCommon c{};

@@ -122,7 +122,7 @@ class Muon:
     # ---------------------------------------------------------------- hot path
     def step(self, weights, grads, clip=None, stream=None):
         """One step of every tensor: weights[i] is updated in place from grads[i] (contiguous
-        GPU tensors of as many elements as shapes[i]). clip: what AdamW.grad_norm returned, the
+        GPU tensors of as many elements as shapes[i]; no weight overlaps another). clip: what AdamW.grad_norm returned, the
         norm over this optimizer's gradients or over more; where it is not finite, nothing
         changes."""
         self._step(self._plan, weights, grads, clip, _stream(stream))

@@ -1,5 +1,6 @@
 """GPU: Newton-Schulz orthogonalisation and the Muon step against the 64-bit oracle, within
 what the kernels' formats allow (oracle/muon_oracle.py)."""
+import ctypes
 import math
 
 import numpy as np
@@ -396,3 +397,31 @@ def test_nothing_around_a_matrix_is_read(rows, cols, dtype):
     fill = [torch.full((1 << 22,), float("nan"), device="cuda") for _ in range(8)]
     del fill
     assert torch.equal(tg.orthogonalize(v), want)
+
+
+def test_weights_that_overlap():
+    """Two matrices' workgroups would write the same values."""
+    opt = tg.Muon([(6, 8), (4, 8), (0, 3, 3)], "f32")
+    buf, g = torch.zeros(12, 8, device="cuda"), torch.zeros(6, 8, device="cuda")
+    none = torch.zeros(0, 3, 3, device="cuda")
+    for second in (buf[:4], buf[5:9]):
+        with pytest.raises(tg.TGradError):
+            opt.step([buf[:6], second, none], [g, g[:4], none])
+    opt.step([buf[6:], buf[:4], none], [g, g[:4], none])
+
+
+def test_in_place():
+    """The C call's result may be its input."""
+    gen = torch.Generator(device="cuda").manual_seed(25)
+    for shape in ((40, 30), (300, 700)):
+        x = matrix(gen, *shape)
+        want = tg.orthogonalize(x)
+        lib = tg.load_library()
+        n = lib.tgrad_orthogonalize_workspace(1, *shape, 0)
+        ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+        co = (ctypes.c_double * 3)(*M.COEFFICIENTS)
+        stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        assert lib.tgrad_orthogonalize(x.data_ptr(), x.numel(), shape[1], x.data_ptr(), 1, *shape, 0, 5, co, 1e-7,
+                                       ws.data_ptr(), stream) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(x, want)
