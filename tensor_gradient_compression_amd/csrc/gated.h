@@ -44,12 +44,23 @@ struct GatedArgs {
   const void* dy;
   int64_t dy_stride;
   void* grads;
+  uint32_t* counters;  // or NULL: cleared for the products behind
   float* row_sums;     // or NULL: sums of dg and du over a tile's rows, as rows of 2 gated_pad(hidden)
 };
 hipError_t launch_gated_forward(const GatedArgs& a, hipStream_t s);
 hipError_t launch_gated_grads(const GatedArgs& a, hipStream_t s);
 // rows of row_sums
 int64_t gated_sum_rows(int64_t rows, uint32_t in, uint32_t hidden);
+
+// How a product behind is divided: a tile, and splits of its sum with what they need of memory:
+// counters and sums that the last workgroup of a tile adds (counted), or a result for every split.
+struct GatedWay {
+  int tile, splits;
+  bool counted;
+  size_t bytes;
+};
+GatedWay gated_dx_way(int64_t rows, uint32_t in, uint32_t hidden, int dt);
+GatedWay gated_dw_way(int64_t rows, uint32_t in, uint32_t hidden, int dt);
 
 // dx = dg Wg + du Wu
 struct GatedDx {
@@ -58,9 +69,9 @@ struct GatedDx {
   int64_t rows;
   uint32_t in, hidden;
   int dt;
-  float* partial;      // gated_dx_splits() sums of rows x in, if more than one
+  GatedWay way;
+  void* sums;          // of way.bytes, if any
 };
-int gated_dx_splits(int64_t rows, uint32_t in, uint32_t hidden);
 hipError_t launch_gated_dx(const GatedDx& a, hipStream_t s);
 
 // dWg = dg^T x, dWu = du^T x, and the biases' gradients
@@ -75,12 +86,12 @@ struct GatedDw {
   int64_t rows;
   uint32_t in, hidden;
   int dt;
-  float* partial;      // gated_dw_splits() sums of 2 gated_pad(hidden) x in, if more than one
+  GatedWay way;
+  void* sums;          // of way.bytes, if any
 };
-int gated_dw_splits(int64_t rows, uint32_t in, uint32_t hidden);
 hipError_t launch_gated_dw(const GatedDw& a, hipStream_t s);
 
-// The tile of the products of g and u: 0: 256 x 256, 1: 128 x 128, 2: 64 x 64, 3: 128 x 256.
+// The tile of the products of g and u: 0: 256 x 256, 1: 128 x 128, 2 and 4: 64 x 64, 3: 128 x 256.
 int gated_tile(int64_t rows, int64_t hidden, int64_t in, bool grads);
 
 template <int DT> struct GatedType;
@@ -116,19 +127,6 @@ __device__ __forceinline__ void three_parts(float x, bf16_t* p) {
   const float r = x - to_f32(p[0]);   // exact, as the next
   p[1] = from_f32<bf16_t>(r);
   p[2] = from_f32<bf16_t>(r - to_f32(p[1]));
-}
-
-// n of 4 values to p
-template <typename T>
-__device__ __forceinline__ void store4(T* p, const T* v, int n, bool vec) {
-  if (vec) {
-    if constexpr (sizeof(T) == 4) *(f32x4*)p = *(const f32x4*)v;
-    else *(uint2*)p = *(const uint2*)v;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) p[i] = v[i];
-  }
 }
 
 }  // namespace tg

@@ -58,7 +58,8 @@ Plan plan_of(const void* x, int64_t x_stride, const void* w_gate, const void* w_
 }
 
 struct Backward {
-  size_t grads, sums, dx, dw, bytes;   // where each begins, behind the copies
+  size_t grads, sums, split, bytes;    // where each begins, behind the copies
+  GatedWay dx, dw;
 };
 Backward backward_of(size_t at, int64_t rows, int64_t in, int64_t hidden, int dtype) {
   Backward b;
@@ -67,11 +68,12 @@ Backward backward_of(size_t at, int64_t rows, int64_t in, int64_t hidden, int dt
   at += up16((size_t)rows * 2 * pad * 2 * (dtype == TGRAD_F32 ? 3 : 1));
   b.sums = at;
   at += up16((size_t)gated_sum_rows(rows, (uint32_t)in, (uint32_t)hidden) * 2 * pad * 4);
-  b.dx = b.dw = at;   // one after the other
-  const int ndx = gated_dx_splits(rows, (uint32_t)in, (uint32_t)hidden);
-  const int ndw = gated_dw_splits(rows, (uint32_t)in, (uint32_t)hidden);
-  const size_t dx = ndx > 1 ? (size_t)ndx * rows * in * 4 : 0, dw = ndw > 1 ? (size_t)ndw * 2 * hidden * in * 4 : 0;
-  b.bytes = at + up16(dx > dw ? dx : dw);
+  b.split = at;       // dx's, then dw's
+  b.dx = gated_dx_way(rows, (uint32_t)in, (uint32_t)hidden, dtype);
+  b.dw = gated_dw_way(rows, (uint32_t)in, (uint32_t)hidden, dtype);
+  // what is counted has its counters first, cleared once for both; results of splits go behind them
+  const size_t most = b.dx.bytes > b.dw.bytes ? b.dx.bytes : b.dw.bytes;
+  b.bytes = at + (most ? MM_MOST_SPLIT * 4 + up16(most) : 0);
   return b;
 }
 
@@ -155,6 +157,7 @@ int tgrad_gated_linear_backward(const void* dy, int64_t dy_stride, const void* x
     a.dy = dy;
     a.dy_stride = rows > 1 ? dy_stride : hidden;
     a.grads = ws + b.grads;
+    a.counters = b.dx.counted || b.dw.counted ? (uint32_t*)(ws + b.split) : nullptr;
     a.row_sums = db_gate ? (float*)(ws + b.sums) : nullptr;
     e = launch_gated_grads(a, s);
     if (e == hipSuccess && dx) {
@@ -167,7 +170,8 @@ int tgrad_gated_linear_backward(const void* dy, int64_t dy_stride, const void* x
       d.in = (uint32_t)in;
       d.hidden = (uint32_t)hidden;
       d.dt = dtype;
-      d.partial = gated_dx_splits(rows, d.in, d.hidden) > 1 ? (float*)(ws + b.dx) : nullptr;
+      d.way = b.dx;
+      d.sums = ws + b.split + (d.way.counted ? 0 : MM_MOST_SPLIT * 4);
       e = launch_gated_dx(d, s);
     }
     if (e != hipSuccess) return TGRAD_EHIP;
@@ -186,7 +190,8 @@ int tgrad_gated_linear_backward(const void* dy, int64_t dy_stride, const void* x
   d.in = (uint32_t)in;
   d.hidden = (uint32_t)hidden;
   d.dt = dtype;
-  d.partial = gated_dw_splits(rows, d.in, d.hidden) > 1 ? (float*)(ws + b.dw) : nullptr;
+  d.way = b.dw;
+  d.sums = ws + b.split + (d.way.counted ? 0 : MM_MOST_SPLIT * 4);
   return status(launch_gated_dw(d, s));
 }
 

@@ -173,6 +173,7 @@ __device__ __forceinline__ bool wide_rows(const void* p, uint32_t cols, int64_t 
 // A lane's eight columns of a row: g in two blocks, u in the two between them.
 template <class S>
 __device__ __forceinline__ void eight(const MmSums<S>& sums, int i, int j, float (&g)[8], float (&u)[8]) {
+  static_assert(S::FN % 4 == 0, "pairs of blocks of both");
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     g[e] = sums.c[i][j + (e >> 2) * 2][e & 3];
@@ -234,6 +235,8 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_grads(const GatedArgs a
   TG_LDS char* const lds = (TG_LDS char*)lds_raw;
   const uint32_t pad = gated_pad(a.hidden);
   const uint32_t nj = (pad + S::BN / 2 - 1) / (S::BN / 2), ni = (uint32_t)((a.rows + S::BM - 1) / S::BM);
+  if (a.counters && blockIdx.x == 0)
+    for (uint32_t i = threadIdx.x; i < MM_MOST_SPLIT; i += S::THREADS) a.counters[i] = 0;
   uint32_t ti, tj;
   tile_at(xcd_order(blockIdx.x, gridDim.x), ni, nj, ti, tj);
   const int64_t row0 = (int64_t)ti * S::BM;
@@ -383,6 +386,7 @@ hipError_t launch_type(bool grads, const GatedArgs& a, hipStream_t s) {
     case 0: return launch_tiles<MmBig, DT>(grads, a, s);
     case 1: return launch_tiles<MmMid, DT>(grads, a, s);
     case 3: return launch_tiles<MmHalf, DT>(false, a, s);   // the forward pass alone
+    case 4: return launch_tiles<MmNearRows, DT>(grads, a, s);
     default: return launch_tiles<MmSmall, DT>(grads, a, s);
   }
 }
@@ -396,17 +400,18 @@ hipError_t launch_any(bool grads, const GatedArgs& a, hipStream_t s) {
 // 256 x 256 where its tiles fill the chip, smaller ones for short sums, whose epilogue is most of the
 // time: two workgroups of a CU overlap theirs (65536 x 256 x 1024 in bf16, the epilogue alike in both:
 // forward 170 us by 128 x 256, 183 by 128 x 128; the gradients, which need more registers, 283 and 221).
-// 64 x 64 for few tiles.
+// 64 x 64 for few tiles: by one workgroup a CU that splits the sum, or two that do not (768 x 2048 over
+// 768, 384 tiles: 11.8 us and 9.2; 768 x 768 over 2048, 144 tiles: 10.6 and 13.0).
 int gated_tile(int64_t rows, int64_t hidden, int64_t in, bool grads) {
   auto tiles = [&](int64_t t) { return ((rows + t - 1) / t) * ((2 * hidden + t - 1) / t); };
   if (tiles(256) >= 200) return in > 1024 ? 0 : grads ? 1 : 3;
-  return tiles(128) >= 200 ? 1 : 2;
+  return tiles(128) >= 200 ? 1 : tiles(64) > 256 ? 4 : 2;
 }
 
 int64_t gated_sum_rows(int64_t rows, uint32_t in, uint32_t hidden) {
   const int t = gated_tile(rows, hidden, in, true);
   auto sums = [&](auto shape) { return (rows + shape.BM - 1) / shape.BM * shape.WM; };
-  return t == 0 ? sums(MmBig{}) : t == 1 ? sums(MmMid{}) : sums(MmSmall{});
+  return t == 0 ? sums(MmBig{}) : t == 1 ? sums(MmMid{}) : t == 2 ? sums(MmSmall{}) : sums(MmNearRows{});
 }
 
 hipError_t launch_gated_forward(const GatedArgs& a, hipStream_t s) { return launch_any(false, a, s); }

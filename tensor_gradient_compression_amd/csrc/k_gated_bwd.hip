@@ -5,22 +5,14 @@
 // over, and dg, du and x by rows, which the weights' gradients sum over. All of these come from
 // LDS through the transposing reads, and no transposed copy is made.
 // The weights' gradients are few tiles and a long sum (over all rows): it is split over
-// workgroups, whose fp32 sums a second kernel joins in their order.
+// workgroups, whose fp32 sums a second kernel joins in their order, or the last workgroup of a tile
+// where the tiles are small.
 #include "gated.h"
 
 namespace tg {
 
 namespace {
 
-// splits of a sum over k of `tiles` tiles: enough workgroups for every CU, and at least 512
-// values of k each
-int splits_of(int64_t tiles, int64_t k, int tile) {
-  const int64_t want = tile == 0 ? 256 : 512;
-  int64_t s = want / (tiles > 0 ? tiles : 1);
-  if (s > k / 512) s = k / 512;
-  if (s > 64) s = 64;
-  return s < 1 ? 1 : (int)s;
-}
 int64_t tiles_of(int64_t ni, int64_t nj, int tile) {
   const int64_t b = tile == 0 ? 256 : tile == 1 ? 128 : 64;
   return ((ni + b - 1) / b) * ((nj + b - 1) / b);
@@ -35,21 +27,74 @@ int tile_of(int64_t ni, int64_t nj, int64_t k) {
 // values of k of each split, whole stages
 int64_t split_size(int64_t k, int splits) { return ((k + splits - 1) / splits + 63) / 64 * 64; }
 
-// 4 sums to row m, columns n.. of a result of `cols` columns, or to a split's
-template <typename T>
-__device__ __forceinline__ void leave(T* out, float* partial, int64_t m, uint32_t n, uint32_t cols, f32x4 c) {
-  const int k = (int)(cols - n < 4 ? cols - n : 4);
-  if (partial) {
-    store4(partial + m * cols + n, (const float*)&c, k, (cols & 3) == 0);
-  } else {
-    T v[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = from_f32<T>(c[e]);
-    store4(out + m * cols + n, v, k, (cols & 3) == 0 && ((uintptr_t)out & (4 * sizeof(T) - 1)) == 0);
+// A product of ni x nj with a sum over k in `segs` segments. Splits: enough workgroups for every CU,
+// with 512 values of k each at least; a 64 x 64 tile's are counted and joined by its last workgroup up to
+// 8 (1000 x 333 x 444 in fp32: dx, 96 tiles, 23.7 us by one workgroup a tile and 23.0 by five; dw, 84
+// tiles, 23.2 and 19.9), more are left to the second kernel, which reads them on all CUs.
+GatedWay way_of(int64_t ni, int64_t nj, int64_t k, int segs) {
+  GatedWay w{tile_of(ni, nj, k), 1, false, 0};
+  const int64_t tiles = tiles_of(ni, nj, w.tile);
+  auto most = [&](int64_t s, int64_t limit) { return s < 1 ? 1 : s < limit ? s : limit; };
+  if (w.tile == 2) {
+    int64_t s = most(MM_MOST_SPLIT / (tiles > 0 ? tiles : 1), k * segs / 512);
+    s = most(s, (k + 63) / 64);
+    if (s > 1 && s <= MM_MOST_SPLITS) {
+      w.counted = true;
+      w.splits = (int)s;
+      w.bytes = mm_split_bytes(tiles, s, 64);
+      w.tile = 4;
+      return w;
+    }
+    if (tiles > 256) w.tile = 4;
   }
+  const int64_t s = most(most((w.tile == 0 ? 256 : 512) / (tiles > 0 ? tiles : 1), k / 512), 64);
+  // none of them empty
+  w.splits = k < 1 ? 1 : (int)((k + split_size(k, (int)s) - 1) / split_size(k, (int)s));
+  return w;
 }
 
-// dx: one sum over the gate's and the other weight's hidden values (65536 x 256 x 1024 in bf16: 95 us, 720
+// The rows lo..hi - 1 of a tile, which are rows `row0`.. of a result of `cols` columns (or of a split's,
+// in fp32), from column n0 on.
+template <typename T, class S>
+__device__ __forceinline__ void leave_as(const MmSums<S>& sums, T* out, int64_t row0, int64_t lo, int64_t hi, uint32_t n0,
+                                         uint32_t cols) {
+  const int lane = threadIdx.x & 63, wave = (int)uniform(threadIdx.x >> 6);
+  const int r = wave / S::WN * S::FM * 16 + (lane & 15);
+  const uint32_t c = wave % S::WN * S::FN * 16 + (lane >> 4) * 4;
+  const MmWindow to(out + row0 * cols + n0);
+  const bool wide = (cols & 3) == 0 && ((uintptr_t)out & (4 * sizeof(T) - 1)) == 0;
+#pragma unroll
+  for (int i = 0; i < S::FM; ++i) {
+    const bool row = r + i * 16 >= lo && r + i * 16 < hi;
+    const uint32_t at = ((uint32_t)(r + i * 16 - (int)lo) * cols + c) * sizeof(T);
+#pragma unroll
+    for (int j = 0; j < S::FN; ++j) {
+      const uint32_t n = n0 + c + j * 16, all = j * 16 * sizeof(T);
+      alignas(16) T v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = from_f32<T>(sums.c[i][j][e]);
+      if constexpr (sizeof(T) == 4) {
+        if (wide) to.store16(*(const u32x4*)v, row && n < cols, at, all);
+        else
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to.store4(__builtin_bit_cast(uint32_t, v[e]), row && n + e < cols, at + e * 4, all);
+      } else {
+        if (wide) to.store8(*(const u32x2*)v, row && n < cols, at, all);
+        else
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to.store2(__builtin_bit_cast(uint16_t, v[e]), row && n + e < cols, at + e * 2, all);
+      }
+    }
+  }
+}
+template <typename T, class S>
+__device__ __forceinline__ void leave(const MmSums<S>& sums, T* out, float* partial, int64_t row0, int64_t lo, int64_t hi,
+                                      uint32_t n0, uint32_t cols) {
+  if (partial) leave_as(sums, partial, row0, lo, hi, n0, cols);
+  else leave_as(sums, out, row0, lo, hi, n0, cols);
+}
+
+// dx: one sum over the gate's and the other weight's hidden values (65536 x 256 x 1024 in bf16: 80 us, 860
 // TFLOP/s, one tile a CU that waits for 268 MB of dg and du; 8192 x 4096 x 8192: 966 us, 1138).
 template <class S, int DT>
 __global__ void __launch_bounds__(S::THREADS, 2) k_gated_dx(const GatedDx a, const int64_t size) {
@@ -60,7 +105,9 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_dx(const GatedDx a, con
   const uint32_t nj = (a.in + S::BN - 1) / S::BN, ni = (uint32_t)((a.rows + S::BM - 1) / S::BM);
   uint32_t ti, tj;
   tile_at(xcd_order(blockIdx.x, gridDim.x), ni, nj, ti, tj);
-  const int64_t row0 = (int64_t)ti * S::BM, k0 = (int64_t)blockIdx.y * size;
+  constexpr bool NEAR = S::MODE == MM_AHEAD;
+  const uint32_t split = NEAR && a.way.counted ? blockIdx.y : 0, splits = NEAR && a.way.counted ? gridDim.y : 1;
+  const int64_t row0 = (int64_t)ti * S::BM, k0 = splits > 1 ? 0 : (int64_t)blockIdx.y * size;
   const uint32_t n0 = tj * S::BN, pad = gated_pad(a.hidden);
   const int64_t k = (int64_t)a.hidden - k0 < size ? (int64_t)a.hidden - k0 : size;   // zeros behind in dg and du
   MmSums<S> sums;
@@ -75,22 +122,13 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_dx(const GatedDx a, con
         g = gated_operand<G::SEGS>(p, GATED_PART_A, q, k0, false);
         w = gated_operand<G::SEGS>(up ? a.wu : a.wg, GATED_PART_B, q, k0, true);
       },
-      2 * G::SEGS, k, row0, n0, a.grads.stride, a.wg.stride);
-  const int lane = threadIdx.x & 63, wave = (int)uniform(threadIdx.x >> 6);
-  const int wm = wave / S::WN, wn = wave % S::WN;
-  float* const part = a.partial ? a.partial + (int64_t)blockIdx.y * a.rows * a.in : nullptr;
-#pragma unroll
-  for (int i = 0; i < S::FM; ++i) {
-    const int64_t m = row0 + (wm * S::FM + i) * 16 + (lane & 15);
-#pragma unroll
-    for (int j = 0; j < S::FN; ++j) {
-      const uint32_t n = n0 + (wn * S::FN + j) * 16 + (lane >> 4) * 4;
-      if (m < a.rows && n < a.in) leave((T*)a.dx, part, m, n, a.in, sums.c[i][j]);
-    }
-  }
+      2 * G::SEGS, k, row0, n0, a.grads.stride, a.wg.stride, split, splits);
+  if (NEAR && !whole_sums(sums, (uint32_t*)a.sums, ti * nj + tj, split, splits, lds)) return;
+  float* const part = a.way.counted || a.way.splits == 1 ? nullptr : (float*)a.sums + (int64_t)blockIdx.y * a.rows * a.in;
+  leave(sums, (T*)a.dx, part, row0, 0, a.rows - row0, n0, a.in);
 }
 
-// dWg and dWu (65536 x 256 x 1024 in bf16: 92 us in 32 splits; 8192 x 4096 x 8192: 1063 us, 1034 TFLOP/s,
+// dWg and dWu (65536 x 256 x 1024 in bf16: 92 us in 32 splits; 8192 x 4096 x 8192: 1002 us, 1098 TFLOP/s,
 // where a library's product of two crossed operands reaches 1112).
 template <class S, int DT>
 __global__ void __launch_bounds__(S::THREADS, 2) k_gated_dw(const GatedDw a, const int64_t size) {
@@ -103,7 +141,9 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_dw(const GatedDw a, con
   uint32_t ti, tj;
   tile_at(xcd_order(blockIdx.x, gridDim.x), ni, nj, ti, tj);
   const uint32_t f0 = ti * S::BM, n0 = tj * S::BN;
-  const int64_t k0 = (int64_t)blockIdx.y * size, k = a.rows - k0 < size ? a.rows - k0 : size;
+  constexpr bool NEAR = S::MODE == MM_AHEAD;
+  const uint32_t split = NEAR && a.way.counted ? blockIdx.y : 0, splits = NEAR && a.way.counted ? gridDim.y : 1;
+  const int64_t k0 = splits > 1 ? 0 : (int64_t)blockIdx.y * size, k = a.rows - k0 < size ? a.rows - k0 : size;
   MmSums<S> sums;
   mm_tile<S, G::MM, true, true, false>(
       sums, lds,
@@ -111,26 +151,18 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_dw(const GatedDw a, con
         g = gated_operand<G::SEGS>(a.grads, GATED_PART_A, s, k0, true);
         x = gated_operand<G::SEGS>(a.x, GATED_PART_B, s, k0, true);
       },
-      G::SEGS, k, f0, n0, a.grads.stride, a.x.stride);
-  const int lane = threadIdx.x & 63, wave = (int)uniform(threadIdx.x >> 6);
-  const int wm = wave / S::WN, wn = wave % S::WN;
-  float* const part = a.partial ? a.partial + (int64_t)blockIdx.y * 2 * a.hidden * a.in : nullptr;
-#pragma unroll
-  for (int i = 0; i < S::FM; ++i) {
-    uint32_t f = f0 + (wm * S::FM + i) * 16 + (lane & 15);
-    const bool up = f >= pad;
-    if (up) f -= pad;
-#pragma unroll
-    for (int j = 0; j < S::FN; ++j) {
-      const uint32_t n = n0 + (wn * S::FN + j) * 16 + (lane >> 4) * 4;
-      if (f >= a.hidden || n >= a.in) continue;
-      leave((T*)(up ? a.dwu : a.dwg), part ? part + (up ? (int64_t)a.hidden * a.in : 0) : nullptr, f, n, a.in, sums.c[i][j]);
-    }
-  }
+      G::SEGS, k, f0, n0, a.grads.stride, a.x.stride, split, splits);
+  if (NEAR && !whole_sums(sums, (uint32_t*)a.sums, ti * nj + tj, split, splits, lds)) return;
+  const int64_t each = (int64_t)a.hidden * a.in;
+  float* const part = a.way.counted || a.way.splits == 1 ? nullptr : (float*)a.sums + (int64_t)blockIdx.y * 2 * each;
+  if (f0 < a.hidden) leave(sums, (T*)a.dwg, part, f0, 0, (int64_t)a.hidden - f0, n0, a.in);
+  const int64_t up = (int64_t)pad - f0;      // the tile's row where the other weight's begin
+  if (up < S::BM)
+    leave(sums, (T*)a.dwu, part ? part + each : nullptr, up < 0 ? -up : 0, up < 0 ? 0 : up, up + a.hidden, n0, a.in);
 }
 
 // out[v] = the sum of the n values v of `rows` rows, in their order; the values from `half` on
-// go to out2 (32 rows of 524288: 14 us, 4.7 TB/s)
+// go to out2 (32 rows of 524288: 11 us, 6 TB/s from the last-level cache)
 template <typename T>
 __global__ void __launch_bounds__(256) k_gated_join(const float* p, int64_t rows, int64_t pitch, int64_t n, T* out,
                                                     T* out2, int64_t half, int64_t half_at) {
@@ -192,19 +224,21 @@ hipError_t launch_tiles(K* k, int64_t tiles, int splits, int64_t size, const A& 
 using Big = MmBig;
 using Mid = MmMid;
 using Small = MmSmall;
+using Near = MmNear;
 
 template <int DT>
 hipError_t dx_type(const GatedDx& a, hipStream_t s) {
-  const int t = tile_of(a.rows, a.in, a.hidden), n = gated_dx_splits(a.rows, a.in, a.hidden);
-  const int64_t tiles = tiles_of(a.rows, a.in, t), size = split_size(a.hidden, n);
+  const int t = a.way.tile, n = a.way.splits;
+  const int64_t tiles = tiles_of(a.rows, a.in, t), size = a.way.counted ? a.hidden : split_size(a.hidden, n);
   hipError_t e = t == 0   ? launch_tiles<Big>(k_gated_dx<Big, DT>, tiles, n, size, a, s)
                  : t == 1 ? launch_tiles<Mid>(k_gated_dx<Mid, DT>, tiles, n, size, a, s)
-                          : launch_tiles<Small>(k_gated_dx<Small, DT>, tiles, n, size, a, s);
-  if (e != hipSuccess || n == 1) return e;
+                 : t == 2 ? launch_tiles<Small>(k_gated_dx<Small, DT>, tiles, n, size, a, s)
+                          : launch_tiles<Near>(k_gated_dx<Near, DT>, tiles, n, size, a, s);
+  if (e != hipSuccess || n == 1 || a.way.counted) return e;
   using T = typename GatedType<DT>::T;
   const int64_t v = a.rows * a.in;
   if ((v + 255) / 256 > 0x7FFFFFFF / 256) return hipErrorInvalidValue;
-  k_gated_join<T><<<(uint32_t)((v + 255) / 256), 256, 0, s>>>(a.partial, n, v, v, (T*)a.dx, (T*)a.dx, v, 0);
+  k_gated_join<T><<<(uint32_t)((v + 255) / 256), 256, 0, s>>>((const float*)a.sums, n, v, v, (T*)a.dx, (T*)a.dx, v, 0);
   return hipGetLastError();
 }
 
@@ -212,16 +246,18 @@ template <int DT>
 hipError_t dw_type(const GatedDw& a, hipStream_t s) {
   using T = typename GatedType<DT>::T;
   const uint32_t pad = gated_pad(a.hidden);
-  const int t = tile_of(2 * (int64_t)pad, a.in, a.rows), n = gated_dw_splits(a.rows, a.in, a.hidden);
-  const int64_t tiles = tiles_of(2 * (int64_t)pad, a.in, t), size = split_size(a.rows, n);
+  const int t = a.way.tile, n = a.way.splits;
+  const int64_t tiles = tiles_of(2 * (int64_t)pad, a.in, t), size = a.way.counted ? a.rows : split_size(a.rows, n);
   hipError_t e = !a.dwg   ? hipSuccess
                  : t == 0 ? launch_tiles<Big>(k_gated_dw<Big, DT>, tiles, n, size, a, s)
                  : t == 1 ? launch_tiles<Mid>(k_gated_dw<Mid, DT>, tiles, n, size, a, s)
-                          : launch_tiles<Small>(k_gated_dw<Small, DT>, tiles, n, size, a, s);
-  if (e == hipSuccess && a.dwg && n > 1) {
+                 : t == 2 ? launch_tiles<Small>(k_gated_dw<Small, DT>, tiles, n, size, a, s)
+                          : launch_tiles<Near>(k_gated_dw<Near, DT>, tiles, n, size, a, s);
+  if (e == hipSuccess && a.dwg && n > 1 && !a.way.counted) {
     const int64_t v = 2 * (int64_t)a.hidden * a.in;
     if ((v + 255) / 256 > 0x7FFFFFFF / 256) return hipErrorInvalidValue;
-    k_gated_join<T><<<(uint32_t)((v + 255) / 256), 256, 0, s>>>(a.partial, n, v, v, (T*)a.dwg, (T*)a.dwu, v / 2, v / 2);
+    k_gated_join<T><<<(uint32_t)((v + 255) / 256), 256, 0, s>>>((const float*)a.sums, n, v, v, (T*)a.dwg, (T*)a.dwu, v / 2,
+                                                                v / 2);
     e = hipGetLastError();
   }
   if (e == hipSuccess && a.dbg) {
@@ -235,17 +271,15 @@ hipError_t dw_type(const GatedDw& a, hipStream_t s) {
 
 }  // namespace
 
-int gated_dx_splits(int64_t rows, uint32_t in, uint32_t hidden) {
-  const int t = tile_of(rows, in, hidden);
-  const int n = splits_of(tiles_of(rows, in, t), hidden, t);
-  // none of them empty
-  return (int)((hidden + split_size(hidden, n) - 1) / split_size(hidden, n));
+GatedWay gated_dx_way(int64_t rows, uint32_t in, uint32_t hidden, int dt) {
+  GatedWay w = way_of(rows, in, hidden, 2 * (dt == DT_F32 ? 6 : 1));
+  if (w.splits > 1 && !w.counted) w.bytes = (size_t)w.splits * rows * in * 4;
+  return w;
 }
-int gated_dw_splits(int64_t rows, uint32_t in, uint32_t hidden) {
-  const int64_t f = 2 * (int64_t)gated_pad(hidden);
-  const int t = tile_of(f, in, rows), n = splits_of(tiles_of(f, in, t), rows, t);
-  if (rows < 1) return 1;
-  return (int)((rows + split_size(rows, n) - 1) / split_size(rows, n));
+GatedWay gated_dw_way(int64_t rows, uint32_t in, uint32_t hidden, int dt) {
+  GatedWay w = way_of(2 * (int64_t)gated_pad(hidden), in, rows, dt == DT_F32 ? 6 : 1);
+  if (w.splits > 1 && !w.counted) w.bytes = (size_t)w.splits * 2 * hidden * in * 4;
+  return w;
 }
 
 hipError_t launch_gated_dx(const GatedDx& a, hipStream_t s) {

@@ -32,7 +32,6 @@ static_assert(sizeof(NsCommon) + sizeof(MuonFirst) + sizeof(MuonTable) + sizeof(
 
 namespace {
 
-typedef float f32x2 __attribute__((ext_vector_type(2)));
 constexpr uint32_t kPartsA = 0x001, kPartsB = 0x010;   // lower upper, upper lower, upper upper
 
 __device__ __forceinline__ void workgroup_sum(double s, double* out) {
@@ -138,7 +137,7 @@ __global__ void __launch_bounds__(256) k_ns_norm(const NsCommon c, const NsSourc
 // counters for whole_sums()
 __device__ __forceinline__ void clear_counters(const NsCommon& c) {
   if (blockIdx.x || !c.counters) return;
-  for (uint32_t i = threadIdx.x; i < NS_MOST_SPLIT; i += 256) c.counters[i] = 0;
+  for (uint32_t i = threadIdx.x; i < MM_MOST_SPLIT; i += 256) c.counters[i] = 0;
 }
 
 // 2^12 / (|U| + eps), by every workgroup from all sums of the matrix in their order
@@ -222,53 +221,6 @@ __device__ __forceinline__ void my_split(const NsParts& p, uint32_t& tile, uint3
   const uint32_t t = xcd_order(blockIdx.x, gridDim.x);
   tile = t / p.splits;
   split = t - tile * p.splits;
-}
-
-// Leaves this workgroup's sums to the last of its tile, which adds all in their order: true for that
-// one, and its sums are the whole. The counter is zero again when it ends. The sums pass the L2s,
-// which the XCDs do not share, by accesses of agent scope; every wave waits until its own are
-// there before the workgroup is counted. (A release and an acquire around plain accesses write back
-// and empty an XCD's L2 for all its workgroups: 777 x 2051 in fp16 took 1057 us with them.)
-template <class S>
-__device__ __forceinline__ bool whole_sums(const NsCommon& c, const NsParts& p, uint32_t tile, uint32_t split, TG_LDS char* lds,
-                                           MmSums<S>& sums) {
-  if (p.splits == 1) return true;
-  TG_LDS uint32_t* const before = (TG_LDS uint32_t*)lds;   // what was there has been read
-  constexpr uint32_t EACH = S::FM * S::FN * S::THREADS * 2;
-  uint64_t* const all = (uint64_t*)(c.counters + NS_MOST_SPLIT) + (uint64_t)tile * p.splits * EACH + threadIdx.x;
-#pragma unroll
-  for (int i = 0; i < S::FM; ++i)
-#pragma unroll
-    for (int j = 0; j < S::FN; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const f32x2 v = {sums.c[i][j][2 * h], sums.c[i][j][2 * h + 1]};
-        __hip_atomic_store(all + split * EACH + ((i * S::FN + j) * 2 + h) * S::THREADS, __builtin_bit_cast(uint64_t, v),
-                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-  wait_vm<0>();
-  __syncthreads();
-  if (threadIdx.x == 0) *before = __hip_atomic_fetch_add(c.counters + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  if (*before != p.splits - 1) return false;
-  if (threadIdx.x == 0) __hip_atomic_store(c.counters + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-#pragma unroll
-  for (int i = 0; i < S::FM; ++i)
-#pragma unroll
-    for (int j = 0; j < S::FN; ++j) sums.c[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (uint32_t q = 0; q < p.splits; ++q)
-#pragma unroll
-    for (int i = 0; i < S::FM; ++i)
-#pragma unroll
-      for (int j = 0; j < S::FN; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const f32x2 v = __builtin_bit_cast(f32x2, __hip_atomic_load(all + q * EACH + ((i * S::FN + j) * 2 + h) * S::THREADS,
-                                                                      __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-          sums.c[i][j][2 * h] += v[0];
-          sums.c[i][j][2 * h + 1] += v[1];
-        }
-  return true;
 }
 
 __device__ __forceinline__ uint32_t whole8(uint32_t n) { return (n + 7u) & ~7u; }
@@ -387,7 +339,7 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_ns_gram(const NsCommon c, con
                                            splits);
   else
     mm_tile<S, DT_F16, true, true, false>(sums, (TG_LDS char*)lds_raw, source, nseg, m.rows, i0, j0, m.ldx, m.ldx, split, splits);
-  if (S::MODE != MM_TURNS && !whole_sums<S>(c, p, tile, split, (TG_LDS char*)lds_raw, sums)) return;
+  if (S::MODE != MM_TURNS && !whole_sums(sums, c.counters, tile, split, p.splits, (TG_LDS char*)lds_raw)) return;
   float* const diag = (float*)(c.ws + m.da);
   const Place<S> at_tile;
   const Symmetric to(c, m, m.a, i0, j0);
@@ -426,7 +378,7 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_ns_poly(const NsCommon c, con
         b = ns_operand(c, m, m.a, m.m, m.ldm, kPartsB, s);
       },
       m.exact ? 3 : 1, whole8(m.m), i0, j0, m.ldm, m.ldm, split, splits);
-  if (S::MODE != MM_TURNS && !whole_sums<S>(c, p, tile, split, (TG_LDS char*)lds_raw, sums)) return;
+  if (S::MODE != MM_TURNS && !whole_sums(sums, c.counters, tile, split, p.splits, (TG_LDS char*)lds_raw)) return;
   float* const db = (float*)(c.ws + m.db);
   const Place<S> at;
   const Symmetric from(c, m, m.a, i0, j0), to(c, m, m.b, i0, j0);
@@ -499,7 +451,7 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_ns_apply(const NsCommon c, co
           b = ns_operand(c, m, m.b, m.m, m.ldm, kPartsB, s);
         },
         nseg, whole8(m.cols), i0, j0, m.ldx, m.ldm, split, splits);
-  if (S::MODE != MM_TURNS && !whole_sums<S>(c, p, tile, split, (TG_LDS char*)lds_raw, sums)) return;
+  if (S::MODE != MM_TURNS && !whole_sums(sums, c.counters, tile, split, p.splits, (TG_LDS char*)lds_raw)) return;
   const float step = (float)(last.lr * m.scale), decay = (float)(1.0 - last.lr * m.wd);
   const Place<S> place;
   const uint64_t first = ((uint64_t)i0 * m.ldx + j0) * 2, part = (uint64_t)m.rows * m.ldx * 2;

@@ -23,6 +23,7 @@
 
 namespace tg {
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -224,6 +225,7 @@ using MmHalf = MmShape<128, 256, 1, 4, MM_EVEN, 32, 3>;
 using MmMid = MmShape<128, 128, 2, 2, MM_EVEN, 64, 2>;
 using MmDeep = MmShape<128, 128, 2, 4, MM_AHEAD, 64, 4>;
 using MmNear = MmShape<64, 64, 2, 2, MM_AHEAD, 64, 4>;
+using MmNearRows = MmShape<64, 64, 4, 1, MM_AHEAD, 64, 4>;   // whole rows of the tile in a wave
 using MmSmall = MmShape<64, 64, 4, 1, MM_ALONE, 32, 4>;
 
 // The sums of a wave: c[i][j] holds, in lane l, row 16 i + (l & 15) and columns
@@ -250,11 +252,14 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
   using LA = MmLoader<S::BM, K, LOADERS, CA>;
   using LB = MmLoader<S::BN, K, LOADERS, CB>;
   constexpr int LOADS = LA::PER + LB::PER;
+  // of two matrices by turns a wave's transfers are whole pairs of blocks, or one block
+  constexpr bool ONE = DUAL && LB::PER * (64 / LB::PIECES) == 16;
+  static_assert(!DUAL || ONE || LB::PER * (64 / LB::PIECES) % 32 == 0, "whole blocks");
   LA la;
   LB lb, lb2;
   la.init(loader, lane, sa);
   lb.template init<DUAL>(loader, lane, sb);
-  if constexpr (DUAL) lb2 = lb;
+  if constexpr (DUAL && !ONE) lb2 = lb;
   MmReader<S::BM, K, FM, CA> ra;
   MmReader<S::BN, K, FN, CB> rb;
   const int wm = ALONE ? 0 : wave / S::WN, wn = ALONE ? 0 : wave % S::WN;
@@ -280,18 +285,17 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
   auto begin = [&](int s) {
     source(s, oa, ob, ob2);
     la.start(oa, ai, from);
-    lb.start(ob, bj, from);
-    if constexpr (DUAL) lb2.start(ob2, bj, from);
+    lb.start(ONE && (loader & 1) ? ob2 : ob, bj, from);
+    if constexpr (DUAL && !ONE) lb2.start(ob2, bj, from);
     rem = (int)many;
   };
   auto after = [&](uint32_t at) { return at == (STAGES - 1) * S::STAGE ? 0u : at + S::STAGE; };
   auto transfers = [&](auto part, uint32_t l) {
     constexpr bool PART = decltype(part)::value;
     la.template issue<PART>(l, loader, rem);
-    if constexpr (!DUAL) {
+    if constexpr (!DUAL || ONE) {
       lb.template issue<PART>(l + LA::BYTES, loader, rem);
     } else {
-      static_assert(LB::PER * (64 / LB::PIECES) % 32 == 0, "a wave's transfers: whole pairs of blocks");
       lb.template issue<PART, true, false>(l + LA::BYTES, loader, rem);
       lb2.template issue<PART, true, true>(l + LA::BYTES, loader, rem);
     }
@@ -305,8 +309,8 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
     rem -= K;
     if (rem > 0) {
       la.next(oa, sa);
-      lb.next(ob, sb);
-      if constexpr (DUAL) lb2.next(ob2, sb);
+      lb.next(ONE && (loader & 1) ? ob2 : ob, sb);
+      if constexpr (DUAL && !ONE) lb2.next(ob2, sb);
     } else if (++seg < nseg) {
       begin(seg);
     }
@@ -467,6 +471,61 @@ __device__ __forceinline__ void mm_tile(MmSums<S>& sums, TG_LDS char* lds, const
       sums.c[0][j] = s;
     }
   }
+}
+
+// At most so many workgroups share sums in a launch, at most so many those of a tile.
+constexpr uint32_t MM_MOST_SPLIT = 512, MM_MOST_SPLITS = 8;
+// Bytes of the counters and the sums.
+inline uint64_t mm_split_bytes(uint64_t tiles, uint64_t splits, uint64_t side) {
+  return splits > 1 ? MM_MOST_SPLIT * 4 + tiles * splits * side * side * 4 : 0;
+}
+
+// Leaves this workgroup's sums to the last of its tile, which adds all in their order: true for that
+// one, and its sums are the whole. Behind MM_MOST_SPLIT counters (zero, and so again when it ends) lie the
+// tiles' sums, a tile's one after another. The sums pass the L2s,
+// which the XCDs do not share, by accesses of agent scope; every wave waits until its own are
+// there before the workgroup is counted. (A release and an acquire around plain accesses write back
+// and empty an XCD's L2 for all its workgroups: 777 x 2051 in fp16 took 1057 us with them.)
+template <class S>
+__device__ __forceinline__ bool whole_sums(MmSums<S>& sums, uint32_t* counters, uint32_t tile, uint32_t split, uint32_t splits,
+                                           TG_LDS char* lds) {
+  if (splits == 1) return true;
+  TG_LDS uint32_t* const before = (TG_LDS uint32_t*)lds;   // what was there has been read
+  constexpr uint32_t EACH = S::FM * S::FN * S::THREADS * 2;
+  uint64_t* const all = (uint64_t*)(counters + MM_MOST_SPLIT) + (uint64_t)tile * splits * EACH + threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < S::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < S::FN; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x2 v = {sums.c[i][j][2 * h], sums.c[i][j][2 * h + 1]};
+        __hip_atomic_store(all + split * EACH + ((i * S::FN + j) * 2 + h) * S::THREADS, __builtin_bit_cast(uint64_t, v),
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+  wait_vm<0>();
+  __syncthreads();
+  if (threadIdx.x == 0) *before = __hip_atomic_fetch_add(counters + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (*before != splits - 1) return false;
+  if (threadIdx.x == 0) __hip_atomic_store(counters + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int i = 0; i < S::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < S::FN; ++j) sums.c[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (uint32_t q = 0; q < splits; ++q)
+#pragma unroll
+    for (int i = 0; i < S::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < S::FN; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f32x2 v = __builtin_bit_cast(f32x2, __hip_atomic_load(all + q * EACH + ((i * S::FN + j) * 2 + h) * S::THREADS,
+                                                                      __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+          sums.c[i][j][2 * h] += v[0];
+          sums.c[i][j][2 * h + 1] += v[1];
+        }
+  return true;
 }
 
 // A matrix around a tile, for what follows a product. Loads and stores at byte offsets from `first`

@@ -36,15 +36,13 @@ struct NsParts {
   bool lower;          // alike: only those with j <= i, ni = nj
   uint32_t splits;     // products: workgroups to a tile, each over a part of the sum
 };
-// Products that are split leave their sums behind the counters, a tile's one after another.
-constexpr uint32_t NS_MOST_SPLIT = 512, NS_MOST_SPLITS = 8;
 
 struct NsCommon {
   const NsMat* mats;   // or NULL: all like `one`, `pitch` bytes of the workspace apart
   NsMat one;
   uint64_t pitch;
   char* ws;
-  uint32_t* counters;  // NS_MOST_SPLIT, or NULL if no product is split
+  uint32_t* counters;  // of whole_sums(), or NULL if no product is split
   const float* clip;   // NULL, or {norm, coefficient}: nothing happens where the norm is not finite
   float ca, cb, cc;
 };

@@ -111,8 +111,6 @@ uint64_t lay_out(NsMat& m, int64_t rows, int64_t cols, int dtype, uint64_t at) {
   m.sums = take(m.chunks * 8ull);
   return at;
 }
-// what a product that is split needs besides
-uint64_t counters_bytes(uint64_t sums) { return sums ? NS_MOST_SPLIT * 4 + sums : 0; }
 uint64_t across(uint64_t n, int tile) { return (n + ns_tile_size(tile) - 1) / ns_tile_size(tile); }
 uint64_t lower_tiles(uint64_t m, int tile) { return across(m, tile) * (across(m, tile) + 1) / 2; }
 
@@ -121,9 +119,7 @@ struct Way {
   int tile = 2;
   uint32_t splits = 1;
   uint64_t tiles = 0;
-  uint64_t sums() const {   // bytes of those that are split
-    return splits > 1 ? tiles * splits * ns_tile_size(tile) * ns_tile_size(tile) * 4 : 0;
-  }
+  uint64_t sums() const { return mm_split_bytes(tiles, splits, ns_tile_size(tile)); }
 };
 // The one after which the compute unit with most to do ends first, in ns, by what was measured:
 // 256 x 256 tiles bring 36 bytes a ns of their operands to LDS (matrix instructions bind them),
@@ -146,8 +142,8 @@ Way choose(const Each& each) {
       total += (double)n * k;
     });
     if (!tiles) return best;
-    for (uint32_t splits = 1; splits <= (tile ? NS_MOST_SPLITS : 1); ++splits) {
-      if (splits > 1 && (tiles * splits > NS_MOST_SPLIT || longest < splits * 256)) break;
+    for (uint32_t splits = 1; splits <= (tile ? MM_MOST_SPLITS : 1); ++splits) {
+      if (splits > 1 && (tiles * splits > MM_MOST_SPLIT || longest < splits * 256)) break;
       const double one = (double)longest / splits, loads = std::ceil(total / 256 / one - 1e-6);
       const double rate = tile == 0 ? 36 : tile == 1 ? 50 : loads > 1 ? 68 : 52;
       const double cost = loads * (one * side * 4 / rate + side * side / 2) +
@@ -340,7 +336,7 @@ int tgrad_muon_init(tgrad_muon_t** out, int n, const int64_t* count, const int64
     }
     const uint64_t bm = up(mats.size() * sizeof(NsMat), 256), bp = up(parts.size() * sizeof(NsPart), 256);
     const uint64_t bt = up((uint64_t)n * 8, 256);
-    if (hipMalloc(&h->block, bm + bp + 2 * bt + ws + counters_bytes(sums)) != hipSuccess) {
+    if (hipMalloc(&h->block, bm + bp + 2 * bt + ws + sums) != hipSuccess) {
       (void)hipGetLastError();
       delete h;
       return TGRAD_ENOMEM;
@@ -457,7 +453,7 @@ int64_t tgrad_orthogonalize_workspace(int64_t count, int64_t rows, int64_t cols,
   const uint64_t each = lay_out(m, rows, cols, dtype, 0);
   if (ns_small_parts(m.rows, m.cols, m.exact != 0)) return 0;
   if ((uint64_t)count > (1ull << 46) / each) return -1;
-  return (int64_t)(each * count + counters_bytes(count ? Ways(m, count).sums() : 0));
+  return (int64_t)(each * count + (count ? Ways(m, count).sums() : 0));
 }
 
 int tgrad_orthogonalize(const void* x, int64_t matrix_stride, int64_t row_stride, void* out, int64_t count,
