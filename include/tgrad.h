@@ -593,8 +593,8 @@ int tgrad_muon_step(tgrad_muon_t *h, void *const *weights, const void *const *gr
  *   dw_gate = dg^T x,  dw_up = du^T x,  db = sums over rows of dg and du
  * act: silu (g / (1 + e^-g)), gelu (g times the normal distribution's probability up to g),
  * sigmoid or relu (with slope 0 at 0). Sums are fp32, y is rounded once. The gradients form g
- * and u again from x; 16-bit dg and du are rounded to that type between the products (db comes
- * from the values before). fp32 products are made of six products of bf16 parts, as exact as
+ * and u again from x; 16-bit dg and du are rounded to that type between the products, up to 2^14
+ * of each carried in two such parts (db comes from the values before). fp32 products are made of six products of bf16 parts, as exact as
  * fp32 sums; a value that is not finite makes what it enters NaN there. Results do not depend
  * on the order in which workgroups run.
  *   x, dy           device, rows x_stride >= in (dy_stride >= hidden, <= 2^20) elements apart

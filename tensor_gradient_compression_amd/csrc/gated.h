@@ -40,10 +40,11 @@ struct GatedArgs {
   int dt, act;
   // forward
   void* y;
-  // backward: dg and du side by side, rows of 2 gated_pad(hidden) values (fp32: three times)
+  // backward: dg and du side by side, rows of 2 gated_pad(hidden) values, `parts` times
   const void* dy;
   int64_t dy_stride;
   void* grads;
+  int parts;
   uint32_t* counters;  // or NULL: cleared for the products behind
   float* row_sums;     // or NULL: sums of dg and du over a tile's rows, as rows of 2 gated_pad(hidden)
 };
@@ -59,8 +60,16 @@ struct GatedWay {
   bool counted;
   size_t bytes;
 };
-GatedWay gated_dx_way(int64_t rows, uint32_t in, uint32_t hidden, int dt);
-GatedWay gated_dw_way(int64_t rows, uint32_t in, uint32_t hidden, int dt);
+GatedWay gated_dx_way(int64_t rows, uint32_t in, uint32_t hidden, int parts);
+GatedWay gated_dw_way(int64_t rows, uint32_t in, uint32_t hidden, int parts);
+
+// The parts of dg and du that the products take. 16-bit ones are rounded once where they are many: the
+// gradients are then sqrt(2) times as far off as their own rounding, since as many independent
+// roundings as there are dg enter them. Few do not average (33 values: 1.55 times): up to 2^14 go in two
+// parts, whose products are bound by their launches anyway.
+inline int gated_grad_parts(int64_t rows, int64_t hidden, int dt) { return dt == DT_F32 ? 3 : rows * hidden <= 1 << 14 ? 2 : 1; }
+// and the segments of a product with them
+inline int gated_grad_segs(int parts) { return parts == 3 ? 6 : parts; }
 
 // dx = dg Wg + du Wu
 struct GatedDx {
@@ -69,6 +78,7 @@ struct GatedDx {
   int64_t rows;
   uint32_t in, hidden;
   int dt;
+  int parts;           // of dg and du
   GatedWay way;
   void* sums;          // of way.bytes, if any
 };
@@ -86,6 +96,7 @@ struct GatedDw {
   int64_t rows;
   uint32_t in, hidden;
   int dt;
+  int parts;           // of dg and du
   GatedWay way;
   void* sums;          // of way.bytes, if any
 };
@@ -109,6 +120,18 @@ __device__ __forceinline__ MmOperand gated_operand(const GatedParts& m, uint32_t
   o.len = crossed ? m.len : m.len - (uint32_t)k0;
   o.stride = m.stride;
   return o;
+}
+
+// The same of dg and du, of which 16-bit ones are in one part or two.
+template <int SEGS>
+__device__ __forceinline__ MmOperand gated_grad_operand(const GatedParts& m, int parts, int s, int64_t k0, bool crossed) {
+  if constexpr (SEGS != 1) {
+    return gated_operand<SEGS>(m, GATED_PART_A, s, k0, crossed);
+  } else {
+    GatedParts p = m;
+    p.p = (const char*)p.p + (parts == 2 && s == 0 ? m.part * 2 : 0);   // the lower part first
+    return gated_operand<1>(p, GATED_PART_A, 0, k0, crossed);
+  }
 }
 
 // A value as three of bf16 that add up to it: each the nearest to what is left, so that the

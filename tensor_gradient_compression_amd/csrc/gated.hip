@@ -59,18 +59,20 @@ Plan plan_of(const void* x, int64_t x_stride, const void* w_gate, const void* w_
 
 struct Backward {
   size_t grads, sums, split, bytes;    // where each begins, behind the copies
+  int parts;
   GatedWay dx, dw;
 };
 Backward backward_of(size_t at, int64_t rows, int64_t in, int64_t hidden, int dtype) {
   Backward b;
   const int64_t pad = gated_pad((uint32_t)hidden);
   b.grads = at;
-  at += up16((size_t)rows * 2 * pad * 2 * (dtype == TGRAD_F32 ? 3 : 1));
+  b.parts = gated_grad_parts(rows, hidden, dtype);
+  at += up16((size_t)rows * 2 * pad * 2 * b.parts);
   b.sums = at;
   at += up16((size_t)gated_sum_rows(rows, (uint32_t)in, (uint32_t)hidden) * 2 * pad * 4);
   b.split = at;       // dx's, then dw's
-  b.dx = gated_dx_way(rows, (uint32_t)in, (uint32_t)hidden, dtype);
-  b.dw = gated_dw_way(rows, (uint32_t)in, (uint32_t)hidden, dtype);
+  b.dx = gated_dx_way(rows, (uint32_t)in, (uint32_t)hidden, b.parts);
+  b.dw = gated_dw_way(rows, (uint32_t)in, (uint32_t)hidden, b.parts);
   // what is counted has its counters first, cleared once for both; results of splits go behind them
   const size_t most = b.dx.bytes > b.dw.bytes ? b.dx.bytes : b.dw.bytes;
   b.bytes = at + (most ? MM_MOST_SPLIT * 4 + up16(most) : 0);
@@ -157,6 +159,7 @@ int tgrad_gated_linear_backward(const void* dy, int64_t dy_stride, const void* x
     a.dy = dy;
     a.dy_stride = rows > 1 ? dy_stride : hidden;
     a.grads = ws + b.grads;
+    a.parts = b.parts;
     a.counters = b.dx.counted || b.dw.counted ? (uint32_t*)(ws + b.split) : nullptr;
     a.row_sums = db_gate ? (float*)(ws + b.sums) : nullptr;
     e = launch_gated_grads(a, s);
@@ -170,6 +173,7 @@ int tgrad_gated_linear_backward(const void* dy, int64_t dy_stride, const void* x
       d.in = (uint32_t)in;
       d.hidden = (uint32_t)hidden;
       d.dt = dtype;
+      d.parts = b.parts;
       d.way = b.dx;
       d.sums = ws + b.split + (d.way.counted ? 0 : MM_MOST_SPLIT * 4);
       e = launch_gated_dx(d, s);
@@ -190,6 +194,7 @@ int tgrad_gated_linear_backward(const void* dy, int64_t dy_stride, const void* x
   d.in = (uint32_t)in;
   d.hidden = (uint32_t)hidden;
   d.dt = dtype;
+  d.parts = b.parts;
   d.way = b.dw;
   d.sums = ws + b.split + (d.way.counted ? 0 : MM_MOST_SPLIT * 4);
   return status(launch_gated_dw(d, s));

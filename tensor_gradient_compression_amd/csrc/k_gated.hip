@@ -170,6 +170,13 @@ __device__ __forceinline__ bool wide_rows(const void* p, uint32_t cols, int64_t 
   return cols % E == 0 && stride % E == 0 && ((uintptr_t)p & 15u) == 0;
 }
 
+// what a value's rounding left, nothing of one that is not finite
+template <typename T>
+__device__ __forceinline__ T rest(float v, T rounded) {
+  const float r = v - to_f32(rounded);
+  return from_f32<T>(__builtin_fabsf(r) <= __builtin_fabsf(v) ? r : 0.0f);
+}
+
 // A lane's eight columns of a row: g in two blocks, u in the two between them.
 template <class S>
 __device__ __forceinline__ void eight(const MmSums<S>& sums, int i, int j, float (&g)[8], float (&u)[8]) {
@@ -310,6 +317,15 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_grads(const GatedArgs a
           const MmWindow to((T*)a.grads + row0 * 2 * (int64_t)pad + f0);
           window_store<T>(to, g, n, true, to_lane, to_all);
           window_store<T>(to, u, n, true, to_lane, to_all + pad * 2);
+          if constexpr (S::BM <= 128) {           // few values: no larger tiles
+            if (a.parts == 2) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) g[e] = rest(dg[e], g[e]), u[e] = rest(du[e], u[e]);
+              const MmWindow more((T*)a.grads + part + row0 * 2 * (int64_t)pad + f0);
+              window_store<T>(more, g, n, true, to_lane, to_all);
+              window_store<T>(more, u, n, true, to_lane, to_all + pad * 2);
+            }
+          }
         }
         __builtin_amdgcn_sched_barrier(0);   // a row after the other: registers for few at a time
       }

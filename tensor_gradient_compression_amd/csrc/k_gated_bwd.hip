@@ -109,20 +109,21 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_dx(const GatedDx a, con
   const uint32_t split = NEAR && a.way.counted ? blockIdx.y : 0, splits = NEAR && a.way.counted ? gridDim.y : 1;
   const int64_t row0 = (int64_t)ti * S::BM, k0 = splits > 1 ? 0 : (int64_t)blockIdx.y * size;
   const uint32_t n0 = tj * S::BN, pad = gated_pad(a.hidden);
+  const int segs = G::SEGS == 1 ? a.parts : G::SEGS;
   const int64_t k = (int64_t)a.hidden - k0 < size ? (int64_t)a.hidden - k0 : size;   // zeros behind in dg and du
   MmSums<S> sums;
   mm_tile<S, G::MM, false, true, false>(
       sums, lds,
       [&](int s, MmOperand& g, MmOperand& w, MmOperand&) {
         // the parts' products of dg Wg, then those of du Wu
-        const int up = s >= G::SEGS, q = up ? s - G::SEGS : s;
+        const int up = s >= segs, q = up ? s - segs : s;
         GatedParts p = a.grads;
         p.p = (const char*)p.p + (up ? (size_t)pad * 2 : 0);
         p.len = pad;
-        g = gated_operand<G::SEGS>(p, GATED_PART_A, q, k0, false);
+        g = gated_grad_operand<G::SEGS>(p, a.parts, q, k0, false);
         w = gated_operand<G::SEGS>(up ? a.wu : a.wg, GATED_PART_B, q, k0, true);
       },
-      2 * G::SEGS, k, row0, n0, a.grads.stride, a.wg.stride, split, splits);
+      2 * segs, k, row0, n0, a.grads.stride, a.wg.stride, split, splits);
   if (NEAR && !whole_sums(sums, (uint32_t*)a.sums, ti * nj + tj, split, splits, lds)) return;
   float* const part = a.way.counted || a.way.splits == 1 ? nullptr : (float*)a.sums + (int64_t)blockIdx.y * a.rows * a.in;
   leave(sums, (T*)a.dx, part, row0, 0, a.rows - row0, n0, a.in);
@@ -148,10 +149,10 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_dw(const GatedDw a, con
   mm_tile<S, G::MM, true, true, false>(
       sums, lds,
       [&](int s, MmOperand& g, MmOperand& x, MmOperand&) {
-        g = gated_operand<G::SEGS>(a.grads, GATED_PART_A, s, k0, true);
+        g = gated_grad_operand<G::SEGS>(a.grads, a.parts, s, k0, true);
         x = gated_operand<G::SEGS>(a.x, GATED_PART_B, s, k0, true);
       },
-      G::SEGS, k, f0, n0, a.grads.stride, a.x.stride, split, splits);
+      G::SEGS == 1 ? a.parts : G::SEGS, k, f0, n0, a.grads.stride, a.x.stride, split, splits);
   if (NEAR && !whole_sums(sums, (uint32_t*)a.sums, ti * nj + tj, split, splits, lds)) return;
   const int64_t each = (int64_t)a.hidden * a.in;
   float* const part = a.way.counted || a.way.splits == 1 ? nullptr : (float*)a.sums + (int64_t)blockIdx.y * 2 * each;
@@ -271,13 +272,13 @@ hipError_t dw_type(const GatedDw& a, hipStream_t s) {
 
 }  // namespace
 
-GatedWay gated_dx_way(int64_t rows, uint32_t in, uint32_t hidden, int dt) {
-  GatedWay w = way_of(rows, in, hidden, 2 * (dt == DT_F32 ? 6 : 1));
+GatedWay gated_dx_way(int64_t rows, uint32_t in, uint32_t hidden, int parts) {
+  GatedWay w = way_of(rows, in, hidden, 2 * gated_grad_segs(parts));
   if (w.splits > 1 && !w.counted) w.bytes = (size_t)w.splits * rows * in * 4;
   return w;
 }
-GatedWay gated_dw_way(int64_t rows, uint32_t in, uint32_t hidden, int dt) {
-  GatedWay w = way_of(2 * (int64_t)gated_pad(hidden), in, rows, dt == DT_F32 ? 6 : 1);
+GatedWay gated_dw_way(int64_t rows, uint32_t in, uint32_t hidden, int parts) {
+  GatedWay w = way_of(2 * (int64_t)gated_pad(hidden), in, rows, gated_grad_segs(parts));
   if (w.splits > 1 && !w.counted) w.bytes = (size_t)w.splits * 2 * hidden * in * 4;
   return w;
 }

@@ -332,3 +332,32 @@ def test_two_streams_at_once():
     for w, runs in zip(want, got):
         for r in runs:
             assert all(torch.equal(a, b) for a, b in zip(w, r))
+
+
+@pytest.mark.parametrize("rows,width,hidden", [(3, 59, 11), (1, 300, 5), (40, 24, 1), (2, 1, 7), (16, 72, 1024), (1, 8, 16384), (16384, 9, 1)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_few_gradients_are_rounded_once(rows, width, hidden, dtype):
+    """Up to 2^14 of dg and du go into their products in two parts, each within half a step of what it
+    stands for: 2^-16 (bf16) and 2^-20 or fp16's least value in all, with fp32's sums beside."""
+    dy, x, wg, wu, _, _ = inputs(rows, width, hidden, dtype, seed=30, bias=False)
+    D, X, Wg, Wu = (t.double().cpu() for t in (dy, x, wg, wu))
+    g, u = X @ Wg.T, X @ Wu.T
+    s = torch.sigmoid(g)
+    dg, du = D * u * s * (1 - s), D * s
+    true = dg @ Wg + du @ Wu, dg.T @ X, du.T @ X
+    terms = dg.abs() @ Wg.abs() + du.abs() @ Wu.abs(), dg.abs().T @ X.abs(), du.abs().T @ X.abs()
+    # g and u carry fp32's rounding of `width` terms, whose change dg and du take in turn
+    eg, eu = (2.0 ** -24 * (width + 4) * X.abs() @ W.abs().T for W in (Wg, Wu))
+    ddg, ddu = (D.abs() * (u.abs() * eg * 0.1 + eu * 0.25), D.abs() * eg * 0.25)
+    moved = ddg @ Wg.abs() + ddu @ Wu.abs(), ddg.T @ X.abs(), ddu.T @ X.abs()
+    part = {"bf16": 2.0 ** -16, "f16": 2.0 ** -20}[dtype]
+    n = max(rows, 2 * hidden)
+    least = 2.0 ** -25 if dtype == "f16" else 0.0
+    flat = least * (Wg.abs().sum(0) + Wu.abs().sum(0)), least * X.abs().sum(0), least * X.abs().sum(0)
+    out = tg.gated_linear_backward(dy, x, wg, wu, activation="sigmoid")
+    for got, t, a, m, f in zip(out, true, terms, moved, flat):
+        before = (part + 2.0 ** -16 + n * 2.0 ** -24) * a + m + f
+        r = G.HALF_ULP[dtype]
+        bound = before + r * (t.abs() + before) + (2.0 ** -25 if dtype == "f16" else 0.0)
+        off = (got.double().cpu() - t).abs()
+        assert torch.all(off <= bound), f"{float((off / bound).max()):.3g} of the bound"
