@@ -523,7 +523,8 @@ int tgrad_layer_norm_backward(const void *dy, int64_t dy_stride, const void *x, 
  * (X) and 2^8: matrices whose X or B leave +-16 or +-256 in some step overflow, which with the
  * usual coefficients none do. X is carried in 22 bits between the steps. bf16 results come from
  * products of the upper parts (11 bits), 3e-4 to 2e-3 of the result's norm off before they are
- * rounded; fp32 and fp16 results from products of both parts, 3e-7 to 1e-5. A matrix of zeros
+ * rounded; fp32 and fp16 results, and those of matrices of up to 1024 values, from products of both
+ * parts, 3e-7 to 1e-5. A matrix of zeros
  * stays one (where eps > 0); one with a value that is not finite becomes NaN.
  *
  * tgrad_orthogonalize: `count` matrices of rows x cols values.
@@ -593,8 +594,9 @@ int tgrad_muon_step(tgrad_muon_t *h, void *const *weights, const void *const *gr
  *   dw_gate = dg^T x,  dw_up = du^T x,  db = sums over rows of dg and du
  * act: silu (g / (1 + e^-g)), gelu (g times the normal distribution's probability up to g),
  * sigmoid or relu (with slope 0 at 0). Sums are fp32, y is rounded once. The gradients form g
- * and u again from x; 16-bit dg and du are rounded to that type between the products, up to 2^14
- * of each carried in two such parts (db comes from the values before). fp32 products are made of six products of bf16 parts, as exact as
+ * and u again from x; 16-bit dg and du are rounded to that type between the products, and few of
+ * them (up to 2^14 of each, or 2^19 for results of up to 2^10) carried in two such parts (db comes
+ * from the values before). fp32 products are made of six products of bf16 parts, as exact as
  * fp32 sums; a value that is not finite makes what it enters NaN there. Results do not depend
  * on the order in which workgroups run.
  *   x, dy           device, rows x_stride >= in (dy_stride >= hidden, <= 2^20) elements apart

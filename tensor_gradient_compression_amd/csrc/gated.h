@@ -65,9 +65,14 @@ GatedWay gated_dw_way(int64_t rows, uint32_t in, uint32_t hidden, int parts);
 
 // The parts of dg and du that the products take. 16-bit ones are rounded once where they are many: the
 // gradients are then sqrt(2) times as far off as their own rounding, since as many independent
-// roundings as there are dg enter them. Few do not average (33 values: 1.55 times): up to 2^14 go in two
-// parts, whose products are bound by their launches anyway.
-inline int gated_grad_parts(int64_t rows, int64_t hidden, int dt) { return dt == DT_F32 ? 3 : rows * hidden <= 1 << 14 ? 2 : 1; }
+// roundings as there are dg enter them. Few do not average (33 values: 1.55 times), nor do few results: up to
+// 2^14 values, or 2^19 of which some result has up to 2^10, go in two parts, whose products are bound by
+// their launches anyway.
+inline int gated_grad_parts(int64_t rows, int64_t in, int64_t hidden, int dt) {
+  if (dt == DT_F32) return 3;
+  const int64_t n = rows * hidden, results = (rows < hidden ? rows : hidden) * in;
+  return n <= 1 << 14 || (n <= 1 << 19 && results <= 1 << 10) ? 2 : 1;
+}
 // and the segments of a product with them
 inline int gated_grad_segs(int parts) { return parts == 3 ? 6 : parts; }
 

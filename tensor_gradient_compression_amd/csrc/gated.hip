@@ -66,7 +66,7 @@ Backward backward_of(size_t at, int64_t rows, int64_t in, int64_t hidden, int dt
   Backward b;
   const int64_t pad = gated_pad((uint32_t)hidden);
   b.grads = at;
-  b.parts = gated_grad_parts(rows, hidden, dtype);
+  b.parts = gated_grad_parts(rows, in, hidden, dtype);
   at += up16((size_t)rows * 2 * pad * 2 * b.parts);
   b.sums = at;
   at += up16((size_t)gated_sum_rows(rows, (uint32_t)in, (uint32_t)hidden) * 2 * pad * 4);

@@ -95,7 +95,7 @@ __device__ __forceinline__ void leave(const MmSums<S>& sums, T* out, float* part
 }
 
 // dx: one sum over the gate's and the other weight's hidden values (65536 x 256 x 1024 in bf16: 80 us, 860
-// TFLOP/s, one tile a CU that waits for 268 MB of dg and du; 8192 x 4096 x 8192: 966 us, 1138).
+// TFLOP/s, one tile a CU that waits for 268 MB of dg and du; 8192 x 4096 x 8192: 927 us, 1186).
 template <class S, int DT>
 __global__ void __launch_bounds__(S::THREADS, 2) k_gated_dx(const GatedDx a, const int64_t size) {
   using G = GatedType<DT>;
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_dx(const GatedDx a, con
   leave(sums, (T*)a.dx, part, row0, 0, a.rows - row0, n0, a.in);
 }
 
-// dWg and dWu (65536 x 256 x 1024 in bf16: 92 us in 32 splits; 8192 x 4096 x 8192: 1002 us, 1098 TFLOP/s,
+// dWg and dWu (65536 x 256 x 1024 in bf16: 92 us in 32 splits; 8192 x 4096 x 8192: 970 us, 1133 TFLOP/s,
 // where a library's product of two crossed operands reaches 1112).
 template <class S, int DT>
 __global__ void __launch_bounds__(S::THREADS, 2) k_gated_dw(const GatedDw a, const int64_t size) {

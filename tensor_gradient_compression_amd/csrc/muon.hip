@@ -52,6 +52,9 @@ constexpr uint64_t kGroup = 128;           // every tensor's momentum starts at 
 constexpr int64_t kMostSide = 1 << 19;     // tiles' offsets stay under 2^31 bytes
 constexpr uint64_t kMostParts = 1 << 21;   // of one launch
 constexpr int kMostSteps = 100;
+// So few values do not average what the products of upper parts are off (2 x 2 in bf16: 1.8 times a
+// rounding), and take those of both in a launch that waits for its barriers anyway.
+constexpr int64_t kFewValues = 1024;
 
 struct OnDevice {
   int prev = -1;
@@ -93,7 +96,7 @@ uint64_t lay_out(NsMat& m, int64_t rows, int64_t cols, int dtype, uint64_t at) {
   m.ldx = line(cols);
   m.m = (uint32_t)(rows < cols ? rows : cols);
   m.ldm = line(m.m);
-  m.exact = dtype != TGRAD_BF16;
+  m.exact = dtype != TGRAD_BF16 || rows * cols <= kFewValues;
   m.wdt = (uint32_t)dtype;
   m.chunks = (uint32_t)(((uint64_t)rows * (m.ldx / 8) + MUON_CHUNK / 8 - 1) / (MUON_CHUNK / 8));
   auto take = [&](uint64_t bytes) {

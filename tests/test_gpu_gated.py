@@ -334,7 +334,7 @@ def test_two_streams_at_once():
             assert all(torch.equal(a, b) for a, b in zip(w, r))
 
 
-@pytest.mark.parametrize("rows,width,hidden", [(3, 59, 11), (1, 300, 5), (40, 24, 1), (2, 1, 7), (16, 72, 1024), (1, 8, 16384), (16384, 9, 1)])
+@pytest.mark.parametrize("rows,width,hidden", [(3, 59, 11), (1, 300, 5), (40, 24, 1), (2, 1, 7), (16, 72, 1024), (1, 8, 16384), (16384, 9, 1), (29, 8, 6136), (30000, 40, 17)])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_few_gradients_are_rounded_once(rows, width, hidden, dtype):
     """Up to 2^14 of dg and du go into their products in two parts, each within half a step of what it

@@ -425,3 +425,14 @@ def test_in_place():
                                        ws.data_ptr(), stream) == 0
         torch.cuda.synchronize()
         assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("rows,cols", [(2, 2), (1, 7), (5, 3), (32, 32), (8, 128)])
+def test_few_values_in_bf16_are_exact_but_for_their_rounding(rows, cols):
+    """Within what fp32 results are off, and half a step."""
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    x = torch.stack([matrix(gen, rows, cols) for _ in range(6)]).bfloat16()
+    for got, u in zip(tg.orthogonalize(x), host(x)):
+        true = M.orthogonalize(u)
+        e2, em = M.bounds(u, true, "f32")
+        assert np.all(np.abs(host(got) - true) <= em + M.rounding(np.abs(true) + em, "bf16"))
