@@ -31,6 +31,12 @@ struct GatedPack {
 };
 hipError_t launch_gated_pack(const GatedPack* a, int n, hipStream_t s);
 
+// Values of k that the tile of g and u from column f0 of the weights on sums over: none behind the weights,
+// where the gradients have tiles for their padding alone.
+__host__ __device__ inline uint32_t gated_sum(const GatedParts& x, const GatedParts& w, uint32_t f0, uint32_t hidden) {
+  return f0 < hidden ? x.len : 0;
+}
+
 struct GatedArgs {
   GatedParts x, wg, wu;
   const void* bg;      // may be NULL: 0

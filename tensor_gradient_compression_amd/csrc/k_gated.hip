@@ -119,7 +119,7 @@ __device__ __forceinline__ void gate_and_up(MmSums<S>& sums, TG_LDS char* lds, c
         g = gated_operand<G::SEGS>(a.wg, GATED_PART_B, s, 0, false);
         u = gated_operand<G::SEGS>(a.wu, GATED_PART_B, s, 0, false);
       },
-      G::SEGS, a.x.len, row0, f0, a.x.stride, a.wg.stride);
+      G::SEGS, gated_sum(a.x, a.wg, f0, a.hidden), row0, f0, a.x.stride, a.wg.stride);
 }
 
 // The biases of eight columns of a lane, gate and up. (All loads of an epilogue go out before its first

@@ -33,6 +33,8 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 #define TG_LDS __attribute__((address_space(3)))
+// what a host program computes too, to check what a tile reads against its operands
+#define TG_BOTH __host__ __device__ __forceinline__
 
 // A matrix of 16-bit values as it lies: `lines` lines of `len` contiguous values, `stride`
 // values apart. `p` and the lines are 16-byte aligned and len is a multiple of 8 (rows are
@@ -46,7 +48,12 @@ struct MmOperand {
 // at most 2^21 values between lines: a tile's offsets stay under 2^31
 constexpr int64_t MM_MOST_STRIDE = 1 << 21;
 
-__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+TG_BOTH uint32_t uniform(uint32_t x) {
+#if __HIP_DEVICE_COMPILE__
+  x = __builtin_amdgcn_readfirstlane(x);
+#endif
+  return x;
+}
 
 // Waits until at most N of this wave's transfers are under way. The compiler knows nothing of
 // them: no read of LDS may move across.
@@ -81,7 +88,7 @@ struct MmLoader {
   // are in the first 16 that it holds of 64, the others in the second: a lane's sums of the
   // two blocks are those of eight rows on end
   template <bool BY_TURNS = false>
-  __device__ __forceinline__ void init(int wave, int lane, uint32_t stride) {
+  TG_BOTH void init(int wave, int lane, uint32_t stride) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int q = wave * PER + i;
@@ -101,28 +108,33 @@ struct MmLoader {
     }
   }
   // straight: how a row's pieces are permuted; crossed: how a k's pairs are
-  __device__ static constexpr int turn_row(int r) { return K == 64 ? r & 7 : (r >> 1) & 3; }
-  __device__ static constexpr int turn(int k) { return ((k & 3) | (((k >> 3) & 1) << 2)) & (ROWS / 16 - 1); }
+  __host__ __device__ static constexpr int turn_row(int r) { return K == 64 ? r & 7 : (r >> 1) & 3; }
+  __host__ __device__ static constexpr int turn(int k) { return ((k & 3) | (((k >> 3) & 1) << 2)) & (ROWS / 16 - 1); }
 
-  // from row `row` and value `k` of k on
-  __device__ __forceinline__ void start(const MmOperand& o, int64_t row, int64_t k) {
+  // from row `row` and value `k` of k on, both inside the operand
+  TG_BOTH void start(const MmOperand& o, int64_t row, int64_t k) {
     const int64_t skip = (CROSSED ? row + k * o.stride : row * o.stride + k) * 2;
     resource((uint64_t)o.p + (uint64_t)skip, ((o.lines - 1) * (int64_t)o.stride + o.len) * 2 - skip);
   }
-  // (what lies behind the operand is none of it; the check takes the stage's offset off the size)
-  __device__ __forceinline__ void resource(uint64_t from, int64_t left) {
+  // (What lies behind the operand is none of it. The check takes the stage's offset off the size, so
+  // that may not pass it: k ends where the operand's lines do.)
+  TG_BOTH void resource(uint64_t from, int64_t left) {
     rs[0] = uniform((uint32_t)from);
     rs[1] = uniform((uint32_t)(from >> 32)) & 0xFFFFu;
     rs[2] = uniform(left <= 0 ? 0u : left >> 32 ? 0xFFFFFFF0u : (uint32_t)left);
     rs[3] = 0x00020000u;
     at = 0;
   }
-  __device__ __forceinline__ void next(const MmOperand& o, uint32_t stride) {
+  TG_BOTH void next(const MmOperand& o, uint32_t stride) {
     at += (CROSSED ? uniform(stride) : 1) * (K * 2);
     if (CROSSED && at >= 0x40000000u) {   // 32 bits do not reach through a long operand
       const uint64_t from = (((uint64_t)rs[1] << 32) | rs[0]) + at;
       resource(from, (int64_t)((uint64_t)o.p + (uint64_t)(((o.lines - 1) * (int64_t)o.stride + o.len) * 2) - from));
     }
+  }
+  // the lane's offset in transfer i of a stage of which only `rem` values of k are there
+  TG_BOTH uint32_t offset(int i, int rem) const {
+    return (int)k_of_lane + (CROSSED ? i * (512 / ROWS) : 0) < rem ? v[i] : 0xFFFFFFF0u;
   }
   // Whether transfer i is of the second matrix of two that alternate.
   __device__ static constexpr bool second(int i) { return ((i * (64 / PIECES)) >> 4) & 1; }
@@ -136,8 +148,7 @@ struct MmLoader {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       if (BY_TURNS && second(i) != SECOND) continue;
-      uint32_t o = v[i];
-      if (PART) o = (int)k_of_lane + (CROSSED ? i * (512 / ROWS) : 0) < rem ? o : 0xFFFFFFF0u;
+      const uint32_t o = PART ? offset(i, rem) : v[i];
       // a scalar register that the vector unit wrote takes five states to reach a transfer
       if (first)
         __asm__ volatile("s_add_u32 m0, %0, %4\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
