@@ -31,10 +31,11 @@ struct GatedPack {
 };
 hipError_t launch_gated_pack(const GatedPack* a, int n, hipStream_t s);
 
-// Values of k that the tile of g and u from column f0 of the weights on sums over: none behind the weights,
-// where the gradients have tiles for their padding alone.
+// Values of k that the tile of g and u from column f0 of the weights on sums over: those that the lines of
+// both x and the weights have (a copy's padding may pass the end of a line that goes as it lies), and none
+// behind the weights, where the gradients have tiles for their padding alone.
 __host__ __device__ inline uint32_t gated_sum(const GatedParts& x, const GatedParts& w, uint32_t f0, uint32_t hidden) {
-  return f0 < hidden ? x.len : 0;
+  return f0 >= hidden ? 0 : x.len < w.len ? x.len : w.len;
 }
 
 struct GatedArgs {

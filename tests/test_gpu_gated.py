@@ -361,3 +361,19 @@ def test_few_gradients_are_rounded_once(rows, width, hidden, dtype):
         bound = before + r * (t.abs() + before) + (2.0 ** -25 if dtype == "f16" else 0.0)
         off = (got.double().cpu() - t).abs()
         assert torch.all(off <= bound), f"{float((off / bound).max()):.3g} of the bound"
+
+
+@pytest.mark.parametrize("rows,width,hidden", [(70, 264, 40), (700, 264, 1001), (3000, 328, 1100), (5000, 264, 1300)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_a_weight_that_is_not_finite_stays_in_its_hidden_value(rows, width, hidden, dtype):
+    """x copied into longer lines beside weights that go as they lie: the other hidden values and
+    their gradients are those of finite weights, bit for bit."""
+    dy, x, wg, wu, bg, bu = inputs(rows, width, hidden, dtype, seed=40, offset=1)
+    y, out = tg.gated_linear_forward(x, wg, wu, bg, bu), tg.gated_linear_backward(dy, x, wg, wu, bg, bu)
+    wg, wu = wg.clone(), wu.clone()
+    wg[1, 0], wu[3, 5] = float("inf"), float("nan")
+    clean = torch.ones(hidden, dtype=torch.bool, device="cuda")
+    clean[[1, 3]] = False
+    assert torch.equal(tg.gated_linear_forward(x, wg, wu, bg, bu)[:, clean], y[:, clean])
+    for a, b in zip(tg.gated_linear_backward(dy, x, wg, wu, bg, bu)[1:], out[1:]):
+        assert torch.equal(a[clean], b[clean])

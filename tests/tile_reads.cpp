@@ -124,7 +124,7 @@ static void newton_schulz(uint32_t rows, uint32_t cols) {
 
 int main() {
   for (int64_t rows : {1, 70, 300})
-    for (uint32_t in : {1u, 8u, 65u, 136u, 320u, 333u})
+    for (uint32_t in : {1u, 8u, 65u, 136u, 264u, 320u, 333u, 520u})
       for (uint32_t hidden : {1u, 33u, 64u, 129u, 257u, 264u, 288u, 289u, 330u}) gated(rows, in, hidden);
   for (uint32_t rows : {1u, 129u, 260u, 333u})
     for (uint32_t cols : {7u, 130u, 257u, 520u}) {
