@@ -281,18 +281,19 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_grads(const GatedArgs a
         }
         float g[8], u[8], dg[8], du[8];
         eight(sums, i, j, g, u);
+        const bool row = row0 + r + i * 16 < a.rows;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float slope;
           const float d = to_f32(dy[i % ROWS][e]);
           const float p = activate<ACT, DT != DT_F32, true>(g[e] + bias[0][e], slope);
-          const bool real = f + e < a.hidden;     // zeros behind
+          const bool real = row && f + e < a.hidden;     // zeros behind (not zero times a bias)
           dg[e] = real ? d * (u[e] + bias[1][e]) * slope : 0.0f;
           du[e] = real ? d * p : 0.0f;
           sg[e] += dg[e];
           su[e] += du[e];
         }
-        const int n = row0 + r + i * 16 < a.rows && f < pad ? 8 : 0;
+        const int n = row && f < pad ? 8 : 0;
         const uint32_t to_lane = (r * 2 * pad + c) * 2, to_all = (i * 32 * pad + j * 8) * 2;
         if constexpr (DT == DT_F32) {
           alignas(16) bf16_t g[3][8], u[3][8];

@@ -377,3 +377,16 @@ def test_a_weight_that_is_not_finite_stays_in_its_hidden_value(rows, width, hidd
     assert torch.equal(tg.gated_linear_forward(x, wg, wu, bg, bu)[:, clean], y[:, clean])
     for a, b in zip(tg.gated_linear_backward(dy, x, wg, wu, bg, bu)[1:], out[1:]):
         assert torch.equal(a[clean], b[clean])
+
+
+@pytest.mark.parametrize("rows", [1, 65, 300])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_behind_the_last_add_nothing(rows, dtype):
+    """Biases at infinity: relu's slope is 1 and its value the gate's, so with dy of ones both biases'
+    gradients are infinite, and where a tile's rows behind the last came in they would be zero times that."""
+    ty = tg.torch_dtype(dtype)
+    x, w = torch.zeros(rows, 8, device="cuda", dtype=ty), torch.zeros(3, 8, device="cuda", dtype=ty)
+    b = torch.tensor([1.0, float("inf"), 2.0], device="cuda").to(ty)
+    out = tg.gated_linear_backward(torch.ones(rows, 3, device="cuda", dtype=ty), x, w, w, b, b, activation="relu")
+    for db in out[3:]:
+        assert torch.equal(db.float(), rows * b.float()), db
