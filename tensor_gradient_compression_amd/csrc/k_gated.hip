@@ -21,7 +21,8 @@ namespace {
 
 // Phi(-x) for x >= 0, the normal distribution's lower tail: t 2^(p(t) - x^2 log2(e) / 2) with
 // t = 1 / (1 + x / sqrt(8)) and p a polynomial fitted to log2(erfcx(x / sqrt 2) / 2t) at
-// Chebyshev points; 3.4e-7 of the value for every x.
+// Chebyshev points, 3.4e-7 of the value for every x. The rounding of the exponent's argument comes
+// on top: 1.4e-6 of the value at x = 5, 3e-6 at 8, 8e-6 at 13.
 __device__ __forceinline__ float normal_tail(float x) {
   const float t = __builtin_amdgcn_rcpf(1.0f + 0.353553391f * x);
   float p = 0.253258819f;
@@ -67,7 +68,7 @@ __device__ __forceinline__ float activate(float g, float& slope) {
       const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(g * -0.721347520f, g, -1.32574806f));
       slope = 0.5f + __builtin_copysignf(__builtin_fmaf(near, e, 0.5f - tail), g);
     }
-    return __builtin_fmaf(0.5f, g + x, -near * tail);
+    return __builtin_fmaxf(g, 0.0f) - near * tail;      // (not the mean of g and |g|, whose sum may overflow)
   } else if constexpr (ACT == GATED_GELU) {
     const float tail = normal_tail(x);
     const float cdf = g < 0.0f ? tail : 1.0f - tail;

@@ -390,3 +390,23 @@ def test_rows_behind_the_last_add_nothing(rows, dtype):
     out = tg.gated_linear_backward(torch.ones(rows, 3, device="cuda", dtype=ty), x, w, w, b, b, activation="relu")
     for db in out[3:]:
         assert torch.equal(db.float(), rows * b.float()), db
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "sigmoid", "relu"])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gates_at_the_ends(act, dtype):
+    """Gates (the biases, over weights of zeros) at their type's ends and at infinity: the limits of the
+    activation and of its slope, which all of these are as far as the type holds them."""
+    ty = tg.torch_dtype(dtype)
+    most = torch.finfo(ty).max
+    g = torch.tensor([-float("inf"), -most, -0.6 * most, -1000.0, 1000.0, 0.6 * most, most, float("inf")], device="cuda").to(ty)
+    n = len(g)
+    x, w, one = torch.zeros(1, 8, device="cuda", dtype=ty), torch.zeros(n, 8, device="cuda", dtype=ty), torch.ones(n, device="cuda", dtype=ty)
+    up = (g > 0).to(ty)
+    value = up if act == "sigmoid" else torch.where(g > 0, g, torch.zeros_like(g))
+    slope = torch.zeros_like(g) if act == "sigmoid" else up
+    y = tg.gated_linear_forward(x, w, w, g, one, activation=act)
+    out = tg.gated_linear_backward(one[None], x, w, w, g, one, activation=act)
+    assert torch.equal(y[0], value), y
+    assert torch.equal(out[3], slope), out[3]
+    assert torch.equal(out[4], value), out[4]
