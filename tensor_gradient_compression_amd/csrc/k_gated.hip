@@ -79,9 +79,10 @@ __device__ __forceinline__ float activate(float g, float& slope) {
     // -infinity times a tail of zero is the limit, zero
     return tail == 0.0f ? (g < 0.0f ? 0.0f : g) : g * cdf;
   } else if constexpr (SHORT) {
-    const float r = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * g));
+    const float e = __builtin_amdgcn_exp2f(-kLog2e * g), r = __builtin_amdgcn_rcpf(1.0f + e);
     if constexpr (ACT == GATED_SIGMOID) {
-      if (SLOPE) slope = __builtin_fmaf(-r, r, r);
+      // 1 - r keeps nothing of r's counterpart e r where that is small
+      if (SLOPE) slope = g > 0.0f ? e * r * r : __builtin_fmaf(-r, r, r);
       return r;
     }
     const float low = __builtin_fmaxf(g, -200.0f);

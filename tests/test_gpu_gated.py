@@ -410,3 +410,26 @@ def test_gates_at_the_ends(act, dtype):
     assert torch.equal(y[0], value), y
     assert torch.equal(out[3], slope), out[3]
     assert torch.equal(out[4], value), out[4]
+
+
+def slopes(gates, act, dtype, terms, own):
+    """The gate's slopes times 6 x 10^4 (dy of 1000 times an other part of 60, so that fp16 holds small
+    ones) against the formula: off by `own` of `terms` and by their rounding."""
+    ty = tg.torch_dtype(dtype)
+    g = gates.to("cuda").to(ty)
+    n, G64 = len(g), host(g)
+    x, w = torch.zeros(1, 8, device="cuda", dtype=ty), torch.zeros(n, 8, device="cuda", dtype=ty)
+    u, dy = torch.full((n,), 60.0, device="cuda", dtype=ty), torch.full((1, n), 1000.0, device="cuda", dtype=ty)
+    off = np.abs(host(tg.gated_linear_backward(dy, x, w, w, g, u, activation=act)[3]) - 6e4 * G.activate(G64, act)[1])
+    before = 6e4 * own(G64) * terms(G64)
+    bound = before + G.HALF_ULP[dtype] * (6e4 * np.abs(G.activate(G64, act)[1]) + before)
+    bound += 2.0 ** -25 if dtype == "f16" else 0.0
+    assert np.all(off <= bound), [(x, f"{y:.3g} of the bound") for x, y in zip(G64, off / bound) if y > 1]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_slopes_of_far_sigmoid_gates(dtype):
+    """Relative to themselves, on both sides: the exponent's argument is rounded twice, and an exponential,
+    a reciprocal, a sum and products by a unit each, six at most."""
+    slopes(torch.arange(-17.0, 17.1, 0.5), "sigmoid", dtype, lambda g: 1 / ((1 + np.exp(-g)) * (1 + np.exp(g))),
+           lambda g: (2 * np.abs(g) + 6 * 2) * 2.0 ** -24)
