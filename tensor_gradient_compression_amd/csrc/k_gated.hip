@@ -62,11 +62,12 @@ __device__ __forceinline__ float activate(float g, float& slope) {
     if (SLOPE) slope = g > 0.0f ? 1.0f : 0.0f;
     return g < 0.0f ? 0.0f : g;
   } else if constexpr (ACT == GATED_GELU && SHORT) {
-    // g Phi(g) = max(g, 0) - |g| Phi(-|g|);  its slope 1/2 +- (1/2 - Phi(-|g|) + |g| phi(g))
+    // g Phi(g) = max(g, 0) - |g| Phi(-|g|);  its slope q = Phi(-|g|) - |g| phi(g) below zero, 1 - q above
     const float tail = short_normal_tail(x), near = __builtin_fminf(x, 30.0f);
     if (SLOPE) {
       const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(g * -0.721347520f, g, -1.32574806f));
-      slope = 0.5f + __builtin_copysignf(__builtin_fmaf(near, e, 0.5f - tail), g);
+      const float q = __builtin_fmaf(-near, e, tail);
+      slope = g < 0.0f ? q : 1.0f - q;
     }
     return __builtin_fmaxf(g, 0.0f) - near * tail;      // (not the mean of g and |g|, whose sum may overflow)
   } else if constexpr (ACT == GATED_GELU) {
