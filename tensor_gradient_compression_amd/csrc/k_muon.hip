@@ -140,23 +140,24 @@ __device__ __forceinline__ void clear_counters(const NsCommon& c) {
   for (uint32_t i = threadIdx.x; i < MM_MOST_SPLIT; i += 256) c.counters[i] = 0;
 }
 
-// 2^12 / (|U| + eps), by every workgroup from all sums of the matrix in their order
-__device__ __forceinline__ float start_scale(const NsCommon& c, const NsMat& m, double eps) {
+// X's factor, by every workgroup from all sums of the matrix in their order
+__device__ __forceinline__ NsScale start_scale(const NsCommon& c, const NsMat& m, double eps) {
   __shared__ double total;
   double s = 0.0;
   const double* const sums = (const double*)(c.ws + m.sums);
   for (uint32_t i = threadIdx.x; i < m.chunks; i += 256) s += sums[i];
   workgroup_sum(s, &total);
   __syncthreads();
-  return (float)((double)NS_X / (__builtin_sqrt(total) + eps));
+  return NsScale(total, eps);
 }
 
 // 8 values of a line of X in their parts
-__device__ __forceinline__ void write_x(const NsCommon& c, const NsMat& m, uint32_t r, uint32_t k, const float* v, float scale) {
+__device__ __forceinline__ void write_x(const NsCommon& c, const NsMat& m, uint32_t r, uint32_t k, const float* v,
+                                        const NsScale& scale) {
   _Float16* const hi = (_Float16*)(c.ws + m.x) + (uint64_t)r * m.ldx + k;
   _Float16 h[8], l[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) two_parts(v[e] * scale, h[e], l[e]);
+  for (int e = 0; e < 8; ++e) two_parts(scale(v[e]), h[e], l[e]);
   *(uint4*)hi = *(const uint4*)h;
   *(uint4*)(hi + (uint64_t)m.rows * m.ldx) = *(const uint4*)l;
 }
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(256) k_muon_start(const NsCommon c, const Muon
   NsMat m;
   uint32_t chunk, none;
   my_part(c, p, blockIdx.x, m, chunk, none);
-  const float scale = start_scale(c, m, eps);
+  const NsScale scale = start_scale(c, m, eps);
   with_type(m.gdt, [&](auto zero) {
     using T = decltype(zero);
     const T* const g = (const T*)f.g[m.tensor] + m.elem;
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(256) k_ns_start(const NsCommon c, const NsSour
   NsMat m;
   uint32_t chunk, none;
   const uint32_t mat = my_part(c, p, blockIdx.x, m, chunk, none);
-  const float scale = start_scale(c, m, eps);
+  const NsScale scale = start_scale(c, m, eps);
   with_type(m.gdt, [&](auto zero) {
     using T = decltype(zero);
     const T* const x = (const T*)f.x + mat * f.matrix_stride;

@@ -225,13 +225,13 @@ __global__ void __launch_bounds__(WAVES * 64, WAVES / 4)
   double total = 0.0;
 #pragma unroll
   for (int i = 0; i < kWaves; ++i) total += sums[i];
-  const float scale = (float)((double)NS_X / (__builtin_sqrt(total) + k.eps));
+  const NsScale scale(total, k.eps);
 #pragma unroll
   for (int s = 0; s < SLOTS; ++s)
 #pragma unroll
     for (int gh = 0; gh < 2 * RB; ++gh)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[s][gh >> 1][gh & 1][e] *= scale;
+      for (int e = 0; e < 4; ++e) x[s][gh >> 1][gh & 1][e] = scale(x[s][gh >> 1][gh & 1][e]);
 
   const bool wide = m.rows <= m.cols;
 #pragma unroll 1

@@ -53,6 +53,22 @@ __device__ __forceinline__ void load_values(const T* p, T* v) { __builtin_memcpy
 template <int N, typename T>
 __device__ __forceinline__ void store_values(T* p, const T* v) { __builtin_memcpy(p, v, N * sizeof(T)); }
 
+// 2^12 / (|U| + eps) from the sum of U's squares, in two factors: a norm below 1.2e-35 has a reciprocal
+// that fp32 does not hold, so such values are lifted by a power of two before.
+struct NsScale {
+  float lift, rest;
+  __device__ __forceinline__ NsScale(double squares, double eps) {
+    const double s = (double)NS_X / (__builtin_sqrt(squares) + eps);
+    lift = 1.0f;
+    rest = (float)s;
+    if (__builtin_expect(rest > 0x1p126f, 0)) {
+      lift = 0x1p100f;
+      rest = (float)(s * 0x1p-100);
+    }
+  }
+  __device__ __forceinline__ float operator()(float v) const { return v * lift * rest; }
+};
+
 // v as two fp16 parts. (Without the empty statement the compiler rounds a product that v is twice,
 // once from its exact value and once from its fp32 one, and where these differ the lower part
 // belongs to another upper part than the one that is stored.)

@@ -436,3 +436,20 @@ def test_few_values_in_bf16_are_exact_but_for_their_rounding(rows, cols):
         true = M.orthogonalize(u)
         e2, em = M.bounds(u, true, "f32")
         assert np.all(np.abs(host(got) - true) <= em + M.rounding(np.abs(true) + em, "bf16"))
+
+
+@pytest.mark.parametrize("size", [1e-36, 1e-41])
+@pytest.mark.parametrize("rows,cols", [(30, 20), (70, 130), (300, 200)])
+def test_norms_whose_reciprocal_fp32_does_not_hold(size, rows, cols):
+    """eps = 0 and values down to fp32's subnormal ones, for orthogonalize and a Muon step from no
+    momentum and weights of zeros (whose update, 0.05 + 0.95 x 0.05 of the gradient, has its direction
+    up to four roundings, which among subnormal numbers are 2^-150 each)."""
+    gen = torch.Generator(device="cuda").manual_seed(32)
+    x = matrix(gen, rows, cols) * size
+    near(tg.orthogonalize(x, eps=0.0), host(x), "f32", "orthogonalize", eps=0.0)
+    if size < 1e-38:
+        return
+    w = torch.zeros(rows, cols, device="cuda")
+    opt = tg.Muon([(rows, cols)], "f32", lr=1.0, weight_decay=0.0, scale=1.0, eps=0.0)
+    opt.step([w], [x])
+    near(-w, host(x), "f32", "step", eps=0.0)
