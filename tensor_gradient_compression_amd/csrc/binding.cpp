@@ -43,7 +43,7 @@ struct Plan {
   tgrad_muon_t* muon = nullptr;
   int device = 0, bits = 32;
   int64_t total = 0;
-  std::vector<int64_t> numel;
+  std::vector<int64_t> numel, cols;   // the latter of Muon's matrices
   std::vector<c10::ScalarType> wt, gt;
   std::vector<void*> w;
   std::vector<const void*> g;
@@ -192,6 +192,16 @@ PyObject* adamw_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Muon's: a contiguous tensor is given flat, or by axes of which the last ones join to a matrix's rows. (The
+// rows may be those of several matrices in one axis.)
+void matrices(const Plan* p, const at::Tensor& t, const char* what, long i) {
+  if (!p->muon || t.dim() < 2 || t.numel() == 0) return;
+  int64_t n = 1;
+  for (int64_t k = t.dim(); n < p->cols[i] && k > 0;) n *= t.size(--k);
+  if (n != p->cols[i])
+    throw Invalid{named(what, i) + ": its last axes do not form rows of " + std::to_string(p->cols[i]) + " values"};
+}
+
 void weights_of(Plan* p, const Sequence& ws) {
   if (ws.size() != (long)p->numel.size())
     throw Invalid{"weights: " + std::to_string(ws.size()) + " tensors, the handle has " +
@@ -203,6 +213,7 @@ void weights_of(Plan* p, const Sequence& ws) {
       throw Invalid{named("weights", i) + ": " + std::to_string(t.numel()) + " elements, expected " +
                     std::to_string(p->numel[i])};
     if (!t.is_contiguous()) throw Invalid{named("weights", i) + ": must be contiguous"};
+    matrices(p, t, "weights", i);
     p->w[i] = data_of(t);
   }
 }
@@ -219,6 +230,7 @@ void gradients(Plan* p, PyObject* list) {
       throw Invalid{named("grads", i) + ": " + std::to_string(t.numel()) + " elements, expected " +
                     std::to_string(p->numel[i])};
     if (!t.is_contiguous()) throw Invalid{named("grads", i) + ": must be contiguous"};
+    matrices(p, t, "grads", i);
     p->g[i] = data_of(t);
   }
 }
@@ -420,16 +432,17 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// muon_plan(handle, device, numels, dtype codes, gradient dtype codes)
+// muon_plan(handle, device, numels, dtype codes, gradient dtype codes, cols)
 PyObject* muon_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    want(n, 5, "muon_plan");
+    want(n, 6, "muon_plan");
     std::vector<int64_t> wt = ints(a[3], "dtypes"), gt = ints(a[4], "grad dtypes");
     std::unique_ptr<Plan> p(new Plan());
     p->muon = (tgrad_muon_t*)PyLong_AsVoidPtr(a[0]);
     p->device = (int)PyLong_AsLong(a[1]);
     if (PyErr_Occurred()) throw Raised{};
     p->numel = ints(a[2], "numels");
+    p->cols = ints(a[5], "cols");
     for (int64_t c : wt) p->wt.push_back(scalar_type((int)c));
     for (int64_t c : gt) p->gt.push_back(scalar_type((int)c));
     p->w.resize(p->numel.size());

@@ -103,7 +103,7 @@ class Muon:
         if rc != _tg.OK:
             raise _tg.TGradError(f"tgrad_muon_init: {self._lib.tgrad_status_string(rc).decode()}")
         self._h = h
-        self._plan = bind.muon_plan(h.value, self.device_index, numels, dts, gts)
+        self._plan = bind.muon_plan(h.value, self.device_index, numels, dts, gts, list(ck))
         self._step = bind.muon_step
 
     # ---------------------------------------------------------------- lifecycle
@@ -122,9 +122,9 @@ class Muon:
     # ---------------------------------------------------------------- hot path
     def step(self, weights, grads, clip=None, stream=None):
         """One step of every tensor: weights[i] is updated in place from grads[i] (contiguous
-        GPU tensors of as many elements as shapes[i]; no weight overlaps another). clip: what AdamW.grad_norm returned, the
-        norm over this optimizer's gradients or over more; where it is not finite, nothing
-        changes."""
+        GPU tensors of as many elements as shapes[i], flat or by axes of which the last join to a row; no
+        weight overlaps another or a gradient). clip: what AdamW.grad_norm returned, the norm over this
+        optimizer's gradients or over more; where it is not finite, nothing changes."""
         self._step(self._plan, weights, grads, clip, _stream(stream))
 
     def set_lr(self, lr: float):

@@ -453,3 +453,31 @@ def test_norms_whose_reciprocal_fp32_does_not_hold(size, rows, cols):
     opt = tg.Muon([(rows, cols)], "f32", lr=1.0, weight_decay=0.0, scale=1.0, eps=0.0)
     opt.step([w], [x])
     near(-w, host(x), "f32", "step", eps=0.0)
+
+
+def test_shapes_that_are_others():
+    """A weight or gradient whose last axes do not form rows of cols values is refused, and not taken as
+    another matrix of as many elements; flat values, axes that do form them and several matrices' rows in one
+    axis are taken."""
+    opt = tg.Muon([(72, 24), (2, 16, 27), (5, 1)], "f32", lr=0.02)
+
+    def given(*shapes):
+        gen = torch.Generator(device="cuda").manual_seed(33)
+        return [torch.randn(math.prod(s), generator=gen, device="cuda").view(s) for s in shapes]
+
+    right = ((72, 24), (2, 16, 27), (5, 1))
+    for i, other in ((0, (24, 72)), (0, (36, 48)), (1, (2, 27, 16)), (1, (27, 32)), (1, (864, 1))):
+        bad = [s if k != i else other for k, s in enumerate(right)]
+        with pytest.raises(ValueError, match="weights"):
+            opt.step(given(*bad), given(*right))
+        with pytest.raises(ValueError, match="grads"):
+            opt.step(given(*right), given(*bad))
+    assert not opt.state["momentum"].any()
+    want = None
+    for form in (right, ((1728,), (32, 3, 3, 3), (5,)), ((8, 9, 24), (2, 16, 3, 9), (1, 5)), ((72, 2, 12), (32, 27), (5, 1, 1))):
+        opt.state["momentum"].zero_()
+        w = given(*form)
+        opt.step(w, given(*form))
+        flat = torch.cat([x.reshape(-1) for x in w])
+        want = flat if want is None else want
+        assert torch.equal(flat, want)
