@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(WAVES * 64, WAVES / 4)
 template <int WAVES, int RB, int SLOTS, bool EXACT, class Table>
 hipError_t launch(const NsCommon& c, const NsSmall& k, const MuonFirst& f, const Table& t, const NsSource& src,
                   const NsParts& p, uint32_t n, hipStream_t s) {
-  if (n > 0x7FFFFFFFu / (WAVES * 64)) return hipErrorInvalidValue;
+  if (n > 0xFFFFFFFFu / (WAVES * 64)) return hipErrorInvalidValue;   // threads of a launch in 32 bits
   auto* const kernel = k_ns_small<WAVES, RB, SLOTS, EXACT, Table>;
   const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, NS_SMALL_LDS);
   if (e != hipSuccess) return e;

@@ -481,3 +481,18 @@ def test_shapes_that_are_others():
         flat = torch.cat([x.reshape(-1) for x in w])
         want = flat if want is None else want
         assert torch.equal(flat, want)
+
+
+def test_as_many_matrices_as_a_launch_takes():
+    """2^21 of them, each of a workgroup of 1024 threads: a row's only singular value goes through the
+    iteration's polynomial from 1 on."""
+    n = 1 << 21
+    x = torch.ones(n, 1, 288, device="cuda", dtype=torch.bfloat16)
+    x[:, 0, 0] = 1 - 2 * (torch.arange(n, device="cuda") % 2)
+    y = tg.orthogonalize(x)
+    a, b, c = M.COEFFICIENTS
+    s = 1.0
+    for _ in range(5):
+        s = s * (a + b * s ** 2 + c * s ** 4)
+    value = s / math.sqrt(288)
+    assert torch.all((y * x).float().sub_(value).abs_() <= 2.0 ** -8 * value)
