@@ -610,8 +610,9 @@ int tgrad_muon_step(tgrad_muon_t *h, void *const *weights, const void *const *gr
  * The workspace's size is that of a call with the same x, strides and weights, whose alignment
  * matters (rows that are not 16-byte aligned or no multiple of 8 values are copied); backward: 0
  * or 1; -1 for invalid sizes. Host only.
- * rows = 0 is valid (the weights' gradients become 0). 1 <= in, hidden <= 2^19. Every pointer
- * is aligned to its element. Errors: TGRAD_EINVAL, TGRAD_EHIP.
+ * rows = 0 is valid (the weights' gradients become 0). rows <= 2^31 - 65537, 1 <= in, hidden <=
+ * 2^19, and the copies of a call hold at most 2^35 values (else TGRAD_EHIP). Every pointer is
+ * aligned to its element. Errors: TGRAD_EINVAL, TGRAD_EHIP.
  */
 enum tgrad_activation { TGRAD_SILU = 0, TGRAD_GELU = 1, TGRAD_SIGMOID = 2, TGRAD_RELU = 3 };
 int64_t tgrad_gated_linear_workspace(const void *x, int64_t x_stride, const void *w_gate,

@@ -5,6 +5,8 @@
 
 namespace tg {
 
+constexpr int64_t kMostThreads = 0xFFFFFFFF;   // of a launch
+
 enum GatedAct { GATED_SILU = 0, GATED_GELU, GATED_SIGMOID, GATED_RELU, GATED_ACTS };
 
 // A matrix in the parts that the products take: one of its own 16-bit values, or three of bf16

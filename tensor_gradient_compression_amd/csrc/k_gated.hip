@@ -391,7 +391,7 @@ template <class S, int DT>
 hipError_t launch_tiles(bool grads, const GatedArgs& a, hipStream_t s) {
   const int64_t ni = (a.rows + S::BM - 1) / S::BM;
   const int64_t nj = ((grads ? gated_pad(a.hidden) : a.hidden) + S::BN / 2 - 1) / (S::BN / 2);
-  if (ni * nj > 0x7FFFFFFF / S::THREADS) return hipErrorInvalidValue;
+  if (ni * nj > kMostThreads / S::THREADS) return hipErrorInvalidValue;
   void (*k)(GatedArgs) = k_gated_forward<S, DT>;
   if constexpr (S::MODE != MM_EVEN || S::BN == 128)   // those of gated_tile()
     if (grads) k = k_gated_grads<S, DT>;
@@ -448,7 +448,7 @@ hipError_t launch_gated_pack(const GatedPack* m, int n, hipStream_t s) {
     groups += ((uint64_t)m[i].rows * (gated_pad(m[i].cols) / 8) + 255) / 256;
   }
   if (groups == 0) return hipSuccess;
-  if (groups > 0x7FFFFFFF / 256) return hipErrorInvalidValue;
+  if (groups > kMostThreads / 256) return hipErrorInvalidValue;
   k_gated_pack<<<(uint32_t)groups, 256, 0, s>>>(a);
   return hipGetLastError();
 }

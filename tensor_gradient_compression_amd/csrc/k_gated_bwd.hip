@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(256) k_gated_join_rows(const float* p, int64_t
 
 template <class S, class K, class A>
 hipError_t launch_tiles(K* k, int64_t tiles, int splits, int64_t size, const A& a, hipStream_t s) {
-  if (tiles > 0x7FFFFFFF / S::THREADS) return hipErrorInvalidValue;
+  if (tiles > kMostThreads / S::THREADS) return hipErrorInvalidValue;
   const hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS_BYTES);
   if (e != hipSuccess) return e;
   k<<<dim3((uint32_t)tiles, (uint32_t)splits), S::THREADS, S::LDS_BYTES, s>>>(a, size);
@@ -238,7 +238,7 @@ hipError_t dx_type(const GatedDx& a, hipStream_t s) {
   if (e != hipSuccess || n == 1 || a.way.counted) return e;
   using T = typename GatedType<DT>::T;
   const int64_t v = a.rows * a.in;
-  if ((v + 255) / 256 > 0x7FFFFFFF / 256) return hipErrorInvalidValue;
+  if ((v + 255) / 256 > kMostThreads / 256) return hipErrorInvalidValue;
   k_gated_join<T><<<(uint32_t)((v + 255) / 256), 256, 0, s>>>((const float*)a.sums, n, v, v, (T*)a.dx, (T*)a.dx, v, 0);
   return hipGetLastError();
 }
@@ -256,7 +256,7 @@ hipError_t dw_type(const GatedDw& a, hipStream_t s) {
                           : launch_tiles<Near>(k_gated_dw<Near, DT>, tiles, n, size, a, s);
   if (e == hipSuccess && a.dwg && n > 1 && !a.way.counted) {
     const int64_t v = 2 * (int64_t)a.hidden * a.in;
-    if ((v + 255) / 256 > 0x7FFFFFFF / 256) return hipErrorInvalidValue;
+    if ((v + 255) / 256 > kMostThreads / 256) return hipErrorInvalidValue;
     k_gated_join<T><<<(uint32_t)((v + 255) / 256), 256, 0, s>>>((const float*)a.sums, n, v, v, (T*)a.dwg, (T*)a.dwu, v / 2,
                                                                 v / 2);
     e = hipGetLastError();

@@ -448,3 +448,21 @@ def test_slopes_of_far_gelu_gates(dtype):
 
     slopes(torch.arange(-6.5, 6.6, 0.25), "gelu", dtype, terms,
            lambda g: (3 * g * g / 2 + 6 * 2) * 2.0 ** -24 + 7.4e-6)
+
+
+def test_more_than_2_to_the_30_rows():
+    """Every value is a sum of few powers of two, exact in any order; the last row is another."""
+    rows = (1 << 30) + (1 << 26)
+    one = dict(device="cuda", dtype=torch.bfloat16)
+    x, w, b = torch.ones(rows, 8, **one), torch.full((8, 8), 0.125, **one), torch.ones(8, **one)
+    x[-1] = 2
+    y = tg.gated_linear_forward(x, w, w, b, b, activation="relu")      # g = u = 2, and 3 in the last row
+    assert torch.all(y[:-1] == 4) and torch.all(y[-1] == 9)
+    y.fill_(1)
+    dx, dwg, dwu, dbg, dbu = tg.gated_linear_backward(y, x, w, w, b, b, activation="relu")
+    assert torch.all(dx[:-1] == 4) and torch.all(dx[-1] == 6)
+    total = torch.tensor(2.0 * rows).bfloat16()
+    for t in (dwg, dwu, dbg, dbu):
+        assert torch.all(t.cpu() == total), t
+    del x, y, dx
+    torch.cuda.empty_cache()
