@@ -466,3 +466,8 @@ def test_more_than_2_to_the_30_rows():
         assert torch.all(t.cpu() == total), t
     del x, y, dx
     torch.cuda.empty_cache()
+
+
+def test_the_largest_tiles_in_fp32():
+    """g and u, dx and the weights' gradients all by 256 x 256, six segments each."""
+    check(*inputs(3000, 2101, 2100, "f32", seed=41), "gelu", "f32")

@@ -496,3 +496,38 @@ def test_as_many_matrices_as_a_launch_takes():
         s = s * (a + b * s ** 2 + c * s ** 4)
     value = s / math.sqrt(288)
     assert torch.all((y * x).float().sub_(value).abs_() <= 2.0 ** -8 * value)
+
+
+# By 128 x 128 and 256 x 256, in one workgroup a unit and in two, wide and tall, of one product of parts and of
+# three, sums whole and shared: A, B and B X each meet all of them among these. (Up to 48 of 500 x 500 A is of 128 x 128
+# tiles, from 24 of 1000 x 1000 on 256 x 256; B X of 64 of 500 x 500 is of 256 x 256.)
+TILES = [(48, 499, 501, "bf16"), (48, 501, 499, "f16"), (24, 1001, 499, "bf16"), (24, 1001, 499, "f32"), (12, 257, 771, "bf16"),
+         (12, 771, 257, "bf16"), (64, 1001, 499, "f16"), (12, 771, 257, "f32"), (12, 257, 771, "f16"), (24, 499, 501, "bf16"),
+         (64, 499, 501, "bf16"), (64, 507, 499, "bf16"), (48, 507, 499, "bf16"), (24, 499, 501, "f32"), (64, 499, 501, "f32"),
+         (24, 1001, 1003, "bf16"), (24, 999, 1001, "f32"), (24, 1007, 1001, "bf16"), (24, 1555, 777, "f16"),
+         (6, 777, 3885, "f16"), (6, 3885, 777, "f32"), (8, 499, 1497, "f32"), (8, 1497, 499, "f16"), (3, 777, 3885, "bf16"),
+         (3, 3885, 777, "bf16"), (1, 1501, 1509, "f16"), (1, 1509, 1501, "f32")]
+
+
+@pytest.mark.parametrize("count,rows,cols,dtype", TILES)
+def test_larger_tiles(count, rows, cols, dtype):
+    """The first and the last matrix, against the oracle; all of them again, bit for bit."""
+    print(f"CASE tiles {count} {rows} {cols} {dtype}", flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(rows + cols)
+    x = torch.stack([matrix(gen, rows, cols) for _ in range(count)]).to(tg.torch_dtype(dtype))
+    y = tg.orthogonalize(x)
+    for i in {0, count - 1}:
+        near(y[i], host(x[i]), dtype, f"matrix {i}")
+    assert torch.equal(tg.orthogonalize(x), y)
+
+
+@pytest.mark.parametrize("count,rows,cols,dtype", [(24, 1001, 1003, "bf16"), (24, 1007, 1001, "f16"), (48, 499, 501, "f32")])
+def test_muon_steps_by_larger_tiles(count, rows, cols, dtype):
+    w, g = tensors([(count, rows, cols)], dtype, dtype, 34)
+    opt = tg.Muon([(count, rows, cols)], dtype, lr=0.05, weight_decay=0.1)
+    before = [x.clone() for x in w]
+    opt.step(w, g)
+    # the last matrix alone, as a tensor of its own
+    last = tg.Muon([(rows, cols)], dtype, lr=0.05, weight_decay=0.1)
+    last.state["momentum"][:rows * cols] = opt.state["momentum"][(count - 1) * rows * cols:count * rows * cols]
+    check_step(last, [w[0][-1]], [g[0][-1]], np.zeros(rows * cols), [before[0][-1]])
