@@ -76,7 +76,8 @@ GatedWay gated_dw_way(int64_t rows, uint32_t in, uint32_t hidden, int parts);
 // gradients are then sqrt(2) times as far off as their own rounding, since as many independent
 // roundings as there are dg enter them. Few do not average (33 values: 1.55 times), nor do few results: up to
 // 2^14 values, or 2^19 of which some result has up to 2^10, go in two parts, whose products are bound by
-// their launches anyway.
+// their launches anyway. (None of them is of 256 x 256 tiles, whose kernel writes one part: 2^14 values are
+// 129 such tiles at most, and where some result has 2^10 values `in` is not above 1024.)
 inline int gated_grad_parts(int64_t rows, int64_t in, int64_t hidden, int dt) {
   if (dt == DT_F32) return 3;
   const int64_t n = rows * hidden, results = (rows < hidden ? rows : hidden) * in;
@@ -117,7 +118,16 @@ struct GatedDw {
 hipError_t launch_gated_dw(const GatedDw& a, hipStream_t s);
 
 // The tile of the products of g and u: 0: 256 x 256, 1: 128 x 128, 2 and 4: 64 x 64, 3: 128 x 256.
-int gated_tile(int64_t rows, int64_t hidden, int64_t in, bool grads);
+// 256 x 256 where its tiles fill the chip, smaller ones for short sums, whose epilogue is most of the
+// time: two workgroups of a CU overlap theirs (65536 x 256 x 1024 in bf16, the epilogue alike in both:
+// forward 170 us by 128 x 256, 183 by 128 x 128; the gradients, which need more registers, 283 and 221).
+// 64 x 64 for few tiles: by one workgroup a CU that splits the sum, or two that do not (768 x 2048 over
+// 768, 384 tiles: 11.8 us and 9.2; 768 x 768 over 2048, 144 tiles: 10.6 and 13.0).
+inline int gated_tile(int64_t rows, int64_t hidden, int64_t in, bool grads) {
+  auto tiles = [&](int64_t t) { return ((rows + t - 1) / t) * ((2 * hidden + t - 1) / t); };
+  if (tiles(256) >= 200) return in > 1024 ? 0 : grads ? 1 : 3;
+  return tiles(128) >= 200 ? 1 : tiles(64) > 256 ? 4 : 2;
+}
 
 template <int DT> struct GatedType;
 template <> struct GatedType<DT_F32> { using T = float; static constexpr int MM = DT_BF16, SEGS = 6; };

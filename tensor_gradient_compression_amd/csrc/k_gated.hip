@@ -417,17 +417,6 @@ hipError_t launch_any(bool grads, const GatedArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// 256 x 256 where its tiles fill the chip, smaller ones for short sums, whose epilogue is most of the
-// time: two workgroups of a CU overlap theirs (65536 x 256 x 1024 in bf16, the epilogue alike in both:
-// forward 170 us by 128 x 256, 183 by 128 x 128; the gradients, which need more registers, 283 and 221).
-// 64 x 64 for few tiles: by one workgroup a CU that splits the sum, or two that do not (768 x 2048 over
-// 768, 384 tiles: 11.8 us and 9.2; 768 x 768 over 2048, 144 tiles: 10.6 and 13.0).
-int gated_tile(int64_t rows, int64_t hidden, int64_t in, bool grads) {
-  auto tiles = [&](int64_t t) { return ((rows + t - 1) / t) * ((2 * hidden + t - 1) / t); };
-  if (tiles(256) >= 200) return in > 1024 ? 0 : grads ? 1 : 3;
-  return tiles(128) >= 200 ? 1 : tiles(64) > 256 ? 4 : 2;
-}
-
 int64_t gated_sum_rows(int64_t rows, uint32_t in, uint32_t hidden) {
   const int t = gated_tile(rows, hidden, in, true);
   auto sums = [&](auto shape) { return (rows + shape.BM - 1) / shape.BM * shape.WM; };

@@ -122,7 +122,18 @@ static void newton_schulz(uint32_t rows, uint32_t cols) {
   }
 }
 
+// dg and du in two parts never meet the kernel of 256 x 256 tiles, which writes one.
+static void two_parts_in_small_tiles() {
+  what = "two parts in the largest tiles";
+  for (int64_t rows = 1; rows <= 1 << 19; rows += rows < 600 ? 1 : rows / 7)
+    for (int64_t hidden = 1; hidden <= 1 << 19; hidden += hidden < 300 ? 1 : hidden / 7)
+      for (int64_t in : {1, 8, 512, 1024, 1025, 1 << 19})
+        if (gated_grad_parts(rows, in, hidden, DT_BF16) == 2 && gated_tile(rows, hidden, in, true) == 0 && failures++ < 5)
+          printf("%s: %lld %lld %lld\n", what, (long long)rows, (long long)in, (long long)hidden);
+}
+
 int main() {
+  two_parts_in_small_tiles();
   for (int64_t rows : {1, 70, 300})
     for (uint32_t in : {1u, 8u, 65u, 136u, 264u, 320u, 333u, 520u})
       for (uint32_t hidden : {1u, 33u, 64u, 129u, 257u, 264u, 288u, 289u, 330u}) gated(rows, in, hidden);
@@ -134,6 +145,6 @@ int main() {
       newton_schulz<MmDeep>(rows, cols);
       newton_schulz<MmNear>(rows, cols);
     }
-  printf("%ld accesses outside\n", failures);
+  printf("%ld failures\n", failures);
   return failures != 0;
 }
