@@ -596,7 +596,8 @@ int tgrad_muon_step(tgrad_muon_t *h, void *const *weights, const void *const *gr
  * sigmoid or relu (with slope 0 at 0). Sums are fp32, y is rounded once. The gradients form g
  * and u again from x; 16-bit dg and du are rounded to that type between the products, and few of
  * them (up to 2^14 of each, or 2^19 for results of up to 2^10) carried in two such parts (db comes
- * from the values before). fp32 products are made of six products of bf16 parts, as exact as
+ * from the values before). In fp16 that is its range too: a dg or du over 65504 is infinite in the
+ * products, also where dx or dw would not be. fp32 products are made of six products of bf16 parts, as exact as
  * fp32 sums; a value that is not finite makes what it enters NaN there. Results do not depend
  * on the order in which workgroups run.
  *   x, dy           device, rows x_stride >= in (dy_stride >= hidden, <= 2^20) elements apart

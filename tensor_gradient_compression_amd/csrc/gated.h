@@ -119,8 +119,11 @@ hipError_t launch_gated_dw(const GatedDw& a, hipStream_t s);
 
 // The tile of the products of g and u: 0: 256 x 256, 1: 128 x 128, 2 and 4: 64 x 64, 3: 128 x 256.
 // 256 x 256 where its tiles fill the chip, smaller ones for short sums, whose epilogue is most of the
-// time: two workgroups of a CU overlap theirs (65536 x 256 x 1024 in bf16, the epilogue alike in both:
-// forward 170 us by 128 x 256, 183 by 128 x 128; the gradients, which need more registers, 283 and 221).
+// time: two workgroups of a CU overlap theirs. 8192 rows to 8192 in bf16 with silu, forward and gradients in
+// us, by 256 x 256 and by smaller tiles:  in = 256: 100, 211 and 91, 186;  512: 155, 257 and 152, 257;
+// 1024: 250, 355 and 269, 371;  2048: 445, 544 and 496, 609;  4096: 865, 924 and 1007, 1095. The smaller one
+// is of 128 x 256 forward (65536 x 256 x 1024: 170 us, 128 x 128 183) and of 128 x 128 for the gradients, which
+// need more registers (128 x 256 283 us, 128 x 128 221).
 // 64 x 64 for few tiles: by one workgroup a CU that splits the sum, or two that do not (768 x 2048 over
 // 768, 384 tiles: 11.8 us and 9.2; 768 x 768 over 2048, 144 tiles: 10.6 and 13.0).
 inline int gated_tile(int64_t rows, int64_t hidden, int64_t in, bool grads) {

@@ -94,8 +94,8 @@ __device__ __forceinline__ void leave(const MmSums<S>& sums, T* out, float* part
   else leave_as(sums, out, row0, lo, hi, n0, cols);
 }
 
-// dx: one sum over the gate's and the other weight's hidden values (65536 x 256 x 1024 in bf16: 80 us, 860
-// TFLOP/s, one tile a CU that waits for 268 MB of dg and du; 8192 x 4096 x 8192: 927 us, 1186).
+// dx: one sum over the gate's and the other weight's hidden values (65536 x 256 x 1024 in bf16: 84 us, 820
+// TFLOP/s, one tile a CU that waits for 268 MB of dg and du; 8192 x 4096 x 8192: 907 us, 1212).
 template <class S, int DT>
 __global__ void __launch_bounds__(S::THREADS, 2) k_gated_dx(const GatedDx a, const int64_t size) {
   using G = GatedType<DT>;
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_dx(const GatedDx a, con
   leave(sums, (T*)a.dx, part, row0, 0, a.rows - row0, n0, a.in);
 }
 
-// dWg and dWu (65536 x 256 x 1024 in bf16: 92 us in 32 splits; 8192 x 4096 x 8192: 970 us, 1133 TFLOP/s,
+// dWg and dWu (65536 x 256 x 1024 in bf16: 93 us in 32 splits; 8192 x 4096 x 8192: 948 us, 1160 TFLOP/s,
 // where a library's product of two crossed operands reaches 1112).
 template <class S, int DT>
 __global__ void __launch_bounds__(S::THREADS, 2) k_gated_dw(const GatedDw a, const int64_t size) {
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_gated_dw(const GatedDw a, con
 }
 
 // out[v] = the sum of the n values v of `rows` rows, in their order; the values from `half` on
-// go to out2 (32 rows of 524288: 11 us, 6 TB/s from the last-level cache)
+// go to out2 (32 rows of 524288: 11.5 us, 5.8 TB/s from the last-level cache)
 template <typename T>
 __global__ void __launch_bounds__(256) k_gated_join(const float* p, int64_t rows, int64_t pitch, int64_t n, T* out,
                                                     T* out2, int64_t half, int64_t half_at) {
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(256) k_gated_join(const float* p, int64_t rows
   else out2[v - half] = from_f32<T>(s);
 }
 // The same for few columns and many rows: a workgroup takes 16 columns, 16 threads each
-// (1024 rows of 2048: 7 us).
+// (1024 rows of 2048: 7.5 us).
 template <typename T>
 __global__ void __launch_bounds__(256) k_gated_join_rows(const float* p, int64_t rows, int64_t pitch, int64_t n, T* out,
                                                          T* out2, int64_t half, int64_t half_at) {

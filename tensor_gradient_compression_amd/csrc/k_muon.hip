@@ -19,9 +19,9 @@
 // 1.7e-3); most of it is the lower part of X that B X leaves out. For fp32 and fp16 results the products take both parts of X, A and B
 // (three products of parts; 3e-7 to 1e-5), which is `exact` here.
 //
-// What bounds it: matrix instructions for large matrices (8192 x 8192 in bf16: 12.2 ms, its products
-// at 800 to 1050 TFLOP/s); launches for middle ones (two, and three for every step; 777 x 2051 in fp16
-// 320 us, in bf16 205); small ones are k_muon_small.hip's. All matrices of a handle share every launch.
+// What bounds it: matrix instructions for large matrices (8192 x 8192 in bf16: 12.0 ms; B X at 1115
+// TFLOP/s, and A and A A, whose 528 tiles are three rounds of 256 with 16 tiles in the last, at 820); launches for middle ones (two, and three for every step; 777 x 2051 in fp16
+// 325 us, in bf16 191); small ones are k_muon_small.hip's. All matrices of a handle share every launch.
 // Of the symmetric products only the tiles on and below the diagonal are formed.
 #include "muon.h"
 #include "muon_common.h"
@@ -72,8 +72,8 @@ __device__ __forceinline__ void load_piece(const T* p, uint32_t n, float* v) {
   for (int e = 0; e < 8; ++e) v[e] = to_f32(raw[e]);
 }
 
-// New momentum, and the sums of squares of the update: memory's (75M values of bf16 gradients 145 us,
-// 5.2 TB/s). The update itself is formed again by the next pass, which costs a gradient's bytes where
+// New momentum, and the sums of squares of the update: memory's (75M values of bf16 gradients 143 us,
+// 5.3 TB/s). The update itself is formed again by the next pass, which costs a gradient's bytes where
 // keeping it would cost four, twice.
 __global__ void __launch_bounds__(256) k_muon_first(const NsCommon c, const MuonFirst f, const MuonTable t,
                                                     const NsParts p) {
@@ -162,7 +162,7 @@ __device__ __forceinline__ void write_x(const NsCommon& c, const NsMat& m, uint3
   *(uint4*)(hi + (uint64_t)m.rows * m.ldx) = *(const uint4*)l;
 }
 
-// X in its parts from the update: memory's (75M values of bf16 gradients 146 us, 5.2 TB/s).
+// X in its parts from the update: memory's (75M values of bf16 gradients 145 us, 5.2 TB/s).
 __global__ void __launch_bounds__(256) k_muon_start(const NsCommon c, const MuonFirst f, const double eps, const NsParts p) {
   if (left_out(c)) return;
   clear_counters(c);
@@ -316,8 +316,8 @@ __device__ __forceinline__ void on_diagonal(const NsMat& m, const Place<S>& at, 
 __device__ __forceinline__ float pick(const float* v, uint32_t e) { return e == 0 ? v[0] : e == 1 ? v[1] : e == 2 ? v[2] : v[3]; }
 
 // A = X X^T (X^T X): its diagonal, and the rest under NS_M. Both operands are X, by its rows or across
-// them. Matrix instructions' and LDS's (18 of 1024 x 4096: 121 us, 640 TFLOP/s on 180 tiles; 8192 x 8192
-// 682, 830), latency's with few tiles (777 x 2051, three products in five splits: 20 us).
+// them. Matrix instructions' and LDS's (18 of 1024 x 4096: 112 us, 690 TFLOP/s on 180 tiles; 8192 x 8192
+// 669, 820), latency's with few tiles (777 x 2051, three products in five splits: 20 us).
 template <class S>
 __global__ void __launch_bounds__(S::THREADS, 2) k_ns_gram(const NsCommon c, const int at, const NsParts p) {
   extern __shared__ char lds_raw[];
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_ns_gram(const NsCommon c, con
 }
 
 // B = b A + c A A from A off its diagonal, O: A A = D D + D O + O D + O O, so that the products
-// see only O. As k_ns_gram (18 of 1024: 52 us; 8192: 683).
+// see only O. As k_ns_gram (18 of 1024: 51 us; 8192: 668).
 template <class S>
 __global__ void __launch_bounds__(S::THREADS, 2) k_ns_poly(const NsCommon c, const NsParts p) {
   extern __shared__ char lds_raw[];
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(S::THREADS, 2) k_ns_poly(const NsCommon c, con
 
 // X = a X + B X (a X + X B), with B's diagonal in fp32 and X's parts read and written where the sums
 // are: 8 bytes a value of reading and writing after the products, which is half of the time where sums are
-// short (18 of 1024 x 4096: 314 us, 154 GFLOP and 600 MB; 8192 x 8192: 1047, 1050 TFLOP/s). The last one
+// short (18 of 1024 x 4096: 309 us, 154 GFLOP and 600 MB; 8192 x 8192: 986, 1115 TFLOP/s). The last one
 // writes the result, or the weights.
 template <class S>
 __global__ void __launch_bounds__(S::THREADS, 2) k_ns_apply(const NsCommon c, const int at, const NsLast last, const NsParts p) {

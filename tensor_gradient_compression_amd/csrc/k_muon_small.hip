@@ -369,7 +369,8 @@ hipError_t launch(const NsCommon& c, const NsSmall& k, const MuonFirst& f, const
 }
 // Matrices of up to eight parts of 16 x 32 have a wave for each; others parts of 32 x 32, which
 // take two thirds of the reads of LDS that set their pace (113 x 156 fp32: 105 us in parts of
-// 16 x 32).
+// 16 x 32, 70 in these). Four to a wave need more registers than there are: 68 to 112 bytes a lane go to
+// memory, in bf16 without a step none.
 template <bool EXACT, class Table>
 hipError_t launch_any(const NsCommon& c, const NsSmall& k, const MuonFirst& f, const Table& t, const NsSource& src,
                       const NsParts& p, uint32_t n, hipStream_t s) {
